@@ -219,6 +219,102 @@ litela_status lite_la_bwd_events(const void* qkv, const void* dout, void* dqkv, 
  * <= 0 means non-causal; a 148-SM device).  0 for invalid arguments or an empty problem. */
 size_t lite_la_bwd_workspace_bytes(int B, int N, int H, int d, int tokens_per_block);
 
+/* ---- head norms with rotation -----------------------------------------------------------
+ *
+ * RMS norm of every query and key head and rotation by position, on packed q|k|v rows, in one
+ * pass: what stands between the qkv projection and the attention (lite_la_fwd, or
+ * lite_la_gated_delta_fwd on views of the packed rows).  Per row and head, x its d channels and w
+ * the weight of q or of k,
+ *     y = R(position) (w * x / sqrt(mean(x^2) + eps)),
+ * where R turns the first `rot` channels in pairs, (a, b) -> (a cos - b sin, b cos + a sin), by
+ * the row `position` of the tables: channels (i, i + rot/2), or (2i, 2i + 1) when `interleaved`.
+ * The sums are fp32; the result is rounded to bf16 once.
+ *
+ * qkv      : bf16 [B, N, (Hq + Hk + Hv)*d], a row's heads of q, then of k, then of v.
+ * out      : the same layout; another buffer (v is copied) or qkv itself (v is left alone).
+ * q_weight, k_weight : fp32 [d], or NULL (ones).
+ * cos, sin : fp32 [table_len, rot/2]; both NULL when rot is 0.
+ * positions: [B, N] int32 (position_bytes 4) or int64 (8), or NULL: a token's index n, which then
+ *            needs table_len >= N.  A negative position marks a padded row: it is left alone
+ *            in place and set to zero in another buffer, and its gradient is zero.  A position
+ *            behind the table gives NaN in the channels that are rotated.
+ * d is 32, 64 or 128; rot a multiple of 16 up to d (LITELA_ERR_UNSUPPORTED otherwise).
+ *
+ * lite_la_qk_norm_rope_bwd: the gradient of sum(dout * out).  dout: bf16, the layout of out;
+ * dqkv: bf16, another buffer than qkv; it may be dout itself.  dq_weight, dk_weight: fp32 [d] or
+ * NULL (not wanted).  workspace: lite_la_qk_norm_rope_workspace_bytes() of device memory, 16-byte
+ * aligned, needed only for the weights' gradients; it belongs to the call until it has finished.
+ * All sums have a fixed order: equal calls give equal bits. */
+litela_status lite_la_qk_norm_rope_fwd(const void* qkv, void* out, const float* q_weight, const float* k_weight,
+                                       const float* cos, const float* sin, const void* positions, int position_bytes,
+                                       int B, int N, int Hq, int Hk, int Hv, int d, int rot, int table_len,
+                                       int interleaved, float eps, cudaStream_t stream);
+litela_status lite_la_qk_norm_rope_bwd(const void* qkv, const void* dout, void* dqkv, const float* q_weight,
+                                       const float* k_weight, float* dq_weight, float* dk_weight, const float* cos,
+                                       const float* sin, const void* positions, int position_bytes, int B, int N,
+                                       int Hq, int Hk, int Hv, int d, int rot, int table_len, int interleaved,
+                                       float eps, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+/* Bytes of workspace lite_la_qk_norm_rope_bwd needs on any device. */
+size_t lite_la_qk_norm_rope_workspace_bytes(int d);
+
+/* ---- the gated delta rule ---------------------------------------------------------------
+ *
+ * Linear attention of language models: causal per token, with a state that decays and that
+ * erases what it writes over.  Per sequence and value head, with q and k of its key head
+ * (h / (Hv/Hk)), the log decay g <= 0 and the write strength beta of a token, and a state S
+ * [d key channels, d value channels],
+ *     S <- e^g S + k (beta (v - e^g S^T k))^T,     out = scale * S^T q.
+ * g = -inf empties the state.  Keys are expected at unit length or below (with beta |k|^2 < 2 the
+ * recurrence is stable); they are taken as they are.  Sums and states are fp32, out is rounded to
+ * bf16 once.
+ *
+ * A view of q, k, v, out or a gradient: bf16 [B, N, heads, d] with any strides (in elements, the
+ * d channels of a head adjacent; multiples of 8) and a 16-byte aligned start, so that the q, k
+ * and v of packed rows are views.  Outputs must not overlap themselves or any input.
+ * g, beta: fp32 [B, N, Hv] with batch and token strides.  States: fp32 [sequences, Hv, d, d],
+ * densely packed, 16-byte aligned; state_in NULL is zeros, state_out NULL is not written;
+ * state_out may be state_in itself.
+ *
+ * cu_seqlens NULL: B sequences of N tokens.  Otherwise (packed) B is the number of sequences in
+ * one buffer of N tokens (the views' batch strides are not used) and sequence s is the tokens
+ * cu_seqlens[s] .. cu_seqlens[s+1] - 1 (device int32, B + 1 values, rising; lengths of 0 are
+ * fine).  Rows behind the last sequence are left as they were, or set to zero when zero_tail is
+ * not 0.  Offsets outside the buffer are cut to it; falling ones give unspecified values.
+ *
+ * workspace: device memory of lite_la_gated_delta_workspace_bytes(), 16-byte aligned, of the
+ * caller: it belongs to the call until it has finished (a captured call: to the graph).  No call
+ * allocates.  d is 32, 64 or 128, Hv a multiple of Hk (LITELA_ERR_UNSUPPORTED otherwise). */
+typedef struct {
+  void* data;
+  long long batch_stride, token_stride, head_stride;
+} lite_la_view;
+
+typedef struct {
+  lite_la_view q, k, v, out;
+  const float* g;
+  const float* beta;
+  long long g_batch_stride, g_token_stride, beta_batch_stride, beta_token_stride;
+  const float* state_in;
+  float* state_out;
+  const int* cu_seqlens;
+  int B, N, Hk, Hv, d;
+  float scale;
+  int zero_tail;
+  void* workspace;
+  size_t workspace_bytes;
+} lite_la_delta_args;
+
+litela_status lite_la_gated_delta_fwd(const lite_la_delta_args* args, cudaStream_t stream);
+size_t lite_la_gated_delta_workspace_bytes(int B, int N, int Hk, int Hv, int d, int packed);
+
+/* The one-token form for serving: token 0 of each of B rows (N must be 1, cu_seqlens NULL), with
+ * the states updated in place: state_in and state_out are the same pool, fp32 [pool, Hv, d, d],
+ * and row b's state is pool entry state_indices[b] (device int32; NULL: entry b, then pool >= B).
+ * A row whose index lies outside the pool (-1 marks a padded row), or that an earlier row has
+ * too, touches no state and gets zeros.  No workspace. */
+litela_status lite_la_gated_delta_step(const lite_la_delta_args* args, const int* state_indices, int pool,
+                                       cudaStream_t stream);
+
 /* Static description of a status code (never NULL). */
 const char* lite_la_status_string(litela_status status);
 

@@ -19,6 +19,8 @@ __all__ = [
     "lite_la_fwd_oproj", "lite_la_out_proj",
     "lite_la_workspace_bytes", "lite_la_release_workspace", "lite_la_forward_form",
     "lite_la_set_paired_min_chunk", "STATUS", "EXPORTED_SYMBOLS",
+    "lite_la_qk_norm_rope", "lite_la_qk_norm_rope_fwd", "lite_la_qk_norm_rope_bwd",
+    "lite_la_gated_delta_fwd", "lite_la_gated_delta_step",
 ]
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -73,6 +75,12 @@ _SIGNATURES = {
     "lite_la_fwd_oproj_events": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_float,
                                           _c_int, _vp, _vp]),
     "lite_la_out_proj": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp]),
+    "lite_la_qk_norm_rope_fwd": (_c_int, [_vp] * 7 + [_c_int] * 10 + [_c_float, _vp]),
+    "lite_la_qk_norm_rope_bwd": (_c_int, [_vp] * 10 + [_c_int] * 10 + [_c_float, _vp, _c_size, _vp]),
+    "lite_la_qk_norm_rope_workspace_bytes": (_c_size, [_c_int]),
+    "lite_la_gated_delta_fwd": (_c_int, [_vp, _vp]),
+    "lite_la_gated_delta_workspace_bytes": (_c_size, [_c_int] * 6),
+    "lite_la_gated_delta_step": (_c_int, [_vp, _vp, _c_int, _vp]),
 }
 EXPORTED_SYMBOLS = tuple(_SIGNATURES)
 
@@ -418,3 +426,10 @@ def lite_la_device_status(stream=None) -> None:
 
 def lite_la_release_workspace() -> None:
     _check(lib().lite_la_release_workspace())
+
+
+# the language-model operators (imported last: they use this module's helpers)
+from .seq import (  # noqa: E402
+    lite_la_gated_delta_fwd, lite_la_gated_delta_step, lite_la_qk_norm_rope, lite_la_qk_norm_rope_bwd,
+    lite_la_qk_norm_rope_fwd,
+)

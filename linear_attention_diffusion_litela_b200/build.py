@@ -17,7 +17,7 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_PATH = os.path.join(PKG_DIR, "liblitela.so")
-SOURCES = ["litela_abi.cu"]
+SOURCES = ["litela_abi.cu", "litela_seq_abi.cu"]
 PEAK_DIR = os.path.join(PKG_DIR, "peaks")
 FFMA_LIB_PATH = os.path.join(PKG_DIR, "liblitela_ffma_peak.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -35,7 +35,7 @@ def _nvcc_shared(out, sources, deps, verbose, extra_flags):
         lib_mtime = os.path.getmtime(out)
         if all(os.path.getmtime(p) <= lib_mtime for p in deps):
             return out
-    cmd = [nvcc_path(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "--shared",
+    cmd = [nvcc_path(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "--shared", "--threads", "0",
            "-Xcompiler", "-fPIC,-O2", "-cudart", "shared", "-Xptxas", "-v" if verbose else "-O3",
            "-I", os.path.join(ROOT, "include"),
            *(extra_flags or []),

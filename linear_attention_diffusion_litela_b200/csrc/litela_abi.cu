@@ -18,6 +18,7 @@
 #include <utility>
 
 #include "../../include/litela.h"
+#include "litela_host.h"
 #include "litela_plan.h"
 #include "litela_bwd.cuh"
 #include "litela_fused.cuh"
@@ -824,6 +825,16 @@ litela_status run_noalloc(const void* qkv, __nv_bfloat16* out, int B, int N, int
 }
 
 }  // namespace
+
+litela_status host_fail(litela_status s, const char* msg) { return fail(s, msg); }
+litela_status host_cuda_fail(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+void host_ok() { g_last_error.clear(); }
+litela_status host_device(int* dev, int* num_sms) {
+  const cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  return device_setup(num_sms);
+}
+
 }  // namespace litela
 
 extern "C" {
@@ -1016,7 +1027,7 @@ litela_status lite_la_device_status(cudaStream_t stream) {
   if (e != cudaSuccess) return litela::cuda_fail(e, "cudaGetDevice");
   e = cudaStreamSynchronize(stream);
   if (e != cudaSuccess) return litela::cuda_fail(e, "cudaStreamSynchronize");
-  int* words[2] = {nullptr, nullptr};
+  int* words[3] = {nullptr, nullptr, litela::delta_error_word(dev)};
   int* words_ws0 = nullptr;
   size_t ctl_words_ws = 0;
   {

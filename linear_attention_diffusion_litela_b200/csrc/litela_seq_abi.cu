@@ -1,0 +1,443 @@
+// C ABI of the language-model operators: the head norms with rotation and the gated delta rule.
+// Argument validation and launches; the operations, layouts and errors are documented in
+// include/litela.h.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/litela.h"
+#include "litela_delta.cuh"
+#include "litela_host.h"
+#include "litela_norm.cuh"
+
+namespace litela {
+
+// set by a kernel whose bounded wait ran out (lite_la_device_status reads and clears it)
+__device__ int g_delta_err;
+
+int* delta_error_word(int) {
+  void* p = nullptr;
+  if (cudaGetSymbolAddress(&p, g_delta_err) != cudaSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  return static_cast<int*>(p);
+}
+
+namespace {
+
+constexpr int kMaxTokens = 1 << 30;
+
+litela_status invalid(const char* msg) { return host_fail(LITELA_ERR_INVALID_ARGUMENT, msg); }
+litela_status unsupported(const char* msg) { return host_fail(LITELA_ERR_UNSUPPORTED, msg); }
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// a span of device memory
+struct Span {
+  uintptr_t lo = 0, hi = 0;
+};
+Span span(const void* p, size_t bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return p == nullptr || bytes == 0 ? Span{} : Span{a, a + bytes};
+}
+bool meet(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+// launches `k` as a programmatic dependent of the previous kernel in the stream when `pdl`
+template <typename... KArgs, typename... Args>
+cudaError_t launch_seq(void (*k)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t stream, bool pdl,
+                       Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k, static_cast<KArgs>(args)...);
+}
+
+// ---------------------------------------------------------------------------------------
+// head norms with rotation
+
+// CTAs of the backward at most: the workspace holds one pair of partial sums for each
+constexpr int kNormMaxGrid = 2048;
+
+struct NormCall {
+  const void *qkv, *dout;
+  void* out;
+  const float *wq, *wk, *cos, *sin;
+  const void* pos;
+  int pos_bytes, B, N, Hq, Hk, Hv, d, rot, table, inter;
+  float eps;
+};
+
+litela_status norm_validate(const NormCall& c, bool bwd, bool* empty) {
+  *empty = false;
+  if (c.B < 0 || c.N < 0 || c.Hq < 0 || c.Hk < 0 || c.Hv < 0) return invalid("B, N, Hq, Hk and Hv must be >= 0");
+  if (c.B > 65535 || c.N > kMaxTokens || c.Hq > 65535 || c.Hk > 65535 || c.Hv > 65535)
+    return invalid("B and the heads must be <= 65535, N <= 2^30");
+  if (c.d != 32 && c.d != 64 && c.d != 128) return unsupported("d must be 32, 64 or 128");
+  if (c.rot < 0 || c.rot > c.d || c.rot % 16 != 0) return unsupported("rot must be a multiple of 16 up to d");
+  if (!std::isfinite(c.eps) || c.eps < 0.f) return invalid("eps must be finite and >= 0");
+  if (c.rot > 0 && c.table < 1) return invalid("the tables need at least one position");
+  if (c.pos != nullptr && c.pos_bytes != 4 && c.pos_bytes != 8) return invalid("position_bytes must be 4 or 8");
+  if (c.rot > 0 && c.pos == nullptr && c.table < c.N) return invalid("the tables are shorter than N");
+  const double elems = (double)c.B * c.N * ((double)c.Hq + c.Hk + c.Hv) * c.d;
+  if (elems > 4.0e18) return invalid("element count overflows int64");
+  if (((long long)c.Hq + c.Hk + c.Hv) * c.d > (1 << 30)) return invalid("a row has more than 2^30 channels");
+  if (elems == 0) {
+    *empty = true;
+    return LITELA_OK;
+  }
+  if (c.qkv == nullptr || c.out == nullptr || (bwd && c.dout == nullptr)) return invalid("null buffer");
+  if (c.rot > 0 && (c.cos == nullptr || c.sin == nullptr)) return invalid("null cos or sin");
+  if (!aligned(c.qkv, 16) || !aligned(c.out, 16) || !aligned(c.dout, 16) || !aligned(c.cos, 16) || !aligned(c.sin, 16))
+    return invalid("buffers and tables must be 16-byte aligned");
+  if (!aligned(c.wq, 4) || !aligned(c.wk, 4) || !aligned(c.pos, c.pos ? c.pos_bytes : 1))
+    return invalid("weights and positions must be aligned to their elements");
+  const size_t n = (size_t)elems * 2;
+  const Span o = span(c.out, n);
+  const bool in_place = bwd ? c.out == c.dout : c.out == c.qkv;
+  if ((bwd && meet(o, span(c.qkv, n))) || (!in_place && meet(o, span(bwd ? c.dout : c.qkv, n))))
+    return invalid(bwd ? "dqkv overlaps qkv or dout" : "out overlaps qkv");
+  const size_t tab = (size_t)c.table * (c.rot / 2) * 4;
+  if (meet(o, span(c.wq, c.d * 4)) || meet(o, span(c.wk, c.d * 4)) || meet(o, span(c.cos, tab)) ||
+      meet(o, span(c.sin, tab)) || meet(o, span(c.pos, (size_t)c.B * c.N * c.pos_bytes)))
+    return invalid("the output overlaps a weight, a table or the positions");
+  return LITELA_OK;
+}
+
+NormPlan norm_plan(const NormCall& c, bool bwd, int num_sms, int* grid) {
+  NormPlan p{};
+  p.x = static_cast<const __nv_bfloat16*>(c.qkv);
+  p.dy = static_cast<const __nv_bfloat16*>(c.dout);
+  p.out = static_cast<__nv_bfloat16*>(c.out);
+  p.wq = c.wq, p.wk = c.wk, p.cos = c.cos, p.sin = c.sin, p.pos = c.pos;
+  p.pos64 = c.pos_bytes == 8;
+  p.rows = (long long)c.B * c.N;
+  p.N = c.N;
+  p.table = c.table;
+  p.rot = c.rot;
+  p.q_ch = c.Hq * c.d;
+  p.qk_ch = (c.Hq + c.Hk) * c.d;
+  p.W = p.qk_ch + c.Hv * c.d;
+  p.copy_v = bwd ? c.out != c.dout : c.out != c.qkv;
+  p.eps = c.eps;
+  // the padded rows of the backward are zeroed whole, v's part of an in-place one too
+  p.steps = (p.W + kNormStep - 1) / kNormStep;
+  // warps per row: enough to give every SM 16 warps, no more than the row has steps
+  const long long want = 16LL * num_sms;
+  p.parts = (int)std::min<long long>(p.steps, std::max<long long>(1, (want + p.rows - 1) / p.rows));
+  const long long ctas = (p.rows * p.parts + kNormWarps - 1) / kNormWarps;
+  // The gradient's CTAs loop, so that few partial sums of the weights' gradients are left to add
+  *grid = (int)std::min<long long>(ctas, bwd ? std::min(kNormMaxGrid, 4 * num_sms) : 1 << 20);
+  return p;
+}
+
+template <bool kBwd>
+cudaError_t norm_launch(const NormPlan& p, int d, bool inter, int grid, cudaStream_t st) {
+#define LITELA_NORM(D, I)                                                                             \
+  return kBwd ? launch_seq(litela_norm_bwd<D, I>, dim3(grid), kNormThreads, 0, st, false, p)          \
+              : launch_seq(litela_norm_fwd<D, I>, dim3(grid), kNormThreads, 0, st, false, p)
+  if (d == 32) {
+    if (inter) LITELA_NORM(32, true);
+    LITELA_NORM(32, false);
+  }
+  if (d == 64) {
+    if (inter) LITELA_NORM(64, true);
+    LITELA_NORM(64, false);
+  }
+  if (inter) LITELA_NORM(128, true);
+  LITELA_NORM(128, false);
+#undef LITELA_NORM
+}
+
+litela_status norm_fwd(const NormCall& c, cudaStream_t st) {
+  bool empty;
+  litela_status s = norm_validate(c, false, &empty);
+  if (s != LITELA_OK || empty) return s;
+  int dev, sms, grid;
+  if ((s = host_device(&dev, &sms)) != LITELA_OK) return s;
+  const NormPlan p = norm_plan(c, false, sms, &grid);
+  if (p.qk_ch == 0 && !p.copy_v) return LITELA_OK;
+  const cudaError_t e = norm_launch<false>(p, c.d, c.inter != 0, grid, st);
+  if (e != cudaSuccess) return host_cuda_fail(e, "launch litela_norm_fwd");
+  host_ok();
+  return LITELA_OK;
+}
+
+litela_status norm_bwd(const NormCall& c, float* dwq, float* dwk, void* ws, size_t ws_bytes, cudaStream_t st) {
+  bool empty;
+  litela_status s = norm_validate(c, true, &empty);
+  if (s != LITELA_OK) return s;
+  if (!aligned(dwq, 4) || !aligned(dwk, 4)) return invalid("the weights' gradients must be 4-byte aligned");
+  const bool weights = dwq != nullptr || dwk != nullptr;
+  const size_t n = (size_t)c.B * c.N * ((size_t)c.Hq + c.Hk + c.Hv) * c.d * 2;
+  const size_t need = lite_la_qk_norm_rope_workspace_bytes(c.d);
+  if (weights && !empty) {
+    if (ws == nullptr || ws_bytes < need || !aligned(ws, 16)) return invalid("workspace missing, too small or misaligned");
+    const Span w = span(ws, ws_bytes), outs[3] = {span(c.out, n), span(dwq, c.d * 4), span(dwk, c.d * 4)};
+    for (const Span& o : outs)
+      if (meet(w, o)) return invalid("the workspace overlaps an output");
+    if (meet(w, span(c.qkv, n)) || meet(w, span(c.dout, n))) return invalid("the workspace overlaps an input");
+    if (meet(outs[0], outs[1]) || meet(outs[0], outs[2]) || meet(outs[1], outs[2])) return invalid("outputs overlap");
+    for (int i = 1; i < 3; ++i)
+      if (meet(outs[i], span(c.qkv, n)) || meet(outs[i], span(c.dout, n)) || meet(outs[i], span(c.wq, c.d * 4)) ||
+          meet(outs[i], span(c.wk, c.d * 4)))
+        return invalid("a weight's gradient overlaps an input");
+  }
+  int dev, sms, grid;
+  if ((s = host_device(&dev, &sms)) != LITELA_OK) return s;
+  if (empty) {   // no rows: the weights' gradients are zero
+    for (float* w : {dwq, dwk})
+      if (w != nullptr) {
+        const cudaError_t e = cudaMemsetAsync(w, 0, c.d * sizeof(float), st);
+        if (e != cudaSuccess) return host_cuda_fail(e, "cudaMemsetAsync");
+      }
+    return LITELA_OK;
+  }
+  NormPlan p = norm_plan(c, true, sms, &grid);
+  p.partials = weights ? static_cast<float*>(ws) : nullptr;
+  cudaError_t e = norm_launch<true>(p, c.d, c.inter != 0, grid, st);
+  if (e != cudaSuccess) return host_cuda_fail(e, "launch litela_norm_bwd");
+  if (weights) {
+    e = launch_seq(litela_norm_weight_grad, dim3(2 * c.d), 32, 0, st, true, static_cast<const float*>(p.partials), grid,
+                   c.d, dwq, dwk);
+    if (e != cudaSuccess) return host_cuda_fail(e, "launch litela_norm_weight_grad");
+  }
+  host_ok();
+  return LITELA_OK;
+}
+
+// ---------------------------------------------------------------------------------------
+// the gated delta rule
+
+// checks a view of [B, N, heads, d]; `out`: no two of its rows may share memory
+litela_status view_check(const lite_la_view& v, int B, int N, int heads, int d, bool out, Span* sp) {
+  *sp = Span{};
+  if (B == 0 || N == 0 || heads == 0) return LITELA_OK;
+  if (v.data == nullptr) return invalid("null q, k, v, out or gradient");
+  if (!aligned(v.data, 16)) return invalid("views must be 16-byte aligned");
+  const struct { long long stride; int size; } dim[3] = {
+      {v.batch_stride, B}, {v.token_stride, N}, {v.head_stride, heads}};
+  double last = d;
+  for (const auto& x : dim) {
+    if (x.size == 1) continue;
+    if (x.stride < 0 || x.stride % 8 != 0) return invalid("view strides must be multiples of 8 and >= 0");
+    last += (double)x.stride * (x.size - 1);
+  }
+  if (last > 4.0e18) return invalid("a view's extent overflows int64");
+  if (out) {   // sorted by stride, each dimension has to step over all of the smaller ones
+    int order[3] = {0, 1, 2};
+    std::sort(order, order + 3, [&](int a, int b) { return dim[a].stride < dim[b].stride; });
+    double extent = d;
+    for (int i : order) {
+      if (dim[i].size == 1) continue;
+      if ((double)dim[i].stride < extent) return invalid("an output view overlaps itself");
+      extent += (double)dim[i].stride * (dim[i].size - 1);
+    }
+  }
+  *sp = span(v.data, (size_t)last * 2);
+  return LITELA_OK;
+}
+
+size_t gate_bytes(int B, int N, int H, long long sb, long long st) {
+  return B == 0 || N == 0 || H == 0 ? 0 : ((size_t)(B - 1) * sb + (size_t)(N - 1) * st + H) * 4;
+}
+
+// inputs' spans of a call, for the outputs to keep clear of
+struct DeltaSpans {
+  Span in[8];
+  int n = 0;
+  void add(const Span& s) { in[n++] = s; }
+  bool hit(const Span& o) const {
+    for (int i = 0; i < n; ++i)
+      if (meet(in[i], o)) return true;
+    return false;
+  }
+};
+
+// host-side checks shared by the gated delta rule's calls; *empty: no sequences or no heads
+litela_status delta_validate(const lite_la_delta_args* a, bool with_out, DeltaSpans* in, Span* out, bool* empty) {
+  *empty = false;
+  if (a == nullptr) return invalid("null args");
+  if (a->B < 0 || a->N < 0 || a->Hk < 0 || a->Hv < 0) return invalid("B, N, Hk and Hv must be >= 0");
+  if (a->B > 65535 || a->Hv > 65535 || a->Hk > 65535 || a->N > kMaxTokens)
+    return invalid("B and the heads must be <= 65535, N <= 2^30");
+  if (a->d != 32 && a->d != 64 && a->d != 128) return unsupported("d must be 32, 64 or 128");
+  if ((a->Hk == 0) != (a->Hv == 0) || (a->Hk > 0 && a->Hv % a->Hk != 0))
+    return unsupported("Hv must be a multiple of Hk");
+  if (!std::isfinite(a->scale)) return invalid("scale must be finite");
+  if (a->B == 0 || a->Hv == 0) {
+    *empty = true;
+    return LITELA_OK;
+  }
+  if ((double)a->B * a->Hv * (a->d / 32) > 2147483647.0) return invalid("too many sequences and heads");
+  const int entries = a->cu_seqlens != nullptr ? 1 : a->B;
+  Span s;
+  litela_status st;
+  if ((st = view_check(a->q, entries, a->N, a->Hk, a->d, false, &s)) != LITELA_OK) return st;
+  in->add(s);
+  if ((st = view_check(a->k, entries, a->N, a->Hk, a->d, false, &s)) != LITELA_OK) return st;
+  in->add(s);
+  if ((st = view_check(a->v, entries, a->N, a->Hv, a->d, false, &s)) != LITELA_OK) return st;
+  in->add(s);
+  if (a->N > 0) {
+    if (a->g == nullptr || a->beta == nullptr) return invalid("null g or beta");
+    if (!aligned(a->g, 4) || !aligned(a->beta, 4)) return invalid("g and beta must be 4-byte aligned");
+    if (a->g_batch_stride < 0 || a->g_token_stride < 0 || a->beta_batch_stride < 0 || a->beta_token_stride < 0)
+      return invalid("strides of g and beta must be >= 0");
+    in->add(span(a->g, gate_bytes(entries, a->N, a->Hv, a->g_batch_stride, a->g_token_stride)));
+    in->add(span(a->beta, gate_bytes(entries, a->N, a->Hv, a->beta_batch_stride, a->beta_token_stride)));
+  }
+  if (!aligned(a->state_in, 16) || !aligned(a->state_out, 16)) return invalid("states must be 16-byte aligned");
+  if (!aligned(a->cu_seqlens, 4)) return invalid("cu_seqlens must be 4-byte aligned");
+  in->add(span(a->cu_seqlens, a->cu_seqlens ? ((size_t)a->B + 1) * 4 : 0));
+  if (with_out) {
+    if ((st = view_check(a->out, entries, a->N, a->Hv, a->d, true, out)) != LITELA_OK) return st;
+    if (in->hit(*out)) return invalid("out overlaps an input");
+  }
+  return LITELA_OK;
+}
+
+litela_status state_check(const lite_la_delta_args* a, size_t bytes, const DeltaSpans& in, const Span& out) {
+  const Span si = span(a->state_in, bytes), so = span(a->state_out, bytes);
+  if (meet(si, out) || meet(so, out)) return invalid("a state overlaps out");
+  if (in.hit(so)) return invalid("state_out overlaps an input");
+  if (a->state_in != a->state_out && meet(si, so)) return invalid("state_out overlaps state_in in part");
+  return LITELA_OK;
+}
+
+DeltaView view_of(const lite_la_view& v) {
+  return DeltaView{static_cast<__nv_bfloat16*>(v.data), v.batch_stride, v.token_stride, v.head_stride};
+}
+
+DeltaArgs delta_args(const lite_la_delta_args* a) {
+  DeltaArgs d{};
+  d.q = view_of(a->q), d.k = view_of(a->k), d.v = view_of(a->v), d.out = view_of(a->out);
+  d.g = a->g, d.beta = a->beta;
+  d.g_sb = a->g_batch_stride, d.g_st = a->g_token_stride;
+  d.b_sb = a->beta_batch_stride, d.b_st = a->beta_token_stride;
+  d.state_in = a->state_in, d.state_out = a->state_out;
+  d.cu = a->cu_seqlens;
+  d.nseq = a->B, d.ntok = a->N, d.Hk = a->Hk, d.Hv = a->Hv;
+  d.scale = a->scale;
+  return d;
+}
+
+litela_status launch_recur(const DeltaArgs& d, int D, cudaStream_t st) {
+  const dim3 grid((unsigned)((long long)d.nseq * d.Hv * (D / kRecurCols)));
+  const cudaError_t e = D == 32   ? launch_seq(litela_delta_recur<32>, grid, kRecurThreads, 0, st, false, d)
+                        : D == 64 ? launch_seq(litela_delta_recur<64>, grid, kRecurThreads, 0, st, false, d)
+                                  : launch_seq(litela_delta_recur<128>, grid, kRecurThreads, 0, st, false, d);
+  return e == cudaSuccess ? LITELA_OK : host_cuda_fail(e, "launch litela_delta_recur");
+}
+
+litela_status delta_fwd(const lite_la_delta_args* a, cudaStream_t st) {
+  DeltaSpans in;
+  Span out;
+  bool empty;
+  litela_status s = delta_validate(a, true, &in, &out, &empty);
+  if (s != LITELA_OK || empty) return s;
+  if ((s = state_check(a, (size_t)a->B * a->Hv * a->d * a->d * 4, in, out)) != LITELA_OK) return s;
+  int dev, sms;
+  if ((s = host_device(&dev, &sms)) != LITELA_OK) return s;
+  const DeltaArgs d = delta_args(a);
+  if (a->zero_tail && a->cu_seqlens != nullptr && a->N > 0) {
+    const cudaError_t e = launch_seq(litela_delta_zero_tail, dim3(sms), 256, 0, st, false, d.out, d.cu, d.nseq, d.ntok,
+                                     a->Hv, a->d);
+    if (e != cudaSuccess) return host_cuda_fail(e, "launch litela_delta_zero_tail");
+  }
+  if ((s = launch_recur(d, a->d, st)) != LITELA_OK) return s;
+  host_ok();
+  return LITELA_OK;
+}
+
+litela_status delta_step(const lite_la_delta_args* a, const int* slots, int pool, cudaStream_t st) {
+  DeltaSpans in;
+  Span out;
+  bool empty;
+  litela_status s = delta_validate(a, true, &in, &out, &empty);
+  if (s != LITELA_OK) return s;
+  if (pool < 0) return invalid("pool must be >= 0");
+  if (a->cu_seqlens != nullptr) return invalid("the one-token form takes no cu_seqlens");
+  if (empty) return LITELA_OK;
+  if (a->N != 1) return invalid("the one-token form needs N = 1");
+  if (a->state_in != a->state_out || a->state_in == nullptr)
+    if (pool > 0 || a->state_in != a->state_out) return invalid("state_in and state_out must be the same pool");
+  if (slots == nullptr && pool < a->B) return invalid("the pool has fewer states than the batch has rows");
+  if (!aligned(slots, 4)) return invalid("state_indices must be 4-byte aligned");
+  in.add(span(slots, slots ? (size_t)a->B * 4 : 0));
+  if (in.hit(out)) return invalid("out overlaps an input");
+  if ((s = state_check(a, (size_t)pool * a->Hv * a->d * a->d * 4, in, out)) != LITELA_OK) return s;
+  int dev, sms;
+  if ((s = host_device(&dev, &sms)) != LITELA_OK) return s;
+  DeltaArgs d = delta_args(a);
+  d.slots = slots;
+  d.nslots = pool;
+  if ((s = launch_recur(d, a->d, st)) != LITELA_OK) return s;
+  host_ok();
+  return LITELA_OK;
+}
+
+// no C++ exception leaves a C entry point
+template <typename F>
+litela_status guarded(F&& f) {
+  try {
+    return f();
+  } catch (...) {
+    return LITELA_ERR_OUT_OF_MEMORY;
+  }
+}
+
+}  // namespace
+}  // namespace litela
+
+extern "C" {
+
+litela_status lite_la_qk_norm_rope_fwd(const void* qkv, void* out, const float* q_weight, const float* k_weight,
+                                       const float* cos, const float* sin, const void* positions, int position_bytes,
+                                       int B, int N, int Hq, int Hk, int Hv, int d, int rot, int table_len,
+                                       int interleaved, float eps, cudaStream_t stream) {
+  return litela::guarded([&] {
+    return litela::norm_fwd({qkv, nullptr, out, q_weight, k_weight, cos, sin, positions, position_bytes, B, N, Hq, Hk,
+                             Hv, d, rot, table_len, interleaved, eps},
+                            stream);
+  });
+}
+
+litela_status lite_la_qk_norm_rope_bwd(const void* qkv, const void* dout, void* dqkv, const float* q_weight,
+                                       const float* k_weight, float* dq_weight, float* dk_weight, const float* cos,
+                                       const float* sin, const void* positions, int position_bytes, int B, int N,
+                                       int Hq, int Hk, int Hv, int d, int rot, int table_len, int interleaved,
+                                       float eps, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return litela::guarded([&] {
+    return litela::norm_bwd({qkv, dout, dqkv, q_weight, k_weight, cos, sin, positions, position_bytes, B, N, Hq, Hk, Hv,
+                             d, rot, table_len, interleaved, eps},
+                            dq_weight, dk_weight, workspace, workspace_bytes, stream);
+  });
+}
+
+size_t lite_la_qk_norm_rope_workspace_bytes(int d) {
+  return d == 32 || d == 64 || d == 128 ? (size_t)litela::kNormMaxGrid * 2 * d * sizeof(float) : 0;
+}
+
+litela_status lite_la_gated_delta_fwd(const lite_la_delta_args* args, cudaStream_t stream) {
+  return litela::guarded([&] { return litela::delta_fwd(args, stream); });
+}
+
+size_t lite_la_gated_delta_workspace_bytes(int, int, int, int, int, int) { return 0; }
+
+litela_status lite_la_gated_delta_step(const lite_la_delta_args* args, const int* state_indices, int pool,
+                                       cudaStream_t stream) {
+  return litela::guarded([&] { return litela::delta_step(args, state_indices, pool, stream); });
+}
+
+}  // extern "C"
