@@ -7,9 +7,11 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "../../include/litela.h"
 #include "litela_delta.cuh"
+#include "litela_delta_chunk.cuh"
 #include "litela_host.h"
 #include "litela_norm.cuh"
 
@@ -340,6 +342,65 @@ litela_status launch_recur(const DeltaArgs& d, int D, cudaStream_t st) {
   return e == cudaSuccess ? LITELA_OK : host_cuda_fail(e, "launch litela_delta_recur");
 }
 
+// shared-memory limits of the chunked kernels, once per device
+litela_status delta_setup(int dev) {
+  static std::mutex mutex;
+  static bool ready[64] = {};
+  std::lock_guard<std::mutex> lock(mutex);
+  if (ready[dev]) return LITELA_OK;
+  cudaError_t e = cudaSuccess;
+  auto set = [&](auto* k, uint32_t bytes) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  };
+  set(litela_delta_prep<32>, PrepCfg<32>::kSmemBytes);
+  set(litela_delta_prep<64>, PrepCfg<64>::kSmemBytes);
+  set(litela_delta_prep<128>, PrepCfg<128>::kSmemBytes);
+  set(litela_delta_chain<32, 32>, ChainCfg<32, 32>::kSmemBytes);
+  set(litela_delta_chain<64, 32>, ChainCfg<64, 32>::kSmemBytes);
+  set(litela_delta_chain<64, 64>, ChainCfg<64, 64>::kSmemBytes);
+  set(litela_delta_chain<128, 32>, ChainCfg<128, 32>::kSmemBytes);
+  set(litela_delta_chain<128, 64>, ChainCfg<128, 64>::kSmemBytes);
+  if (e != cudaSuccess) return host_cuda_fail(e, "cudaFuncSetAttribute(dynamic shared memory)");
+  ready[dev] = true;
+  return LITELA_OK;
+}
+
+// The recurrence or the chunks.  A call of at most this many tokens (of each batch entry; packed:
+// of all sequences, whose lengths only the device knows) runs the recurrence.
+constexpr int kRecurMaxTokens = 32;
+bool delta_recurs(int ntok) { return ntok <= kRecurMaxTokens; }
+
+template <int kD>
+cudaError_t launch_prep(const DeltaArgs& d, uint8_t* prep, cudaStream_t st) {
+  const long long slots = delta_slots(d.nseq, d.ntok, d.cu != nullptr);
+  return launch_seq(litela_delta_prep<kD>, dim3((unsigned)(slots * d.Hv)), kPrepThreads, PrepCfg<kD>::kSmemBytes, st,
+                    false, d, prep);
+}
+
+template <int kD, int kCols>
+cudaError_t launch_chain(const DeltaArgs& d, const uint8_t* prep, int* err, cudaStream_t st) {
+  return launch_seq(litela_delta_chain<kD, kCols>, dim3((unsigned)((long long)d.nseq * d.Hv * (kD / kCols))),
+                    kChainThreads, ChainCfg<kD, kCols>::kSmemBytes, st, true, d, prep, err);
+}
+
+litela_status launch_chunks(const DeltaArgs& d, int D, void* ws, int dev, int sms, cudaStream_t st) {
+  litela_status s = delta_setup(dev);
+  if (s != LITELA_OK) return s;
+  uint8_t* prep = static_cast<uint8_t*>(ws);
+  int* err = delta_error_word(dev);
+  cudaError_t e = D == 32 ? launch_prep<32>(d, prep, st) : D == 64 ? launch_prep<64>(d, prep, st) : launch_prep<128>(d, prep, st);
+  if (e != cudaSuccess) return host_cuda_fail(e, "launch litela_delta_prep");
+  // 64 columns a CTA where that already gives every SM one, else 32
+  const bool wide = D > 32 && (long long)d.nseq * d.Hv * (D / 64) >= sms;
+  if (D == 32)
+    e = launch_chain<32, 32>(d, prep, err, st);
+  else if (D == 64)
+    e = wide ? launch_chain<64, 64>(d, prep, err, st) : launch_chain<64, 32>(d, prep, err, st);
+  else
+    e = wide ? launch_chain<128, 64>(d, prep, err, st) : launch_chain<128, 32>(d, prep, err, st);
+  return e == cudaSuccess ? LITELA_OK : host_cuda_fail(e, "launch litela_delta_chain");
+}
+
 litela_status delta_fwd(const lite_la_delta_args* a, cudaStream_t st) {
   DeltaSpans in;
   Span out;
@@ -347,6 +408,18 @@ litela_status delta_fwd(const lite_la_delta_args* a, cudaStream_t st) {
   litela_status s = delta_validate(a, true, &in, &out, &empty);
   if (s != LITELA_OK || empty) return s;
   if ((s = state_check(a, (size_t)a->B * a->Hv * a->d * a->d * 4, in, out)) != LITELA_OK) return s;
+  const bool recurs = delta_recurs(a->N);
+  if (!recurs) {
+    const size_t need = lite_la_gated_delta_workspace_bytes(a->B, a->N, a->Hk, a->Hv, a->d, a->cu_seqlens != nullptr);
+    const Span w = span(a->workspace, a->workspace_bytes);
+    if (a->workspace == nullptr || a->workspace_bytes < need || !aligned(a->workspace, 16))
+      return invalid("workspace missing, too small or misaligned");
+    const size_t states = (size_t)a->B * a->Hv * a->d * a->d * 4;
+    if (meet(w, out) || in.hit(w) || meet(w, span(a->state_in, states)) || meet(w, span(a->state_out, states)))
+      return invalid("the workspace overlaps a buffer of the call");
+    if (delta_slots(a->B, a->N, a->cu_seqlens != nullptr) * (double)a->Hv > 2147483647.0)
+      return invalid("too many chunks and heads");
+  }
   int dev, sms;
   if ((s = host_device(&dev, &sms)) != LITELA_OK) return s;
   const DeltaArgs d = delta_args(a);
@@ -355,9 +428,9 @@ litela_status delta_fwd(const lite_la_delta_args* a, cudaStream_t st) {
                                      a->Hv, a->d);
     if (e != cudaSuccess) return host_cuda_fail(e, "launch litela_delta_zero_tail");
   }
-  if ((s = launch_recur(d, a->d, st)) != LITELA_OK) return s;
-  host_ok();
-  return LITELA_OK;
+  s = recurs ? launch_recur(d, a->d, st) : launch_chunks(d, a->d, a->workspace, dev, sms, st);
+  if (s == LITELA_OK) host_ok();
+  return s;
 }
 
 litela_status delta_step(const lite_la_delta_args* a, const int* slots, int pool, cudaStream_t st) {
@@ -433,7 +506,10 @@ litela_status lite_la_gated_delta_fwd(const lite_la_delta_args* args, cudaStream
   return litela::guarded([&] { return litela::delta_fwd(args, stream); });
 }
 
-size_t lite_la_gated_delta_workspace_bytes(int, int, int, int, int, int) { return 0; }
+size_t lite_la_gated_delta_workspace_bytes(int B, int N, int Hk, int Hv, int d, int packed) {
+  if (B <= 0 || N <= 0 || Hk <= 0 || Hv <= 0 || (d != 32 && d != 64 && d != 128) || litela::delta_recurs(N)) return 0;
+  return (size_t)litela::delta_slots(B, N, packed != 0) * Hv * litela::kPrepBytes;
+}
 
 litela_status lite_la_gated_delta_step(const lite_la_delta_args* args, const int* state_indices, int pool,
                                        cudaStream_t stream) {
