@@ -10,9 +10,12 @@
 // chunks with them.
 //
 // Precision.  States are fp32 and stay in registers.  An fp32 operand of a tensor-core product is
-// entered as a bf16 pair (hi + lo, 2^-17 relative) and the products hi*hi, hi*lo, lo*hi are summed
-// in fp32: a single bf16 rounding (2^-8) of T, R, U or S0 would show in the states.  K, Q and V are
-// bf16 already.  G is summed in fp64: differences of large sums of decays would lose in fp32.
+// entered as two or three bf16 terms (each the rounding of what the ones before it leave: 2^-17 and
+// 2^-25 relative) whose products are summed in fp32.  R and U take three: they are the rows that
+// the state is a sum of, and with two terms the state was 3.4e-6 off (2.5e-6 from either alone).  T and
+// S0 take two: T's large entries are near its unit diagonal and S0 enters a difference with V
+// (3e-7 and 3e-9 of the state).  K, Q and V are bf16 already.  G is summed in fp64: differences of
+// large sums of decays would lose in fp32.
 //
 // A NaN or an infinity must not reach the tokens before its own: 0 * NaN inside a product would
 // carry it there.  So non-finite entries are taken out of A, P and R, the first token that had one
@@ -29,9 +32,13 @@ namespace litela {
 
 constexpr int kChunk = 64;
 
-// One chunk and value head's prepared block: [T; P T] as the A operand image of a tcgen05 product
-// (128 rows x 64 columns bf16, K-major, 128-byte swizzle), hi then lo, then per-token factors
+// One chunk and value head's prepared block: T^T and (P T)^T as images of tcgen05 A operands (MN-major:
+// 64 rows x 128 columns bf16 in two blocks of 64 columns, 128-byte swizzle), the hi terms, the lo
+// terms, then per-token factors.  The columns (the product's rows, TMEM lanes) hold 16 rows of T,
+// the same 16 rows of P T, the next 16 rows of T and so on, as do the rows of K and Q in the chain's
+// tile: every warp's quarter of the lanes then has 16 tokens of either kind.
 constexpr uint32_t kImgHalf = 128 * 128;
+__host__ __device__ constexpr int lane_of(int token) { return 32 * (token / 16) + token % 16; }
 constexpr uint32_t kPrepFactors = 2 * kImgHalf;
 constexpr uint32_t kPrepBytes = kPrepFactors + 1024;
 // fp32 at kPrepFactors: e^G [64], e^(G_C - G) [64] (0 behind the end), beta [64] (0 behind the
@@ -73,6 +80,40 @@ __device__ __forceinline__ bool delta_find(const DeltaArgs& a, long long slot, i
   return n0 >= 0 && n0 < q.len;
 }
 
+// two fp32 values in one 64-bit register: Blackwell adds and multiplies both in one instruction
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 f2_out(F2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+// the two values of a packed bf16 word
+__device__ __forceinline__ F2 f2_bf16(uint32_t w) {
+  return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&h);
@@ -89,54 +130,78 @@ __device__ __forceinline__ void split_frag(const float (*c)[4], uint32_t* hi, ui
   split_bf16(c[1][0], c[1][1], hi[2], lo[2]);
   split_bf16(c[1][2], c[1][3], hi[3], lo[3]);
 }
-// D += A B with both as bf16 pairs
-__device__ __forceinline__ void mma_split(float* d, const uint32_t* ahi, const uint32_t* alo, const uint32_t* bhi,
-                                          const uint32_t* blo) {
-  sm100::mma_16816(d, ahi, bhi);
-  sm100::mma_16816(d, ahi, blo);
-  sm100::mma_16816(d, alo, bhi);
-}
-
 // byte offset of bf16 element (row, column < 64) in a tile of 128-byte rows, 128-byte swizzle
 __device__ __forceinline__ uint32_t sw128(int row, int col) {
   return (uint32_t)(row * 128 + ((((col >> 3) ^ row) & 7) << 4) + (col & 7) * 2);
 }
 
 // ---------------------------------------------------------------------------------------
-// litela_delta_prep: T and P T of one chunk and value head per CTA, 4 warps, warp w the rows
-// 16 w .. 16 w + 15.
+// litela_delta_prep: T and P T of one chunk and value head per CTA, transposed (the image).
 //
 // mma.sync: the operands are one chunk's, 64 rows, and T is made of 16 x 16 blocks where each
 // product waits for the one before; a tcgen05 product would be a sixth full and go through TMEM and
-// shared memory for each block.  T by blocks of 16: the diagonal blocks by substitution, one lane
-// a column; below them, block column j by warp j: T_ij = -T_ii sum_m A_im T_mj, computed transposed
-// (X_i = T_ij^T) so that a product's accumulators are the next one's left operand in registers.
-constexpr int kPrepThreads = 128;
-constexpr int kPrepLd = 68;   // row of the fp32 matrices, padded
+// shared memory for each block.  Eight warps: warp w has half of the columns of rows 16 (w / 2) on.
+//   1. K and Q by cp.async; G, and D's factors.  With m the first row of r's block of 16 and c
+//      before it, D_rc = e^(G_r - G_m) e^(G_m - G_c): 160 exponentials instead of 1536, both
+//      factors at most 1.
+//   2. K K^T and Q K^T below the diagonal; A and P as bf16 pairs, A's diagonal blocks in fp32.
+//   3. T's diagonal blocks by substitution, one lane a column.
+//   4. The blocks below them, block column j by warp j, T_ij = -T_ii sum_m A_im T_mj, computed
+//      transposed (X_i = T_ij^T), so that a product's accumulators are the next one's left operand
+//      in registers, and the image's values.
+//   5. (P T)^T = T^T P^T.
+// One chunk is a chain of about 10k cycles of latencies; three CTAs an SM overlap.
+constexpr int kPrepThreads = 256;
+constexpr int kPrepLd = 72;   // row of P, padded
+constexpr int kDiagLd = 24;   // row of T's diagonal blocks, padded
+constexpr uint32_t kImgBlock = 64 * 128;   // half of the columns of an image, one bf16 term
+// byte offset in the image of (row, token of T); of P T: 32 bytes on, before the swizzle
+__device__ __forceinline__ uint32_t img_off(int row, int token, int is_p) {
+  const int m = lane_of(token) + 16 * is_p;
+  return (m >> 6) * kImgBlock + sw128(row, m & 63);
+}
 
 template <int kD>
 struct PrepCfg {
   static constexpr int kLd = kD + 8;   // row of K and Q, padded
   static constexpr uint32_t kRows = 2 * kChunk * kLd * 2;
   static constexpr uint32_t kUnion = kRows > 2 * kImgHalf ? kRows : 2 * kImgHalf;   // K, Q; then the image
-  static constexpr uint32_t kMat = kChunk * kPrepLd * 4;
-  static constexpr uint32_t kSmemBytes = kUnion + 2 * kMat + kChunk * 8 + kChunk * 4 + 16 + 128;
+  static constexpr uint32_t kOffP = kUnion;                                  // P, hi and lo
+  static constexpr uint32_t kOffDiag = kOffP + 2 * kChunk * kPrepLd * 2;     // T's diagonal blocks, hi and lo
+  static constexpr uint32_t kOffA = kOffDiag + 2 * kChunk * kDiagLd * 2;     // A's diagonal blocks, fp32
+  static constexpr uint32_t kOffG = kOffA + kChunk * 17 * 4;
+  static constexpr uint32_t kOffBeta = kOffG + kChunk * 8;
+  static constexpr uint32_t kOffRow = kOffBeta + kChunk * 4;                 // e^(G_r - G_m)
+  static constexpr uint32_t kOffCol = kOffRow + kChunk * 4;                  // e^(G_m - G_c), by block of r
+  static constexpr uint32_t kOffBad = kOffCol + 4 * 48 * 4;
+  static constexpr uint32_t kSmemBytes = kOffBad + 16 + 128;
+  static_assert(3 * (kSmemBytes + 1024) <= 228 * 1024, "three CTAs an SM");
 };
 
+__device__ __forceinline__ void ldmatrix_x4(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
 template <int kD>
-__global__ void __launch_bounds__(kPrepThreads) litela_delta_prep(const DeltaArgs a, uint8_t* __restrict__ prep) {
+__global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const DeltaArgs a, uint8_t* __restrict__ prep) {
   using namespace sm100;
   using Cfg = PrepCfg<kD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-  __nv_bfloat16* Ks = reinterpret_cast<__nv_bfloat16*>(smem);
-  __nv_bfloat16* Qs = Ks + kChunk * Cfg::kLd;
-  uint8_t* image = smem;
-  float* As = reinterpret_cast<float*>(smem + Cfg::kUnion);
-  float* Tt = As + kChunk * kPrepLd;                 // T transposed: Tt[column][row]
-  double* G = reinterpret_cast<double*>(Tt + kChunk * kPrepLd);
-  float* beta = reinterpret_cast<float*>(G + kChunk);
-  int* bad = reinterpret_cast<int*>(beta + kChunk);
+  // the image, hi and lo; until (P T)^T is made A's pair stands in its places, (row, column) of A at
+  // img_off(row, column, 1)
+  uint8_t *Ih = smem, *Il = smem + kImgHalf;
+  __nv_bfloat16* Pm = reinterpret_cast<__nv_bfloat16*>(smem + Cfg::kOffP);
+  __nv_bfloat16* Td = reinterpret_cast<__nv_bfloat16*>(smem + Cfg::kOffDiag);
+  float* Ad = reinterpret_cast<float*>(smem + Cfg::kOffA);
+  double* G = reinterpret_cast<double*>(smem + Cfg::kOffG);
+  float* beta = reinterpret_cast<float*>(smem + Cfg::kOffBeta);
+  float* rowf = reinterpret_cast<float*>(smem + Cfg::kOffRow);
+  float* colf = reinterpret_cast<float*>(smem + Cfg::kOffCol);
+  int* bad = reinterpret_cast<int*>(smem + Cfg::kOffBad);
+  constexpr uint32_t kPLo = kChunk * kPrepLd, kTdLo = kChunk * kDiagLd;   // elements to the lo term
 
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, gr = lane >> 2, t2 = (lane & 3) * 2;
   pdl_launch_dependents();   // the chain waits for this grid before it reads what it wrote
@@ -147,11 +212,19 @@ __global__ void __launch_bounds__(kPrepThreads) litela_delta_prep(const DeltaArg
   if (!delta_find(a, slot, lane, s, sq, n0)) return;
   const int len = min(kChunk, sq.len - n0);
 
-  for (int i = tid; i < 2 * kChunk * (kD / 8); i += kPrepThreads) {
-    const int c = i % (kD / 8), r = (i / (kD / 8)) % kChunk, m = i / (kChunk * (kD / 8));
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (r < len) x = *reinterpret_cast<const uint4*>(delta_row(m ? a.q : a.k, sq, n0 + r, hk) + c * 8);
-    *reinterpret_cast<uint4*>((m ? Qs : Ks) + r * Cfg::kLd + c * 8) = x;
+  {   // a thread copies one 16-byte column of every (2048 / kD)-th row
+    constexpr int kC = kD / 8, kStep = kPrepThreads / kC;
+    const int c = tid % kC, r0 = tid / kC;
+    const __nv_bfloat16* kp = delta_row(a.k, sq, n0, hk) + c * 8;
+    const __nv_bfloat16* qp = delta_row(a.q, sq, n0, hk) + c * 8;
+    const uint32_t dst = smem_u32(smem) + c * 16;
+#pragma unroll
+    for (int r = r0; r < kChunk; r += kStep) {
+      const bool real = r < len;
+      cp_async_16(dst + r * (Cfg::kLd * 2), kp + (real ? r * a.k.st : 0), real);
+      cp_async_16(dst + (kChunk + r) * (Cfg::kLd * 2), qp + (real ? r * a.q.st : 0), real);
+    }
+    cp_async_commit();
   }
   if (w == 0) {   // G, two tokens a lane
     double x[2];
@@ -177,183 +250,243 @@ __global__ void __launch_bounds__(kPrepThreads) litela_delta_prep(const DeltaArg
     *bad = kChunk;
   }
   __syncthreads();
+  uint8_t* dst = prep + (slot * a.Hv + h) * (long long)kPrepBytes;
+  if (tid < kChunk) {
+    rowf[tid] = expf((float)(G[tid] - G[tid & ~15]));
+  } else if (tid < kChunk + 96) {   // blocks 1, 2, 3 of r have 16, 32, 48 columns before them
+    const int i = tid - kChunk, b = i < 16 ? 1 : i < 48 ? 2 : 3, c = i - (b == 1 ? 0 : b == 2 ? 16 : 48);
+    colf[b * 48 + c] = expf((float)(G[16 * b] - G[c]));
+  } else if (tid >= 192) {   // the chain's factors
+    float* fac = reinterpret_cast<float*>(dst + kPrepFactors);
+    const int n = tid - 192;
+    const double end = G[len - 1];
+    fac[kFacDecay + n] = expf((float)G[n]);
+    fac[kFacToEnd + n] = n < len ? expf((float)(end - G[n])) : 0.f;
+    fac[kFacBeta + n] = beta[n];
+    if (n == 0) fac[kFacChunk] = expf((float)end);
+  }
+  cp_async_wait<0>();
+  __syncthreads();
 
-  // K K^T and Q K^T, the warp's 16 rows, columns up to its diagonal block
-  float accA[8][4], P[8][4];
+  // K K^T and Q K^T: rows 16 rb .., the warp's rb + 1 tiles of 8 columns of the 2 rb + 2
+  const int rb = w >> 1, tile0 = (w & 1) * (rb + 1);
+  float accA[4][4], accP[4][4];
 #pragma unroll
-  for (int n = 0; n < 8; ++n)
+  for (int n = 0; n < 4; ++n)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) accA[n][i] = P[n][i] = 0.f;
+    for (int i = 0; i < 4; ++i) accA[n][i] = accP[n][i] = 0.f;
   {
-    const uint32_t* kr = reinterpret_cast<const uint32_t*>(Ks + (16 * w + gr) * Cfg::kLd + t2);
-    const uint32_t* qr = reinterpret_cast<const uint32_t*>(Qs + (16 * w + gr) * Cfg::kLd + t2);
-    const uint32_t* br = reinterpret_cast<const uint32_t*>(Ks + gr * Cfg::kLd + t2);
-    constexpr int kW = Cfg::kLd / 2;   // a row in words
+    const uint32_t base = smem_u32(smem);
+    const uint32_t ka = base + (16 * rb + (lane & 15)) * (Cfg::kLd * 2) + (lane >> 4) * 16;
+    const uint32_t qa = ka + kChunk * (Cfg::kLd * 2);
+    const uint32_t ba = base + (8 * tile0 + (lane & 7)) * (Cfg::kLd * 2) + (lane >> 3) * 16;
 #pragma unroll
-    for (int ks = 0; ks < kD / 16; ++ks) {
-      const uint32_t ka[4] = {kr[ks * 8], kr[8 * kW + ks * 8], kr[ks * 8 + 4], kr[8 * kW + ks * 8 + 4]};
-      const uint32_t qa[4] = {qr[ks * 8], qr[8 * kW + ks * 8], qr[ks * 8 + 4], qr[8 * kW + ks * 8 + 4]};
+    for (int ks = 0; ks < kD / 32; ++ks) {   // 32 channels
+      uint32_t k0[4], k1[4], q0[4], q1[4];
+      ldmatrix_x4(k0, ka + ks * 64);
+      ldmatrix_x4(k1, ka + ks * 64 + 32);
+      ldmatrix_x4(q0, qa + ks * 64);
+      ldmatrix_x4(q1, qa + ks * 64 + 32);
 #pragma unroll
-      for (int n = 0; n < 8; ++n)
-        if (n < 2 * w + 2) {
-          const uint32_t b[2] = {br[n * 8 * kW + ks * 8], br[n * 8 * kW + ks * 8 + 4]};
-          mma_16816(accA[n], ka, b);
-          mma_16816(P[n], qa, b);
+      for (int n = 0; n < 4; ++n)
+        if (n <= rb) {
+          uint32_t b[4];
+          ldmatrix_x4(b, ba + n * 8 * (Cfg::kLd * 2) + ks * 64);
+          mma_16816(accA[n], k0, b);
+          mma_16816(accP[n], q0, b);
+          mma_16816(accA[n], k1, b + 2);
+          mma_16816(accP[n], q1, b + 2);
         }
     }
   }
+  __syncthreads();   // K and Q are done with: the image takes their place
+  const int r0 = 16 * rb + gr;
+  const float rf[2] = {rowf[r0], rowf[r0 + 8]}, bt[2] = {beta[r0], beta[r0 + 8]};
 #pragma unroll
-  for (int n = 0; n < 8; ++n)
-    if (n < 2 * w + 2) {
+  for (int n = 0; n < 4; ++n)
+    if (n <= rb) {
+      const int c0 = 8 * (tile0 + n) + t2;
+      const bool diag = c0 >= 16 * rb;   // the same for the whole tile
+      float D[4];
+      if (diag) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = r0 + (i >> 1) * 8, c = c0 + (i & 1);
+          D[i] = c <= r ? expf((float)(G[r] - G[c])) : 0.f;
+        }
+      } else {
+        const float2 cf = *reinterpret_cast<const float2*>(colf + rb * 48 + c0);
+        D[0] = rf[0] * cf.x, D[1] = rf[0] * cf.y, D[2] = rf[1] * cf.x, D[3] = rf[1] * cf.y;
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = 16 * w + gr + (i >> 1) * 8, c = 8 * n + t2 + (i & 1);
-        const float D = c <= r ? expf((float)(G[r] - G[c])) : 0.f;
-        accA[n][i] = c < r ? beta[r] * accA[n][i] * D : 0.f;
-        P[n][i] = c <= r ? P[n][i] * (a.scale * D) : 0.f;
-        if (!isfinite(accA[n][i]) || !isfinite(P[n][i])) {
-          accA[n][i] = P[n][i] = 0.f;
+        const int r = r0 + (i >> 1) * 8, c = c0 + (i & 1);
+        float x = c < r ? bt[i >> 1] * accA[n][i] * D[i] : 0.f;
+        float y = c <= r ? accP[n][i] * (a.scale * D[i]) : 0.f;
+        if (!isfinite(x) || !isfinite(y)) {
+          x = y = 0.f;
           atomicMin(bad, r);
         }
+        accA[n][i] = x;
+        accP[n][i] = y;
       }
-      float* dst = As + (16 * w + gr) * kPrepLd + 8 * n + t2;
-      *reinterpret_cast<float2*>(dst) = make_float2(accA[n][0], accA[n][1]);
-      *reinterpret_cast<float2*>(dst + 8 * kPrepLd) = make_float2(accA[n][2], accA[n][3]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = r0 + 8 * i;
+        uint32_t hi, lo;
+        split_bf16(accP[n][2 * i], accP[n][2 * i + 1], hi, lo);
+        *reinterpret_cast<uint32_t*>(Pm + r * kPrepLd + c0) = hi;
+        *reinterpret_cast<uint32_t*>(Pm + kPLo + r * kPrepLd + c0) = lo;
+        if (diag) {
+          Ad[r * 17 + c0 - 16 * rb] = accA[n][2 * i];
+          Ad[r * 17 + c0 - 16 * rb + 1] = accA[n][2 * i + 1];
+        } else {
+          split_bf16(accA[n][2 * i], accA[n][2 * i + 1], hi, lo);
+          *reinterpret_cast<uint32_t*>(Ih + img_off(r, c0, 1)) = hi;
+          *reinterpret_cast<uint32_t*>(Il + img_off(r, c0, 1)) = lo;
+        }
+      }
     }
-  __syncwarp();
-
-  // the diagonal block: lane j solves for column j, x_i = delta_ij - sum_m<i A_im x_m
-  if (lane < 16) {
-    float x[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float v = i == lane ? 1.f : 0.f;
-      const float* row = As + (16 * w + i) * kPrepLd + 16 * w;
-#pragma unroll
-      for (int m = 0; m < i; ++m) v -= row[m] * x[m];
-      x[i] = v;
+  for (int i = tid; i < kChunk * 8; i += kPrepThreads) {   // T^T is zero left of its diagonal blocks
+    const int r = i >> 3, c = (i & 7) * 8;
+    if ((c >> 4) < (r >> 4)) {
+      *reinterpret_cast<uint4*>(Ih + img_off(r, c, 0)) = make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4*>(Il + img_off(r, c, 0)) = make_uint4(0u, 0u, 0u, 0u);
     }
-    float4* dst = reinterpret_cast<float4*>(Tt + (16 * w + lane) * kPrepLd + 16 * w);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
   }
   __syncthreads();
 
-  // the blocks below it, block column w
+  // the diagonal block of warp w: lane j solves for column j, x_i = delta_ij - sum_m<i A_im x_m
+  if (w < 4 && lane < 16) {
+    float x[16];
+    const float* blk = Ad + 16 * w * 17;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float v = i == lane ? 1.f : 0.f, u = 0.f;
+#pragma unroll
+      for (int m = 0; m < i; ++m) {
+        if (m & 1)
+          u -= blk[i * 17 + m] * x[m];
+        else
+          v -= blk[i * 17 + m] * x[m];
+      }
+      x[i] = v + u;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      uint32_t hi, lo;
+      split_bf16(x[i], x[i + 1], hi, lo);
+      const uint32_t o = img_off(16 * w + lane, 16 * w + i, 0);
+      *reinterpret_cast<uint32_t*>(Ih + o) = hi;
+      *reinterpret_cast<uint32_t*>(Il + o) = lo;
+      uint16_t* td = reinterpret_cast<uint16_t*>(Td) + (16 * w + i) * kDiagLd + lane;
+      td[0] = (uint16_t)hi, td[kDiagLd] = (uint16_t)(hi >> 16);
+      td[kTdLo] = (uint16_t)lo, td[kTdLo + kDiagLd] = (uint16_t)(lo >> 16);
+    }
+  }
+  __syncthreads();
+
+  // the blocks below them, block column w
   if (w < 3) {
-    uint32_t xh[3][4], xl[3][4];   // X_m of the rows m = w + slot
+    uint32_t xh[3][4], xl[3][4];   // X of the block rows w, w + 1, w + 2
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t o = img_off(16 * w + gr + (q & 1) * 8, 16 * w + t2 + (q >> 1) * 8, 0);
+      xh[0][q] = *reinterpret_cast<const uint32_t*>(Ih + o);
+      xl[0][q] = *reinterpret_cast<const uint32_t*>(Il + o);
+    }
 #pragma unroll
     for (int e = 0; e < 3; ++e) {
       const int i = w + 1 + e;   // T's block row that this step makes
       if (i < 4) {
-        if (e == 0) {
-          float c[2][4];
-          const float* src = Tt + (16 * w + gr) * kPrepLd + 16 * w + t2;
+        float r[2][4] = {}, rs[2][4] = {};
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) c[n][q] = src[(q >> 1) * 8 * kPrepLd + 8 * n + (q & 1)];
-          split_frag(c, xh[0], xl[0]);
-        }
-        float r[2][4] = {};
-#pragma unroll
-        for (int m = 0; m <= e; ++m) {   // sum over T's block rows w + m
+        for (int m = 0; m <= e; ++m)   // sum over T's block rows w + m
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            const float* src = As + (16 * i + 8 * n + gr) * kPrepLd + 16 * (w + m) + t2;
-            uint32_t bh[2], bl[2];
-            split_bf16(src[0], src[1], bh[0], bl[0]);
-            split_bf16(src[8], src[9], bh[1], bl[1]);
-            mma_split(r[n], xh[m], xl[m], bh, bl);
+            const uint32_t o = img_off(16 * i + 8 * n + gr, 16 * (w + m) + t2, 1);
+            const uint32_t o8 = img_off(16 * i + 8 * n + gr, 16 * (w + m) + t2 + 8, 1);
+            const uint32_t bh[2] = {*reinterpret_cast<const uint32_t*>(Ih + o), *reinterpret_cast<const uint32_t*>(Ih + o8)};
+            const uint32_t bl[2] = {*reinterpret_cast<const uint32_t*>(Il + o), *reinterpret_cast<const uint32_t*>(Il + o8)};
+            mma_16816(r[n], xh[m], bh);
+            mma_16816(rs[n], xh[m], bl);
+            mma_16816(rs[n], xl[m], bh);
           }
-        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) r[n][q] += rs[n][q];
         uint32_t rh[4], rl[4];
         split_frag(r, rh, rl);
-        float x[2][4] = {};
+        float x[2][4] = {}, xs[2][4] = {};
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const float* src = Tt + (16 * i + t2) * kPrepLd + 16 * i + 8 * n + gr;   // T_ii[n][k] = Tt[k][n]
-          uint32_t bh[2], bl[2];
-          split_bf16(src[0], src[kPrepLd], bh[0], bl[0]);
-          split_bf16(src[8 * kPrepLd], src[9 * kPrepLd], bh[1], bl[1]);
-          mma_split(x[n], rh, rl, bh, bl);
+          const uint32_t* td = reinterpret_cast<const uint32_t*>(Td + (16 * i + 8 * n + gr) * kDiagLd + t2);
+          const uint32_t bh[2] = {td[0], td[4]}, bl[2] = {td[kTdLo / 2], td[kTdLo / 2 + 4]};
+          mma_16816(x[n], rh, bh);
+          mma_16816(xs[n], rh, bl);
+          mma_16816(xs[n], rl, bh);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) x[n][q] = -x[n][q];
-          float* dst = Tt + (16 * w + gr) * kPrepLd + 16 * i + 8 * n + t2;
-          *reinterpret_cast<float2*>(dst) = make_float2(x[n][0], x[n][1]);
-          *reinterpret_cast<float2*>(dst + 8 * kPrepLd) = make_float2(x[n][2], x[n][3]);
+          for (int q = 0; q < 4; ++q) x[n][q] = -(x[n][q] + xs[n][q]);
         }
-        if (e < 2) split_frag(x, xh[e + 1], xl[e + 1]);
+        uint32_t fh[4], fl[4];
+        split_frag(x, fh, fl);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t o = img_off(16 * w + gr + (q & 1) * 8, 16 * i + t2 + (q >> 1) * 8, 0);
+          *reinterpret_cast<uint32_t*>(Ih + o) = fh[q];
+          *reinterpret_cast<uint32_t*>(Il + o) = fl[q];
+          if (e < 2) {
+            xh[e + 1][q] = fh[q];
+            xl[e + 1][q] = fl[q];
+          }
+        }
       }
     }
   }
   __syncthreads();
 
-  // T into the image (K and Q are no longer needed), thread = row, 8 columns at a time
-  for (int i = tid; i < kChunk * 8; i += kPrepThreads) {
-    const int row = i & 63, c0 = (i >> 6) * 8;
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int c = c0 + 2 * q;
-      const float x0 = c <= row ? Tt[c * kPrepLd + row] : 0.f, x1 = c + 1 <= row ? Tt[(c + 1) * kPrepLd + row] : 0.f;
-      split_bf16(x0, x1, hi[q], lo[q]);
-    }
-    *reinterpret_cast<uint4*>(image + sw128(row, c0)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(image + kImgHalf + sw128(row, c0)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-  }
-  // P T, the warp's rows: sum over the blocks k up to its diagonal one, T's columns up to block k
+  // (P T)^T = T^T P^T: columns (rows of P) 16 rb + 8 (w & 1) .., rows up to block rb
   {
-    float acc[8][4];
+    const int i0 = 16 * rb + 8 * (w & 1);
+    const uint32_t* pr = reinterpret_cast<const uint32_t*>(Pm + (i0 + gr) * kPrepLd + t2);
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
+    for (int nb = 0; nb < 4; ++nb) {
+      float x[4] = {}, xs[4] = {};
+      if (nb <= rb)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+        for (int kb = 0; kb < 4; ++kb)
+          if (kb >= nb && kb <= rb) {
+            uint32_t th[4], tl[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (k <= w) {
-        uint32_t ph[4], pl[4];
-        split_frag(&P[2 * k], ph, pl);
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-          if (n < 2 * k + 2) {
-            const float* src = Tt + (8 * n + gr) * kPrepLd + 16 * k + t2;
-            // inside the diagonal block Tt holds T's zeros above the diagonal
-            uint32_t bh[2], bl[2];
-            split_bf16(src[0], src[1], bh[0], bl[0]);
-            split_bf16(src[8], src[9], bh[1], bl[1]);
-            mma_split(acc[n], ph, pl, bh, bl);
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t o = img_off(16 * nb + gr + (q & 1) * 8, 16 * kb + t2 + (q >> 1) * 8, 0);
+              th[q] = *reinterpret_cast<const uint32_t*>(Ih + o);
+              tl[q] = *reinterpret_cast<const uint32_t*>(Il + o);
+            }
+            const uint32_t bh[2] = {pr[8 * kb], pr[8 * kb + 4]};
+            const uint32_t bl[2] = {pr[kPLo / 2 + 8 * kb], pr[kPLo / 2 + 8 * kb + 4]};
+            mma_16816(x, th, bh);
+            mma_16816(xs, th, bl);
+            mma_16816(xs, tl, bh);
           }
-      }
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int q = 0; q < 2; ++q) {
         uint32_t hi, lo;
-        split_bf16(acc[n][2 * r], acc[n][2 * r + 1], hi, lo);
-        const uint32_t o = sw128(kChunk + 16 * w + gr + 8 * r, 8 * n + t2);
-        *reinterpret_cast<uint32_t*>(image + o) = hi;
-        *reinterpret_cast<uint32_t*>(image + kImgHalf + o) = lo;
+        split_bf16(x[2 * q] + xs[2 * q], x[2 * q + 1] + xs[2 * q + 1], hi, lo);
+        const uint32_t o = img_off(16 * nb + gr + 8 * q, i0 + t2, 1);
+        *reinterpret_cast<uint32_t*>(Ih + o) = hi;   // (all of A has been read)
+        *reinterpret_cast<uint32_t*>(Il + o) = lo;
       }
-  }
-  uint8_t* dst = prep + (slot * a.Hv + h) * (long long)kPrepBytes;
-  float* fac = reinterpret_cast<float*>(dst + kPrepFactors);
-  if (tid < kChunk) {
-    const double end = G[len - 1];
-    fac[kFacDecay + tid] = expf((float)G[tid]);
-    fac[kFacToEnd + tid] = tid < len ? expf((float)(end - G[tid])) : 0.f;
-    fac[kFacBeta + tid] = beta[tid];
-    if (tid == 0) {
-      fac[kFacChunk] = expf((float)end);
-      reinterpret_cast<int*>(fac)[kFacBad] = *bad;
     }
   }
+  if (tid == 0) reinterpret_cast<int*>(dst + kPrepFactors)[kFacBad] = *bad;
   fence_proxy_async_smem();
   __syncthreads();
   if (tid == 0) {
-    bulk_store(dst, image, 2 * kImgHalf);
+    bulk_store(dst, smem, 2 * kImgHalf);
     bulk_commit_group();
-    bulk_wait_group<0>();
+    bulk_wait_group_read<0>();
   }
 }
 
@@ -362,74 +495,139 @@ __global__ void __launch_bounds__(kPrepThreads) litela_delta_prep(const DeltaArg
 // state's columns (columns do not meet, so a state is cut by columns over CTAs).
 //
 // Three tcgen05 products per chunk, each with M = 128 rows, fp32 accumulators in TMEM:
-//     X1 = [K; Q] S0           (rows: 64 of K, 64 of Q; K dimension d)
-//     X2 = [T; P T] R          (K dimension 64)
+//     X1 = [K; Q] S0           (rows: 16 of K, 16 of Q, 16 of K ..; K dimension d)
+//     X2 = [T; P T] R          (rows alike; K dimension 64)
 //     X3 = K^T (e^(G_C - G) U) (rows: d; K dimension 64)
 // Between them eight warps take the accumulators to registers, form R, then U, then the new state,
 // and write them as bf16 pairs into shared memory as the next product's B operand.  The chain of
 // these six steps is what a chunk costs; the loads of the next chunks, the output rows' arithmetic
 // and their stores run beside it.  All B operands are tiles of 128-byte rows (row: K index, 64 bf16 columns,
-// MN-major): with kCols = 64 a hi and a lo tile; with kCols = 32 one tile with hi and lo side by
-// side, whose products land in two column ranges that the readers add.
+// MN-major): with kCols = 64 one tile per bf16 term; with kCols = 32 two terms side by side in a
+// tile, whose products land in column ranges of their own that the readers add.
 //
-// Warps: 0-7 accumulators (warp % 4: TMEM lanes; warp / 4: which half of the columns), 8 issues
-// the products, 9-12 load (cp.async for the strided K, Q, V rows; one bulk copy for the prepared
-// block).  Every wait is bounded; a time-out is recorded in *err.
+// Warps: 0-7 accumulators (warp % 4: TMEM lanes; warp / 4: which half of the columns), 8 and 9 load
+// (cp.async for the strided K, Q, V rows; one bulk copy for the prepared block), 10 issues the
+// products.  The accumulator warps hand over with named barriers (one-way ~40 cycles; an mbarrier wait
+// costs ~170 here even when its phase is over), the tensor core with mbarriers, which one lane of a
+// warp polls; waits for loads stand where a warp would idle anyway.  A tcgen05 product of 16 of the K dimension takes ~47
+// cycles whatever N <= 96 is, so the terms go side by side where that saves products.
+// Every mbarrier wait is bounded; after a time-out (recorded in *err) all roles run their loops to
+// the end without waiting, so that the named barriers stay matched.
 constexpr int kChainStages = 2;
-constexpr int kChainThreads = 13 * 32;
-constexpr int kLoadThreads = 4 * 32;
+constexpr int kAccWarps = 8;
+constexpr int kIssueWarp = kAccWarps + 2;   // on a scheduler whose accumulator warps have rows of Q
+constexpr int kLoadWarps = 2;
+constexpr int kChainThreads = (kAccWarps + 1 + kLoadWarps) * 32;   // 11 warps: up to 168 registers a thread
+constexpr int kLoadThreads = kLoadWarps * 32;
 constexpr uint32_t kChainTmem = 256;
 enum : int { kErrChainLoad = 0x510, kErrChainMma = 0x520, kErrChainAcc = 0x530 };
+// named barriers: S0, R and U are in shared memory (accumulator warps arrive, the issuer waits)
+enum : int { kBarS = 1, kBarR = 2, kBarU = 3 };
+constexpr int kBarThreads = (kAccWarps + 1) * 32;
 
 template <int kD, int kCols>
 struct ChainCfg {
   static constexpr int kBlocks = kD > 64 ? 2 : 1;                 // 64-channel blocks of K and Q
-  static constexpr uint32_t kKQ = kBlocks * 16384;                // per block: 64 rows of K, 64 of Q
+  static constexpr uint32_t kKQ = kBlocks * 16384;                // per block: 64 rows of K and of Q
   static constexpr uint32_t kVLd = kCols * 2 + 16;                // padded row of V
   static constexpr uint32_t kV = 64 * kVLd;
   static constexpr uint32_t kOffPrep = kKQ;
   static constexpr uint32_t kOffV = kKQ + kPrepBytes;
   static constexpr uint32_t kStage = (kOffV + kV + 1023) / 1024 * 1024;
-  static constexpr int kTiles = kCols == 64 ? 2 : 1;              // tiles of a B operand
+  static constexpr int kSTiles = kCols == 64 ? 2 : 1;             // tiles of S0 (two terms)
+  static constexpr int kRTiles = kCols == 64 ? 3 : 2;             // tiles of R and U (three terms)
   static constexpr uint32_t kSTile = kD * 128, kRTile = 64 * 128;
   static constexpr uint32_t kOffS = kChainStages * kStage;
-  static constexpr uint32_t kOffR = kOffS + kTiles * kSTile;
-  static constexpr uint32_t kOffBars = kOffR + kTiles * kRTile;
+  static constexpr uint32_t kOffR = kOffS + kSTiles * kSTile;
+  static constexpr uint32_t kOffBars = kOffR + kRTiles * kRTile;
+  // TMEM columns of the three products
+  static constexpr uint32_t kX1 = 0, kX2 = 64, kX3 = kCols == 64 ? 128 : 160;
   static constexpr uint32_t kSmemBytes = kOffBars + 256 + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory above the 227 KB per-block limit");
+  static_assert(kLoadThreads == kChunk, "a loading thread prefetches one row");
 };
 
-// kN accumulators of this thread's TMEM lane from column c of a product's 64 columns
-template <int kCols, int kN>
-__device__ __forceinline__ void chain_acc(uint32_t taddr, int c, float* x) {
-  using namespace sm100;
-  if (kCols == 64) {
-    uint32_t r[32];
-    tmem_ld_x32(taddr + c, r);
-    tmem_wait_ld();
+// A warp's share of a product whose B operand has kTerms terms.  chain_acc: its 32 lanes, kN columns
+// from c on, a lane's columns to its thread.  chain_frag: 16 of its lanes, 8 kG columns from c on: thread
+// t gets the rows t / 4 and t / 4 + 8, columns 2 (t % 4) of each 8, as x[2 g + half].
+template <int kN>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r) {
+  if constexpr (kN == 32) sm100::tmem_ld_x32(taddr, r);
+  if constexpr (kN == 16) sm100::tmem_ld_x16(taddr, r);
+  if constexpr (kN == 8) sm100::tmem_ld_x8(taddr, r);
+}
+template <int kCols, int kTerms, int kN>
+__device__ __forceinline__ void chain_acc(uint32_t taddr, int c, F2* x) {
+  constexpr int kRanges = kCols == 64 ? 1 : kTerms;
+  uint32_t r[kRanges][kN];
 #pragma unroll
-    for (int i = 0; i < kN; ++i) x[i] = __uint_as_float(r[i]);
-  } else {   // the hi and the lo operand's columns
-    uint32_t r[16], l[16];
-    tmem_ld_x16(taddr + c, r);
-    tmem_ld_x16(taddr + 32 + c, l);
-    tmem_wait_ld();
+  for (int t = 0; t < kRanges; ++t) tmem_ld<kN>(taddr + 32 * t + c, r[t]);
+  sm100::tmem_wait_ld();
+  auto get = [&](int t, int i) { return f2(__uint_as_float(r[t][2 * i]), __uint_as_float(r[t][2 * i + 1])); };
 #pragma unroll
-    for (int i = 0; i < kN; ++i) x[i] = __uint_as_float(r[i]) + __uint_as_float(l[i]);
+  for (int i = 0; i < kN / 2; ++i) {   // the small terms first
+    x[i] = get(kRanges - 1, i);
+#pragma unroll
+    for (int t = kRanges - 2; t >= 0; --t) x[i] = f2_add(x[i], get(t, i));
+  }
+}
+template <int kCols, int kTerms, int kG>
+__device__ __forceinline__ void chain_frag(uint32_t taddr, int c, F2* x) {
+  constexpr int kRanges = kCols == 64 ? 1 : kTerms;
+  uint32_t r[kRanges][4 * kG];
+#pragma unroll
+  for (int t = 0; t < kRanges; ++t) {
+    if constexpr (kG == 1) sm100::tmem_ld_16x256b_x1(taddr + 32 * t + c, r[t]);
+    if constexpr (kG == 2) sm100::tmem_ld_16x256b_x2(taddr + 32 * t + c, r[t]);
+    if constexpr (kG == 4) sm100::tmem_ld_16x256b_x4(taddr + 32 * t + c, r[t]);
+  }
+  sm100::tmem_wait_ld();
+  auto get = [&](int t, int i) { return f2(__uint_as_float(r[t][2 * i]), __uint_as_float(r[t][2 * i + 1])); };
+#pragma unroll
+  for (int i = 0; i < 2 * kG; ++i) {
+    x[i] = get(kRanges - 1, i);
+#pragma unroll
+    for (int t = kRanges - 2; t >= 0; --t) x[i] = f2_add(x[i], get(t, i));
   }
 }
 
-// kN values of a B operand's row, columns c .. c + kN - 1, as a bf16 pair
-template <int kCols, int kN>
-__device__ __forceinline__ void chain_put(uint8_t* tile, uint32_t lo_tile, int row, int c, const float* x) {
+// the next bf16 term of a pair, which it leaves
+__device__ __forceinline__ uint32_t next_term(F2& y, bool last) {
+  const float2 z = f2_out(y);
+  const uint32_t w = pack_bf16(z.x, z.y);
+  if (!last) y = f2_fma(f2_bf16(w), f2(-1.f, -1.f), y);
+  return w;
+}
+// Into a B operand: kN values (pairs) of a row, columns c .. c + kN - 1, in kTerms bf16 terms
+template <int kCols, int kTerms, int kN>
+__device__ __forceinline__ void chain_put(uint8_t* tile, uint32_t tile_bytes, int row, int c, const F2* x) {
 #pragma unroll
   for (int i = 0; i < kN; i += 8) {
-    uint32_t hi[4], lo[4];
+    F2 y[4] = {x[i / 2], x[i / 2 + 1], x[i / 2 + 2], x[i / 2 + 3]};
 #pragma unroll
-    for (int q = 0; q < 4; ++q) split_bf16(x[i + 2 * q], x[i + 2 * q + 1], hi[q], lo[q]);
-    *reinterpret_cast<uint4*>(tile + sw128(row, c + i)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(kCols == 64 ? tile + lo_tile + sw128(row, c + i) : tile + sw128(row, 32 + c + i)) =
-        make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    for (int t = 0; t < kTerms; ++t) {
+      uint32_t w[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) w[q] = next_term(y[q], t + 1 == kTerms);
+      uint8_t* dst = kCols == 64 ? tile + t * tile_bytes + sw128(row, c + i)
+                                 : tile + (t / 2) * tile_bytes + sw128(row, (t & 1) * 32 + c + i);
+      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+// ... a thread's part of chain_frag's arrangement; row: of its first half, c: its first column
+template <int kCols, int kTerms, int kG>
+__device__ __forceinline__ void chain_put_frag(uint8_t* tile, uint32_t tile_bytes, int row, int c, const F2* x) {
+#pragma unroll
+  for (int i = 0; i < 2 * kG; ++i) {
+    F2 y = x[i];
+    const int r = row + (i & 1) * 8, cc = c + (i >> 1) * 8;
+#pragma unroll
+    for (int t = 0; t < kTerms; ++t) {
+      uint8_t* dst = kCols == 64 ? tile + t * tile_bytes + sw128(r, cc)
+                                 : tile + (t / 2) * tile_bytes + sw128(r, (t & 1) * 32 + cc);
+      *reinterpret_cast<uint32_t*>(dst) = next_term(y, t + 1 == kTerms);
+    }
   }
 }
 
@@ -438,19 +636,15 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, int* __restrict__ err) {
   using namespace sm100;
   using Cfg = ChainCfg<kD, kCols>;
-  constexpr int kN = kCols / 2;   // columns of an accumulator warp
+  constexpr int kN = kCols * 4 / kAccWarps;   // columns of an accumulator warp
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stile = smem + Cfg::kOffS;
   uint8_t* rtile = smem + Cfg::kOffR;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::kOffBars);   // K, Q, V rows landed
-  uint64_t* pfull = full + kChainStages;                                // the prepared block landed
-  uint64_t* empty = pfull + kChainStages;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::kOffBars);   // K, Q, V and the block landed
+  uint64_t* empty = full + kChainStages;
   uint64_t* done = empty + kChainStages;   // X1, X2, X3
-  uint64_t* sready = done + 3;
-  uint64_t* rready = sready + 1;
-  uint64_t* uready = rready + 1;
-  uint64_t* drained = uready + 1;
+  uint64_t* drained = done + 3;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* first_bad = reinterpret_cast<int*>(tmem_holder + 2);   // first token whose R was not finite
@@ -466,20 +660,16 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, int* __r
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kChainStages; ++i) {
-      mbar_init(&full[i], 4);
-      mbar_init(&pfull[i], 1);
-      mbar_init(&empty[i], 9);
+      mbar_init(&full[i], kLoadWarps + 1);
+      mbar_init(&empty[i], kAccWarps + 1);
     }
     for (int i = 0; i < 3; ++i) mbar_init(&done[i], 1);
-    mbar_init(sready, 8);
-    mbar_init(rready, 4);
-    mbar_init(uready, 4);
     mbar_init(drained, 1);
     *abort_flag = 0;
     *first_bad = 0x7fffffff;
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (warp == kIssueWarp) {
     tmem_alloc(tmem_holder, kChainTmem);
     tmem_relinquish();
   }
@@ -488,197 +678,270 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, int* __r
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_holder;
 
-  if (warp < 8) {
+  if (warp < kAccWarps) {
+    constexpr int kG = kN / 8;
     const int quad = warp & 3, c0 = (warp >> 2) * kN, row = quad * 32 + lane;
-    const uint32_t ta = tmem + ((uint32_t)(quad * 32) << 16);
-    const bool has_state = row < kD;       // this thread has a row of the state
-    const bool is_q = quad >= 2;           // ... of the first two products: a row of Q, else of K
-    const int tok = row & 63;
+    const uint32_t ta = tmem + ((uint32_t)(quad * 32) << 16), tq = ta + (16u << 16);   // lanes of K's, of Q's rows
+    const bool has_state = row < kD;                                 // this thread has a row of the state
+    const int tok = quad * 16 + (lane >> 2), fc = c0 + (lane & 3) * 2;   // chain_frag: tokens tok and tok + 8
     const long long sbase = ((long long)s * a.Hv + h) * (kD * kD) + (long long)row * kD + part * kCols + c0;
-    float S[kN];
+    F2 S[kN / 2];
 #pragma unroll
-    for (int i = 0; i < kN; ++i) S[i] = 0.f;
+    for (int i = 0; i < kN / 2; ++i) S[i] = f2(0.f, 0.f);
     if (has_state && a.state_in != nullptr)
 #pragma unroll
       for (int i = 0; i < kN; i += 4) {
         const float4 x = *reinterpret_cast<const float4*>(a.state_in + sbase + i);
-        S[i] = x.x, S[i + 1] = x.y, S[i + 2] = x.z, S[i + 3] = x.w;
+        S[i / 2] = f2(x.x, x.y), S[i / 2 + 1] = f2(x.z, x.w);
       }
     bool ok = true;
-    auto hand = [&](uint64_t* bar) {   // this warp's shared-memory writes and TMEM reads are done
-      fence_proxy_async_smem();
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar);
-    };
     auto wait = [&](uint64_t* bar, int phase, int code) {
-      ok = ok && mbar_wait(bar, phase & 1, abort_flag, err, kErrChainAcc | code);
+      if (ok) ok = mbar_wait(bar, phase & 1, abort_flag, err, kErrChainAcc | code);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after_sync();
-      return ok;
     };
-    if (nchunk > 0) {
-      if (has_state) chain_put<kCols, kN>(stile, Cfg::kSTile, row, c0, S);
-      hand(sready);
-    }
-    for (int n = 0; n < nchunk; ++n) {
+    auto hand = [&](int id, int count) {   // this warp's shared-memory writes and TMEM reads are done
+      fence_proxy_async_smem();
+      tc_fence_before_sync();
+      bar_arrive(id, count);
+    };
+    float decay[2] = {}, to_end[2] = {}, beta[2] = {}, chunk_decay = 0.f;
+    int prep_bad = 0;
+    uint32_t v[2 * kG];
+    auto fetch = [&](int n) {   // chunk n's factors and values
       const int st = n % kChainStages;
-      uint8_t* stage = smem + st * Cfg::kStage;
-      if (!wait(&full[st], n / kChainStages, 0) || !wait(&pfull[st], n / kChainStages, 1)) break;
+      const uint8_t* stage = smem + st * Cfg::kStage;
+      wait(&full[st], n / kChainStages, 0);
       const float* fac = reinterpret_cast<const float*>(stage + Cfg::kOffPrep + kPrepFactors);
-      const float decay = fac[kFacDecay + tok], to_end = fac[kFacToEnd + tok], beta = fac[kFacBeta + tok];
-      const float chunk_decay = fac[kFacChunk];
-      const int prep_bad = reinterpret_cast<const int*>(fac)[kFacBad];
-      uint4 v[kN / 8];
-      if (!is_q)
 #pragma unroll
-        for (int i = 0; i < kN / 8; ++i)
-          v[i] = *reinterpret_cast<const uint4*>(stage + Cfg::kOffV + tok * Cfg::kVLd + c0 * 2 + i * 16);
+      for (int i = 0; i < 2; ++i) {
+        decay[i] = fac[kFacDecay + tok + 8 * i];
+        to_end[i] = fac[kFacToEnd + tok + 8 * i];
+        beta[i] = fac[kFacBeta + tok + 8 * i];
+      }
+      chunk_decay = fac[kFacChunk];
+      prep_bad = reinterpret_cast<const int*>(fac)[kFacBad];
+#pragma unroll
+      for (int i = 0; i < 2 * kG; ++i)
+        v[i] = *reinterpret_cast<const uint32_t*>(stage + Cfg::kOffV + (tok + (i & 1) * 8) * Cfg::kVLd + (fc + (i >> 1) * 8) * 2);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
-      float x[kN];
-      if (!wait(&done[0], n, 2)) break;
-      if (!is_q) {   // R = beta (v - e^G K S0)
-        chain_acc<kCols, kN>(ta, c0, x);
-        float zero = 0.f;   // stays 0 while all are finite
+    };
+    if (nchunk > 0) {
+      if (has_state) chain_put<kCols, 2, kN>(stile, Cfg::kSTile, row, c0, S);
+      hand(kBarS, kBarThreads);
+    }
+    for (int n = 0; n < nchunk; ++n) {
+      fetch(n);   // while the first product runs
+      F2 x[kN / 2], y[kN / 2];
+      wait(&done[0], n, 2);
+      // R = beta (v - e^G K S0)
+      chain_frag<kCols, 2, kG>(ta + Cfg::kX1, c0, x);
+      F2 zero = f2(0.f, 0.f);   // stays 0 while all are finite
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const uint32_t wv = reinterpret_cast<const uint32_t*>(v)[i / 2];
-          x[i] = beta * (__uint_as_float((i & 1) ? wv & 0xFFFF0000u : wv << 16) - decay * x[i]);
-          zero += 0.f * x[i];
-        }
-        if (zero != 0.f) {
-#pragma unroll
-          for (int i = 0; i < kN; ++i) x[i] = 0.f;
-          atomicMin(first_bad, n * kChunk + tok);
-        }
-        chain_put<kCols, kN>(rtile, Cfg::kRTile, tok, c0, x);
-        hand(rready);
-      } else {       // the output's share of S0
-        chain_acc<kCols, kN>(ta, c0, x);
-#pragma unroll
-        for (int i = 0; i < kN; ++i) x[i] *= a.scale * decay;
+      for (int i = 0; i < 2 * kG; ++i) {
+        const float d = decay[i & 1], b = beta[i & 1];
+        x[i] = f2_mul(f2(b, b), f2_fma(f2(-d, -d), x[i], f2_bf16(v[i])));
+        zero = f2_fma(f2(0.f, 0.f), x[i], zero);
       }
-      if (!wait(&done[1], n, 3)) break;
-      const bool bad = tok >= prep_bad || n * kChunk + tok >= *static_cast<volatile int*>(first_bad);
+      const float2 z = f2_out(zero);
+      if (z.x + z.y != 0.f) {
+#pragma unroll
+        for (int i = 0; i < 2 * kG; ++i) {
+          const float2 xi = f2_out(x[i]);
+          if (!isfinite(xi.x) || !isfinite(xi.y)) atomicMin(first_bad, n * kChunk + tok + (i & 1) * 8);
+          x[i] = f2(0.f, 0.f);
+        }
+      }
+      chain_put_frag<kCols, 3, kG>(rtile, Cfg::kRTile, tok, fc, x);
+      hand(kBarR, kBarThreads);
+      chain_frag<kCols, 2, kG>(tq + Cfg::kX1, c0, y);   // the output's share of S0
+#pragma unroll
+      for (int i = 0; i < 2 * kG; ++i) {
+        const float d = a.scale * decay[i & 1];
+        y[i] = f2_mul(f2(d, d), y[i]);
+      }
+      wait(&done[1], n, 3);
+      const int bad_from = min(prep_bad, *static_cast<volatile int*>(first_bad) - n * kChunk);
       const float nan = __int_as_float(0x7fffffff);
-      if (!is_q) {   // e^(G_C - G) U
-        chain_acc<kCols, kN>(ta + 64, c0, x);
+      // e^(G_C - G) U
+      chain_frag<kCols, 3, kG>(ta + Cfg::kX2, c0, x);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) x[i] = bad ? nan : x[i] * to_end;
-        chain_put<kCols, kN>(rtile, Cfg::kRTile, tok, c0, x);
-        hand(uready);
-      } else {
-        float y[kN];
-        chain_acc<kCols, kN>(ta + 64, c0, y);
-#pragma unroll
-        for (int i = 0; i < kN; ++i) y[i] = bad ? nan : y[i] + x[i];
-        if (n * kChunk + tok < sq.len) {
-          uint4* o = reinterpret_cast<uint4*>(const_cast<__nv_bfloat16*>(delta_row(a.out, sq, n * kChunk + tok, h)) +
-                                              part * kCols + c0);
-#pragma unroll
-          for (int i = 0; i < kN; i += 8)
-            o[i / 8] = make_uint4(pack_bf16(y[i], y[i + 1]), pack_bf16(y[i + 2], y[i + 3]),
-                                  pack_bf16(y[i + 4], y[i + 5]), pack_bf16(y[i + 6], y[i + 7]));
-        }
+      for (int i = 0; i < 2 * kG; ++i) {
+        const float e = tok + (i & 1) * 8 >= bad_from ? nan : to_end[i & 1];
+        x[i] = f2_mul(f2(e, e), x[i]);
       }
-      if (!wait(&done[2], n, 4)) break;
+      chain_put_frag<kCols, 3, kG>(rtile, Cfg::kRTile, tok, fc, x);
+      hand(kBarU, kBarThreads);
+      // the output, while the third product runs
+      chain_frag<kCols, 3, kG>(tq + Cfg::kX2, c0, x);
+#pragma unroll
+      for (int i = 0; i < 2 * kG; ++i) {
+        const int t = tok + (i & 1) * 8;
+        const float2 o = f2_out(f2_add(x[i], y[i]));
+        if (n * kChunk + t < sq.len)
+          *reinterpret_cast<uint32_t*>(const_cast<__nv_bfloat16*>(delta_row(a.out, sq, n * kChunk + t, h)) + part * kCols +
+                                       fc + (i >> 1) * 8) = t >= bad_from ? 0x7fff7fffu : pack_bf16(o.x, o.y);
+      }
+      wait(&done[2], n, 4);
       if (has_state) {   // (a warp's 32 rows are all of the state, or none)
-        chain_acc<kCols, kN>(ta + 128, c0, x);
+        chain_acc<kCols, 3, kN>(ta + Cfg::kX3, c0, x);
+        const F2 d2 = f2(chunk_decay, chunk_decay);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) S[i] = chunk_decay * S[i] + x[i];
-        if (n + 1 < nchunk) chain_put<kCols, kN>(stile, Cfg::kSTile, row, c0, S);
+        for (int i = 0; i < kN / 2; ++i) S[i] = f2_fma(d2, S[i], x[i]);
+        if (n + 1 < nchunk) chain_put<kCols, 2, kN>(stile, Cfg::kSTile, row, c0, S);
       }
-      if (n + 1 < nchunk) hand(sready);
+      if (n + 1 < nchunk) hand(kBarS, kBarThreads);
     }
     if (ok && has_state && a.state_out != nullptr)
 #pragma unroll
       for (int i = 0; i < kN; i += 4)
-        *reinterpret_cast<float4*>(a.state_out + sbase + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
-  } else if (warp == 8) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(128, 64, false, true);
-      constexpr uint32_t idesc_t = idesc_bf16_f32(128, 64, true, true);
-      const uint32_t sa = smem_u32(stile), ra = smem_u32(rtile);
+        *reinterpret_cast<float4*>(a.state_out + sbase + i) =
+            make_float4(f2_out(S[i / 2]).x, f2_out(S[i / 2]).y, f2_out(S[i / 2 + 1]).x, f2_out(S[i / 2 + 1]).y);
+  } else if (warp == kIssueWarp) {
+    {
+      // kCols = 32: the terms of R side by side, 96 columns over two tiles
+      constexpr int kRN = kCols == 64 ? 64 : 96;
+      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 64, false, true);
+      constexpr uint32_t idesc_r = idesc_bf16_f32(128, kRN, true, true);
+      constexpr uint32_t idesc_1 = idesc_bf16_f32(128, 32, true, true);
+      // descriptors of each operand's first 16 of the K dimension; an offset of n bytes adds n / 16
+      const uint64_t sdesc = smem_desc(smem_u32(stile), 1024, 1024, kSwizzle128B);
+      const uint64_t rdesc = smem_desc(smem_u32(rtile), Cfg::kRTile, 1024, kSwizzle128B);
+      const uint64_t kqdesc = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+      const uint64_t imgdesc = smem_desc(smem_u32(smem) + Cfg::kOffPrep, kImgBlock, 1024, kSwizzle128B);
+      // K^T: M over channels, 16 tokens every 32 rows.  d = 128: the second 64 channels are the next
+      // block.  Smaller d: rows 64 on take other rows, results that nobody reads.
+      const uint64_t ktdesc = smem_desc(smem_u32(smem), kD > 64 ? 16384 : 8192, 1024, kSwizzle128B);
+      bool ok = true;
       auto wait = [&](uint64_t* bar, int phase, int code) {
-        const bool ok = mbar_wait(bar, phase & 1, abort_flag, err, kErrChainMma | code);
-        tc_fence_after_sync();
-        return ok;
+        if (ok && lane == 0) ok = mbar_spin(bar, phase & 1, abort_flag, err, kErrChainMma | code);
+        ok = __all_sync(0xffffffffu, ok);
       };
+      if (nchunk > 0) {
+        wait(&full[0], 0, 0);
+      }
       for (int n = 0; n < nchunk; ++n) {
         const int st = n % kChainStages;
-        const uint32_t kq = smem_u32(smem + st * Cfg::kStage), img = kq + Cfg::kOffPrep;
-        if (!wait(&full[st], n / kChainStages, 0) || !wait(sready, n, 1)) break;
+        const uint64_t off = st * (Cfg::kStage / 16);
+        bar_sync(kBarS, kBarThreads);
+        tc_fence_after_sync();
+        if (ok && lane == 0) {
 #pragma unroll
-        for (int ks = 0; ks < kD / 16; ++ks) {
-          const uint64_t ad = smem_desc(kq + (ks / 4) * 16384 + (ks % 4) * 32, 16, 1024, kSwizzle128B);
+          for (int t = Cfg::kSTiles - 1; t >= 0; --t)   // the small terms first
 #pragma unroll
-          for (int t = 0; t < Cfg::kTiles; ++t)
-            umma_bf16(tmem, ad, smem_desc(sa + t * Cfg::kSTile + ks * 2048, 1024, 1024, kSwizzle128B), idesc, ks | t);
+            for (int ks = 0; ks < kD / 16; ++ks)
+              umma_bf16(tmem + Cfg::kX1, kqdesc + off + (ks / 4) * 1024 + (ks % 4) * 2,
+                        sdesc + t * (Cfg::kSTile / 16) + ks * 128, idesc_s, ks > 0 || t < Cfg::kSTiles - 1);
+          umma_commit(&done[0]);
         }
-        umma_commit(&done[0]);
-        if (!wait(&pfull[st], n / kChainStages, 2) || !wait(rready, n, 3)) break;
+        __syncwarp();
+        bar_sync(kBarR, kBarThreads);
+        tc_fence_after_sync();
+        if (ok && lane == 0) {
+          if (kCols == 64) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          const uint64_t hi = smem_desc(img + ks * 32, 16, 1024, kSwizzle128B);
-          const uint64_t lo = smem_desc(img + kImgHalf + ks * 32, 16, 1024, kSwizzle128B);
-          const uint64_t b = smem_desc(ra + ks * 2048, 1024, 1024, kSwizzle128B);
-          umma_bf16(tmem + 64, hi, b, idesc, ks);
-          if (Cfg::kTiles == 2)
-            umma_bf16(tmem + 64, hi, smem_desc(ra + Cfg::kRTile + ks * 2048, 1024, 1024, kSwizzle128B), idesc, 1u);
-          umma_bf16(tmem + 64, lo, b, idesc, 1u);
+            for (int t = 2; t >= 1; --t)
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                umma_bf16(tmem + Cfg::kX2, imgdesc + off + ks * 128, rdesc + t * (Cfg::kRTile / 16) + ks * 128, idesc_r,
+                          ks > 0 || t < 2);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              umma_bf16(tmem + Cfg::kX2, imgdesc + off + kImgHalf / 16 + ks * 128, rdesc + ks * 128, idesc_r, 1u);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              umma_bf16(tmem + Cfg::kX2, imgdesc + off + ks * 128, rdesc + ks * 128, idesc_r, 1u);
+          } else {   // T's and P T's lo terms with R's first term alone
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              umma_bf16(tmem + Cfg::kX2, imgdesc + off + ks * 128, rdesc + ks * 128, idesc_r, ks > 0);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              umma_bf16(tmem + Cfg::kX2, imgdesc + off + kImgHalf / 16 + ks * 128, rdesc + ks * 128, idesc_1, 1u);
+          }
+          umma_commit(&done[1]);
         }
-        umma_commit(&done[1]);
-        if (!wait(uready, n, 4)) break;
+        __syncwarp();
+        bar_sync(kBarU, kBarThreads);
+        tc_fence_after_sync();
+        if (ok && lane == 0) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          // K^T: M over channels.  d = 128: the second 64 are the next block.  Smaller d: rows 64
-          // on take Q's channels, results that nobody reads.
-          const uint64_t ad = smem_desc(kq + ks * 2048, kD > 64 ? 16384 : 8192, 1024, kSwizzle128B);
+          for (int t = (kCols == 64 ? 2 : 0); t >= 0; --t)
 #pragma unroll
-          for (int t = 0; t < Cfg::kTiles; ++t)
-            umma_bf16(tmem + 128, ad, smem_desc(ra + t * Cfg::kRTile + ks * 2048, 1024, 1024, kSwizzle128B), idesc_t,
-                      ks | t);
+            for (int ks = 0; ks < 4; ++ks)
+              umma_bf16(tmem + Cfg::kX3, ktdesc + off + ks * 256, rdesc + t * (Cfg::kRTile / 16) + ks * 128, idesc_r,
+                        ks > 0 || t < (kCols == 64 ? 2 : 0));
+          umma_commit(&done[2]);
+          umma_commit(&empty[st]);
         }
-        umma_commit(&done[2]);
-        umma_commit(&empty[st]);
+        __syncwarp();
+        if (n + 1 < nchunk) {   // while the accumulator warps make the next S0
+          wait(&full[(n + 1) % kChainStages], (n + 1) / kChainStages, 0);
+        }
       }
-      // products in flight end before the memory under them is given back
-      umma_commit(drained);
-      mbar_drain(drained, 0);
+      if (lane == 0) {
+        // products in flight end before the memory under them is given back
+        umma_commit(drained);
+        mbar_drain(drained, 0);
+      }
     }
   } else {
-    const int t = threadIdx.x - 9 * 32;
+    const int t = threadIdx.x - (warp > kIssueWarp ? kAccWarps + 1 : kAccWarps) * 32;
     pdl_wait_primary();
     fence_proxy_async_global();   // the prepared blocks are read by bulk copies
     int issued = 0;
+    // A thread copies one 16-byte column of every kStep-th row, of K and Q and of V: its places in a
+    // stage differ by constants, its places in memory by a stride.
+    constexpr int kC = kD / 8, kStep = kLoadThreads / kC, kVC = kCols / 8, kVStep = kLoadThreads / kVC;
+    const int r0 = t / kC, c = t % kC, vr0 = t / kVC;
+    const uint32_t kq0 = smem_u32(smem) + (c / 8) * 16384 + sw128(lane_of(r0), (c % 8) * 8);
+    const uint32_t v0 = smem_u32(smem) + Cfg::kOffV + vr0 * Cfg::kVLd + (t % kVC) * 16;
+    const __nv_bfloat16* kp = delta_row(a.k, sq, r0, hk) + c * 8;
+    const __nv_bfloat16* qp = delta_row(a.q, sq, r0, hk) + c * 8;
+    const __nv_bfloat16* vp = delta_row(a.v, sq, vr0, h) + part * kCols + (t % kVC) * 8;
+    const long long kstep = kStep * a.k.st, qstep = kStep * a.q.st, vstep = kVStep * a.v.st;
     for (int n = 0; n < nchunk; ++n) {
       const int st = n % kChainStages;
-      bool ok = n < kChainStages ||
-                mbar_wait(&empty[st], (n / kChainStages - 1) & 1, abort_flag, err, kErrChainLoad | st);
+      const bool ok = n < kChainStages || lane != 0 ||
+                      mbar_wait(&empty[st], (n / kChainStages - 1) & 1, abort_flag, err, kErrChainLoad | st);
       if (!__all_sync(0xffffffffu, ok)) break;
-      uint8_t* stage = smem + st * Cfg::kStage;
       if (t == 0) {
-        mbar_arrive_expect_tx(&pfull[st], kPrepBytes);
-        bulk_load(stage + Cfg::kOffPrep, blocks + n * block_step, kPrepBytes, &pfull[st]);
+        mbar_arrive_expect_tx(&full[st], kPrepBytes);
+        bulk_load(smem + st * Cfg::kStage + Cfg::kOffPrep, blocks + n * block_step, kPrepBytes, &full[st]);
       }
       issued = n + 1;
       const int n0 = n * kChunk, len = min(kChunk, sq.len - n0);
-      const uint32_t kq = smem_u32(stage), vs = kq + Cfg::kOffV;
-#pragma unroll 4
-      for (int i = t; i < 128 * (kD / 8); i += kLoadThreads) {
-        const int c = i % (kD / 8), r = i / (kD / 8);   // row: 64 of K, then 64 of Q
-        const int tok = r & 63;
-        const bool real = tok < len;
-        const __nv_bfloat16* src = delta_row(r < 64 ? a.k : a.q, sq, n0 + (real ? tok : 0), hk) + c * 8;
-        cp_async_16(kq + (c / 8) * 16384 + sw128(r, (c % 8) * 8), src, real);
+      const uint32_t dkq = kq0 + st * Cfg::kStage, dv = v0 + st * Cfg::kStage;
+#pragma unroll
+      for (int i = 0; i < kChunk / kStep; ++i) {
+        // row r0 + i kStep (r0 < kStep, powers of two: the swizzle is r0's, xor the step's); Q's row is 16 on
+        const uint32_t o = (dkq ^ (((i * kStep) & 7) << 4)) + lane_of(i * kStep) * 128;
+        const bool real = r0 + i * kStep < len;
+        cp_async_16(o, real ? kp : a.k.p, real);
+        cp_async_16(o + 2048, real ? qp : a.q.p, real);
+        kp += kstep;
+        qp += qstep;
       }
-#pragma unroll 4
-      for (int i = t; i < 64 * (kCols / 8); i += kLoadThreads) {
-        const int c = i % (kCols / 8), tok = i / (kCols / 8);
-        const bool real = tok < len;
-        cp_async_16(vs + tok * Cfg::kVLd + c * 16, delta_row(a.v, sq, n0 + (real ? tok : 0), h) + part * kCols + c * 8,
-                    real);
+#pragma unroll
+      for (int i = 0; i < kChunk / kVStep; ++i) {
+        const bool real = vr0 + i * kVStep < len;
+        cp_async_16(dv + i * kVStep * Cfg::kVLd, real ? vp : a.v.p, real);
+        vp += vstep;
+      }
+      if (n + 1 < nchunk) {   // the next chunk's rows and block into L2: their turn comes a chunk later
+        const int r = n0 + kChunk + t;
+        if (r < sq.len) {
+          const __nv_bfloat16 *k = delta_row(a.k, sq, r, hk), *q = delta_row(a.q, sq, r, hk);
+          prefetch_l2(k);
+          prefetch_l2(q);
+          if (kD > 64) {
+            prefetch_l2(k + 64);
+            prefetch_l2(q + 64);
+          }
+          prefetch_l2(delta_row(a.v, sq, r, h) + part * kCols);
+        }
+        if (t == 0) bulk_prefetch_l2(blocks + (n + 1) * block_step, kPrepBytes);
       }
       cp_async_commit();
       cp_async_wait<0>();
@@ -688,11 +951,11 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, int* __r
     }
     if (t == 0 && *abort_flag)   // bulk copies still in flight land before the CTA exits
       for (int i = issued > kChainStages ? issued - kChainStages : 0; i < issued; ++i)
-        mbar_drain(&pfull[i % kChainStages], (i / kChainStages) & 1);
+        mbar_drain(&full[i % kChainStages], (i / kChainStages) & 1);
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kIssueWarp) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, kChainTmem);
   }
