@@ -2,23 +2,29 @@
 //
 // With G_i the sum of the log decays of a chunk's tokens up to i, S0 the state before the chunk,
 // D_ij = e^(G_i - G_j) for i >= j, and the chunk's rows as matrices K, Q, V [64, d]:
-//     A = diag(beta) (K K^T . D) below the diagonal,  T = (I + A)^-1,  P = scale (Q K^T . D)
-//     R = diag(beta) (V - diag(e^G) K S0),            U = T R            (the written values)
-//     out = scale diag(e^G) Q S0 + P T R,             S = e^G_C S0 + K^T diag(e^(G_C - G)) U.
-// T and P T need no state: litela_delta_prep makes them for all chunks at once.  What is left of
-// a chunk are three products that follow one another, and litela_delta_chain walks a sequence's
-// chunks with them.
+//     L = K K^T . D below the diagonal,               P = scale (Q K^T . D),
+//     E = V - diag(e^G) K S0                          (what the state before the chunk gets wrong)
+//     W = (I + L diag(beta))^-1 E                     (what the state before each token gets wrong)
+//     U = diag(beta) W                                (the written values)
+//     out = scale diag(e^G) Q S0 + P U,               S = e^G_C S0 + K^T diag(e^(G_C - G)) U.
+// With T = (I + diag(beta) L)^-1 and X = L T (both need no state):
+//     W = E - X R,   P U = P T R,   R = diag(beta) E.
+// litela_delta_prep makes X and P T for all chunks at once.  What is left of a chunk are three
+// products that follow one another, and litela_delta_chain walks a sequence's chunks with them.
+// (X rather than T: the unit diagonal's share of W stays in fp32 registers, and W is there for the
+// gradient of beta, where beta may be 0.)
 //
 // Precision.  States are fp32 and stay in registers.  An fp32 operand of a tensor-core product is
 // entered as two or three bf16 terms (each the rounding of what the ones before it leave: 2^-17 and
-// 2^-25 relative) whose products are summed in fp32.  R and U take three: they are the rows that
-// the state is a sum of, and with two terms the state was 3.4e-6 off (2.5e-6 from either alone).  T and
-// S0 take two: T's large entries are near its unit diagonal and S0 enters a difference with V
-// (3e-7 and 3e-9 of the state).  K, Q and V are bf16 already.  G is summed in fp64: differences of
-// large sums of decays would lose in fp32.
+// 2^-25 relative) whose products are summed in fp32.  U, of which the state is a sum, takes three
+// (with two the state was 2.4e-6 off), R three and X two by all but the smallest products (with two
+// and two the state of slowly decaying heads was 1.2e-6 off, d = 128, 0.8e-6 now), S0 two: it enters
+// as a correction of V.  K, Q
+// and V are bf16 already.  G is summed in fp64: differences of large sums of decays would lose in
+// fp32.
 //
 // A NaN or an infinity must not reach the tokens before its own: 0 * NaN inside a product would
-// carry it there.  So non-finite entries are taken out of A, P and R, the first token that had one
+// carry it there.  So non-finite entries are taken out of L, P and E, the first token that had one
 // is kept, and it and all later tokens of the sequence (and the state) get NaN.
 #pragma once
 
@@ -32,17 +38,17 @@ namespace litela {
 
 constexpr int kChunk = 64;
 
-// One chunk and value head's prepared block: T^T and (P T)^T as images of tcgen05 A operands (MN-major:
+// One chunk and value head's prepared block: X^T and (P T)^T as images of tcgen05 A operands (MN-major:
 // 64 rows x 128 columns bf16 in two blocks of 64 columns, 128-byte swizzle), the hi terms, the lo
-// terms, then per-token factors.  The columns (the product's rows, TMEM lanes) hold 16 rows of T,
-// the same 16 rows of P T, the next 16 rows of T and so on, as do the rows of K and Q in the chain's
+// terms, then per-token factors.  The columns (the product's rows, TMEM lanes) hold 16 rows of X,
+// the same 16 rows of P T, the next 16 rows of X and so on, as do the rows of K and Q in the chain's
 // tile: every warp's quarter of the lanes then has 16 tokens of either kind.
 constexpr uint32_t kImgHalf = 128 * 128;
 __host__ __device__ constexpr int lane_of(int token) { return 32 * (token / 16) + token % 16; }
 constexpr uint32_t kPrepFactors = 2 * kImgHalf;
 constexpr uint32_t kPrepBytes = kPrepFactors + 1024;
 // fp32 at kPrepFactors: e^G [64], e^(G_C - G) [64] (0 behind the end), beta [64] (0 behind the
-// end), then e^G_C and (int32) the first token of the chunk with a non-finite A or P, or 64
+// end), then e^G_C and (int32) the first token of the chunk with a non-finite L or P, or 64
 constexpr int kFacDecay = 0, kFacToEnd = 64, kFacBeta = 128, kFacChunk = 192, kFacBad = 193;
 
 // Chunk slots.  A batch of equal lengths: sequence s has the slots s * ceil(N / 64) + c.  Packed:
@@ -56,18 +62,18 @@ __device__ __forceinline__ long long delta_slot0(const DeltaArgs& a, int s, cons
 }
 
 // The sequence of a slot and its chunk there (whole warp); false for an empty slot.
-__device__ __forceinline__ bool delta_find(const DeltaArgs& a, long long slot, int lane, int& s, DeltaSeq& q, int& n0) {
+__device__ __forceinline__ bool delta_find(const DeltaArgs& a, int slot, int lane, int& s, DeltaSeq& q, int& n0) {
   if (a.cu == nullptr) {
     const int nc = (a.ntok + kChunk - 1) / kChunk;
-    s = (int)(slot / nc);
+    s = slot / nc;
     q = delta_seq(a, s);
-    n0 = (int)(slot - (long long)s * nc) * kChunk;
+    n0 = (slot - s * nc) * kChunk;
     return true;
   }
   int lo = 0, hi = a.nseq;   // the last s with cu[s] / 64 + s <= slot is in [lo, hi)
   while (true) {
     const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-    const bool below = at < hi && (long long)(min(max(a.cu[at], 0), a.ntok) / kChunk) + at <= slot;
+    const bool below = at < hi && min(max(a.cu[at], 0), a.ntok) / kChunk + at <= slot;
     const int n = __popc(__ballot_sync(0xffffffffu, below));
     if (n == 0) return false;
     lo += (n - 1) * step;
@@ -76,7 +82,7 @@ __device__ __forceinline__ bool delta_find(const DeltaArgs& a, long long slot, i
   }
   s = lo;
   q = delta_seq(a, s);
-  n0 = (int)(slot - delta_slot0(a, s, q)) * kChunk;
+  n0 = (slot - (int)delta_slot0(a, s, q)) * kChunk;
   return n0 >= 0 && n0 < q.len;
 }
 
@@ -136,26 +142,28 @@ __device__ __forceinline__ uint32_t sw128(int row, int col) {
 }
 
 // ---------------------------------------------------------------------------------------
-// litela_delta_prep: T and P T of one chunk and value head per CTA, transposed (the image).
+// litela_delta_prep: X and P T of one chunk and value head per CTA, transposed (the image).
 //
-// mma.sync: the operands are one chunk's, 64 rows, and T is made of 16 x 16 blocks where each
+// mma.sync: the operands are one chunk's, 64 rows, and X is made of 16 x 16 blocks where each
 // product waits for the one before; a tcgen05 product would be a sixth full and go through TMEM and
-// shared memory for each block.  Eight warps: warp w has half of the columns of rows 16 (w / 2) on.
+// shared memory for each block.
 //   1. K and Q by cp.async; G, and D's factors.  With m the first row of r's block of 16 and c
 //      before it, D_rc = e^(G_r - G_m) e^(G_m - G_c): 160 exponentials instead of 1536, both
 //      factors at most 1.
-//   2. K K^T and Q K^T below the diagonal; A and P as bf16 pairs, A's diagonal blocks in fp32.
-//   3. T's diagonal blocks by substitution, one lane a column.
-//   4. The blocks below them, block column j by warp j, T_ij = -T_ii sum_m A_im T_mj, computed
-//      transposed (X_i = T_ij^T), so that a product's accumulators are the next one's left operand
-//      in registers, and the image's values.
-//   5. (P T)^T = T^T P^T.
-// One chunk is a chain of about 10k cycles of latencies; three CTAs an SM overlap.
+//   2. K K^T and Q K^T up to the diagonal, to shared memory in fp32; there D makes them L (bf16 pairs;
+//      the diagonal blocks stay in fp32) and P.
+//   3. X's diagonal blocks by substitution, one lane a column: x_i = L_ij - sum_m<i L_im beta_m x_m.
+//   4. The blocks below them, block column j by one warp:
+//      X_ij = (I - X_ii diag(beta)) (L_ij - sum_m L_im diag(beta) X_mj),
+//      computed transposed, so that a product's accumulators are the next one's left operand in
+//      registers, and the image's values.
+//   5. P T = P - (P diag(beta)) X.
+// A chunk is a chain of latencies, a fetch of instructions being one of them: a CTA runs through its
+// code once.  So loops stay rolled, and three CTAs an SM overlap.
 constexpr int kPrepThreads = 256;
-constexpr int kPrepLd = 72;   // row of P, padded
-constexpr int kDiagLd = 24;   // row of T's diagonal blocks, padded
+constexpr int kPrepLd = 68;   // row of L and P in fp32, padded
 constexpr uint32_t kImgBlock = 64 * 128;   // half of the columns of an image, one bf16 term
-// byte offset in the image of (row, token of T); of P T: 32 bytes on, before the swizzle
+// byte offset in the image of (row, token of X); of P T: 32 bytes on, before the swizzle
 __device__ __forceinline__ uint32_t img_off(int row, int token, int is_p) {
   const int m = lane_of(token) + 16 * is_p;
   return (m >> 6) * kImgBlock + sw128(row, m & 63);
@@ -166,14 +174,14 @@ struct PrepCfg {
   static constexpr int kLd = kD + 8;   // row of K and Q, padded
   static constexpr uint32_t kRows = 2 * kChunk * kLd * 2;
   static constexpr uint32_t kUnion = kRows > 2 * kImgHalf ? kRows : 2 * kImgHalf;   // K, Q; then the image
-  static constexpr uint32_t kOffP = kUnion;                                  // P, hi and lo
-  static constexpr uint32_t kOffDiag = kOffP + 2 * kChunk * kPrepLd * 2;     // T's diagonal blocks, hi and lo
-  static constexpr uint32_t kOffA = kOffDiag + 2 * kChunk * kDiagLd * 2;     // A's diagonal blocks, fp32
-  static constexpr uint32_t kOffG = kOffA + kChunk * 17 * 4;
+  static constexpr uint32_t kOffL = kUnion;                                  // L, fp32
+  static constexpr uint32_t kOffP = kOffL + kChunk * kPrepLd * 4;
+  static constexpr uint32_t kOffG = kOffP + kChunk * kPrepLd * 4;
   static constexpr uint32_t kOffBeta = kOffG + kChunk * 8;
   static constexpr uint32_t kOffRow = kOffBeta + kChunk * 4;                 // e^(G_r - G_m)
   static constexpr uint32_t kOffCol = kOffRow + kChunk * 4;                  // e^(G_m - G_c), by block of r
-  static constexpr uint32_t kOffBad = kOffCol + 4 * 48 * 4;
+  static constexpr uint32_t kOffRel = kOffCol + 4 * 48 * 4;                  // G_r - G_m, two fp32 terms
+  static constexpr uint32_t kOffBad = kOffRel + kChunk * 8;
   static constexpr uint32_t kSmemBytes = kOffBad + 16 + 128;
   static_assert(3 * (kSmemBytes + 1024) <= 228 * 1024, "three CTAs an SM");
 };
@@ -183,6 +191,22 @@ __device__ __forceinline__ void ldmatrix_x4(uint32_t* r, uint32_t addr) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
 }
+__device__ __forceinline__ void ldmatrix_x4_t(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void stmatrix_x4_t(uint32_t addr, const uint32_t* r) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+// d += A B, both pairs of fragments (B: hi in b[0], b[1], lo in b[2], b[3])
+__device__ __forceinline__ void mma_pair(float* d, const uint32_t* ah, const uint32_t* al, const uint32_t* b) {
+  sm100::mma_16816(d, al, b);
+  sm100::mma_16816(d, ah, b + 2);
+  sm100::mma_16816(d, ah, b);
+}
 
 template <int kD>
 __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const DeltaArgs a, uint8_t* __restrict__ prep) {
@@ -190,58 +214,59 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
   using Cfg = PrepCfg<kD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-  // the image, hi and lo; until (P T)^T is made A's pair stands in its places, (row, column) of A at
+  // the image, hi and lo; until (P T)^T is made L's pair stands in its places, (row, column) of L at
   // img_off(row, column, 1)
   uint8_t *Ih = smem, *Il = smem + kImgHalf;
-  __nv_bfloat16* Pm = reinterpret_cast<__nv_bfloat16*>(smem + Cfg::kOffP);
-  __nv_bfloat16* Td = reinterpret_cast<__nv_bfloat16*>(smem + Cfg::kOffDiag);
-  float* Ad = reinterpret_cast<float*>(smem + Cfg::kOffA);
+  float* Lf = reinterpret_cast<float*>(smem + Cfg::kOffL);
+  float* Pf = reinterpret_cast<float*>(smem + Cfg::kOffP);
   double* G = reinterpret_cast<double*>(smem + Cfg::kOffG);
   float* beta = reinterpret_cast<float*>(smem + Cfg::kOffBeta);
   float* rowf = reinterpret_cast<float*>(smem + Cfg::kOffRow);
   float* colf = reinterpret_cast<float*>(smem + Cfg::kOffCol);
+  float2* rel = reinterpret_cast<float2*>(smem + Cfg::kOffRel);
   int* bad = reinterpret_cast<int*>(smem + Cfg::kOffBad);
-  constexpr uint32_t kPLo = kChunk * kPrepLd, kTdLo = kChunk * kDiagLd;   // elements to the lo term
 
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, gr = lane >> 2, t2 = (lane & 3) * 2;
   pdl_launch_dependents();   // the chain waits for this grid before it reads what it wrote
-  const int h = blockIdx.x % a.Hv, hk = h / (a.Hv / a.Hk);
-  const long long slot = blockIdx.x / a.Hv;
+  const int slot = blockIdx.x / a.Hv, h = blockIdx.x - slot * a.Hv, hk = h / (a.Hv / a.Hk);
   int s, n0;
   DeltaSeq sq;
   if (!delta_find(a, slot, lane, s, sq, n0)) return;
   const int len = min(kChunk, sq.len - n0);
 
-  {   // a thread copies one 16-byte column of every (2048 / kD)-th row
+  double g0[2] = {0.0, 0.0};   // two tokens a lane
+  if (w == 0) {
+    const float* g = a.g + sq.entry * a.g_sb + (long long)(sq.first + n0) * a.g_st + h;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (2 * lane + j < len) g0[j] = (double)clamp_decay(g[(2 * lane + j) * a.g_st]);
+  }
+  {   // a thread copies one 16-byte column of every kStep-th row
     constexpr int kC = kD / 8, kStep = kPrepThreads / kC;
     const int c = tid % kC, r0 = tid / kC;
-    const __nv_bfloat16* kp = delta_row(a.k, sq, n0, hk) + c * 8;
-    const __nv_bfloat16* qp = delta_row(a.q, sq, n0, hk) + c * 8;
-    const uint32_t dst = smem_u32(smem) + c * 16;
+    const __nv_bfloat16* kp = delta_row(a.k, sq, n0 + r0, hk) + c * 8;
+    const __nv_bfloat16* qp = delta_row(a.q, sq, n0 + r0, hk) + c * 8;
+    const long long ks = kStep * a.k.st, qs = kStep * a.q.st;
+    const uint32_t dst = smem_u32(smem) + r0 * (Cfg::kLd * 2) + c * 16;
 #pragma unroll
-    for (int r = r0; r < kChunk; r += kStep) {
-      const bool real = r < len;
-      cp_async_16(dst + r * (Cfg::kLd * 2), kp + (real ? r * a.k.st : 0), real);
-      cp_async_16(dst + (kChunk + r) * (Cfg::kLd * 2), qp + (real ? r * a.q.st : 0), real);
+    for (int i = 0; i < kChunk / kStep; ++i) {
+      const bool real = r0 + i * kStep < len;
+      cp_async_16(dst + i * kStep * (Cfg::kLd * 2), real ? kp : a.k.p, real);
+      cp_async_16(dst + (kChunk + i * kStep) * (Cfg::kLd * 2), real ? qp : a.q.p, real);
+      kp += ks;
+      qp += qs;
     }
     cp_async_commit();
   }
-  if (w == 0) {   // G, two tokens a lane
-    double x[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int n = 2 * lane + j;
-      x[j] = n < len ? (double)clamp_decay(a.g[sq.entry * a.g_sb + (long long)(sq.first + n0 + n) * a.g_st + h]) : 0.0;
-    }
-    x[1] += x[0];
-    double run = x[1];
+  if (w == 0) {
+    g0[1] += g0[0];
+    double run = g0[1];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const double y = __shfl_up_sync(0xffffffffu, run, o);
       if (lane >= o) run += y;
     }
-    const double before = run - x[1];
-    G[2 * lane] = before + x[0];
+    G[2 * lane] = run - g0[1] + g0[0];
     G[2 * lane + 1] = run;
   } else if (w < 3) {
     const int n = tid - 32;
@@ -250,9 +275,11 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
     *bad = kChunk;
   }
   __syncthreads();
-  uint8_t* dst = prep + (slot * a.Hv + h) * (long long)kPrepBytes;
+  uint8_t* dst = prep + ((long long)slot * a.Hv + h) * kPrepBytes;
   if (tid < kChunk) {
-    rowf[tid] = expf((float)(G[tid] - G[tid & ~15]));
+    const double d = G[tid] - G[tid & ~15];
+    rel[tid] = make_float2((float)d, (float)(d - (double)(float)d));
+    rowf[tid] = expf((float)d);
   } else if (tid < kChunk + 96) {   // blocks 1, 2, 3 of r have 16, 32, 48 columns before them
     const int i = tid - kChunk, b = i < 16 ? 1 : i < 48 ? 2 : 3, c = i - (b == 1 ? 0 : b == 2 ? 16 : 48);
     colf[b * 48 + c] = expf((float)(G[16 * b] - G[c]));
@@ -268,217 +295,258 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
   cp_async_wait<0>();
   __syncthreads();
 
-  // K K^T and Q K^T: rows 16 rb .., the warp's rb + 1 tiles of 8 columns of the 2 rb + 2
-  const int rb = w >> 1, tile0 = (w & 1) * (rb + 1);
-  float accA[4][4], accP[4][4];
+  {   // K K^T (even warps) and Q K^T (odd ones): rows 16 rb .., the 2 rb + 2 tiles of 8 columns
+    const int rb = w >> 1, is_p = w & 1;
+    float acc[8][4];
 #pragma unroll
-  for (int n = 0; n < 4; ++n)
+    for (int n = 0; n < 8; ++n)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) accA[n][i] = accP[n][i] = 0.f;
-  {
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
     const uint32_t base = smem_u32(smem);
-    const uint32_t ka = base + (16 * rb + (lane & 15)) * (Cfg::kLd * 2) + (lane >> 4) * 16;
-    const uint32_t qa = ka + kChunk * (Cfg::kLd * 2);
-    const uint32_t ba = base + (8 * tile0 + (lane & 7)) * (Cfg::kLd * 2) + (lane >> 3) * 16;
-#pragma unroll
+    const uint32_t aa = base + (is_p * kChunk + 16 * rb + (lane & 15)) * (Cfg::kLd * 2) + (lane >> 4) * 16;
+    const uint32_t ba = base + (lane & 7) * (Cfg::kLd * 2) + (lane >> 3) * 16;
+#pragma unroll 1
     for (int ks = 0; ks < kD / 32; ++ks) {   // 32 channels
-      uint32_t k0[4], k1[4], q0[4], q1[4];
-      ldmatrix_x4(k0, ka + ks * 64);
-      ldmatrix_x4(k1, ka + ks * 64 + 32);
-      ldmatrix_x4(q0, qa + ks * 64);
-      ldmatrix_x4(q1, qa + ks * 64 + 32);
+      uint32_t a0[4], a1[4];
+      ldmatrix_x4(a0, aa + ks * 64);
+      ldmatrix_x4(a1, aa + ks * 64 + 32);
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
-        if (n <= rb) {
+      for (int n = 0; n < 8; ++n)
+        if (n < 2 * rb + 2) {
           uint32_t b[4];
           ldmatrix_x4(b, ba + n * 8 * (Cfg::kLd * 2) + ks * 64);
-          mma_16816(accA[n], k0, b);
-          mma_16816(accP[n], q0, b);
-          mma_16816(accA[n], k1, b + 2);
-          mma_16816(accP[n], q1, b + 2);
+          mma_16816(acc[n], a0, b);
+          mma_16816(acc[n], a1, b + 2);
         }
     }
+    float* dst = (is_p ? Pf : Lf) + (16 * rb + gr) * kPrepLd + t2;
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+      if (n < 2 * rb + 2) {
+        *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(acc[n][0], acc[n][1]);
+        *reinterpret_cast<float2*>(dst + 8 * kPrepLd + 8 * n) = make_float2(acc[n][2], acc[n][3]);
+      }
   }
   __syncthreads();   // K and Q are done with: the image takes their place
-  const int r0 = 16 * rb + gr;
-  const float rf[2] = {rowf[r0], rowf[r0 + 8]}, bt[2] = {beta[r0], beta[r0 + 8]};
-#pragma unroll
-  for (int n = 0; n < 4; ++n)
-    if (n <= rb) {
-      const int c0 = 8 * (tile0 + n) + t2;
-      const bool diag = c0 >= 16 * rb;   // the same for the whole tile
-      float D[4];
-      if (diag) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = r0 + (i >> 1) * 8, c = c0 + (i & 1);
-          D[i] = c <= r ? expf((float)(G[r] - G[c])) : 0.f;
-        }
-      } else {
-        const float2 cf = *reinterpret_cast<const float2*>(colf + rb * 48 + c0);
-        D[0] = rf[0] * cf.x, D[1] = rf[0] * cf.y, D[2] = rf[1] * cf.x, D[3] = rf[1] * cf.y;
+  // D makes them L and P: a thread has 4 columns of every block of 16 up to the diagonal one of a row
+  int first = kChunk;
+  {
+    const int r = tid >> 2, c0 = (tid & 3) * 4, rb = r >> 4;
+    const float rf = rowf[r];
+    const float2 rr = rel[r];
+    const float4* cf = reinterpret_cast<const float4*>(colf + rb * 48 + c0);
+    float4 *ls = reinterpret_cast<float4*>(Lf + r * kPrepLd + c0), *ps = reinterpret_cast<float4*>(Pf + r * kPrepLd + c0);
+    // L's pair in the image: block cb of 16 columns stands 64 bytes (before the swizzle) or a block on
+    uint8_t* image = Ih + r * 128 + (c0 & 4) * 2;
+    const uint32_t chunk = (uint32_t)(((2 + (c0 >> 3)) ^ r) & 7) << 4;
+    auto scaled = [&](float4* src, const float* f) {
+      const float4 x = *src;
+      float4 y = make_float4(x.x * f[0], x.y * f[1], x.z * f[2], x.w * f[3]);
+      if (0.f * y.x + 0.f * y.y + 0.f * y.z + 0.f * y.w != 0.f) {   // not finite
+        first = min(first, r);
+        y.x = isfinite(y.x) ? y.x : 0.f, y.y = isfinite(y.y) ? y.y : 0.f;
+        y.z = isfinite(y.z) ? y.z : 0.f, y.w = isfinite(y.w) ? y.w : 0.f;
       }
+      return y;
+    };
+#pragma unroll 1
+    for (int cb = 0; cb < rb; ++cb) {
+      const float4 c4 = cf[4 * cb];
+      float f[4] = {rf * c4.x, rf * c4.y, rf * c4.z, rf * c4.w};
+      const float4 y = scaled(ls + 4 * cb, f);
+      uint32_t hi[2], lo[2];
+      split_bf16(y.x, y.y, hi[0], lo[0]);
+      split_bf16(y.z, y.w, hi[1], lo[1]);
+      uint8_t* dst = image + (cb >> 1) * kImgBlock + (chunk ^ ((cb & 1) << 6));
+      *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(dst + kImgHalf) = make_uint2(lo[0], lo[1]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = r0 + (i >> 1) * 8, c = c0 + (i & 1);
-        float x = c < r ? bt[i >> 1] * accA[n][i] * D[i] : 0.f;
-        float y = c <= r ? accP[n][i] * (a.scale * D[i]) : 0.f;
-        if (!isfinite(x) || !isfinite(y)) {
-          x = y = 0.f;
-          atomicMin(bad, r);
-        }
-        accA[n][i] = x;
-        accP[n][i] = y;
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = r0 + 8 * i;
-        uint32_t hi, lo;
-        split_bf16(accP[n][2 * i], accP[n][2 * i + 1], hi, lo);
-        *reinterpret_cast<uint32_t*>(Pm + r * kPrepLd + c0) = hi;
-        *reinterpret_cast<uint32_t*>(Pm + kPLo + r * kPrepLd + c0) = lo;
-        if (diag) {
-          Ad[r * 17 + c0 - 16 * rb] = accA[n][2 * i];
-          Ad[r * 17 + c0 - 16 * rb + 1] = accA[n][2 * i + 1];
-        } else {
-          split_bf16(accA[n][2 * i], accA[n][2 * i + 1], hi, lo);
-          *reinterpret_cast<uint32_t*>(Ih + img_off(r, c0, 1)) = hi;
-          *reinterpret_cast<uint32_t*>(Il + img_off(r, c0, 1)) = lo;
-        }
-      }
+      for (int e = 0; e < 4; ++e) f[e] *= a.scale;
+      ps[4 * cb] = scaled(ps + 4 * cb, f);
     }
-  for (int i = tid; i < kChunk * 8; i += kPrepThreads) {   // T^T is zero left of its diagonal blocks
-    const int r = i >> 3, c = (i & 7) * 8;
-    if ((c >> 4) < (r >> 4)) {
-      *reinterpret_cast<uint4*>(Ih + img_off(r, c, 0)) = make_uint4(0u, 0u, 0u, 0u);
-      *reinterpret_cast<uint4*>(Il + img_off(r, c, 0)) = make_uint4(0u, 0u, 0u, 0u);
+    float f[4];   // the diagonal block: L below the diagonal, P with it
+    const int below = r - 16 * rb - c0;   // columns of the four that are left of the diagonal
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 rc = rel[16 * rb + c0 + e];
+      const float x = expf((rr.x - rc.x) + (rr.y - rc.y));   // (infinite above the diagonal)
+      f[e] = below >= e ? x : 0.f;
     }
+    float4 y = scaled(ls + 4 * rb, f);
+    ls[4 * rb] = make_float4(below == 0 ? 0.f : y.x, below == 1 ? 0.f : y.y, below == 2 ? 0.f : y.z, below == 3 ? 0.f : y.w);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] *= a.scale;
+    ps[4 * rb] = scaled(ps + 4 * rb, f);
   }
+  if (first < kChunk) atomicMin(bad, first);
+  // the blocks of X^T (P T) left of its diagonal blocks are zero: six of 16 rows x 32 bytes
+  auto clear = [&](int p) {
+    if (tid < 192) {
+      const int blk = tid >> 5, rb = blk < 1 ? 1 : blk < 3 ? 2 : 3, cb = blk - (rb == 1 ? 0 : rb == 2 ? 1 : 3);
+      const uint32_t o = img_off(16 * rb + ((lane >> 1) & 15), 16 * cb + (lane & 1) * 8, p);
+      *reinterpret_cast<uint4*>(Ih + o) = make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4*>(Il + o) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  clear(0);
   __syncthreads();
 
-  // the diagonal block of warp w: lane j solves for column j, x_i = delta_ij - sum_m<i A_im x_m
+  // X's diagonal block w: lane j solves for column j
   if (w < 4 && lane < 16) {
-    float x[16];
-    const float* blk = Ad + 16 * w * 17;
+    float x[16], bx[16];
+    const float* blk = Lf + 16 * w * kPrepLd + 16 * w;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      float v = i == lane ? 1.f : 0.f, u = 0.f;
+      float v[4] = {blk[i * kPrepLd + lane], 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int m = 0; m < i; ++m) {
-        if (m & 1)
-          u -= blk[i * 17 + m] * x[m];
-        else
-          v -= blk[i * 17 + m] * x[m];
+      for (int m = 0; m < i; m += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(blk + i * kPrepLd + m);
+        v[0] -= l.x * bx[m];
+        if (m + 1 < i) v[1] -= l.y * bx[m + 1];
+        if (m + 2 < i) v[2] -= l.z * bx[m + 2];
+        if (m + 3 < i) v[3] -= l.w * bx[m + 3];
       }
-      x[i] = v + u;
+      x[i] = i > lane ? (v[0] + v[1]) + (v[2] + v[3]) : 0.f;
+      bx[i] = beta[16 * w + i] * x[i];
     }
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      uint32_t hi, lo;
-      split_bf16(x[i], x[i + 1], hi, lo);
+    for (int i = 0; i < 16; i += 8) {
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) split_bf16(x[i + 2 * q], x[i + 2 * q + 1], hi[q], lo[q]);
       const uint32_t o = img_off(16 * w + lane, 16 * w + i, 0);
-      *reinterpret_cast<uint32_t*>(Ih + o) = hi;
-      *reinterpret_cast<uint32_t*>(Il + o) = lo;
-      uint16_t* td = reinterpret_cast<uint16_t*>(Td) + (16 * w + i) * kDiagLd + lane;
-      td[0] = (uint16_t)hi, td[kDiagLd] = (uint16_t)(hi >> 16);
-      td[kTdLo] = (uint16_t)lo, td[kTdLo + kDiagLd] = (uint16_t)(lo >> 16);
+      *reinterpret_cast<uint4*>(Ih + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(Il + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
   }
   __syncthreads();
 
   // the blocks below them, block column w
   if (w < 3) {
-    uint32_t xh[3][4], xl[3][4];   // X of the block rows w, w + 1, w + 2
+    uint32_t yh[3][4], yl[3][4];   // -(diag(beta) X)^T of the block rows w, w + 1, w + 2 (zero: not made yet)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t o = img_off(16 * w + gr + (q & 1) * 8, 16 * w + t2 + (q >> 1) * 8, 0);
-      xh[0][q] = *reinterpret_cast<const uint32_t*>(Ih + o);
-      xl[0][q] = *reinterpret_cast<const uint32_t*>(Il + o);
-    }
+    for (int m = 0; m < 3; ++m)
 #pragma unroll
-    for (int e = 0; e < 3; ++e) {
-      const int i = w + 1 + e;   // T's block row that this step makes
-      if (i < 4) {
-        float r[2][4] = {}, rs[2][4] = {};
+      for (int q = 0; q < 4; ++q) yh[m][q] = yl[m][q] = 0u;
+    {
+      float y[2][4];
 #pragma unroll
-        for (int m = 0; m <= e; ++m)   // sum over T's block rows w + m
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const uint32_t o = img_off(16 * i + 8 * n + gr, 16 * (w + m) + t2, 1);
-            const uint32_t o8 = img_off(16 * i + 8 * n + gr, 16 * (w + m) + t2 + 8, 1);
-            const uint32_t bh[2] = {*reinterpret_cast<const uint32_t*>(Ih + o), *reinterpret_cast<const uint32_t*>(Ih + o8)};
-            const uint32_t bl[2] = {*reinterpret_cast<const uint32_t*>(Il + o), *reinterpret_cast<const uint32_t*>(Il + o8)};
-            mma_16816(r[n], xh[m], bh);
-            mma_16816(rs[n], xh[m], bl);
-            mma_16816(rs[n], xl[m], bh);
-          }
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) r[n][q] += rs[n][q];
-        uint32_t rh[4], rl[4];
-        split_frag(r, rh, rl);
-        float x[2][4] = {}, xs[2][4] = {};
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const uint32_t* td = reinterpret_cast<const uint32_t*>(Td + (16 * i + 8 * n + gr) * kDiagLd + t2);
-          const uint32_t bh[2] = {td[0], td[4]}, bl[2] = {td[kTdLo / 2], td[kTdLo / 2 + 4]};
-          mma_16816(x[n], rh, bh);
-          mma_16816(xs[n], rh, bl);
-          mma_16816(xs[n], rl, bh);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) x[n][q] = -(x[n][q] + xs[n][q]);
+        for (int q = 0; q < 2; ++q) {
+          const int i = 16 * w + 8 * n + t2;
+          const uint32_t o = img_off(16 * w + gr + q * 8, i, 0);
+          const uint32_t hi = *reinterpret_cast<const uint32_t*>(Ih + o), lo = *reinterpret_cast<const uint32_t*>(Il + o);
+          const float2 v = f2_out(f2_add(f2_bf16(hi), f2_bf16(lo)));
+          y[n][2 * q] = -beta[i] * v.x;
+          y[n][2 * q + 1] = -beta[i + 1] * v.y;
         }
-        uint32_t fh[4], fl[4];
-        split_frag(x, fh, fl);
+      split_frag(y, yh[0], yl[0]);
+    }
+    // matrices by lane / 8: hi of 0..7 and 8..15 of the K dimension, then lo
+    const uint32_t term = smem_u32(smem) + (lane >> 4) * kImgHalf;
+    const int l8 = lane & 7, k8 = ((lane >> 3) & 1) * 8;
+#pragma unroll 1
+    for (int i = w + 1; i < 4; ++i) {   // X's block row i
+      float x[2][4];
+      {   // L_ij transposed: matrices by lane / 8: rows 0..7 of L, columns 0..7 and 8..15; rows 8..15
+        uint32_t hi[4], lo[4];
+        const uint32_t o = smem_u32(smem) + img_off(16 * i + l8 + (lane >> 4) * 8, 16 * w + k8, 1);
+        ldmatrix_x4_t(hi, o);
+        ldmatrix_x4_t(lo, o + kImgHalf);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const uint32_t o = img_off(16 * w + gr + (q & 1) * 8, 16 * i + t2 + (q >> 1) * 8, 0);
-          *reinterpret_cast<uint32_t*>(Ih + o) = fh[q];
-          *reinterpret_cast<uint32_t*>(Il + o) = fl[q];
-          if (e < 2) {
-            xh[e + 1][q] = fh[q];
-            xl[e + 1][q] = fl[q];
-          }
+          const float2 v = f2_out(f2_add(f2_bf16(hi[q]), f2_bf16(lo[q])));
+          x[q >> 1][2 * (q & 1)] = v.x;
+          x[q >> 1][2 * (q & 1) + 1] = v.y;
         }
       }
+#pragma unroll
+      for (int m = 0; m < 3; ++m)   // sum over X's block rows w + m before i
+        if (w + m < i)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            uint32_t b[4];
+            ldmatrix_x4(b, term + img_off(16 * i + 8 * n + l8, 16 * (w + m) + k8, 1));
+            mma_pair(x[n], yh[m], yl[m], b);
+          }
+      float br[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) br[n][q] = -beta[16 * i + 8 * n + t2 + (q & 1)] * x[n][q];
+      uint32_t rh[4], rl[4];
+      split_frag(br, rh, rl);
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {   // X_ii^T stands as rows of the K dimension
+        uint32_t b[4];
+        ldmatrix_x4_t(b, term + img_off(16 * i + l8 + k8, 16 * i + 8 * n, 0));
+        mma_pair(x[n], rh, rl, b);
+      }
+      split_frag(x, rh, rl);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t o = img_off(16 * w + gr + (q & 1) * 8, 16 * i + t2 + (q >> 1) * 8, 0);
+        *reinterpret_cast<uint32_t*>(Ih + o) = rh[q];
+        *reinterpret_cast<uint32_t*>(Il + o) = rl[q];
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[n][q] *= -beta[16 * i + 8 * n + t2 + (q & 1)];
+      split_frag(x, rh, rl);
+#pragma unroll
+      for (int m = 1; m < 3; ++m)
+        if (i == w + m)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) yh[m][q] = rh[q], yl[m][q] = rl[q];
     }
   }
   __syncthreads();
 
-  // (P T)^T = T^T P^T: columns (rows of P) 16 rb + 8 (w & 1) .., rows up to block rb
+  // P T = P - (P diag(beta)) X: rows 16 rb .., the warp's rb + 1 tiles of 8 columns of the 2 rb + 2
+  clear(1);   // (all of L has been read)
   {
-    const int i0 = 16 * rb + 8 * (w & 1);
-    const uint32_t* pr = reinterpret_cast<const uint32_t*>(Pm + (i0 + gr) * kPrepLd + t2);
+    const int rb = w >> 1, tile0 = (w & 1) * (rb + 1), r0 = 16 * rb + gr;
+    const uint32_t term = smem_u32(smem) + (lane >> 4) * kImgHalf;
+    const int l8 = lane & 7, k8 = ((lane >> 3) & 1) * 8;
+    const uint32_t xrow = term + img_off(8 * tile0 + l8, k8, 0);   // X^T's row; block k: 64 bytes (xor), a block on
+    float acc[4][4];
 #pragma unroll
-    for (int nb = 0; nb < 4; ++nb) {
-      float x[4] = {}, xs[4] = {};
-      if (nb <= rb)
-#pragma unroll
-        for (int kb = 0; kb < 4; ++kb)
-          if (kb >= nb && kb <= rb) {
-            uint32_t th[4], tl[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t o = img_off(16 * nb + gr + (q & 1) * 8, 16 * kb + t2 + (q >> 1) * 8, 0);
-              th[q] = *reinterpret_cast<const uint32_t*>(Ih + o);
-              tl[q] = *reinterpret_cast<const uint32_t*>(Il + o);
-            }
-            const uint32_t bh[2] = {pr[8 * kb], pr[8 * kb + 4]};
-            const uint32_t bl[2] = {pr[kPLo / 2 + 8 * kb], pr[kPLo / 2 + 8 * kb + 4]};
-            mma_16816(x, th, bh);
-            mma_16816(xs, th, bl);
-            mma_16816(xs, tl, bh);
-          }
+    for (int n = 0; n < 4; ++n)
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        uint32_t hi, lo;
-        split_bf16(x[2 * q] + xs[2 * q], x[2 * q + 1] + xs[2 * q + 1], hi, lo);
-        const uint32_t o = img_off(16 * nb + gr + 8 * q, i0 + t2, 1);
-        *reinterpret_cast<uint32_t*>(Ih + o) = hi;   // (all of A has been read)
-        *reinterpret_cast<uint32_t*>(Il + o) = lo;
+        float2 v = make_float2(0.f, 0.f);
+        if (n <= rb) v = *reinterpret_cast<const float2*>(Pf + (r0 + 8 * q) * kPrepLd + 8 * (tile0 + n) + t2);
+        acc[n][2 * q] = v.x;
+        acc[n][2 * q + 1] = v.y;
       }
+#pragma unroll 1
+    for (int k = 0; k <= rb; ++k) {
+      uint32_t ph[4], pl[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c = 16 * k + t2 + (q >> 1) * 8;
+        const float2 v = *reinterpret_cast<const float2*>(Pf + (r0 + (q & 1) * 8) * kPrepLd + c);
+        const float2 bc = *reinterpret_cast<const float2*>(beta + c);
+        split_bf16(-bc.x * v.x, -bc.y * v.y, ph[q], pl[q]);
+      }
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        if (n <= rb && (tile0 + n) / 2 <= k) {
+          uint32_t b[4];
+          ldmatrix_x4(b, (xrow ^ ((k & 1) << 6)) + (k >> 1) * kImgBlock + n * 1024);
+          mma_pair(acc[n], ph, pl, b);
+        }
     }
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+      if (n <= rb) {   // matrices by lane / 8: hi of rows 0..7 and 8..15, lo
+        uint32_t v[4];
+        split_bf16(acc[n][0], acc[n][1], v[0], v[2]);
+        split_bf16(acc[n][2], acc[n][3], v[1], v[3]);
+        stmatrix_x4_t((((xrow ^ 32) ^ ((rb & 1) << 6)) + (rb >> 1) * kImgBlock) + n * 1024, v);
+      }
   }
   if (tid == 0) reinterpret_cast<int*>(dst + kPrepFactors)[kFacBad] = *bad;
   fence_proxy_async_smem();
@@ -496,9 +564,9 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
 //
 // Three tcgen05 products per chunk, each with M = 128 rows, fp32 accumulators in TMEM:
 //     X1 = [K; Q] S0           (rows: 16 of K, 16 of Q, 16 of K ..; K dimension d)
-//     X2 = [T; P T] R          (rows alike; K dimension 64)
+//     X2 = [X; P T] R          (rows alike; K dimension 64)
 //     X3 = K^T (e^(G_C - G) U) (rows: d; K dimension 64)
-// Between them eight warps take the accumulators to registers, form R, then U, then the new state,
+// Between them eight warps take the accumulators to registers, form E and R, then W and U, then the new state,
 // and write them as bf16 pairs into shared memory as the next product's B operand.  The chain of
 // these six steps is what a chunk costs; the loads of the next chunks, the output rows' arithmetic
 // and their stores run beside it.  All B operands are tiles of 128-byte rows (row: K index, 64 bf16 columns,
@@ -631,11 +699,20 @@ __device__ __forceinline__ void chain_put_frag(uint8_t* tile, uint32_t tile_byte
   }
 }
 
-template <int kD, int kCols>
+// What a training step's forward leaves for its backward, per chunk slot and value head: S0 as the B
+// operand tiles of the chain (kCols = 32: d rows x 128 bytes for each 32 columns, two terms), and
+// W in fp32 [64, d].
+struct DeltaSaved {
+  uint8_t* states;
+  float* w;
+};
+
+template <int kD, int kCols, bool kSave>
 __global__ void __launch_bounds__(kChainThreads, 1)
-litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, int* __restrict__ err) {
+litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, const DeltaSaved saved, int* __restrict__ err) {
   using namespace sm100;
   using Cfg = ChainCfg<kD, kCols>;
+  static_assert(kCols == 32 || !kSave, "saved states are tiles of 32 columns");
   constexpr int kN = kCols * 4 / kAccWarps;   // columns of an accumulator warp
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -655,7 +732,8 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, int* __r
   const int hk = h / (a.Hv / a.Hk);
   const DeltaSeq sq = delta_seq(a, s);
   const int nchunk = (sq.len + kChunk - 1) / kChunk;
-  const uint8_t* blocks = prep + (delta_slot0(a, s, sq) * a.Hv + h) * (long long)kPrepBytes;
+  const long long slot0 = delta_slot0(a, s, sq);
+  const uint8_t* blocks = prep + (slot0 * a.Hv + h) * (long long)kPrepBytes;
   const long long block_step = (long long)a.Hv * kPrepBytes;
 
   if (threadIdx.x == 0) {
@@ -733,15 +811,16 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, int* __r
     }
     for (int n = 0; n < nchunk; ++n) {
       fetch(n);   // while the first product runs
-      F2 x[kN / 2], y[kN / 2];
+      F2 e[kN / 2], x[kN / 2], y[kN / 2];
       wait(&done[0], n, 2);
-      // R = beta (v - e^G K S0)
-      chain_frag<kCols, 2, kG>(ta + Cfg::kX1, c0, x);
+      // E = v - e^G K S0, R = beta E
+      chain_frag<kCols, 2, kG>(ta + Cfg::kX1, c0, e);
       F2 zero = f2(0.f, 0.f);   // stays 0 while all are finite
 #pragma unroll
       for (int i = 0; i < 2 * kG; ++i) {
         const float d = decay[i & 1], b = beta[i & 1];
-        x[i] = f2_mul(f2(b, b), f2_fma(f2(-d, -d), x[i], f2_bf16(v[i])));
+        e[i] = f2_fma(f2(-d, -d), e[i], f2_bf16(v[i]));
+        x[i] = f2_mul(f2(b, b), e[i]);
         zero = f2_fma(f2(0.f, 0.f), x[i], zero);
       }
       const float2 z = f2_out(zero);
@@ -764,15 +843,23 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, int* __r
       wait(&done[1], n, 3);
       const int bad_from = min(prep_bad, *static_cast<volatile int*>(first_bad) - n * kChunk);
       const float nan = __int_as_float(0x7fffffff);
-      // e^(G_C - G) U
+      // W = E - X R, e^(G_C - G) U = e^(G_C - G) beta W
       chain_frag<kCols, 3, kG>(ta + Cfg::kX2, c0, x);
 #pragma unroll
       for (int i = 0; i < 2 * kG; ++i) {
-        const float e = tok + (i & 1) * 8 >= bad_from ? nan : to_end[i & 1];
-        x[i] = f2_mul(f2(e, e), x[i]);
+        const float f = tok + (i & 1) * 8 >= bad_from ? nan : to_end[i & 1] * beta[i & 1];
+        e[i] = f2_fma(f2(-1.f, -1.f), x[i], e[i]);
+        x[i] = f2_mul(f2(f, f), e[i]);
       }
       chain_put_frag<kCols, 3, kG>(rtile, Cfg::kRTile, tok, fc, x);
       hand(kBarU, kBarThreads);
+      if constexpr (kSave) {
+        float* w = saved.w + ((slot0 + n) * a.Hv + h) * (long long)(kChunk * kD) + part * kCols + fc;
+#pragma unroll
+        for (int i = 0; i < 2 * kG; ++i)
+          *reinterpret_cast<float2*>(w + (tok + (i & 1) * 8) * kD + (i >> 1) * 8) =
+              tok + (i & 1) * 8 >= bad_from ? make_float2(nan, nan) : f2_out(e[i]);
+      }
       // the output, while the third product runs
       chain_frag<kCols, 3, kG>(tq + Cfg::kX2, c0, x);
 #pragma unroll
@@ -800,11 +887,10 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, int* __r
             make_float4(f2_out(S[i / 2]).x, f2_out(S[i / 2]).y, f2_out(S[i / 2 + 1]).x, f2_out(S[i / 2 + 1]).y);
   } else if (warp == kIssueWarp) {
     {
-      // kCols = 32: the terms of R side by side, 96 columns over two tiles
-      constexpr int kRN = kCols == 64 ? 64 : 96;
+      // kCols = 32: three terms of R and of U over two tiles
       constexpr uint32_t idesc_s = idesc_bf16_f32(128, 64, false, true);
-      constexpr uint32_t idesc_r = idesc_bf16_f32(128, kRN, true, true);
-      constexpr uint32_t idesc_1 = idesc_bf16_f32(128, 32, true, true);
+      constexpr uint32_t idesc_r = idesc_bf16_f32(128, kCols == 64 ? 64 : 96, true, true);
+      constexpr uint32_t idesc_2 = idesc_bf16_f32(128, 64, true, true);
       // descriptors of each operand's first 16 of the K dimension; an offset of n bytes adds n / 16
       const uint64_t sdesc = smem_desc(smem_u32(stile), 1024, 1024, kSwizzle128B);
       const uint64_t rdesc = smem_desc(smem_u32(rtile), Cfg::kRTile, 1024, kSwizzle128B);
@@ -826,6 +912,10 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, int* __r
         const uint64_t off = st * (Cfg::kStage / 16);
         bar_sync(kBarS, kBarThreads);
         tc_fence_after_sync();
+        if (kSave && lane == 0) {
+          bulk_store(saved.states + (((slot0 + n) * a.Hv + h) * kParts + part) * (long long)Cfg::kSTile, stile, Cfg::kSTile);
+          bulk_commit_group();
+        }
         if (ok && lane == 0) {
 #pragma unroll
           for (int t = Cfg::kSTiles - 1; t >= 0; --t)   // the small terms first
@@ -839,32 +929,34 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, int* __r
         bar_sync(kBarR, kBarThreads);
         tc_fence_after_sync();
         if (ok && lane == 0) {
+          // hi by all three terms of R, lo by the first two
           if (kCols == 64) {
 #pragma unroll
-            for (int t = 2; t >= 1; --t)
+            for (int t = 2; t >= 0; --t) {
+              if (t < 2)
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                  umma_bf16(tmem + Cfg::kX2, imgdesc + off + kImgHalf / 16 + ks * 128,
+                            rdesc + t * (Cfg::kRTile / 16) + ks * 128, idesc_r, 1u);
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
                 umma_bf16(tmem + Cfg::kX2, imgdesc + off + ks * 128, rdesc + t * (Cfg::kRTile / 16) + ks * 128, idesc_r,
                           ks > 0 || t < 2);
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              umma_bf16(tmem + Cfg::kX2, imgdesc + off + kImgHalf / 16 + ks * 128, rdesc + ks * 128, idesc_r, 1u);
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              umma_bf16(tmem + Cfg::kX2, imgdesc + off + ks * 128, rdesc + ks * 128, idesc_r, 1u);
-          } else {   // T's and P T's lo terms with R's first term alone
+            }
+          } else {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
               umma_bf16(tmem + Cfg::kX2, imgdesc + off + ks * 128, rdesc + ks * 128, idesc_r, ks > 0);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              umma_bf16(tmem + Cfg::kX2, imgdesc + off + kImgHalf / 16 + ks * 128, rdesc + ks * 128, idesc_1, 1u);
+              umma_bf16(tmem + Cfg::kX2, imgdesc + off + kImgHalf / 16 + ks * 128, rdesc + ks * 128, idesc_2, 1u);
           }
           umma_commit(&done[1]);
         }
         __syncwarp();
         bar_sync(kBarU, kBarThreads);
         tc_fence_after_sync();
+        if (kSave && lane == 0) bulk_wait_group_read<0>();   // before the tile of S0 is written again
         if (ok && lane == 0) {
 #pragma unroll
           for (int t = (kCols == 64 ? 2 : 0); t >= 0; --t)

@@ -355,11 +355,11 @@ litela_status delta_setup(int dev) {
   set(litela_delta_prep<32>, PrepCfg<32>::kSmemBytes);
   set(litela_delta_prep<64>, PrepCfg<64>::kSmemBytes);
   set(litela_delta_prep<128>, PrepCfg<128>::kSmemBytes);
-  set(litela_delta_chain<32, 32>, ChainCfg<32, 32>::kSmemBytes);
-  set(litela_delta_chain<64, 32>, ChainCfg<64, 32>::kSmemBytes);
-  set(litela_delta_chain<64, 64>, ChainCfg<64, 64>::kSmemBytes);
-  set(litela_delta_chain<128, 32>, ChainCfg<128, 32>::kSmemBytes);
-  set(litela_delta_chain<128, 64>, ChainCfg<128, 64>::kSmemBytes);
+  set(litela_delta_chain<32, 32, false>, ChainCfg<32, 32>::kSmemBytes);
+  set(litela_delta_chain<64, 32, false>, ChainCfg<64, 32>::kSmemBytes);
+  set(litela_delta_chain<64, 64, false>, ChainCfg<64, 64>::kSmemBytes);
+  set(litela_delta_chain<128, 32, false>, ChainCfg<128, 32>::kSmemBytes);
+  set(litela_delta_chain<128, 64, false>, ChainCfg<128, 64>::kSmemBytes);
   if (e != cudaSuccess) return host_cuda_fail(e, "cudaFuncSetAttribute(dynamic shared memory)");
   ready[dev] = true;
   return LITELA_OK;
@@ -377,10 +377,10 @@ cudaError_t launch_prep(const DeltaArgs& d, uint8_t* prep, cudaStream_t st) {
                     false, d, prep);
 }
 
-template <int kD, int kCols>
-cudaError_t launch_chain(const DeltaArgs& d, const uint8_t* prep, int* err, cudaStream_t st) {
-  return launch_seq(litela_delta_chain<kD, kCols>, dim3((unsigned)((long long)d.nseq * d.Hv * (kD / kCols))),
-                    kChainThreads, ChainCfg<kD, kCols>::kSmemBytes, st, true, d, prep, err);
+template <int kD, int kCols, bool kSave = false>
+cudaError_t launch_chain(const DeltaArgs& d, const uint8_t* prep, int* err, cudaStream_t st, DeltaSaved saved = {}) {
+  return launch_seq(litela_delta_chain<kD, kCols, kSave>, dim3((unsigned)((long long)d.nseq * d.Hv * (kD / kCols))),
+                    kChainThreads, ChainCfg<kD, kCols>::kSmemBytes, st, true, d, prep, saved, err);
 }
 
 litela_status launch_chunks(const DeltaArgs& d, int D, void* ws, int dev, int sms, cudaStream_t st) {
