@@ -339,9 +339,10 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
     // L's pair in the image: block cb of 16 columns stands 64 bytes (before the swizzle) or a block on
     uint8_t* image = Ih + r * 128 + (c0 & 4) * 2;
     const uint32_t chunk = (uint32_t)(((2 + (c0 >> 3)) ^ r) & 7) << 4;
-    auto scaled = [&](float4* src, const float* f) {
+    auto scaled = [&](float4* src, const float* f, int real = 4) {   // the first `real` columns, zeros
       const float4 x = *src;
-      float4 y = make_float4(x.x * f[0], x.y * f[1], x.z * f[2], x.w * f[3]);
+      float4 y = make_float4(real > 0 ? x.x * f[0] : 0.f, real > 1 ? x.y * f[1] : 0.f, real > 2 ? x.z * f[2] : 0.f,
+                             real > 3 ? x.w * f[3] : 0.f);
       if (0.f * y.x + 0.f * y.y + 0.f * y.z + 0.f * y.w != 0.f) {   // not finite
         first = min(first, r);
         y.x = isfinite(y.x) ? y.x : 0.f, y.y = isfinite(y.y) ? y.y : 0.f;
@@ -364,19 +365,17 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
       for (int e = 0; e < 4; ++e) f[e] *= a.scale;
       ps[4 * cb] = scaled(ps + 4 * cb, f);
     }
-    float f[4];   // the diagonal block: L below the diagonal, P with it
-    const int below = r - 16 * rb - c0;   // columns of the four that are left of the diagonal
+    float f[4];   // the diagonal block: L below the diagonal, P with it (what f is above it is not used)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 rc = rel[16 * rb + c0 + e];
-      const float x = expf((rr.x - rc.x) + (rr.y - rc.y));   // (infinite above the diagonal)
-      f[e] = below >= e ? x : 0.f;
+      f[e] = expf((rr.x - rc.x) + (rr.y - rc.y));
     }
-    float4 y = scaled(ls + 4 * rb, f);
-    ls[4 * rb] = make_float4(below == 0 ? 0.f : y.x, below == 1 ? 0.f : y.y, below == 2 ? 0.f : y.z, below == 3 ? 0.f : y.w);
+    const int below = r - 16 * rb - c0;   // columns of the four that are left of the diagonal
+    ls[4 * rb] = scaled(ls + 4 * rb, f, below);
 #pragma unroll
     for (int e = 0; e < 4; ++e) f[e] *= a.scale;
-    ps[4 * rb] = scaled(ps + 4 * rb, f);
+    ps[4 * rb] = scaled(ps + 4 * rb, f, below + 1);
   }
   if (first < kChunk) atomicMin(bad, first);
   // the blocks of X^T (P T) left of its diagonal blocks are zero: six of 16 rows x 32 bytes
