@@ -307,6 +307,37 @@ typedef struct {
 litela_status lite_la_gated_delta_fwd(const lite_la_delta_args* args, cudaStream_t stream);
 size_t lite_la_gated_delta_workspace_bytes(int B, int N, int Hk, int Hv, int d, int packed);
 
+/* The forward of a training step: lite_la_gated_delta_fwd that also keeps what its gradient needs in
+ * `saved`, device memory of lite_la_gated_delta_saved_bytes(), 16-byte aligned (per 64 tokens and
+ * value head: 33 KB + 4 d^2 + 256 d bytes).  It needs no workspace, and state_out must not be NULL.
+ *
+ * lite_la_gated_delta_bwd: the gradients of sum(dout * out) + sum(dstate_out * state_out).  args
+ * are the forward's (out is not used), saved is what it left and state_out what it wrote; workspace:
+ * lite_la_gated_delta_bwd_workspace_bytes().  dout: a view of the layout of out; dq, dk [B, N, Hk, d]
+ * and dv [B, N, Hv, d]: views; a key head's gradient is the sum over its value heads, in a fixed
+ * order.  dg, dbeta: fp32 [B, N, Hv], dense.  dstate_out, dstate_in: as state_out and state_in, or
+ * NULL (zeros; not wanted); state_out may be NULL when dstate_out is.  All rows are written: those of
+ * no sequence with zeros.  The sums are fp32; equal calls give equal bits.
+ *
+ * A NaN or infinite value of a token (or of the state before a sequence) makes out of that token, of
+ * all later tokens and the state NaN in the heads that read it; earlier tokens keep their values.
+ * The gradients of such a sequence are unspecified; other sequences are not touched. */
+typedef struct {
+  lite_la_view dout, dq, dk, dv;
+  float* dg;
+  float* dbeta;
+  const float* dstate_out;
+  const float* state_out;
+  float* dstate_in;
+} lite_la_delta_grads;
+
+litela_status lite_la_gated_delta_fwd_save(const lite_la_delta_args* args, void* saved, size_t saved_bytes,
+                                           cudaStream_t stream);
+size_t lite_la_gated_delta_saved_bytes(int B, int N, int Hk, int Hv, int d, int packed);
+litela_status lite_la_gated_delta_bwd(const lite_la_delta_args* args, const lite_la_delta_grads* grads,
+                                      const void* saved, size_t saved_bytes, cudaStream_t stream);
+size_t lite_la_gated_delta_bwd_workspace_bytes(int B, int N, int Hk, int Hv, int d, int packed);
+
 /* The one-token form for serving: token 0 of each of B rows (N must be 1, cu_seqlens NULL), with
  * the states updated in place: state_in and state_out are the same pool, fp32 [pool, Hv, d, d],
  * and row b's state is pool entry state_indices[b] (device int32; NULL: entry b, then pool >= B).

@@ -20,7 +20,8 @@ __all__ = [
     "lite_la_workspace_bytes", "lite_la_release_workspace", "lite_la_forward_form",
     "lite_la_set_paired_min_chunk", "STATUS", "EXPORTED_SYMBOLS",
     "lite_la_qk_norm_rope", "lite_la_qk_norm_rope_fwd", "lite_la_qk_norm_rope_bwd",
-    "lite_la_gated_delta_fwd", "lite_la_gated_delta_step",
+    "lite_la_gated_delta", "lite_la_gated_delta_fwd", "lite_la_gated_delta_fwd_save", "lite_la_gated_delta_bwd",
+    "lite_la_gated_delta_step",
 ]
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -81,6 +82,10 @@ _SIGNATURES = {
     "lite_la_gated_delta_fwd": (_c_int, [_vp, _vp]),
     "lite_la_gated_delta_workspace_bytes": (_c_size, [_c_int] * 6),
     "lite_la_gated_delta_step": (_c_int, [_vp, _vp, _c_int, _vp]),
+    "lite_la_gated_delta_fwd_save": (_c_int, [_vp, _vp, _c_size, _vp]),
+    "lite_la_gated_delta_saved_bytes": (_c_size, [_c_int] * 6),
+    "lite_la_gated_delta_bwd": (_c_int, [_vp, _vp, _vp, _c_size, _vp]),
+    "lite_la_gated_delta_bwd_workspace_bytes": (_c_size, [_c_int] * 6),
 }
 EXPORTED_SYMBOLS = tuple(_SIGNATURES)
 
@@ -430,6 +435,6 @@ def lite_la_release_workspace() -> None:
 
 # the language-model operators (imported last: they use this module's helpers)
 from .seq import (  # noqa: E402
-    lite_la_gated_delta_fwd, lite_la_gated_delta_step, lite_la_qk_norm_rope, lite_la_qk_norm_rope_bwd,
-    lite_la_qk_norm_rope_fwd,
+    lite_la_gated_delta, lite_la_gated_delta_bwd, lite_la_gated_delta_fwd, lite_la_gated_delta_fwd_save,
+    lite_la_gated_delta_step, lite_la_qk_norm_rope, lite_la_qk_norm_rope_bwd, lite_la_qk_norm_rope_fwd,
 )

@@ -1,0 +1,821 @@
+// Gradient of the gated delta rule over whole sequences, from what a forward kept (DeltaSaved and the
+// prepared blocks).  Names as in litela_delta_chunk.cuh; do is the gradient of out, G' that of the
+// state behind a chunk, dU that of the written values, and with w_i the gradient of what token i
+// writes, before beta:
+//     dU = P^T do + diag(e^(G_C - G)) K G',     w = T^T dU,     y = diag(beta) w,     dv = y,
+//     G' (before the chunk) = e^G_C G' + scale Q^T diag(e^G) do - K^T diag(e^G) y,
+//     dbeta_i = w_i . W_i
+//     dq = scale diag(e^G) do S0^T + (M1 . D) K,            M1 = scale do U^T with and below the diagonal,
+//     dk = (M1 . D)^T Q + diag(e^(G_C - G)) U G'^T - diag(e^G) y S0^T - (M2 . D) K - (M2 . D)^T K,
+//                                                           M2 = y U^T below the diagonal,
+//     dg_t = <S_C, G'> + sum over s >= t in the chunk of (q_s . dq_s - y_s . v_s).
+// The last line: a decay multiplies the state before its token, so its gradient is <state, gradient>
+// there, and from a token to the one before it <S, G'> changes by out . do - dv . v.
+//
+// litela_delta_back walks a sequence's chunks from the last to the first (as litela_delta_chain, with
+// the same three products a chunk) and leaves y and each chunk's G'; litela_delta_grads makes the rest,
+// all chunks at once.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cstdint>
+
+#include "litela_delta_chunk.cuh"
+
+namespace litela {
+
+struct DeltaGrads {
+  DeltaView dout, dq, dk, dv;      // dq, dk: key heads
+  float* dg;                       // [entry, token, Hv], dense
+  float* dbeta;
+  const float* dstate_out;         // [sequence][Hv][d][d] or null (zeros)
+  const float* state_out;          // the forward's, for dstate_out
+  float* dstate_in;                // or null
+  // between the two kernels, per chunk slot and value head
+  uint8_t* gstates;                // G' as DeltaSaved's states
+  float* y;                        // [64, d]
+  float* rows;                     // [d / 32][2][2][64]: w . W and y . v of half of 32 columns
+  float* ends;                     // [d / 32][8]: shares of <S_C, G'>
+};
+
+// ---------------------------------------------------------------------------------------
+// litela_delta_back: one CTA walks the chunks of one sequence and value head for 32 columns of the
+// state's gradient.  Per chunk, each product with M = 128 rows (tcgen05, fp32 accumulators in TMEM):
+//     X1 = [K; Q] G'                                            (the rows of K are used)
+//     X2 = X^T (-diag(beta) Z) + (P T)^T do,  Z = diag(e^(G_C - G)) K G'      (64 rows)
+//     X3 = [K; Q]^T [-diag(e^G) y; scale diag(e^G) do]
+// so that w = Z + X2 (T = I - diag(beta) X) and G' = e^G_C G' + X3.
+// The prepared block's image holds X^T and (P T)^T row by row, which here is a K-major A operand.  Its
+// rows are tokens in order, and so are K's and Q's here (not interleaved): Z and X2 have to meet in
+// the same TMEM lanes.  The warps of those lanes (quarters 0 and 1) do the rows of K; the others
+// prepare do.
+template <int kD>
+struct BackCfg {
+  static constexpr int kCols = 32;
+  static constexpr int kBlocks = kD > 64 ? 2 : 1;
+  static constexpr uint32_t kKQ = kBlocks * 16384;                // per block: 64 rows of K, 64 of Q
+  static constexpr uint32_t kVLd = kCols * 2 + 16;
+  static constexpr uint32_t kOffPrep = kKQ;
+  static constexpr uint32_t kOffDo = (kKQ + kPrepBytes + 1023) / 1024 * 1024;   // do: 64 rows of 128 bytes, 32 columns
+  static constexpr uint32_t kOffV = kOffDo + 64 * 128;
+  static constexpr uint32_t kStage = (kOffV + 64 * kVLd + 1023) / 1024 * 1024;
+  static constexpr uint32_t kSTile = kD * 128, kRTile = 128 * 128;
+  static constexpr uint32_t kOffS = kChainStages * kStage;
+  static constexpr uint32_t kOffR = kOffS + kSTile;               // Z, then y, in rows 0..63; do in rows 64..127
+  static constexpr uint32_t kOffBars = kOffR + 2 * kRTile;
+  static constexpr uint32_t kSmemBytes = kOffBars + 256 + 1024;
+  static constexpr uint32_t kX1 = 0, kX2 = 64, kX3 = 160;
+  static_assert(kSmemBytes <= 232448, "shared memory above the 227 KB per-block limit");
+};
+enum : int { kErrBackLoad = 0x610, kErrBackMma = 0x620, kErrBackAcc = 0x630 };
+
+template <int kD>
+__global__ void __launch_bounds__(kChainThreads, 1)
+litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restrict__ prep, const DeltaSaved saved,
+                  int* __restrict__ err) {
+  using namespace sm100;
+  using Cfg = BackCfg<kD>;
+  constexpr int kCols = Cfg::kCols, kN = 16, kParts = kD / kCols;
+  static_assert(kAccWarps == 8, "a warp has half of the columns");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* stile = smem + Cfg::kOffS;
+  uint8_t* rtile = smem + Cfg::kOffR;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::kOffBars);
+  uint64_t* empty = full + kChainStages;
+  uint64_t* done = empty + kChainStages;
+  uint64_t* drained = done + 3;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = blockIdx.x % kParts, h = (blockIdx.x / kParts) % a.Hv, s = blockIdx.x / (kParts * a.Hv);
+  const int hk = h / (a.Hv / a.Hk);
+  const DeltaSeq sq = delta_seq(a, s);
+  const int nchunk = (sq.len + kChunk - 1) / kChunk;
+  const long long slot0 = delta_slot0(a, s, sq);
+  const uint8_t* blocks = prep + (slot0 * a.Hv + h) * (long long)kPrepBytes;
+  const long long block_step = (long long)a.Hv * kPrepBytes;
+
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kChainStages; ++i) {
+      mbar_init(&full[i], kLoadWarps + 1);
+      mbar_init(&empty[i], kAccWarps + 1);
+    }
+    for (int i = 0; i < 3; ++i) mbar_init(&done[i], 1);
+    mbar_init(drained, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kIssueWarp) {
+    tmem_alloc(tmem_holder, kChainTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_holder;
+
+  if (warp < kAccWarps) {
+    const int quad = warp & 3, c0 = (warp >> 2) * kN, row = quad * 32 + lane, tok = row & 63;
+    const uint32_t ta = tmem + ((uint32_t)(quad * 32) << 16);
+    const bool has_state = row < kD, is_k = quad < 2;
+    const long long sbase = ((long long)s * a.Hv + h) * (kD * kD) + (long long)row * kD + part * kCols + c0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int phase, int code) {
+      if (ok) ok = mbar_wait(bar, phase & 1, abort_flag, err, kErrBackAcc | code);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after_sync();
+    };
+    auto hand = [&](int id) {
+      fence_proxy_async_smem();
+      tc_fence_before_sync();
+      bar_arrive(id, kBarThreads);
+    };
+    // this warp's share of <S, G'> behind chunk n
+    auto put_end = [&](int n, float dot) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if (lane == 0) gr.ends[(((slot0 + n) * a.Hv + h) * kParts + part) * 8 + warp] = dot;
+    };
+    F2 S[kN / 2];
+#pragma unroll
+    for (int i = 0; i < kN / 2; ++i) S[i] = f2(0.f, 0.f);
+    float dot = 0.f;
+    if (has_state && gr.dstate_out != nullptr)
+#pragma unroll
+      for (int i = 0; i < kN; i += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(gr.dstate_out + sbase + i);
+        const float4 z = *reinterpret_cast<const float4*>(gr.state_out + sbase + i);
+        S[i / 2] = f2(x.x, x.y), S[i / 2 + 1] = f2(x.z, x.w);
+        dot += x.x * z.x + x.y * z.y + x.z * z.z + x.w * z.w;
+      }
+    if (nchunk > 0) {
+      put_end(nchunk - 1, dot);
+      if (has_state) chain_put<kCols, 2, kN>(stile, Cfg::kSTile, row, c0, S);
+      hand(kBarS);
+    }
+    for (int it = 0; it < nchunk; ++it) {
+      const int n = nchunk - 1 - it, st = it % kChainStages;
+      const uint8_t* stage = smem + st * Cfg::kStage;
+      const long long sh = (slot0 + n) * a.Hv + h;
+      // W's row; the state before the chunk, this thread's row of it
+      float4 wrow[kN / 4];
+      uint4 s0[kN / 4];
+      if (is_k) {
+        const float4* src = reinterpret_cast<const float4*>(saved.w + (sh * kChunk + tok) * kD + part * kCols + c0);
+#pragma unroll
+        for (int i = 0; i < kN / 4; ++i) wrow[i] = __ldg(src + i);
+      }
+      if (has_state && n > 0) {
+        const uint8_t* src = saved.states + (sh * kParts + part) * (long long)Cfg::kSTile;
+#pragma unroll
+        for (int i = 0; i < kN / 8; ++i) {
+          s0[i] = __ldg(reinterpret_cast<const uint4*>(src + sw128(row, c0 + 8 * i)));
+          s0[kN / 8 + i] = __ldg(reinterpret_cast<const uint4*>(src + sw128(row, 32 + c0 + 8 * i)));
+        }
+      }
+      wait(&full[st], it / kChainStages, 0);
+      const float* fac = reinterpret_cast<const float*>(stage + Cfg::kOffPrep + kPrepFactors);
+      const float decay = fac[kFacDecay + tok], to_end = fac[kFacToEnd + tok], beta = fac[kFacBeta + tok];
+      const float chunk_decay = fac[kFacChunk];
+      uint4 v[kN / 8];   // v's row, or do's
+#pragma unroll
+      for (int i = 0; i < kN / 8; ++i)
+        v[i] = is_k ? *reinterpret_cast<const uint4*>(stage + Cfg::kOffV + tok * Cfg::kVLd + c0 * 2 + i * 16)
+                    : *reinterpret_cast<const uint4*>(stage + Cfg::kOffDo + sw128(tok, c0 + i * 8));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+      F2 x[kN / 2], z[kN / 2];
+      if (!is_k) {   // scale e^G do
+        const F2 f = f2(a.scale * decay, a.scale * decay);
+#pragma unroll
+        for (int i = 0; i < kN / 2; ++i) x[i] = f2_mul(f, f2_bf16(reinterpret_cast<const uint32_t*>(v)[i]));
+        chain_put<kCols, 3, kN>(rtile, Cfg::kRTile, 64 + tok, c0, x);
+        hand(kBarR);
+        hand(kBarU);
+      } else {
+        wait(&done[0], it, 1);
+        chain_acc<kCols, 2, kN>(ta + Cfg::kX1, c0, z);
+        const F2 f = f2(to_end, to_end), mb = f2(-beta, -beta);
+#pragma unroll
+        for (int i = 0; i < kN / 2; ++i) {
+          z[i] = f2_mul(f, z[i]);
+          x[i] = f2_mul(mb, z[i]);
+        }
+        chain_put<kCols, 3, kN>(rtile, Cfg::kRTile, tok, c0, x);
+        hand(kBarR);
+        wait(&done[1], it, 2);
+        chain_acc<kCols, 3, kN>(ta + Cfg::kX2, c0, x);
+        const F2 b2 = f2(beta, beta), d2 = f2(-decay, -decay);
+        F2 y[kN / 2];
+#pragma unroll
+        for (int i = 0; i < kN / 2; ++i) {
+          z[i] = f2_add(z[i], x[i]);   // w
+          y[i] = f2_mul(b2, z[i]);
+          x[i] = f2_mul(d2, y[i]);
+        }
+        chain_put<kCols, 3, kN>(rtile, Cfg::kRTile, tok, c0, x);
+        hand(kBarU);
+        // while the third product runs: dv, y and the rows' shares
+        F2 wdot = f2(0.f, 0.f), vdot = f2(0.f, 0.f);
+        uint32_t o[kN / 2];
+        float4* yd = reinterpret_cast<float4*>(gr.y + (sh * kChunk + tok) * kD + part * kCols + c0);
+#pragma unroll
+        for (int i = 0; i < kN / 2; ++i) {
+          const float* wr = reinterpret_cast<const float*>(wrow) + 2 * i;
+          wdot = f2_fma(z[i], f2(wr[0], wr[1]), wdot);
+          vdot = f2_fma(y[i], f2_bf16(reinterpret_cast<const uint32_t*>(v)[i]), vdot);
+          const float2 yy = f2_out(y[i]);
+          o[i] = pack_bf16(yy.x, yy.y);
+          if (i & 1) {
+            const float2 yp = f2_out(y[i - 1]);
+            yd[i / 2] = make_float4(yp.x, yp.y, yy.x, yy.y);
+          }
+        }
+        const float2 wd = f2_out(wdot), vd = f2_out(vdot);
+        float* rw = gr.rows + ((sh * kParts + part) * 2 * 2 + (warp >> 2)) * kChunk + tok;
+        rw[0] = wd.x + wd.y;
+        rw[2 * kChunk] = vd.x + vd.y;
+        if (n * kChunk + tok < sq.len) {
+          uint4* dst = reinterpret_cast<uint4*>(const_cast<__nv_bfloat16*>(delta_row(gr.dv, sq, n * kChunk + tok, h)) +
+                                                part * kCols + c0);
+#pragma unroll
+          for (int i = 0; i < kN / 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+      }
+      wait(&done[2], it, 3);
+      if (has_state) {
+        chain_acc<kCols, 3, kN>(ta + Cfg::kX3, c0, x);
+        const F2 d2 = f2(chunk_decay, chunk_decay);
+#pragma unroll
+        for (int i = 0; i < kN / 2; ++i) S[i] = f2_fma(d2, S[i], x[i]);
+        if (n > 0) chain_put<kCols, 2, kN>(stile, Cfg::kSTile, row, c0, S);
+      }
+      if (n > 0) {
+        hand(kBarS);
+        F2 d = f2(0.f, 0.f);
+        if (has_state) {
+#pragma unroll
+          for (int i = 0; i < kN / 2; ++i) {
+            const uint32_t hi = reinterpret_cast<const uint32_t*>(s0)[i], lo = reinterpret_cast<const uint32_t*>(s0)[kN / 2 + i];
+            d = f2_fma(S[i], f2_add(f2_bf16(hi), f2_bf16(lo)), d);
+          }
+        }
+        const float2 dd = f2_out(d);
+        put_end(n - 1, dd.x + dd.y);
+      }
+    }
+    if (ok && has_state && gr.dstate_in != nullptr)
+#pragma unroll
+      for (int i = 0; i < kN; i += 4)
+        *reinterpret_cast<float4*>(gr.dstate_in + sbase + i) =
+            make_float4(f2_out(S[i / 2]).x, f2_out(S[i / 2]).y, f2_out(S[i / 2 + 1]).x, f2_out(S[i / 2 + 1]).y);
+  } else if (warp == kIssueWarp) {
+    constexpr uint32_t idesc_1 = idesc_bf16_f32(128, 64, false, true);     // [K; Q] G'
+    constexpr uint32_t idesc_z = idesc_bf16_f32(128, 96, false, true);     // X^T Z, three terms
+    constexpr uint32_t idesc_z2 = idesc_bf16_f32(128, 64, false, true);    // two terms
+    constexpr uint32_t idesc_do = idesc_bf16_f32(128, 32, false, true);    // (P T)^T do
+    constexpr uint32_t idesc_3 = idesc_bf16_f32(128, 96, true, true);      // [K; Q]^T ..
+    const uint64_t sdesc = smem_desc(smem_u32(stile), 1024, 1024, kSwizzle128B);
+    const uint64_t rdesc = smem_desc(smem_u32(rtile), Cfg::kRTile, 1024, kSwizzle128B);
+    const uint64_t kqdesc = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+    const uint64_t imgdesc = smem_desc(smem_u32(smem) + Cfg::kOffPrep, 16, 1024, kSwizzle128B);
+    const uint64_t dodesc = smem_desc(smem_u32(smem) + Cfg::kOffDo, 1024, 1024, kSwizzle128B);
+    // [K; Q]^T: M over channels, 128 rows.  d <= 64: rows 64 on of the product take whatever follows
+    const uint64_t ktdesc = smem_desc(smem_u32(smem), kD > 64 ? 16384 : 1024, 1024, kSwizzle128B);
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int phase, int code) {
+      if (ok && lane == 0) ok = mbar_spin(bar, phase & 1, abort_flag, err, kErrBackMma | code);
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    if (nchunk > 0) wait(&full[0], 0, 0);
+    for (int it = 0; it < nchunk; ++it) {
+      const int n = nchunk - 1 - it, st = it % kChainStages;
+      const uint64_t off = st * (Cfg::kStage / 16);
+      bar_sync(kBarS, kBarThreads);
+      tc_fence_after_sync();
+      if (lane == 0) {
+        bulk_store(gr.gstates + (((slot0 + n) * a.Hv + h) * kParts + part) * (long long)Cfg::kSTile, stile, Cfg::kSTile);
+        bulk_commit_group();
+        if (ok) {
+#pragma unroll
+          for (int ks = 0; ks < kD / 16; ++ks)
+            umma_bf16(tmem + Cfg::kX1, kqdesc + off + (ks / 4) * 1024 + (ks % 4) * 2, sdesc + ks * 128, idesc_1, ks > 0);
+          umma_commit(&done[0]);
+        }
+      }
+      __syncwarp();
+      bar_sync(kBarR, kBarThreads);
+      tc_fence_after_sync();
+      if (ok && lane == 0) {
+        // the image's columns: 16 tokens of X, the same 16 of P T, ..
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          umma_bf16(tmem + Cfg::kX2, imgdesc + off + (ks / 2) * (kImgBlock / 16) + (ks % 2) * 4, rdesc + ks * 128, idesc_z,
+                    ks > 0);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          umma_bf16(tmem + Cfg::kX2, imgdesc + off + (kImgHalf + (ks / 2) * kImgBlock) / 16 + (ks % 2) * 4, rdesc + ks * 128,
+                    idesc_z2, 1u);
+#pragma unroll
+        for (int t = 1; t >= 0; --t)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            umma_bf16(tmem + Cfg::kX2, imgdesc + off + (t * kImgHalf + (ks / 2) * kImgBlock) / 16 + (ks % 2) * 4 + 2,
+                      dodesc + off + ks * 128, idesc_do, 1u);
+        umma_commit(&done[1]);
+      }
+      __syncwarp();
+      bar_sync(kBarU, kBarThreads);
+      tc_fence_after_sync();
+      if (lane == 0) {
+        bulk_wait_group_read<0>();   // before G's tile is written again
+        if (ok) {
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            umma_bf16(tmem + Cfg::kX3, ktdesc + off + ks * 128, rdesc + ks * 128, idesc_3, ks > 0);
+          umma_commit(&done[2]);
+          umma_commit(&empty[st]);
+        }
+      }
+      __syncwarp();
+      if (it + 1 < nchunk) wait(&full[(it + 1) % kChainStages], (it + 1) / kChainStages, 0);
+    }
+    if (lane == 0) {
+      umma_commit(drained);
+      mbar_drain(drained, 0);
+      bulk_wait_group<0>();
+    }
+  } else {
+    const int t = threadIdx.x - (warp > kIssueWarp ? kAccWarps + 1 : kAccWarps) * 32;
+    int issued = 0;
+    constexpr int kC = kD / 8, kStep = kLoadThreads / kC, kVC = kCols / 8, kVStep = kLoadThreads / kVC;
+    const int r0 = t / kC, c = t % kC, vr0 = t / kVC, vc = t % kVC;
+    const uint32_t kq0 = smem_u32(smem) + (c / 8) * 16384 + sw128(r0, (c % 8) * 8);
+    const uint32_t v0 = smem_u32(smem) + Cfg::kOffV + vr0 * Cfg::kVLd + vc * 16;
+    const uint32_t do0 = smem_u32(smem) + Cfg::kOffDo;
+    const long long kstep = kStep * a.k.st, qstep = kStep * a.q.st, vstep = kVStep * a.v.st, dstep = kVStep * gr.dout.st;
+    for (int it = 0; it < nchunk; ++it) {
+      const int n = nchunk - 1 - it, st = it % kChainStages;
+      const bool ok = it < kChainStages || lane != 0 ||
+                      mbar_wait(&empty[st], (it / kChainStages - 1) & 1, abort_flag, err, kErrBackLoad | st);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (t == 0) {
+        mbar_arrive_expect_tx(&full[st], kPrepBytes);
+        bulk_load(smem + st * Cfg::kStage + Cfg::kOffPrep, blocks + n * block_step, kPrepBytes, &full[st]);
+      }
+      issued = it + 1;
+      const int n0 = n * kChunk, len = min(kChunk, sq.len - n0);
+      const uint32_t dkq = kq0 + st * Cfg::kStage, dv = v0 + st * Cfg::kStage, ddo = do0 + st * Cfg::kStage;
+      const __nv_bfloat16* kp = delta_row(a.k, sq, n0 + r0, hk) + c * 8;
+      const __nv_bfloat16* qp = delta_row(a.q, sq, n0 + r0, hk) + c * 8;
+      const __nv_bfloat16* vp = delta_row(a.v, sq, n0 + vr0, h) + part * kCols + vc * 8;
+      const __nv_bfloat16* dp = delta_row(gr.dout, sq, n0 + vr0, h) + part * kCols + vc * 8;
+#pragma unroll
+      for (int i = 0; i < kChunk / kStep; ++i) {
+        const uint32_t o = (dkq ^ (((i * kStep) & 7) << 4)) + i * kStep * 128;
+        const bool real = r0 + i * kStep < len;
+        cp_async_16(o, real ? kp : a.k.p, real);
+        cp_async_16(o + 8192, real ? qp : a.q.p, real);
+        kp += kstep;
+        qp += qstep;
+      }
+#pragma unroll
+      for (int i = 0; i < kChunk / kVStep; ++i) {
+        const int r = vr0 + i * kVStep;
+        const bool real = r < len;
+        cp_async_16(dv + i * kVStep * Cfg::kVLd, real ? vp : a.v.p, real);
+        cp_async_16(ddo + sw128(r, vc * 8), real ? dp : gr.dout.p, real);
+        vp += vstep;
+        dp += dstep;
+      }
+      if (n > 0) {   // the chunk before into L2
+        const int r = n0 - kChunk + t;
+        const __nv_bfloat16 *k = delta_row(a.k, sq, r, hk), *q = delta_row(a.q, sq, r, hk);
+        prefetch_l2(k);
+        prefetch_l2(q);
+        if (kD > 64) {
+          prefetch_l2(k + 64);
+          prefetch_l2(q + 64);
+        }
+        prefetch_l2(delta_row(a.v, sq, r, h) + part * kCols);
+        prefetch_l2(delta_row(gr.dout, sq, r, h) + part * kCols);
+        if (t == 0) bulk_prefetch_l2(blocks + (n - 1) * block_step, kPrepBytes);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[st]);
+    }
+    if (t == 0 && *abort_flag)
+      for (int i = issued > kChainStages ? issued - kChainStages : 0; i < issued; ++i)
+        mbar_drain(&full[i % kChainStages], (i / kChainStages) & 1);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kIssueWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kChainTmem);
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// litela_delta_grads: dq, dk, dg and dbeta of one chunk and key head per CTA, its value heads one
+// after another (their shares of dq and dk are summed in registers, in a fixed order).
+//
+// mma.sync, 8 warps: warp w has 16 rows (w / 2) and half of the columns.  States and gradients stream
+// through a ring of tiles of 32 columns; U and y are entered as bf16 pairs.  dq and dk of one head
+// take 12 products of 64 rows; the states' and the gradients' bytes (16 d^2 a chunk and head) are
+// what bounds it.
+constexpr int kGradThreads = 256;
+constexpr int kGradLd = 72;   // row of the 64 x 64 matrices, padded
+constexpr int kGradRing = 3;
+
+template <int kD>
+struct GradCfg {
+  static constexpr int kLd = kD + 8;
+  static constexpr uint32_t kRows = kChunk * kLd * 2;              // 64 rows of d, bf16
+  static constexpr uint32_t kTile = kD * 128;
+  static constexpr uint32_t kOffK = 0, kOffQ = kRows, kOffDo = 2 * kRows;
+  static constexpr uint32_t kOffU = 3 * kRows, kOffY = 5 * kRows;  // pairs
+  static constexpr uint32_t kOffM = 7 * kRows;                     // M1 . D and M2 . D, pairs
+  static constexpr uint32_t kMat = kChunk * kGradLd * 2;
+  static constexpr uint32_t kOffTile = (kOffM + 4 * kMat + 127) / 128 * 128;
+  static constexpr uint32_t kOffG = kOffTile + kGradRing * kTile;
+  static constexpr uint32_t kOffRel = kOffG + kChunk * 8;          // as in litela_delta_prep
+  static constexpr uint32_t kOffRow = kOffRel + kChunk * 8;
+  static constexpr uint32_t kOffCol = kOffRow + kChunk * 4;
+  static constexpr uint32_t kOffFac = kOffCol + 4 * 48 * 4;        // e^G, e^(G_C - G), beta
+  static constexpr uint32_t kOffSum = kOffFac + 3 * kChunk * 4;    // q . dq: [2][64]
+  static constexpr uint32_t kSmemBytes = kOffSum + 2 * kChunk * 4 + 1024;
+  static_assert(kSmemBytes <= 232448, "shared memory above the 227 KB per-block limit");
+};
+
+template <int kD>
+__global__ void __launch_bounds__(kGradThreads, 1)
+litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restrict__ prep, const DeltaSaved saved) {
+  using namespace sm100;
+  using Cfg = GradCfg<kD>;
+  constexpr int kParts = kD / 32, kT = kD / 16;   // tiles of 8 columns of a warp's half of d
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  double* G = reinterpret_cast<double*>(smem + Cfg::kOffG);
+  float2* rel = reinterpret_cast<float2*>(smem + Cfg::kOffRel);
+  float* rowf = reinterpret_cast<float*>(smem + Cfg::kOffRow);
+  float* colf = reinterpret_cast<float*>(smem + Cfg::kOffCol);
+  float* fac = reinterpret_cast<float*>(smem + Cfg::kOffFac);
+  float* qsum = reinterpret_cast<float*>(smem + Cfg::kOffSum);
+
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g4 = lane >> 2, t2 = (lane & 3) * 2;
+  const int rb = w >> 1, hf = w & 1, l8 = lane & 7, k8 = ((lane >> 3) & 1) * 8;
+  const int slot = blockIdx.x / a.Hk, hk = blockIdx.x - slot * a.Hk, group = a.Hv / a.Hk;
+  int s, n0;
+  DeltaSeq sq;
+  if (!delta_find(a, slot, lane, s, sq, n0)) return;
+  const int len = min(kChunk, sq.len - n0);
+  const uint32_t base = smem_u32(smem);
+
+  // 64 rows of a view into shared memory
+  auto copy_rows = [&](const DeltaView& v, int head, uint32_t dst) {
+    constexpr int kC = kD / 8, kStep = kGradThreads / kC;
+    const int c = tid % kC, r0 = tid / kC;
+    const __nv_bfloat16* p = delta_row(v, sq, n0 + r0, head) + c * 8;
+#pragma unroll
+    for (int i = 0; i < kChunk / kStep; ++i) {
+      const bool real = r0 + i * kStep < len;
+      cp_async_16(base + dst + (r0 + i * kStep) * (Cfg::kLd * 2) + c * 16, real ? p : v.p, real);
+      p += kStep * v.st;
+    }
+  };
+  copy_rows(a.k, hk, Cfg::kOffK);
+  copy_rows(a.q, hk, Cfg::kOffQ);
+  pdl_wait_primary();   // y, G' and the shares come from litela_delta_back
+
+  float dq[kT][4], dk[kT][4];
+#pragma unroll
+  for (int n = 0; n < kT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dq[n][i] = dk[n][i] = 0.f;
+  float before = 0.f;   // tid < 64: q . dq of this token's value heads so far
+
+#pragma unroll 1
+  for (int hv = 0; hv < group; ++hv) {
+    const int h = hk * group + hv;
+    const long long sh = (long long)slot * a.Hv + h;
+    // tile p of the states (p < kParts), then of the gradients
+    auto load_tile = [&](int p) {
+      const uint8_t* src = (p < kParts ? saved.states + (sh * kParts + p) * (long long)Cfg::kTile
+                                       : gr.gstates + (sh * kParts + p - kParts) * (long long)Cfg::kTile);
+      const uint32_t dst = base + Cfg::kOffTile + (p % kGradRing) * Cfg::kTile;
+#pragma unroll 1
+      for (int i = tid * 16; i < (int)Cfg::kTile; i += kGradThreads * 16) cp_async_16(dst + i, src + i, true);
+    };
+    copy_rows(gr.dout, h, Cfg::kOffDo);
+    load_tile(0);
+    cp_async_commit();
+    load_tile(1);
+    cp_async_commit();
+    const float* pf = reinterpret_cast<const float*>(prep + sh * kPrepBytes + kPrepFactors);
+    if (tid < 192) fac[tid] = pf[tid];
+    if (w == 7) {   // G, two tokens a lane
+      double x[2] = {0.0, 0.0};
+      const float* g = a.g + sq.entry * a.g_sb + (long long)(sq.first + n0) * a.g_st + h;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (2 * lane + j < len) x[j] = (double)clamp_decay(g[(2 * lane + j) * a.g_st]);
+      x[1] += x[0];
+      double run = x[1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += y;
+      }
+      G[2 * lane] = run - x[1] + x[0];
+      G[2 * lane + 1] = run;
+    }
+    __syncthreads();
+    if (tid < kChunk) {
+      const double d = G[tid] - G[tid & ~15];
+      rel[tid] = make_float2((float)d, (float)(d - (double)(float)d));
+      rowf[tid] = expf((float)d);
+    } else if (tid < kChunk + 96) {
+      const int i = tid - kChunk, b = i < 16 ? 1 : i < 48 ? 2 : 3, c = i - (b == 1 ? 0 : b == 2 ? 16 : 48);
+      colf[b * 48 + c] = expf((float)(G[16 * b] - G[c]));
+    }
+    // U = beta W and y as pairs, 4 columns of a row at a time
+#pragma unroll 1
+    for (int i = tid; i < kChunk * kD / 4; i += kGradThreads) {
+      const int r = i / (kD / 4), c = (i % (kD / 4)) * 4;
+      const float b = fac[kFacBeta + r];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const float4 x = *reinterpret_cast<const float4*>((m ? gr.y : saved.w) + (sh * kChunk + r) * kD + c);
+        const float f = m ? 1.f : b;
+        uint32_t hi[2], lo[2];
+        split_bf16(f * x.x, f * x.y, hi[0], lo[0]);
+        split_bf16(f * x.z, f * x.w, hi[1], lo[1]);
+        uint8_t* dst = smem + (m ? Cfg::kOffY : Cfg::kOffU) + (r * Cfg::kLd + c) * 2;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(dst + Cfg::kRows) = make_uint2(lo[0], lo[1]);
+      }
+    }
+    cp_async_wait<1>();   // do and the first tile (K and Q)
+    __syncthreads();
+
+    // M1 = do U^T and M2 = y U^T: rows 16 rb .., the warp's rb + 1 tiles of the 2 rb + 2 (d: K dimension)
+    const int tile0 = hf * (rb + 1);
+    {
+      float m1[4][4], m2[4][4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m1[n][i] = m2[n][i] = 0.f;
+      const uint32_t arow = (16 * rb + (lane & 15)) * (Cfg::kLd * 2) + (lane >> 4) * 16;
+      // matrices by lane / 8: hi of 0..7 and 8..15 of the K dimension, lo
+      const uint32_t brow = base + Cfg::kOffU + (lane >> 4) * Cfg::kRows + (8 * tile0 + l8) * (Cfg::kLd * 2) + k8 * 2;
+#pragma unroll 1
+      for (int ks = 0; ks < kD / 16; ++ks) {
+        uint32_t ad[4], yh[4], yl[4];
+        ldmatrix_x4(ad, base + Cfg::kOffDo + arow + ks * 32);
+        ldmatrix_x4(yh, base + Cfg::kOffY + arow + ks * 32);
+        ldmatrix_x4(yl, base + Cfg::kOffY + Cfg::kRows + arow + ks * 32);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          if (n <= rb) {
+            uint32_t b[4];
+            ldmatrix_x4(b, brow + n * 8 * (Cfg::kLd * 2) + ks * 32);
+            mma_16816(m1[n], ad, b + 2);
+            mma_16816(m1[n], ad, b);
+            mma_pair(m2[n], yh, yl, b);
+          }
+      }
+      // by D; M1 by scale, M2 negated
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        if (n <= rb) {
+          const int c = 8 * (tile0 + n) + t2;
+          const bool diag = c >= 16 * rb;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int r = 16 * rb + g4 + 8 * q;
+            float d[2];
+            if (diag) {
+              const float2 rr = rel[r], ra = rel[c], rc = rel[c + 1];
+              d[0] = expf((rr.x - ra.x) + (rr.y - ra.y));
+              d[1] = expf((rr.x - rc.x) + (rr.y - rc.y));
+            } else {
+              const float2 cf = *reinterpret_cast<const float2*>(colf + rb * 48 + c);
+              d[0] = rowf[r] * cf.x, d[1] = rowf[r] * cf.y;
+            }
+            uint32_t hi, lo;
+            uint8_t* dst = smem + Cfg::kOffM + (r * kGradLd + c) * 2;
+            split_bf16(c <= r ? a.scale * d[0] * m1[n][2 * q] : 0.f, c + 1 <= r ? a.scale * d[1] * m1[n][2 * q + 1] : 0.f, hi, lo);
+            *reinterpret_cast<uint32_t*>(dst) = hi;
+            *reinterpret_cast<uint32_t*>(dst + Cfg::kMat) = lo;
+            split_bf16(c < r ? -d[0] * m2[n][2 * q] : 0.f, c + 1 < r ? -d[1] * m2[n][2 * q + 1] : 0.f, hi, lo);
+            *reinterpret_cast<uint32_t*>(dst + 2 * Cfg::kMat) = hi;
+            *reinterpret_cast<uint32_t*>(dst + 3 * Cfg::kMat) = lo;
+          }
+        }
+    }
+    __syncthreads();
+
+    // the 64 x 64 matrices with K and Q: columns [hf d / 2, + d / 2) of dq and dk
+    {
+      const uint32_t kcol = base + Cfg::kOffK + (l8 + k8) * (Cfg::kLd * 2) + hf * kD + (lane >> 4) * 16;   // two tiles
+      const uint32_t qcol = kcol + (Cfg::kOffQ - Cfg::kOffK);
+      const uint32_t mrow = base + Cfg::kOffM + ((16 * rb + (lane & 15)) * kGradLd + (lane >> 4) * 8) * 2;
+#pragma unroll 1
+      for (int kb = 0; kb <= rb; ++kb) {   // rows 16 rb: blocks up to the diagonal
+        uint32_t ah[4], al[4], ch[4], cl[4];
+        ldmatrix_x4(ah, mrow + kb * 32);
+        ldmatrix_x4(al, mrow + Cfg::kMat + kb * 32);
+        ldmatrix_x4(ch, mrow + 2 * Cfg::kMat + kb * 32);
+        ldmatrix_x4(cl, mrow + 3 * Cfg::kMat + kb * 32);
+#pragma unroll
+        for (int n = 0; n < kT; n += 2) {
+          uint32_t b[4];   // tile n: b[0], b[1]; tile n + 1: b[2], b[3]
+          ldmatrix_x4_t(b, kcol + kb * 16 * (Cfg::kLd * 2) + n * 16);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            mma_16816(dq[n + e], al, b + 2 * e);
+            mma_16816(dq[n + e], ah, b + 2 * e);
+            mma_16816(dk[n + e], cl, b + 2 * e);
+            mma_16816(dk[n + e], ch, b + 2 * e);
+          }
+        }
+      }
+      // transposed: rows of dk are columns of the matrices
+      const uint32_t mcol = base + Cfg::kOffM + ((l8 + (lane >> 4) * 8) * kGradLd + 16 * rb + k8) * 2;
+#pragma unroll 1
+      for (int kb = rb; kb < 4; ++kb) {
+        uint32_t ah[4], al[4], ch[4], cl[4];
+        const uint32_t o = mcol + kb * 16 * kGradLd * 2;
+        ldmatrix_x4_t(ah, o);
+        ldmatrix_x4_t(al, o + Cfg::kMat);
+        ldmatrix_x4_t(ch, o + 2 * Cfg::kMat);
+        ldmatrix_x4_t(cl, o + 3 * Cfg::kMat);
+#pragma unroll
+        for (int n = 0; n < kT; n += 2) {
+          uint32_t b[4], c[4];
+          ldmatrix_x4_t(b, qcol + kb * 16 * (Cfg::kLd * 2) + n * 16);
+          ldmatrix_x4_t(c, kcol + kb * 16 * (Cfg::kLd * 2) + n * 16);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            mma_16816(dk[n + e], al, b + 2 * e);
+            mma_16816(dk[n + e], ah, b + 2 * e);
+            mma_16816(dk[n + e], cl, c + 2 * e);
+            mma_16816(dk[n + e], ch, c + 2 * e);
+          }
+        }
+      }
+    }
+    // do S0^T, y S0^T, then U G'^T, 32 columns of the state (K dimension) at a time
+    const int r0 = 16 * rb + g4;
+    const uint32_t arow = (16 * rb + (lane & 15)) * (Cfg::kLd * 2) + (lane >> 4) * 16;
+    auto tile_b = [&](uint32_t* b, int p, int n, int ks) {   // rows (channels) of the tile: hi, lo
+      const int row = hf * (kD / 2) + 8 * n + l8, col = 16 * ks + k8 + (lane >> 4) * 32;
+      ldmatrix_x4(b, base + Cfg::kOffTile + (p % kGradRing) * Cfg::kTile + sw128(row, col));
+    };
+    {
+      float x[kT][4], y[kT][4];
+#pragma unroll
+      for (int n = 0; n < kT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[n][i] = y[n][i] = 0.f;
+#pragma unroll 1
+      for (int p = 0; p < kParts; ++p) {
+        if (p + 2 < 2 * kParts) load_tile(p + 2);
+        cp_async_commit();
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          uint32_t ad[4], yh[4], yl[4];
+          const uint32_t o = arow + (2 * p + ks) * 32;
+          ldmatrix_x4(ad, base + Cfg::kOffDo + o);
+          ldmatrix_x4(yh, base + Cfg::kOffY + o);
+          ldmatrix_x4(yl, base + Cfg::kOffY + Cfg::kRows + o);
+#pragma unroll
+          for (int n = 0; n < kT; ++n) {
+            uint32_t b[4];
+            tile_b(b, p, n, ks);
+            mma_16816(x[n], ad, b + 2);
+            mma_16816(x[n], ad, b);
+            mma_pair(y[n], yh, yl, b);
+          }
+        }
+        cp_async_wait<1>();
+        __syncthreads();   // the next tile has landed, and everyone is done with this one's neighbour
+      }
+      const float e0 = fac[kFacDecay + r0], e1 = fac[kFacDecay + r0 + 8];
+#pragma unroll
+      for (int n = 0; n < kT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float e = i < 2 ? e0 : e1;
+          dq[n][i] += a.scale * e * x[n][i];
+          dk[n][i] -= e * y[n][i];
+        }
+    }
+    {
+      float x[kT][4];
+#pragma unroll
+      for (int n = 0; n < kT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[n][i] = 0.f;
+#pragma unroll 1
+      for (int p = kParts; p < 2 * kParts; ++p) {
+        if (p + 2 < 2 * kParts) load_tile(p + 2);
+        cp_async_commit();
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          uint32_t uh[4], ul[4];
+          const uint32_t o = arow + (2 * (p - kParts) + ks) * 32;
+          ldmatrix_x4(uh, base + Cfg::kOffU + o);
+          ldmatrix_x4(ul, base + Cfg::kOffU + Cfg::kRows + o);
+#pragma unroll
+          for (int n = 0; n < kT; ++n) {
+            uint32_t b[4];
+            tile_b(b, p, n, ks);
+            mma_pair(x[n], uh, ul, b);
+          }
+        }
+        cp_async_wait<1>();
+        __syncthreads();
+      }
+      const float e0 = fac[kFacToEnd + r0], e1 = fac[kFacToEnd + r0 + 8];
+#pragma unroll
+      for (int n = 0; n < kT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dk[n][i] += (i < 2 ? e0 : e1) * x[n][i];
+    }
+    // q . dq of the heads so far
+    {
+      float d[2] = {0.f, 0.f};
+#pragma unroll
+      for (int n = 0; n < kT; ++n)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t qv = *reinterpret_cast<const uint32_t*>(
+              smem + Cfg::kOffQ + ((r0 + 8 * q) * Cfg::kLd + hf * (kD / 2) + 8 * n + t2) * 2);
+          d[q] += dq[n][2 * q] * __uint_as_float(qv << 16) + dq[n][2 * q + 1] * __uint_as_float(qv & 0xFFFF0000u);
+        }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        d[q] += __shfl_xor_sync(0xffffffffu, d[q], 1);
+        d[q] += __shfl_xor_sync(0xffffffffu, d[q], 2);
+        if ((lane & 3) == 0) qsum[hf * kChunk + r0 + 8 * q] = d[q];
+      }
+    }
+    __syncthreads();
+    if (tid < kChunk) {
+      const float now = qsum[tid] + qsum[kChunk + tid];
+      const float* rw = gr.rows + sh * kParts * 4 * kChunk + tid;   // [part][which][half][token]
+      float wd = 0.f, vd = 0.f, end = 0.f;
+      for (int p = 0; p < kParts; ++p, rw += 4 * kChunk) {
+        wd += rw[0] + rw[kChunk];
+        vd += rw[2 * kChunk] + rw[3 * kChunk];
+      }
+      for (int i = 0; i < kParts * 8; ++i) end += gr.ends[sh * kParts * 8 + i];
+      fac[tid] = tid < len ? (now - before) - vd : 0.f;
+      before = now;
+      if (tid < len) gr.dbeta[((long long)sq.entry * a.ntok + sq.first + n0 + tid) * a.Hv + h] = wd;
+      asm volatile("barrier.cta.sync 1, 64;" ::: "memory");
+      if (tid < len) {   // the sum from this token on
+        float x = end;
+        for (int i = len - 1; i >= tid; --i) x += fac[i];
+        gr.dg[((long long)sq.entry * a.ntok + sq.first + n0 + tid) * a.Hv + h] = x;
+      }
+    }
+    __syncthreads();
+  }
+
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int r = 16 * rb + g4 + 8 * q;
+    if (r < len) {
+      __nv_bfloat16* dqp = const_cast<__nv_bfloat16*>(delta_row(gr.dq, sq, n0 + r, hk)) + hf * (kD / 2) + t2;
+      __nv_bfloat16* dkp = const_cast<__nv_bfloat16*>(delta_row(gr.dk, sq, n0 + r, hk)) + hf * (kD / 2) + t2;
+#pragma unroll
+      for (int n = 0; n < kT; ++n) {
+        *reinterpret_cast<uint32_t*>(dqp + 8 * n) = pack_bf16(dq[n][2 * q], dq[n][2 * q + 1]);
+        *reinterpret_cast<uint32_t*>(dkp + 8 * n) = pack_bf16(dk[n][2 * q], dk[n][2 * q + 1]);
+      }
+    }
+  }
+}
+
+// zeros in the rows of a packed [token, head] fp32 array that no sequence has
+__global__ void __launch_bounds__(256) litela_delta_zero_gates(float* dg, float* db, const int* cu, int nseq, int ntok,
+                                                              int heads) {
+  const int b = min(max(cu[0], 0), ntok), e = min(max(cu[nseq], b), ntok);
+  const long long n = (long long)(b + ntok - e) * heads;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+    const long long o = i < (long long)b * heads ? i : i + (long long)(e - b) * heads;
+    dg[o] = db[o] = 0.f;
+  }
+}
+
+}  // namespace litela

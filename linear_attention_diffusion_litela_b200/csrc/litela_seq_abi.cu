@@ -11,6 +11,7 @@
 
 #include "../../include/litela.h"
 #include "litela_delta.cuh"
+#include "litela_delta_bwd.cuh"
 #include "litela_delta_chunk.cuh"
 #include "litela_host.h"
 #include "litela_norm.cuh"
@@ -360,6 +361,15 @@ litela_status delta_setup(int dev) {
   set(litela_delta_chain<64, 64, false>, ChainCfg<64, 64>::kSmemBytes);
   set(litela_delta_chain<128, 32, false>, ChainCfg<128, 32>::kSmemBytes);
   set(litela_delta_chain<128, 64, false>, ChainCfg<128, 64>::kSmemBytes);
+  set(litela_delta_chain<32, 32, true>, ChainCfg<32, 32>::kSmemBytes);
+  set(litela_delta_chain<64, 32, true>, ChainCfg<64, 32>::kSmemBytes);
+  set(litela_delta_chain<128, 32, true>, ChainCfg<128, 32>::kSmemBytes);
+  set(litela_delta_back<32>, BackCfg<32>::kSmemBytes);
+  set(litela_delta_back<64>, BackCfg<64>::kSmemBytes);
+  set(litela_delta_back<128>, BackCfg<128>::kSmemBytes);
+  set(litela_delta_grads<32>, GradCfg<32>::kSmemBytes);
+  set(litela_delta_grads<64>, GradCfg<64>::kSmemBytes);
+  set(litela_delta_grads<128>, GradCfg<128>::kSmemBytes);
   if (e != cudaSuccess) return host_cuda_fail(e, "cudaFuncSetAttribute(dynamic shared memory)");
   ready[dev] = true;
   return LITELA_OK;
@@ -401,36 +411,181 @@ litela_status launch_chunks(const DeltaArgs& d, int D, void* ws, int dev, int sm
   return e == cudaSuccess ? LITELA_OK : host_cuda_fail(e, "launch litela_delta_chain");
 }
 
-litela_status delta_fwd(const lite_la_delta_args* a, cudaStream_t st) {
+// bytes of a call's buffers per chunk slot and value head, and their places
+struct DeltaBytes {
+  size_t n;   // slots x value heads
+  size_t prep, states, rows, shares, ends;
+  explicit DeltaBytes(const DeltaArgs& d, int D) : DeltaBytes(d.nseq, d.ntok, d.Hv, D, d.cu != nullptr) {}
+  DeltaBytes(int B, int N, int Hv, int D, bool packed)
+      : n((size_t)delta_slots(B, N, packed) * Hv),
+        prep(up(n * kPrepBytes)),
+        states(up(n * D * D * 4)),
+        rows(up(n * kChunk * D * 4)),
+        shares(up(n * (D / 32) * 4 * kChunk * 4)),
+        ends(up(n * (D / 32) * 8 * 4)) {}
+  static size_t up(size_t x) { return (x + 255) / 256 * 256; }
+  size_t saved() const { return prep + states + rows; }
+  size_t back() const { return states + rows + shares + ends; }
+};
+
+bool delta_sizes_ok(int B, int N, int Hk, int Hv, int d) {
+  return B > 0 && N > 0 && Hk > 0 && Hv > 0 && (d == 32 || d == 64 || d == 128);
+}
+
+DeltaSaved delta_saved(const DeltaBytes& b, void* saved) {
+  uint8_t* p = static_cast<uint8_t*>(saved);
+  return DeltaSaved{p + b.prep, reinterpret_cast<float*>(p + b.prep + b.states)};
+}
+
+template <int kD>
+cudaError_t launch_save(const DeltaArgs& d, void* saved, int* err, cudaStream_t st) {
+  uint8_t* prep = static_cast<uint8_t*>(saved);
+  const cudaError_t e = launch_prep<kD>(d, prep, st);
+  if (e != cudaSuccess) return e;
+  return launch_chain<kD, 32, true>(d, prep, err, st, delta_saved(DeltaBytes(d, kD), saved));
+}
+
+template <int kD>
+cudaError_t launch_back(const DeltaArgs& d, const DeltaGrads& g, const void* saved, int* err, cudaStream_t st) {
+  const uint8_t* prep = static_cast<const uint8_t*>(saved);
+  const DeltaSaved kept = delta_saved(DeltaBytes(d, kD), const_cast<void*>(saved));
+  cudaError_t e = launch_seq(litela_delta_back<kD>, dim3((unsigned)((long long)d.nseq * d.Hv * (kD / 32))), kChainThreads,
+                             BackCfg<kD>::kSmemBytes, st, false, d, g, prep, kept, err);
+  if (e != cudaSuccess || d.ntok == 0) return e;
+  const long long slots = delta_slots(d.nseq, d.ntok, d.cu != nullptr);
+  return launch_seq(litela_delta_grads<kD>, dim3((unsigned)(slots * d.Hk)), kGradThreads, GradCfg<kD>::kSmemBytes, st, true,
+                    d, g, prep, kept);
+}
+
+// a call's workspace or kept data: present, aligned and clear of the call's other buffers
+litela_status buffer_check(const lite_la_delta_args* a, const void* p, size_t bytes, size_t need, const DeltaSpans& in,
+                           const Span& out, const char* missing, const char* overlap) {
+  if (need > 0 && (p == nullptr || bytes < need || !aligned(p, 16))) return invalid(missing);
+  const Span w = span(p, need);
+  const size_t states = (size_t)a->B * a->Hv * a->d * a->d * 4;
+  if (meet(w, out) || in.hit(w) || meet(w, span(a->state_in, states)) || meet(w, span(a->state_out, states)))
+    return invalid(overlap);
+  if (delta_slots(a->B, a->N, a->cu_seqlens != nullptr) * (double)a->Hv > 2147483647.0)
+    return invalid("too many chunks and heads");
+  return LITELA_OK;
+}
+
+litela_status zero_tail(const lite_la_delta_args* a, const lite_la_view& v, int heads, int sms, cudaStream_t st) {
+  const cudaError_t e = launch_seq(litela_delta_zero_tail, dim3(sms), 256, 0, st, false, view_of(v), a->cu_seqlens, a->B,
+                                   a->N, heads, a->d);
+  return e == cudaSuccess ? LITELA_OK : host_cuda_fail(e, "launch litela_delta_zero_tail");
+}
+
+litela_status delta_fwd(const lite_la_delta_args* a, bool save, void* saved, size_t saved_bytes, cudaStream_t st) {
   DeltaSpans in;
   Span out;
   bool empty;
   litela_status s = delta_validate(a, true, &in, &out, &empty);
   if (s != LITELA_OK || empty) return s;
   if ((s = state_check(a, (size_t)a->B * a->Hv * a->d * a->d * 4, in, out)) != LITELA_OK) return s;
-  const bool recurs = delta_recurs(a->N);
-  if (!recurs) {
-    const size_t need = lite_la_gated_delta_workspace_bytes(a->B, a->N, a->Hk, a->Hv, a->d, a->cu_seqlens != nullptr);
-    const Span w = span(a->workspace, a->workspace_bytes);
-    if (a->workspace == nullptr || a->workspace_bytes < need || !aligned(a->workspace, 16))
-      return invalid("workspace missing, too small or misaligned");
-    const size_t states = (size_t)a->B * a->Hv * a->d * a->d * 4;
-    if (meet(w, out) || in.hit(w) || meet(w, span(a->state_in, states)) || meet(w, span(a->state_out, states)))
-      return invalid("the workspace overlaps a buffer of the call");
-    if (delta_slots(a->B, a->N, a->cu_seqlens != nullptr) * (double)a->Hv > 2147483647.0)
-      return invalid("too many chunks and heads");
+  const bool recurs = !save && delta_recurs(a->N);
+  const DeltaBytes bytes(a->B, a->N, a->Hv, a->d, a->cu_seqlens != nullptr);
+  if (save) {
+    if (a->state_out == nullptr) return invalid("a training step's forward needs state_out");
+    s = buffer_check(a, saved, saved_bytes, bytes.saved(), in, out, "saved missing, too small or misaligned",
+                     "saved overlaps a buffer of the call");
+  } else if (!recurs) {
+    s = buffer_check(a, a->workspace, a->workspace_bytes, bytes.prep, in, out, "workspace missing, too small or misaligned",
+                     "the workspace overlaps a buffer of the call");
   }
+  if (s != LITELA_OK) return s;
   int dev, sms;
   if ((s = host_device(&dev, &sms)) != LITELA_OK) return s;
   const DeltaArgs d = delta_args(a);
-  if (a->zero_tail && a->cu_seqlens != nullptr && a->N > 0) {
-    const cudaError_t e = launch_seq(litela_delta_zero_tail, dim3(sms), 256, 0, st, false, d.out, d.cu, d.nseq, d.ntok,
-                                     a->Hv, a->d);
-    if (e != cudaSuccess) return host_cuda_fail(e, "launch litela_delta_zero_tail");
+  if (a->zero_tail && a->cu_seqlens != nullptr && a->N > 0 && (s = zero_tail(a, a->out, a->Hv, sms, st)) != LITELA_OK)
+    return s;
+  if (save) {
+    if ((s = delta_setup(dev)) != LITELA_OK) return s;
+    if (d.ntok == 0) {
+      s = launch_recur(d, a->d, st);   // the states alone
+    } else {
+      int* err = delta_error_word(dev);
+      const cudaError_t e = a->d == 32   ? launch_save<32>(d, saved, err, st)
+                            : a->d == 64 ? launch_save<64>(d, saved, err, st)
+                                         : launch_save<128>(d, saved, err, st);
+      if (e != cudaSuccess) return host_cuda_fail(e, "launch the forward of a training step");
+    }
+  } else {
+    s = recurs ? launch_recur(d, a->d, st) : launch_chunks(d, a->d, a->workspace, dev, sms, st);
   }
-  s = recurs ? launch_recur(d, a->d, st) : launch_chunks(d, a->d, a->workspace, dev, sms, st);
   if (s == LITELA_OK) host_ok();
   return s;
+}
+
+litela_status delta_bwd(const lite_la_delta_args* a, const lite_la_delta_grads* g, const void* saved, size_t saved_bytes,
+                        cudaStream_t st) {
+  if (g == nullptr) return invalid("null grads");
+  DeltaSpans in;
+  Span out, sp[3];
+  bool empty;
+  litela_status s = delta_validate(a, false, &in, &out, &empty);
+  if (s != LITELA_OK || empty) return s;
+  const int entries = a->cu_seqlens != nullptr ? 1 : a->B;
+  Span dout;
+  if ((s = view_check(g->dout, entries, a->N, a->Hv, a->d, false, &dout)) != LITELA_OK) return s;
+  in.add(dout);
+  if ((s = view_check(g->dq, entries, a->N, a->Hk, a->d, true, &sp[0])) != LITELA_OK ||
+      (s = view_check(g->dk, entries, a->N, a->Hk, a->d, true, &sp[1])) != LITELA_OK ||
+      (s = view_check(g->dv, entries, a->N, a->Hv, a->d, true, &sp[2])) != LITELA_OK)
+    return s;
+  if (a->N > 0 && (g->dg == nullptr || g->dbeta == nullptr)) return invalid("null dg or dbeta");
+  if (!aligned(g->dg, 4) || !aligned(g->dbeta, 4)) return invalid("dg and dbeta must be 4-byte aligned");
+  if (!aligned(g->dstate_out, 16) || !aligned(g->dstate_in, 16) || !aligned(g->state_out, 16))
+    return invalid("states and their gradients must be 16-byte aligned");
+  if (g->dstate_out != nullptr && g->state_out == nullptr) return invalid("dstate_out needs the forward's state_out");
+  const DeltaBytes bytes(a->B, a->N, a->Hv, a->d, a->cu_seqlens != nullptr);
+  const size_t states = (size_t)a->B * a->Hv * a->d * a->d * 4, gates = (size_t)entries * a->N * a->Hv * 4;
+  if ((s = buffer_check(a, saved, saved_bytes, a->N > 0 ? bytes.saved() : 0, in, Span{}, "saved missing, too small or misaligned",
+                        "saved overlaps a buffer of the call")) != LITELA_OK ||
+      (s = buffer_check(a, a->workspace, a->workspace_bytes, a->N > 0 ? bytes.back() : 0, in, Span{},
+                        "workspace missing, too small or misaligned", "the workspace overlaps a buffer of the call")) !=
+          LITELA_OK)
+    return s;
+  in.add(span(saved, a->N > 0 ? bytes.saved() : 0));
+  const Span ins[2] = {span(g->dstate_out, states), span(g->state_out, states)};
+  // dq, dk, dv may be views of one buffer between one another's rows: only their spans against inputs
+  // and the dense outputs are checked
+  const Span outs[7] = {sp[0], sp[1], sp[2], span(g->dg, gates), span(g->dbeta, gates), span(g->dstate_in, states),
+                        span(a->workspace, a->N > 0 ? bytes.back() : 0)};
+  for (int i = 0; i < 7; ++i) {
+    if (in.hit(outs[i]) || (i != 5 && meet(outs[i], ins[0])) || meet(outs[i], ins[1])) return invalid("an output overlaps an input");
+    for (int j = i + 1; j < 7; ++j)
+      if (j > 2 && meet(outs[i], outs[j])) return invalid("outputs overlap");
+  }
+  if (g->dstate_in != nullptr && g->dstate_in != g->dstate_out && meet(outs[5], ins[0]))
+    return invalid("dstate_in overlaps dstate_out in part");
+  int dev, sms;
+  if ((s = host_device(&dev, &sms)) != LITELA_OK || (s = delta_setup(dev)) != LITELA_OK) return s;
+  if (a->cu_seqlens != nullptr && a->N > 0) {
+    if ((s = zero_tail(a, g->dq, a->Hk, sms, st)) != LITELA_OK || (s = zero_tail(a, g->dk, a->Hk, sms, st)) != LITELA_OK ||
+        (s = zero_tail(a, g->dv, a->Hv, sms, st)) != LITELA_OK)
+      return s;
+    const cudaError_t e = launch_seq(litela_delta_zero_gates, dim3(sms), 256, 0, st, false, g->dg, g->dbeta, a->cu_seqlens, a->B,
+                                     a->N, a->Hv);
+    if (e != cudaSuccess) return host_cuda_fail(e, "launch litela_delta_zero_gates");
+  }
+  DeltaArgs d = delta_args(a);
+  DeltaGrads gr{};
+  gr.dout = view_of(g->dout), gr.dq = view_of(g->dq), gr.dk = view_of(g->dk), gr.dv = view_of(g->dv);
+  gr.dg = g->dg, gr.dbeta = g->dbeta;
+  gr.dstate_out = g->dstate_out, gr.state_out = g->state_out, gr.dstate_in = g->dstate_in;
+  uint8_t* ws = static_cast<uint8_t*>(a->workspace);
+  gr.gstates = ws;
+  gr.y = reinterpret_cast<float*>(ws + bytes.states);
+  gr.rows = reinterpret_cast<float*>(ws + bytes.states + bytes.rows);
+  gr.ends = reinterpret_cast<float*>(ws + bytes.states + bytes.rows + bytes.shares);
+  int* err = delta_error_word(dev);
+  const cudaError_t e = a->d == 32   ? launch_back<32>(d, gr, saved, err, st)
+                        : a->d == 64 ? launch_back<64>(d, gr, saved, err, st)
+                                     : launch_back<128>(d, gr, saved, err, st);
+  if (e != cudaSuccess) return host_cuda_fail(e, "launch the gated delta rule's gradient");
+  host_ok();
+  return LITELA_OK;
 }
 
 litela_status delta_step(const lite_la_delta_args* a, const int* slots, int pool, cudaStream_t st) {
@@ -503,12 +658,30 @@ size_t lite_la_qk_norm_rope_workspace_bytes(int d) {
 }
 
 litela_status lite_la_gated_delta_fwd(const lite_la_delta_args* args, cudaStream_t stream) {
-  return litela::guarded([&] { return litela::delta_fwd(args, stream); });
+  return litela::guarded([&] { return litela::delta_fwd(args, false, nullptr, 0, stream); });
 }
 
 size_t lite_la_gated_delta_workspace_bytes(int B, int N, int Hk, int Hv, int d, int packed) {
-  if (B <= 0 || N <= 0 || Hk <= 0 || Hv <= 0 || (d != 32 && d != 64 && d != 128) || litela::delta_recurs(N)) return 0;
-  return (size_t)litela::delta_slots(B, N, packed != 0) * Hv * litela::kPrepBytes;
+  if (!litela::delta_sizes_ok(B, N, Hk, Hv, d) || litela::delta_recurs(N)) return 0;
+  return litela::DeltaBytes(B, N, Hv, d, packed != 0).prep;
+}
+
+litela_status lite_la_gated_delta_fwd_save(const lite_la_delta_args* args, void* saved, size_t saved_bytes,
+                                           cudaStream_t stream) {
+  return litela::guarded([&] { return litela::delta_fwd(args, true, saved, saved_bytes, stream); });
+}
+
+size_t lite_la_gated_delta_saved_bytes(int B, int N, int Hk, int Hv, int d, int packed) {
+  return litela::delta_sizes_ok(B, N, Hk, Hv, d) ? litela::DeltaBytes(B, N, Hv, d, packed != 0).saved() : 0;
+}
+
+litela_status lite_la_gated_delta_bwd(const lite_la_delta_args* args, const lite_la_delta_grads* grads,
+                                      const void* saved, size_t saved_bytes, cudaStream_t stream) {
+  return litela::guarded([&] { return litela::delta_bwd(args, grads, saved, saved_bytes, stream); });
+}
+
+size_t lite_la_gated_delta_bwd_workspace_bytes(int B, int N, int Hk, int Hv, int d, int packed) {
+  return litela::delta_sizes_ok(B, N, Hk, Hv, d) ? litela::DeltaBytes(B, N, Hv, d, packed != 0).back() : 0;
 }
 
 litela_status lite_la_gated_delta_step(const lite_la_delta_args* args, const int* state_indices, int pool,

@@ -31,6 +31,12 @@ class DeltaArgs(ctypes.Structure):
                 ("zero_tail", _c_int), ("workspace", _vp), ("workspace_bytes", _c_size)]
 
 
+class DeltaGrads(ctypes.Structure):
+    """lite_la_delta_grads"""
+    _fields_ = [("dout", View), ("dq", View), ("dk", View), ("dv", View), ("dg", _vp), ("dbeta", _vp),
+                ("dstate_out", _vp), ("state_out", _vp), ("dstate_in", _vp)]
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -129,6 +135,8 @@ def _norm_function():
     if "norm" not in _FUNCTIONS:
         torch = _torch()
 
+        from torch.autograd.function import once_differentiable
+
         class QKNormRope(torch.autograd.Function):
             @staticmethod
             def forward(ctx, qkv, q_weight, k_weight, cos, sin, positions, kw):
@@ -138,6 +146,7 @@ def _norm_function():
                                                 positions=positions, **kw)
 
             @staticmethod
+            @once_differentiable
             def backward(ctx, grad):
                 qkv, q_weight, k_weight, cos, sin, positions = ctx.saved_tensors
                 if grad.dtype != torch.bfloat16 or not grad.is_contiguous():
@@ -215,15 +224,7 @@ def _delta_args(q, k, v, g, beta, scale, cu_seqlens):
     return a, int(a.B)
 
 
-def lite_la_gated_delta_fwd(q, k, v, g, beta, state_in=None, state_out=None, cu_seqlens=None, scale=None, out=None,
-                            stream=None):
-    """The gated delta rule over whole sequences.  q, k: bf16 [B, N, Hk, d], v: bf16 [B, N, Hv, d]
-    (any strides with adjacent channels, so views of packed rows do); g (log decay), beta: fp32
-    [B, N, Hv].  state_in: fp32 [sequences, Hv, d, d] or None (zeros); state_out is allocated when
-    None and may be state_in.  cu_seqlens (int32 [sequences + 1], on the device) packs sequences
-    of different lengths into one buffer (B = 1).  scale defaults to d ** -0.5.  Returns (out bf16
-    [B, N, Hv, d], state_out); rows behind the last packed sequence are left as they are in `out`
-    (zeros when it is allocated here)."""
+def _delta_forward(q, k, v, g, beta, state_in, state_out, cu_seqlens, scale, out, stream, save):
     torch = _torch()
     a, S = _delta_args(q, k, v, g, beta, scale, cu_seqlens)
     d, Hv, device = int(a.d), int(a.Hv), q.device
@@ -236,13 +237,124 @@ def lite_la_gated_delta_fwd(q, k, v, g, beta, state_in=None, state_out=None, cu_
         out = torch.empty(v.shape, dtype=torch.bfloat16, device=device)
         a.zero_tail = 1
     a.out = _view(out, "out", tuple(v.shape), device)
-    ws = torch.empty(int(lib().lite_la_gated_delta_workspace_bytes(a.B, a.N, a.Hk, Hv, d, int(cu_seqlens is not None))),
+    size = lib().lite_la_gated_delta_saved_bytes if save else lib().lite_la_gated_delta_workspace_bytes
+    buf = torch.empty(int(size(a.B, a.N, a.Hk, Hv, d, int(cu_seqlens is not None))), dtype=torch.uint8, device=device)
+    _on_stream(buf, stream)
+    with torch.cuda.device(device):
+        if save:
+            _check(lib().lite_la_gated_delta_fwd_save(ctypes.byref(a), buf.data_ptr(), buf.numel(),
+                                                      _stream_handle(stream, device)))
+        else:
+            a.workspace, a.workspace_bytes = buf.data_ptr(), buf.numel()
+            _check(lib().lite_la_gated_delta_fwd(ctypes.byref(a), _stream_handle(stream, device)))
+    return out, state_out, buf
+
+
+def lite_la_gated_delta_fwd(q, k, v, g, beta, state_in=None, state_out=None, cu_seqlens=None, scale=None, out=None,
+                            stream=None):
+    """The gated delta rule over whole sequences.  q, k: bf16 [B, N, Hk, d], v: bf16 [B, N, Hv, d]
+    (any strides with adjacent channels, so views of packed rows do); g (log decay), beta: fp32
+    [B, N, Hv].  state_in: fp32 [sequences, Hv, d, d] or None (zeros); state_out is allocated when
+    None and may be state_in.  cu_seqlens (int32 [sequences + 1], on the device) packs sequences
+    of different lengths into one buffer (B = 1).  scale defaults to d ** -0.5.  Returns (out bf16
+    [B, N, Hv, d], state_out); rows behind the last packed sequence are left as they are in `out`
+    (zeros when it is allocated here)."""
+    return _delta_forward(q, k, v, g, beta, state_in, state_out, cu_seqlens, scale, out, stream, False)[:2]
+
+
+def lite_la_gated_delta_fwd_save(q, k, v, g, beta, state_in=None, state_out=None, cu_seqlens=None, scale=None,
+                                 out=None, stream=None):
+    """lite_la_gated_delta_fwd that also returns what lite_la_gated_delta_bwd needs: (out, state_out,
+    saved)."""
+    return _delta_forward(q, k, v, g, beta, state_in, state_out, cu_seqlens, scale, out, stream, True)
+
+
+def lite_la_gated_delta_bwd(q, k, v, g, beta, dout, saved, state_out=None, dstate_out=None, state_in=None,
+                            cu_seqlens=None, scale=None, stream=None):
+    """Gradients of sum(dout * out) + sum(dstate_out * state_out) for the forward that left `saved`
+    (lite_la_gated_delta_fwd_save with the same arguments) and wrote state_out: (dq, dk, dv bf16, dg,
+    dbeta fp32, dstate_in fp32 or None without state_in)."""
+    torch = _torch()
+    a, S = _delta_args(q, k, v, g, beta, scale, cu_seqlens)
+    d, Hv, device = int(a.d), int(a.Hv), q.device
+    gr = DeltaGrads()
+    gr.dout = _view(dout, "dout", tuple(v.shape), device)
+    if not isinstance(saved, torch.Tensor) or saved.dtype != torch.uint8 or not saved.is_contiguous() \
+            or saved.device != device:
+        raise TypeError("saved must be what lite_la_gated_delta_fwd_save returned")
+    shape = (S, Hv, d, d)
+    dstate_in = None
+    if state_in is not None:
+        a.state_in = _states(state_in, "state_in", shape, device)
+        dstate_in = torch.empty(shape, dtype=torch.float32, device=device)
+        gr.dstate_in = dstate_in.data_ptr()
+    if dstate_out is not None:
+        gr.dstate_out = _states(dstate_out, "dstate_out", shape, device)
+        gr.state_out = _states(state_out, "state_out", shape, device)
+    dq, dk, dv = (torch.empty(t.shape, dtype=torch.bfloat16, device=device) for t in (q, k, v))
+    dg, dbeta = (torch.empty(g.shape, dtype=torch.float32, device=device) for _ in range(2))
+    gr.dq, gr.dk = _view(dq, "dq", tuple(q.shape), device), _view(dk, "dk", tuple(q.shape), device)
+    gr.dv = _view(dv, "dv", tuple(v.shape), device)
+    gr.dg, gr.dbeta = dg.data_ptr(), dbeta.data_ptr()
+    ws = torch.empty(int(lib().lite_la_gated_delta_bwd_workspace_bytes(a.B, a.N, a.Hk, Hv, d,
+                                                                       int(cu_seqlens is not None))),
                      dtype=torch.uint8, device=device)
     _on_stream(ws, stream)
     a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
     with torch.cuda.device(device):
-        _check(lib().lite_la_gated_delta_fwd(ctypes.byref(a), _stream_handle(stream, device)))
-    return out, state_out
+        _check(lib().lite_la_gated_delta_bwd(ctypes.byref(a), ctypes.byref(gr), saved.data_ptr(), saved.numel(),
+                                             _stream_handle(stream, device)))
+    return dq, dk, dv, dg, dbeta, dstate_in
+
+
+def _delta_function():
+    if "delta" not in _FUNCTIONS:
+        torch = _torch()
+        from torch.autograd.function import once_differentiable
+
+        class GatedDelta(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, q, k, v, g, beta, state_in, cu_seqlens, scale):
+                ctx.set_materialize_grads(False)
+                out, state_out, saved = lite_la_gated_delta_fwd_save(q, k, v, g, beta, state_in=state_in,
+                                                                     cu_seqlens=cu_seqlens, scale=scale)
+                ctx.save_for_backward(q, k, v, g, beta, state_in, cu_seqlens, state_out, saved)
+                ctx.scale = scale
+                return out, state_out
+
+            @staticmethod
+            @once_differentiable
+            def backward(ctx, dout, dstate):
+                q, k, v, g, beta, state_in, cu_seqlens, state_out, saved = ctx.saved_tensors
+                if dout is None:
+                    dout = torch.zeros_like(v, memory_format=torch.contiguous_format)
+                dout = dout.to(torch.bfloat16)
+                try:
+                    _view(dout, "dout", tuple(v.shape), q.device)
+                    strides_ok = dout.data_ptr() % 16 == 0 and all(x % 8 == 0 for x in dout.stride()[:3])
+                except TypeError:
+                    strides_ok = False
+                if not strides_ok:
+                    dout = dout.contiguous()
+                if dstate is not None:
+                    dstate = dstate.float().contiguous()
+                grads = lite_la_gated_delta_bwd(q, k, v, g, beta, dout, saved, state_out=state_out, dstate_out=dstate,
+                                                state_in=state_in, cu_seqlens=cu_seqlens, scale=ctx.scale)
+                return (*grads, None, None)
+
+        _FUNCTIONS["delta"] = GatedDelta
+    return _FUNCTIONS["delta"]
+
+
+def lite_la_gated_delta(q, k, v, g, beta, state_in=None, cu_seqlens=None, scale=None):
+    """lite_la_gated_delta_fwd that torch autograd can differentiate: returns (out, state_out) with
+    gradients for q, k, v, g, beta and state_in.  The forward keeps its states (one per 64 tokens) for
+    the backward; where no gradient is wanted it does not."""
+    torch = _torch()
+    if not torch.is_grad_enabled() or not any(isinstance(t, torch.Tensor) and t.requires_grad
+                                              for t in (q, k, v, g, beta, state_in)):
+        return lite_la_gated_delta_fwd(q, k, v, g, beta, state_in=state_in, cu_seqlens=cu_seqlens, scale=scale)
+    return _delta_function().apply(q, k, v, g, beta, state_in, cu_seqlens, scale)
 
 
 def lite_la_gated_delta_step(q, k, v, g, beta, states, state_indices=None, scale=None, out=None, stream=None):

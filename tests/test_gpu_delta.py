@@ -315,3 +315,173 @@ def test_empty():
     e = [x[:0] for x in (t["q"], t["k"], t["v"], t["g"], t["beta"])]
     out, state = ll.lite_la_gated_delta_fwd(*e)
     assert out.shape[0] == 0 and state.shape[0] == 0
+
+
+# ---------------------------------------------------------------------------------------
+# gradients
+
+
+def leaves(t):
+    names = ["q", "k", "v", "g", "beta"] + (["state_in"] if t["state_in"] is not None else [])
+    return names, [t[n].detach().clone().requires_grad_() for n in names]
+
+
+def autograd(t, with_state=True):
+    names, x = leaves(t)
+    kw = dict(zip(names, x))
+    out, state = ll.lite_la_gated_delta(*(kw[n] for n in ("q", "k", "v", "g", "beta")), state_in=kw.get("state_in"),
+                                        cu_seqlens=t["cu"])
+    if with_state:
+        grads = torch.autograd.grad((out, state), x, (t["dout"], t["dstate"]))
+    else:
+        grads = torch.autograd.grad(out, x, t["dout"])
+    return out, state, dict(zip(names, grads))
+
+
+def check_grads(t, out, state, grads, with_state=True):
+    ll.lite_la_device_status()
+    if not with_state:
+        t = dict(t, dstate=torch.zeros_like(t["dstate"]))
+    for i, e, sl, (o, S, (dq, dk, dv, dg, db, dS)) in ref(t, grads=True):
+        assert close16(out[e, sl], o) and close32(state[i], S), "forward of sequence %d" % i
+        for n, want in (("q", dq), ("k", dk), ("v", dv)):
+            assert close16(grads[n][e, sl], want), "d%s of sequence %d" % (n, i)
+        # dg_t = <S, G> at the chunk's end + the sum from t on of (q . dq - v . dv): where the true value
+        # is small (0 for a first token without a state) these sums cancel.  Each of their terms is off by
+        # at most F32 of the sum of its absolute products, and so is the difference: the largest such sum of
+        # a head is the measure, not dg.
+        terms = [np.abs(np64(t["v"][e, sl]) * dv).sum(-1),
+                 np.abs(np.repeat(np64(t["q"][e, sl]) * dq, dv.shape[1] // dq.shape[1], 1)).sum(-1)]
+        bound = 4 * F32 * (np.maximum(*terms).max(0, initial=0.0) + np.abs(dg).max(0, initial=0.0)) + 1e-30
+        assert (np.abs(np64(grads["g"][e, sl]) - dg) <= bound).all(), "dg of sequence %d" % i
+        assert close32(grads["beta"][e, sl].T, db.T, 2), "dbeta of sequence %d" % i
+        if "state_in" in grads:
+            assert close32(grads["state_in"][i], dS, 2), "dstate of sequence %d" % i
+
+
+@pytest.mark.parametrize("lens,packed,Hk,Hv,d,carry", SHAPES)
+def test_gradients(lens, packed, Hk, Hv, d, carry):
+    t = make(lens, packed, Hk, Hv, d, carry, seed=sum(lens) + d)
+    check_grads(t, *autograd(t))
+    check_grads(t, *autograd(t, False), with_state=False)
+
+
+@pytest.mark.parametrize("lens,packed,Hk,Hv,d,carry", [([70, 20], True, 1, 2, 64, True), ([150], False, 1, 1, 128, True)])
+@pytest.mark.parametrize("case", ["strong decay", "resets", "no decay", "no write", "full write"])
+def test_gradients_at_the_ends_of_the_gates(lens, packed, Hk, Hv, d, carry, case):
+    t = make(lens, packed, Hk, Hv, d, carry, seed=5)
+    if case == "strong decay":
+        t["g"] = t["g"] - 30
+    elif case == "resets":
+        t["g"][:, ::7] = -float("inf")
+    elif case == "no decay":
+        t["g"] = torch.zeros_like(t["g"])
+    elif case == "no write":
+        t["beta"] = torch.zeros_like(t["beta"])
+    else:
+        t["beta"] = torch.ones_like(t["beta"])
+    with np.errstate(under="ignore"):
+        check_grads(t, *autograd(t))
+
+
+def test_gradient_against_differences():
+    """Central differences of the kernels' own forward in the gates and the values: out and state are
+    linear in v exactly; in g and beta the step leaves a relative 1e-3."""
+    t = make([130], False, 1, 2, 64, True, seed=3)
+    _, _, grads = autograd(t)
+
+    def loss(**kw):
+        u = dict(t, **kw)
+        out, state = fwd(u)
+        # out's bf16 rounding is random: its share of the loss averages over 16640 values
+        return (out.double() * t["dout"].double()).sum() + (state.double() * t["dstate"].double()).sum()
+
+    rng = torch.Generator(device="cuda").manual_seed(9)
+    for n, step in (("g", 0.05), ("beta", 0.05), ("state_in", 0.5)):
+        dirn = torch.randn(t[n].shape, generator=rng, device="cuda")
+        num = (loss(**{n: t[n] + step * dirn}) - loss(**{n: t[n] - step * dirn})) / (2 * step)
+        ana = (grads[n].double() * dirn.double()).sum()
+        # rounding of out: 2^-9 typical, |out dout| summed as random signs, over the step
+        out = fwd(t)[0].double()
+        noise = 2.0 ** -9 * float((out * t["dout"].double()).norm()) / step
+        curve = 0.01 * float((grads[n].double() * dirn.double()).norm())
+        assert abs(float(num - ana)) <= 6 * noise + 5 * curve + 0.01 * abs(float(ana)), (n, float(num), float(ana))
+
+
+def test_gradient_of_shared_and_strided_inputs():
+    """Packed rows as the leaf: views of it go in, one gradient comes back; broadcast keys too."""
+    B, N, Hk, Hv, d = 2, 100, 2, 4, 64
+    t = make([N] * B, False, Hk, Hv, d, False)
+    want = autograd(t)[2]
+    row = torch.cat([t[n].flatten(2) for n in ("q", "k", "v")], -1).requires_grad_()
+    h = row.view(B, N, -1, d)
+    out, state = ll.lite_la_gated_delta(h[:, :, :Hk], h[:, :, Hk:2 * Hk], h[:, :, 2 * Hk:], t["g"], t["beta"])
+    got, = torch.autograd.grad((out, state), row, (t["dout"], t["dstate"]))
+    assert torch.equal(got, torch.cat([want[n].flatten(2) for n in ("q", "k", "v")], -1))
+    # one key head expanded over two
+    k1 = t["k"][:, :, :1].clone().requires_grad_()
+    u = dict(t, k=k1.detach().expand(B, N, Hk, d).contiguous())
+    out, state = ll.lite_la_gated_delta(t["q"], k1.expand(B, N, Hk, d), t["v"], t["g"], t["beta"])
+    got, = torch.autograd.grad((out, state), k1, (t["dout"], t["dstate"]))
+    assert torch.equal(got, autograd(u)[2]["k"].sum(2, keepdim=True))
+    # an incoming gradient with heads before tokens, and one of fp32
+    out, state = ll.lite_la_gated_delta(*(x.requires_grad_() for x in (t["q"], t["k"], t["v"])), t["g"], t["beta"])
+    by_head = t["dout"].transpose(1, 2).contiguous().transpose(1, 2)
+    got = torch.autograd.grad((out, state), t["q"], (by_head, t["dstate"]))[0]
+    assert torch.equal(got, want["q"])
+
+
+def test_gradient_rows_of_no_sequence():
+    t = make([90, 41], True, 1, 2, 64, True)
+    want = autograd(t)[2]
+    for n in ("q", "k", "v", "g", "beta", "dout"):
+        t[n] = torch.cat([t[n], torch.full_like(t[n][:, :40], float("nan"))], 1)
+    got = autograd(t)[2]
+    for n in want:
+        if n != "state_in":
+            assert torch.equal(got[n][:, :131], want[n]) and not got[n][:, 131:].any(), n
+        else:
+            assert torch.equal(got[n], want[n])
+
+
+def test_gradient_streams_graphs_and_equal_bits():
+    t = make([150, 70], True, 1, 2, 64, True)
+    _, _, want = autograd(t)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = autograd(t)[2]
+    torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(got[n], want[n]) for n in want)
+    args = [t[n] for n in ("q", "k", "v", "g", "beta")]
+    out, state, saved = ll.lite_la_gated_delta_fwd_save(*args, state_in=t["state_in"], cu_seqlens=t["cu"], stream=s)
+    got = ll.lite_la_gated_delta_bwd(*args, t["dout"], saved, state_out=state, dstate_out=t["dstate"],
+                                     state_in=t["state_in"], cu_seqlens=t["cu"], stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(a, want[n]) for a, n in zip(got, ("q", "k", "v", "g", "beta", "state_in")))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, state, saved = ll.lite_la_gated_delta_fwd_save(*args, state_in=t["state_in"], cu_seqlens=t["cu"])
+        got = ll.lite_la_gated_delta_bwd(*args, t["dout"], saved, state_out=state, dstate_out=t["dstate"],
+                                         state_in=t["state_in"], cu_seqlens=t["cu"])
+    for _ in range(2):
+        for x in got:
+            x.zero_()
+        graph.replay()
+        assert all(torch.equal(a, want[n]) for a, n in zip(got, ("q", "k", "v", "g", "beta", "state_in")))
+
+
+def test_no_gradient_wanted():
+    t = make([100], False, 1, 1, 32, False)
+    want, want_s = fwd(t)
+    x = [t[n].clone().requires_grad_() for n in ("q", "k", "v", "g", "beta")]
+    with torch.no_grad():
+        out, s = ll.lite_la_gated_delta(*x)
+    assert torch.equal(out, want) and not out.requires_grad
+    out, s = ll.lite_la_gated_delta(*x)
+    assert torch.equal(out, want) and torch.equal(s, want_s) and out.requires_grad
+    g = torch.autograd.grad(s, x[1], torch.ones_like(s))[0]     # the state alone is used
+    assert torch.isfinite(g).all() and g.any()
+    with pytest.raises(RuntimeError):
+        y = torch.autograd.grad(out.float().sum(), x[0], create_graph=True)[0]
+        torch.autograd.grad(y.float().sum(), x[1])
