@@ -9,71 +9,81 @@ the package:
 """
 from __future__ import annotations
 
-import ctypes
+import struct
 
-from . import _check, _stream_handle, _torch, lib
+from . import _check, _torch, lib
 
-_vp, _c_int, _c_float, _c_size, _c_ll = (ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t,
-                                         ctypes.c_longlong)
-
-
-class View(ctypes.Structure):
-    """lite_la_view"""
-    _fields_ = [("data", _vp), ("batch_stride", _c_ll), ("token_stride", _c_ll), ("head_stride", _c_ll)]
-
-
-class DeltaArgs(ctypes.Structure):
-    """lite_la_delta_args"""
-    _fields_ = [("q", View), ("k", View), ("v", View), ("out", View), ("g", _vp), ("beta", _vp),
-                ("g_batch_stride", _c_ll), ("g_token_stride", _c_ll), ("beta_batch_stride", _c_ll),
-                ("beta_token_stride", _c_ll), ("state_in", _vp), ("state_out", _vp), ("cu_seqlens", _vp),
-                ("B", _c_int), ("N", _c_int), ("Hk", _c_int), ("Hv", _c_int), ("d", _c_int), ("scale", _c_float),
-                ("zero_tail", _c_int), ("workspace", _vp), ("workspace_bytes", _c_size)]
-
-
-class DeltaGrads(ctypes.Structure):
-    """lite_la_delta_grads"""
-    _fields_ = [("dout", View), ("dq", View), ("dk", View), ("dv", View), ("dg", _vp), ("dbeta", _vp),
-                ("dstate_out", _vp), ("state_out", _vp), ("dstate_in", _vp)]
+# The argument structs of include/litela.h, packed in one go: a ctypes.Structure filled field by field
+# took longer than the kernel of a one-token call.  A view is (pointer, batch, token, head stride).
+_VIEW = "Pqqq"
+_DELTA_ARGS = struct.Struct("@" + 4 * _VIEW + "PPqqqqPPPiiiiifiPN")    # lite_la_delta_args
+_DELTA_GRADS = struct.Struct("@" + 4 * _VIEW + "PPPPP")                 # lite_la_delta_grads
+_NO_VIEW = (0, 0, 0, 0)
 
 
 def _ptr(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
+
+
+def _call(fn, dev, stream, *args):
+    """fn(*args, stream) on device `dev`; stream None: torch's current one there."""
+    cuda = _torch().cuda
+    handle = (cuda.current_stream(dev) if stream is None else stream).cuda_stream
+    if cuda.current_device() == dev:
+        _check(fn(*args, handle))
+    else:
+        with cuda.device(dev):
+            _check(fn(*args, handle))
+
+
+def _on_stream(t, stream):
+    """A buffer that torch made on the current stream is used on `stream`: torch must not hand its
+    memory on before that stream is done with it."""
+    if stream is not None:
+        t.record_stream(stream)
 
 
 # ---------------------------------------------------------------------------------------
 # head norms with rotation
 
 
-def _norm_args(qkv, Hq, Hk, d, q_weight, k_weight, cos, sin, positions):
-    """Checks; returns (B, N, Hv, rot, table_len, position_bytes)."""
+def _rows(t, name, shape, dev):
+    if t.dtype is not _torch().bfloat16 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise TypeError("%s must be a contiguous bf16 tensor of qkv's shape on qkv's device" % name)
+    return t.data_ptr()
+
+
+def _norm_args(qkv, Hq, Hk, d, q_weight, k_weight, cos, sin, positions, eps, interleaved):
+    """Checks; returns (device, (cos, sin, positions, .. eps) as the C calls take them)."""
     torch = _torch()
-    if not isinstance(qkv, torch.Tensor) or not qkv.is_cuda or qkv.dtype != torch.bfloat16 or qkv.dim() != 3 \
+    if not isinstance(qkv, torch.Tensor) or not qkv.is_cuda or qkv.dtype is not torch.bfloat16 or qkv.dim() != 3 \
             or not qkv.is_contiguous():
         raise TypeError("qkv must be a contiguous bf16 CUDA tensor [B, N, (Hq + Hk + Hv)*d]")
     B, N, W = qkv.shape
+    dev = qkv.get_device()
     if d <= 0 or W % d != 0 or W // d < Hq + Hk or Hq < 0 or Hk < 0:
         raise ValueError("qkv last dim %d is not (Hq + Hk + Hv)*d with Hq = %d, Hk = %d, d = %d" % (W, Hq, Hk, d))
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and (w.dtype != torch.float32 or tuple(w.shape) != (d,) or not w.is_contiguous()
-                              or w.device != qkv.device):
-            raise TypeError("%s must be a contiguous fp32 tensor [d] on qkv's device" % name)
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype is not torch.float32 or w.shape != (d,) or not w.is_contiguous()
+                              or w.get_device() != dev):
+            raise TypeError("q_weight and k_weight must be contiguous fp32 tensors [d] on qkv's device")
     if (cos is None) != (sin is None):
         raise TypeError("cos and sin come together")
-    rot = table = 0
+    rot = table = pos_bytes = 0
     if cos is not None:
+        shape = cos.shape
         for t in (cos, sin):
-            if t.dtype != torch.float32 or t.dim() != 2 or not t.is_contiguous() or t.device != qkv.device \
-                    or t.shape != cos.shape:
+            if t.dtype is not torch.float32 or len(shape) != 2 or t.shape != shape or not t.is_contiguous() \
+                    or t.get_device() != dev:
                 raise TypeError("cos and sin must be contiguous fp32 tensors [positions, rot/2] on qkv's device")
-        table, rot = int(cos.shape[0]), 2 * int(cos.shape[1])
-    bytes_ = 0
+        table, rot = shape[0], 2 * shape[1]
     if positions is not None:
-        if positions.dtype not in (torch.int32, torch.int64) or tuple(positions.shape) != (B, N) \
-                or not positions.is_contiguous() or positions.device != qkv.device:
+        if positions.dtype not in (torch.int32, torch.int64) or positions.shape != (B, N) \
+                or not positions.is_contiguous() or positions.get_device() != dev:
             raise TypeError("positions must be a contiguous int32 or int64 tensor [B, N] on qkv's device")
-        bytes_ = positions.element_size()
-    return B, N, W // d - Hq - Hk, rot, table, bytes_
+        pos_bytes = positions.element_size()
+    return dev, (_ptr(cos), _ptr(sin), _ptr(positions), pos_bytes, B, N, Hq, Hk, W // d - Hq - Hk, d, rot, table,
+                 int(interleaved), eps)
 
 
 def lite_la_qk_norm_rope_fwd(qkv, Hq: int, Hk: int, d: int = 32, q_weight=None, k_weight=None, cos=None, sin=None,
@@ -81,16 +91,12 @@ def lite_la_qk_norm_rope_fwd(qkv, Hq: int, Hk: int, d: int = 32, q_weight=None, 
     """RMS norm of every q and k head of packed rows (bf16 [B, N, (Hq + Hk + Hv)*d]) and rotation
     by position; returns out in qkv's layout (v copied).  out=qkv works in place.  A row at a
     negative position is padding: left alone in place, zeros otherwise."""
-    torch = _torch()
-    B, N, Hv, rot, table, pb = _norm_args(qkv, Hq, Hk, d, q_weight, k_weight, cos, sin, positions)
+    dev, args = _norm_args(qkv, Hq, Hk, d, q_weight, k_weight, cos, sin, positions, eps, interleaved)
     if out is None:
-        out = torch.empty_like(qkv)
-    elif out.dtype != torch.bfloat16 or out.shape != qkv.shape or not out.is_contiguous() or out.device != qkv.device:
-        raise TypeError("out must be a contiguous bf16 tensor of qkv's shape on qkv's device")
-    with torch.cuda.device(qkv.device):
-        _check(lib().lite_la_qk_norm_rope_fwd(
-            qkv.data_ptr(), out.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions), pb,
-            B, N, Hq, Hk, Hv, d, rot, table, int(interleaved), eps, _stream_handle(stream, qkv.device)))
+        out = _torch().empty_like(qkv)
+        _on_stream(out, stream)
+    o = _rows(out, "out", qkv.shape, dev)
+    _call(lib().lite_la_qk_norm_rope_fwd, dev, stream, qkv.data_ptr(), o, _ptr(q_weight), _ptr(k_weight), *args)
     return out
 
 
@@ -100,32 +106,23 @@ def lite_la_qk_norm_rope_bwd(qkv, dout, Hq: int, Hk: int, d: int = 32, q_weight=
     """Gradient of sum(dout * out): returns (dqkv bf16, dq_weight, dk_weight fp32; None for a
     weight that is None).  dqkv=dout works in place."""
     torch = _torch()
-    B, N, Hv, rot, table, pb = _norm_args(qkv, Hq, Hk, d, q_weight, k_weight, cos, sin, positions)
-    for t, name in ((dout, "dout"), (dqkv, "dqkv")):
-        if t is not None and (t.dtype != torch.bfloat16 or t.shape != qkv.shape or not t.is_contiguous()
-                              or t.device != qkv.device):
-            raise TypeError("%s must be a contiguous bf16 tensor of qkv's shape on qkv's device" % name)
+    dev, args = _norm_args(qkv, Hq, Hk, d, q_weight, k_weight, cos, sin, positions, eps, interleaved)
     if dqkv is None:
         dqkv = torch.empty_like(qkv)
+        _on_stream(dqkv, stream)
+    do, dx = _rows(dout, "dout", qkv.shape, dev), _rows(dqkv, "dqkv", qkv.shape, dev)
     dwq = None if q_weight is None else torch.empty_like(q_weight)
     dwk = None if k_weight is None else torch.empty_like(k_weight)
-    ws = None
+    size, ws = 0, None
     if dwq is not None or dwk is not None:
-        ws = torch.empty(int(lib().lite_la_qk_norm_rope_workspace_bytes(d)), dtype=torch.uint8, device=qkv.device)
-        _on_stream(ws, stream)
-    with torch.cuda.device(qkv.device):
-        _check(lib().lite_la_qk_norm_rope_bwd(
-            qkv.data_ptr(), dout.data_ptr(), dqkv.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(dwq), _ptr(dwk),
-            _ptr(cos), _ptr(sin), _ptr(positions), pb, B, N, Hq, Hk, Hv, d, rot, table, int(interleaved), eps,
-            _ptr(ws), 0 if ws is None else ws.numel(), _stream_handle(stream, qkv.device)))
+        size = lib().lite_la_qk_norm_rope_workspace_bytes(d)
+        ws = torch.empty(size, dtype=torch.uint8, device=qkv.device)
+        for t in (ws, dwq, dwk):
+            if t is not None:
+                _on_stream(t, stream)
+    _call(lib().lite_la_qk_norm_rope_bwd, dev, stream, qkv.data_ptr(), do, dx, _ptr(q_weight), _ptr(k_weight),
+          _ptr(dwq), _ptr(dwk), *args, _ptr(ws), size)
     return dqkv, dwq, dwk
-
-
-def _on_stream(t, stream):
-    """A workspace that torch made on the current stream is used on `stream`: torch must not hand
-    its memory on before that stream is done with it."""
-    if stream is not None:
-        t.record_stream(stream)
 
 
 _FUNCTIONS = {}
@@ -170,83 +167,106 @@ def lite_la_qk_norm_rope(qkv, Hq: int, Hk: int, d: int = 32, q_weight=None, k_we
 # the gated delta rule
 
 
-def _view(t, name, shape, device):
-    """lite_la_view of a bf16 [B, N, heads, d] tensor with adjacent channels."""
+def _view(t, name, shape, dev):
+    """A bf16 tensor [B, N, heads, d] with adjacent channels as (pointer, strides)."""
     torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16 or tuple(t.shape) != shape \
-            or t.device != device:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev:
         raise TypeError("%s must be a bf16 CUDA tensor %s on q's device" % (name, list(shape)))
-    if t.stride(-1) != 1 and t.numel() > 0:
+    sb, st, sh, sc = t.stride()
+    if sc != 1 and t.numel() > 0:
         raise TypeError("%s: the channels of a head must be adjacent" % name)
-    # a dimension of one has no stride
-    return View(t.data_ptr(), *(0 if n == 1 else s for n, s in zip(t.shape[:3], t.stride()[:3])))
+    B, N, H, _ = shape   # a dimension of one has no stride
+    return t.data_ptr(), 0 if B == 1 else sb, 0 if N == 1 else st, 0 if H == 1 else sh
 
 
-def _gate(t, name, shape, device):
+def _token_view(t, name, shape, dev):
+    """... [B, heads, d]: one token"""
     torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or tuple(t.shape) != shape or t.device != device \
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev:
+        raise TypeError("%s must be a bf16 CUDA tensor %s on q's device" % (name, list(shape)))
+    sb, sh, sc = t.stride()
+    if sc != 1 and t.numel() > 0:
+        raise TypeError("%s: the channels of a head must be adjacent" % name)
+    return t.data_ptr(), 0 if shape[0] == 1 else sb, 0, 0 if shape[1] == 1 else sh
+
+
+def _gate(t, name, shape, dev):
+    """An fp32 tensor [B, (N,) Hv] as (pointer, batch, token stride)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.shape != shape or t.get_device() != dev \
             or (t.stride(-1) != 1 and shape[-1] > 1 and t.numel() > 0):
         raise TypeError("%s must be an fp32 tensor %s on q's device with adjacent heads" % (name, list(shape)))
-    return t.data_ptr(), 0 if shape[0] == 1 else t.stride(0), 0 if shape[1] == 1 else t.stride(1)
+    return t.data_ptr(), 0 if shape[0] == 1 else t.stride(0), 0 if len(shape) == 2 or shape[1] == 1 else t.stride(1)
 
 
-def _states(t, name, shape, device):
+def _states(t, name, shape, dev):
     torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or tuple(t.shape) != shape \
-            or not t.is_contiguous() or t.device != device:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.shape != shape or t.get_device() != dev \
+            or not t.is_contiguous():
         raise TypeError("%s must be a contiguous fp32 tensor %s on q's device" % (name, list(shape)))
     return t.data_ptr()
 
 
-def _delta_args(q, k, v, g, beta, scale, cu_seqlens):
-    """The fields that every call has; returns (args, sequences)."""
-    torch = _torch()
-    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
-        raise TypeError("q must be a bf16 CUDA tensor [B, N, Hk, d]")
-    if not isinstance(v, torch.Tensor) or v.dim() != 4:
-        raise TypeError("v must be a bf16 CUDA tensor [B, N, Hv, d]")
-    B, N, Hk, d = q.shape
-    Hv, device = int(v.shape[2]), q.device
-    a = DeltaArgs()
-    a.q, a.k = _view(q, "q", (B, N, Hk, d), device), _view(k, "k", (B, N, Hk, d), device)
-    a.v = _view(v, "v", (B, N, Hv, d), device)
-    a.g, a.g_batch_stride, a.g_token_stride = _gate(g, "g", (B, N, Hv), device)
-    a.beta, a.beta_batch_stride, a.beta_token_stride = _gate(beta, "beta", (B, N, Hv), device)
-    a.scale = float(d) ** -0.5 if scale is None and d > 0 else float(scale or 0.0)
-    a.B, a.N, a.Hk, a.Hv, a.d = B, N, Hk, Hv, d
-    if cu_seqlens is not None:
-        if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 \
-                or not cu_seqlens.is_contiguous() or cu_seqlens.device != device or cu_seqlens.numel() < 1:
-            raise TypeError("cu_seqlens must be a contiguous int32 tensor [sequences + 1] on q's device")
-        if B != 1:
-            raise ValueError("packed sequences come in one buffer: B must be 1, not %d" % B)
-        a.cu_seqlens, a.B = cu_seqlens.data_ptr(), cu_seqlens.numel() - 1
-    return a, int(a.B)
+class _Delta:
+    """The checked arguments of a call over whole sequences."""
+
+    def __init__(self, q, k, v, g, beta, scale, cu_seqlens):
+        torch = _torch()
+        if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
+            raise TypeError("q must be a bf16 CUDA tensor [B, N, Hk, d]")
+        if not isinstance(v, torch.Tensor) or v.dim() != 4:
+            raise TypeError("v must be a bf16 CUDA tensor [B, N, Hv, d]")
+        B, N, Hk, d = q.shape
+        Hv, dev = v.shape[2], q.get_device()
+        self.device, self.dev, self.qshape, self.vshape = q.device, dev, (B, N, Hk, d), (B, N, Hv, d)
+        self.views = (*_view(q, "q", self.qshape, dev), *_view(k, "k", self.qshape, dev),
+                      *_view(v, "v", self.vshape, dev))
+        gp, g_sb, g_st = _gate(g, "g", (B, N, Hv), dev)
+        bp, b_sb, b_st = _gate(beta, "beta", (B, N, Hv), dev)
+        self.gates = (gp, bp, g_sb, g_st, b_sb, b_st)
+        self.scale = float(d) ** -0.5 if scale is None and d > 0 else float(scale or 0.0)
+        self.cu, self.S = 0, B
+        if cu_seqlens is not None:
+            if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dtype is not torch.int32 \
+                    or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() or cu_seqlens.get_device() != dev \
+                    or cu_seqlens.numel() < 1:
+                raise TypeError("cu_seqlens must be a contiguous int32 tensor [sequences + 1] on q's device")
+            if B != 1:
+                raise ValueError("packed sequences come in one buffer: B must be 1, not %d" % B)
+            self.cu, self.S = cu_seqlens.data_ptr(), cu_seqlens.numel() - 1
+        self.sizes = (self.S, N, Hk, Hv, d)
+        self.states = (self.S, Hv, d, d)
+
+    def bytes(self, fn):
+        return fn(*self.sizes, int(self.cu != 0))
+
+    def pack(self, out, state_in, state_out, zero_tail, ws, ws_bytes):
+        return _DELTA_ARGS.pack(*self.views, *out, *self.gates, state_in, state_out, self.cu, *self.sizes, self.scale,
+                                zero_tail, ws, ws_bytes)
 
 
 def _delta_forward(q, k, v, g, beta, state_in, state_out, cu_seqlens, scale, out, stream, save):
     torch = _torch()
-    a, S = _delta_args(q, k, v, g, beta, scale, cu_seqlens)
-    d, Hv, device = int(a.d), int(a.Hv), q.device
-    if state_in is not None:
-        a.state_in = _states(state_in, "state_in", (S, Hv, d, d), device)
+    a = _Delta(q, k, v, g, beta, scale, cu_seqlens)
+    si = 0 if state_in is None else _states(state_in, "state_in", a.states, a.dev)
     if state_out is None:
-        state_out = torch.empty((S, Hv, d, d), dtype=torch.float32, device=device)
-    a.state_out = _states(state_out, "state_out", (S, Hv, d, d), device)
+        state_out = torch.empty(a.states, dtype=torch.float32, device=a.device)
+        _on_stream(state_out, stream)
+    so = _states(state_out, "state_out", a.states, a.dev)
+    zero_tail = int(out is None)
     if out is None:
-        out = torch.empty(v.shape, dtype=torch.bfloat16, device=device)
-        a.zero_tail = 1
-    a.out = _view(out, "out", tuple(v.shape), device)
-    size = lib().lite_la_gated_delta_saved_bytes if save else lib().lite_la_gated_delta_workspace_bytes
-    buf = torch.empty(int(size(a.B, a.N, a.Hk, Hv, d, int(cu_seqlens is not None))), dtype=torch.uint8, device=device)
-    _on_stream(buf, stream)
-    with torch.cuda.device(device):
-        if save:
-            _check(lib().lite_la_gated_delta_fwd_save(ctypes.byref(a), buf.data_ptr(), buf.numel(),
-                                                      _stream_handle(stream, device)))
-        else:
-            a.workspace, a.workspace_bytes = buf.data_ptr(), buf.numel()
-            _check(lib().lite_la_gated_delta_fwd(ctypes.byref(a), _stream_handle(stream, device)))
+        out = torch.empty(a.vshape, dtype=torch.bfloat16, device=a.device)
+        _on_stream(out, stream)
+    o = _view(out, "out", a.vshape, a.dev)
+    L = lib()
+    size = a.bytes(L.lite_la_gated_delta_saved_bytes if save else L.lite_la_gated_delta_workspace_bytes)
+    buf = torch.empty(size, dtype=torch.uint8, device=a.device) if size or save else None
+    if buf is not None:
+        _on_stream(buf, stream)
+    if save:
+        _call(L.lite_la_gated_delta_fwd_save, a.dev, stream, a.pack(o, si, so, zero_tail, 0, 0), buf.data_ptr(), size)
+    else:
+        _call(L.lite_la_gated_delta_fwd, a.dev, stream, a.pack(o, si, so, zero_tail, _ptr(buf), size))
     return out, state_out, buf
 
 
@@ -275,35 +295,31 @@ def lite_la_gated_delta_bwd(q, k, v, g, beta, dout, saved, state_out=None, dstat
     (lite_la_gated_delta_fwd_save with the same arguments) and wrote state_out: (dq, dk, dv bf16, dg,
     dbeta fp32, dstate_in fp32 or None without state_in)."""
     torch = _torch()
-    a, S = _delta_args(q, k, v, g, beta, scale, cu_seqlens)
-    d, Hv, device = int(a.d), int(a.Hv), q.device
-    gr = DeltaGrads()
-    gr.dout = _view(dout, "dout", tuple(v.shape), device)
-    if not isinstance(saved, torch.Tensor) or saved.dtype != torch.uint8 or not saved.is_contiguous() \
-            or saved.device != device:
+    a = _Delta(q, k, v, g, beta, scale, cu_seqlens)
+    do = _view(dout, "dout", a.vshape, a.dev)
+    if not isinstance(saved, torch.Tensor) or saved.dtype is not torch.uint8 or not saved.is_contiguous() \
+            or saved.get_device() != a.dev:
         raise TypeError("saved must be what lite_la_gated_delta_fwd_save returned")
-    shape = (S, Hv, d, d)
-    dstate_in = None
+    new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=a.device)  # noqa: E731
+    si = dstate_in = None
     if state_in is not None:
-        a.state_in = _states(state_in, "state_in", shape, device)
-        dstate_in = torch.empty(shape, dtype=torch.float32, device=device)
-        gr.dstate_in = dstate_in.data_ptr()
+        si, dstate_in = _states(state_in, "state_in", a.states, a.dev), new(a.states, torch.float32)
+    dso = so = 0
     if dstate_out is not None:
-        gr.dstate_out = _states(dstate_out, "dstate_out", shape, device)
-        gr.state_out = _states(state_out, "state_out", shape, device)
-    dq, dk, dv = (torch.empty(t.shape, dtype=torch.bfloat16, device=device) for t in (q, k, v))
-    dg, dbeta = (torch.empty(g.shape, dtype=torch.float32, device=device) for _ in range(2))
-    gr.dq, gr.dk = _view(dq, "dq", tuple(q.shape), device), _view(dk, "dk", tuple(q.shape), device)
-    gr.dv = _view(dv, "dv", tuple(v.shape), device)
-    gr.dg, gr.dbeta = dg.data_ptr(), dbeta.data_ptr()
-    ws = torch.empty(int(lib().lite_la_gated_delta_bwd_workspace_bytes(a.B, a.N, a.Hk, Hv, d,
-                                                                       int(cu_seqlens is not None))),
-                     dtype=torch.uint8, device=device)
-    _on_stream(ws, stream)
-    a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
-    with torch.cuda.device(device):
-        _check(lib().lite_la_gated_delta_bwd(ctypes.byref(a), ctypes.byref(gr), saved.data_ptr(), saved.numel(),
-                                             _stream_handle(stream, device)))
+        dso = _states(dstate_out, "dstate_out", a.states, a.dev)
+        so = _states(state_out, "state_out", a.states, a.dev)
+    dq, dk, dv = (new(shape, torch.bfloat16) for shape in (a.qshape, a.qshape, a.vshape))
+    dg, dbeta = (new(a.vshape[:3], torch.float32) for _ in range(2))
+    size = a.bytes(lib().lite_la_gated_delta_bwd_workspace_bytes)
+    ws = new(size, torch.uint8)
+    for t in (dq, dk, dv, dg, dbeta, dstate_in, ws):
+        if t is not None:
+            _on_stream(t, stream)
+    grads = _DELTA_GRADS.pack(*do, *_view(dq, "dq", a.qshape, a.dev), *_view(dk, "dk", a.qshape, a.dev),
+                              *_view(dv, "dv", a.vshape, a.dev), dg.data_ptr(), dbeta.data_ptr(), dso, so,
+                              _ptr(dstate_in))
+    _call(lib().lite_la_gated_delta_bwd, a.dev, stream, a.pack(_NO_VIEW, si or 0, 0, 0, ws.data_ptr(), size), grads,
+          saved.data_ptr(), saved.numel())
     return dq, dk, dv, dg, dbeta, dstate_in
 
 
@@ -329,12 +345,7 @@ def _delta_function():
                 if dout is None:
                     dout = torch.zeros_like(v, memory_format=torch.contiguous_format)
                 dout = dout.to(torch.bfloat16)
-                try:
-                    _view(dout, "dout", tuple(v.shape), q.device)
-                    strides_ok = dout.data_ptr() % 16 == 0 and all(x % 8 == 0 for x in dout.stride()[:3])
-                except TypeError:
-                    strides_ok = False
-                if not strides_ok:
+                if dout.stride(-1) != 1 or dout.data_ptr() % 16 != 0 or any(x % 8 for x in dout.stride()[:3]):
                     dout = dout.contiguous()
                 if dstate is not None:
                     dstate = dstate.float().contiguous()
@@ -364,23 +375,24 @@ def lite_la_gated_delta_step(q, k, v, g, beta, states, state_indices=None, scale
     outside the pool, or with one that an earlier row has, touches no state and gets zeros.
     Returns out bf16 [B, Hv, d]."""
     torch = _torch()
-    if not all(isinstance(t, torch.Tensor) and t.dim() == 3 for t in (q, k, v)) \
-            or not all(isinstance(t, torch.Tensor) and t.dim() == 2 for t in (g, beta)):
-        raise TypeError("q, k must be [B, Hk, d], v [B, Hv, d], g and beta [B, Hv]")
-    a, B = _delta_args(*(t.unsqueeze(1) for t in (q, k, v, g, beta)), scale, None)
-    d, Hv, device = int(a.d), int(a.Hv), q.device
-    if not isinstance(states, torch.Tensor) or states.dim() != 4:
-        raise TypeError("states must be a contiguous fp32 tensor [pool, Hv, d, d]")
-    a.state_in = a.state_out = _states(states, "states", (int(states.shape[0]), Hv, d, d), device)
-    if state_indices is not None and (state_indices.dtype != torch.int32 or tuple(state_indices.shape) != (B,)
-                                      or not state_indices.is_contiguous() or state_indices.device != device):
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3 or not isinstance(v, torch.Tensor) \
+            or v.dim() != 3 or not isinstance(states, torch.Tensor) or states.dim() != 4:
+        raise TypeError("q, k must be [B, Hk, d], v [B, Hv, d] and states [pool, Hv, d, d] CUDA tensors")
+    B, Hk, d = q.shape
+    Hv, pool, dev = v.shape[1], states.shape[0], q.get_device()
+    shape = (B, Hv, d)
+    gp, g_sb, _ = _gate(g, "g", (B, Hv), dev)
+    bp, b_sb, _ = _gate(beta, "beta", (B, Hv), dev)
+    st = _states(states, "states", (pool, Hv, d, d), dev)
+    if state_indices is not None and (state_indices.dtype is not torch.int32 or state_indices.shape != (B,)
+                                      or not state_indices.is_contiguous() or state_indices.get_device() != dev):
         raise TypeError("state_indices must be a contiguous int32 tensor [B] on q's device")
     if out is None:
-        out = torch.empty((B, Hv, d), dtype=torch.bfloat16, device=device)
-    elif not isinstance(out, torch.Tensor) or tuple(out.shape) != (B, Hv, d):
-        raise TypeError("out must be a bf16 CUDA tensor [B, Hv, d]")
-    a.out = _view(out.unsqueeze(1), "out", (B, 1, Hv, d), device)
-    with torch.cuda.device(device):
-        _check(lib().lite_la_gated_delta_step(ctypes.byref(a), _ptr(state_indices), int(states.shape[0]),
-                                              _stream_handle(stream, device)))
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        _on_stream(out, stream)
+    args = _DELTA_ARGS.pack(*_token_view(q, "q", (B, Hk, d), dev), *_token_view(k, "k", (B, Hk, d), dev),
+                            *_token_view(v, "v", shape, dev), *_token_view(out, "out", shape, dev), gp, bp, g_sb, 0,
+                            b_sb, 0, st, st, 0, B, 1, Hk, Hv, d,
+                            float(d) ** -0.5 if scale is None and d > 0 else float(scale or 0.0), 0, 0, 0)
+    _call(lib().lite_la_gated_delta_step, dev, stream, args, _ptr(state_indices), pool)
     return out
