@@ -33,7 +33,7 @@ struct DeltaGrads {
   float* dstate_in;                // or null
   // between the two kernels, per chunk slot and value head
   uint8_t* gstates;                // G' as DeltaSaved's states
-  float* y;                        // [64, d]
+  uint8_t* y;                      // bf16 pair: [2][64, d]
   float* rows;                     // [d / 32][2][2][64]: w . W and y . v of half of 32 columns
   float* ends;                     // [d / 32][8]: shares of <S_C, G'>
 };
@@ -220,19 +220,20 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
         hand(kBarU);
         // while the third product runs: dv, y and the rows' shares
         F2 wdot = f2(0.f, 0.f), vdot = f2(0.f, 0.f);
-        uint32_t o[kN / 2];
-        float4* yd = reinterpret_cast<float4*>(gr.y + (sh * kChunk + tok) * kD + part * kCols + c0);
+        uint32_t o[kN / 2], ol[kN / 2];   // y's pair; the first term is dv
 #pragma unroll
         for (int i = 0; i < kN / 2; ++i) {
           const float* wr = reinterpret_cast<const float*>(wrow) + 2 * i;
           wdot = f2_fma(z[i], f2(wr[0], wr[1]), wdot);
           vdot = f2_fma(y[i], f2_bf16(reinterpret_cast<const uint32_t*>(v)[i]), vdot);
-          const float2 yy = f2_out(y[i]);
-          o[i] = pack_bf16(yy.x, yy.y);
-          if (i & 1) {
-            const float2 yp = f2_out(y[i - 1]);
-            yd[i / 2] = make_float4(yp.x, yp.y, yy.x, yy.y);
-          }
+          o[i] = next_term(y[i], false);
+          ol[i] = next_term(y[i], true);
+        }
+        uint4* yd = reinterpret_cast<uint4*>(gr.y + ((sh * 2 * kChunk + tok) * kD + part * kCols + c0) * 2);
+#pragma unroll
+        for (int i = 0; i < kN / 8; ++i) {
+          yd[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          yd[kChunk * kD / 8 + i] = make_uint4(ol[4 * i], ol[4 * i + 1], ol[4 * i + 2], ol[4 * i + 3]);
         }
         const float2 wd = f2_out(wdot), vd = f2_out(vdot);
         float* rw = gr.rows + ((sh * kParts + part) * 2 * 2 + (warp >> 2)) * kChunk + tok;
@@ -426,16 +427,17 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
 // litela_delta_grads: dq, dk, dg and dbeta of one chunk and key head per CTA, its value heads one
 // after another (their shares of dq and dk are summed in registers, in a fixed order).
 //
-// mma.sync, 8 warps: warp w has 16 rows (w / 2) and half of the columns.  States and gradients stream
-// through a ring of tiles of 32 columns; U and y are entered as bf16 pairs.  dq and dk of one head
+// mma.sync, 16 warps (d = 32: 8): a warp has 16 rows and a quarter (half) of the columns.  States and
+// gradients stream through a ring of tiles of 32 columns; U and y are entered as bf16 pairs.  dq and dk of one head
 // take 12 products of 64 rows; the states' and the gradients' bytes (16 d^2 a chunk and head) are
 // what bounds it.
-constexpr int kGradThreads = 256;
 constexpr int kGradLd = 72;   // row of the 64 x 64 matrices, padded
 constexpr int kGradRing = 3;
 
 template <int kD>
 struct GradCfg {
+  static constexpr int kCW = kD >= 64 ? 4 : 2;                     // warps beside one another
+  static constexpr int kThreads = 4 * kCW * 32;
   static constexpr int kLd = kD + 8;
   static constexpr uint32_t kRows = kChunk * kLd * 2;              // 64 rows of d, bf16
   static constexpr uint32_t kTile = kD * 128;
@@ -444,33 +446,34 @@ struct GradCfg {
   static constexpr uint32_t kOffM = 7 * kRows;                     // M1 . D and M2 . D, pairs
   static constexpr uint32_t kMat = kChunk * kGradLd * 2;
   static constexpr uint32_t kOffTile = (kOffM + 4 * kMat + 127) / 128 * 128;
-  static constexpr uint32_t kOffG = kOffTile + kGradRing * kTile;
-  static constexpr uint32_t kOffRel = kOffG + kChunk * 8;          // as in litela_delta_prep
-  static constexpr uint32_t kOffRow = kOffRel + kChunk * 8;
-  static constexpr uint32_t kOffCol = kOffRow + kChunk * 4;
-  static constexpr uint32_t kOffFac = kOffCol + 4 * 48 * 4;        // e^G, e^(G_C - G), beta
-  static constexpr uint32_t kOffSum = kOffFac + 3 * kChunk * 4;    // q . dq: [2][64]
-  static constexpr uint32_t kSmemBytes = kOffSum + 2 * kChunk * 4 + 1024;
+  static constexpr uint32_t kOffFac = kOffTile + kGradRing * kTile;   // the prepared block's factors
+  static constexpr uint32_t kOffSum = kOffFac + kFactorBytes;                // q . dq: [warps beside one another][64]
+  static constexpr uint32_t kSmemBytes = kOffSum + kCW * kChunk * 4 + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory above the 227 KB per-block limit");
 };
 
+__device__ __forceinline__ float sum_warp(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
 template <int kD>
-__global__ void __launch_bounds__(kGradThreads, 1)
+__global__ void __launch_bounds__(GradCfg<kD>::kThreads, 1)
 litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restrict__ prep, const DeltaSaved saved) {
   using namespace sm100;
   using Cfg = GradCfg<kD>;
-  constexpr int kParts = kD / 32, kT = kD / 16;   // tiles of 8 columns of a warp's half of d
+  constexpr int kThreads = Cfg::kThreads, kCW = Cfg::kCW;
+  constexpr int kParts = kD / 32, kT = kD / 8 / kCW;   // kT: tiles of 8 columns of d that a warp has
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  double* G = reinterpret_cast<double*>(smem + Cfg::kOffG);
-  float2* rel = reinterpret_cast<float2*>(smem + Cfg::kOffRel);
-  float* rowf = reinterpret_cast<float*>(smem + Cfg::kOffRow);
-  float* colf = reinterpret_cast<float*>(smem + Cfg::kOffCol);
   float* fac = reinterpret_cast<float*>(smem + Cfg::kOffFac);
+  const float *rowf = fac + kFacRow, *colf = fac + kFacCol;
+  const float2* rel = reinterpret_cast<const float2*>(fac + kFacRel);
   float* qsum = reinterpret_cast<float*>(smem + Cfg::kOffSum);
 
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g4 = lane >> 2, t2 = (lane & 3) * 2;
-  const int rb = w >> 1, hf = w & 1, l8 = lane & 7, k8 = ((lane >> 3) & 1) * 8;
+  const int rb = w / kCW, cw = w % kCW, l8 = lane & 7, k8 = ((lane >> 3) & 1) * 8;
   const int slot = blockIdx.x / a.Hk, hk = blockIdx.x - slot * a.Hk, group = a.Hv / a.Hk;
   int s, n0;
   DeltaSeq sq;
@@ -480,7 +483,7 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
 
   // 64 rows of a view into shared memory
   auto copy_rows = [&](const DeltaView& v, int head, uint32_t dst) {
-    constexpr int kC = kD / 8, kStep = kGradThreads / kC;
+    constexpr int kC = kD / 8, kStep = kThreads / kC;
     const int c = tid % kC, r0 = tid / kC;
     const __nv_bfloat16* p = delta_row(v, sq, n0 + r0, head) + c * 8;
 #pragma unroll
@@ -511,92 +514,88 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
                                        : gr.gstates + (sh * kParts + p - kParts) * (long long)Cfg::kTile);
       const uint32_t dst = base + Cfg::kOffTile + (p % kGradRing) * Cfg::kTile;
 #pragma unroll 1
-      for (int i = tid * 16; i < (int)Cfg::kTile; i += kGradThreads * 16) cp_async_16(dst + i, src + i, true);
+      for (int i = tid * 16; i < (int)Cfg::kTile; i += kThreads * 16) cp_async_16(dst + i, src + i, true);
     };
     copy_rows(gr.dout, h, Cfg::kOffDo);
+    {   // y's pair: 128 rows
+      constexpr int kC = kD / 8, kStep = kThreads / kC;
+      const int c = tid % kC, r = tid / kC;
+      const uint8_t* src = gr.y + sh * (2 * kChunk * kD * 2) + tid * 16;
+      const uint32_t dst = base + Cfg::kOffY + r * (Cfg::kLd * 2) + c * 16;
+#pragma unroll
+      for (int i = 0; i < 2 * kChunk / kStep; ++i) cp_async_16(dst + i * kStep * (Cfg::kLd * 2), src + i * kThreads * 16, true);
+    }
+    if (tid < (int)kFactorBytes / 16) cp_async_16(base + Cfg::kOffFac + tid * 16, prep + sh * kPrepBytes + kPrepFactors + tid * 16, true);
     load_tile(0);
     cp_async_commit();
     load_tile(1);
     cp_async_commit();
-    const float* pf = reinterpret_cast<const float*>(prep + sh * kPrepBytes + kPrepFactors);
-    if (tid < 192) fac[tid] = pf[tid];
-    if (w == 7) {   // G, two tokens a lane
-      double x[2] = {0.0, 0.0};
-      const float* g = a.g + sq.entry * a.g_sb + (long long)(sq.first + n0) * a.g_st + h;
+    // this token's sums (tid < 64): w . W, y . v, and the chunk's <S, G'>; W's values: all in flight at once
+    constexpr int kQ = kChunk * kD / 4 / kThreads;   // 4 columns of a row at a time
+    float4 wv[kQ];
+    const float4* wp = reinterpret_cast<const float4*>(saved.w + sh * kChunk * kD) + tid;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        if (2 * lane + j < len) x[j] = (double)clamp_decay(g[(2 * lane + j) * a.g_st]);
-      x[1] += x[0];
-      double run = x[1];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += y;
-      }
-      G[2 * lane] = run - x[1] + x[0];
-      G[2 * lane + 1] = run;
-    }
-    __syncthreads();
+    for (int i = 0; i < kQ; ++i) wv[i] = __ldg(wp + i * kThreads);
+    float wd = 0.f, vd = 0.f, end = 0.f;
     if (tid < kChunk) {
-      const double d = G[tid] - G[tid & ~15];
-      rel[tid] = make_float2((float)d, (float)(d - (double)(float)d));
-      rowf[tid] = expf((float)d);
-    } else if (tid < kChunk + 96) {
-      const int i = tid - kChunk, b = i < 16 ? 1 : i < 48 ? 2 : 3, c = i - (b == 1 ? 0 : b == 2 ? 16 : 48);
-      colf[b * 48 + c] = expf((float)(G[16 * b] - G[c]));
-    }
-    // U = beta W and y as pairs, 4 columns of a row at a time
-#pragma unroll 1
-    for (int i = tid; i < kChunk * kD / 4; i += kGradThreads) {
-      const int r = i / (kD / 4), c = (i % (kD / 4)) * 4;
-      const float b = fac[kFacBeta + r];
+      const float* rw = gr.rows + sh * kParts * 4 * kChunk + tid;   // [part][which][half][token]
+      float x[kParts][4];
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const float4 x = *reinterpret_cast<const float4*>((m ? gr.y : saved.w) + (sh * kChunk + r) * kD + c);
-        const float f = m ? 1.f : b;
-        uint32_t hi[2], lo[2];
-        split_bf16(f * x.x, f * x.y, hi[0], lo[0]);
-        split_bf16(f * x.z, f * x.w, hi[1], lo[1]);
-        uint8_t* dst = smem + (m ? Cfg::kOffY : Cfg::kOffU) + (r * Cfg::kLd + c) * 2;
-        *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(dst + Cfg::kRows) = make_uint2(lo[0], lo[1]);
+      for (int p = 0; p < kParts; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[p][i] = __ldcg(rw + (p * 4 + i) * kChunk);
+      if (lane < kParts * 8) end = __ldcg(gr.ends + sh * kParts * 8 + lane);
+#pragma unroll
+      for (int p = 0; p < kParts; ++p) {
+        wd += x[p][0] + x[p][1];
+        vd += x[p][2] + x[p][3];
       }
+      end = sum_warp(end);
     }
-    cp_async_wait<1>();   // do and the first tile (K and Q)
+    cp_async_wait<1>();   // do, y, the factors and the first tile (K and Q)
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kQ; ++i) {   // U = beta W
+      const int q = i * kThreads + tid, r = q / (kD / 4), c = (q % (kD / 4)) * 4;
+      const float f = fac[kFacBeta + r];
+      uint32_t hi[2], lo[2];
+      split_bf16(f * wv[i].x, f * wv[i].y, hi[0], lo[0]);
+      split_bf16(f * wv[i].z, f * wv[i].w, hi[1], lo[1]);
+      uint8_t* dst = smem + Cfg::kOffU + (r * Cfg::kLd + c) * 2;
+      *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(dst + Cfg::kRows) = make_uint2(lo[0], lo[1]);
+    }
     __syncthreads();
 
-    // M1 = do U^T and M2 = y U^T: rows 16 rb .., the warp's rb + 1 tiles of the 2 rb + 2 (d: K dimension)
-    const int tile0 = hf * (rb + 1);
+    // M1 = do U^T and M2 = y U^T: rows 16 rb .., of the 2 rb + 2 tiles of columns up to the diagonal block
+    // cw, cw + kCW, ..  (d: K dimension; tiles beyond are computed along and not kept)
+    constexpr int kMT = 8 / kCW;
     {
-      float m1[4][4], m2[4][4];
+      float m1[kMT][4], m2[kMT][4];
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+      for (int n = 0; n < kMT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) m1[n][i] = m2[n][i] = 0.f;
       const uint32_t arow = (16 * rb + (lane & 15)) * (Cfg::kLd * 2) + (lane >> 4) * 16;
       // matrices by lane / 8: hi of 0..7 and 8..15 of the K dimension, lo
-      const uint32_t brow = base + Cfg::kOffU + (lane >> 4) * Cfg::kRows + (8 * tile0 + l8) * (Cfg::kLd * 2) + k8 * 2;
+      const uint32_t brow = base + Cfg::kOffU + (lane >> 4) * Cfg::kRows + (8 * cw + l8) * (Cfg::kLd * 2) + k8 * 2;
 #pragma unroll 1
       for (int ks = 0; ks < kD / 16; ++ks) {
         uint32_t ad[4], yh[4], yl[4];
         ldmatrix_x4(ad, base + Cfg::kOffDo + arow + ks * 32);
         ldmatrix_x4(yh, base + Cfg::kOffY + arow + ks * 32);
         ldmatrix_x4(yl, base + Cfg::kOffY + Cfg::kRows + arow + ks * 32);
+        uint32_t b[kMT][4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-          if (n <= rb) {
-            uint32_t b[4];
-            ldmatrix_x4(b, brow + n * 8 * (Cfg::kLd * 2) + ks * 32);
-            mma_16816(m1[n], ad, b + 2);
-            mma_16816(m1[n], ad, b);
-            mma_pair(m2[n], yh, yl, b);
-          }
+        for (int n = 0; n < kMT; ++n) ldmatrix_x4(b[n], brow + n * 8 * kCW * (Cfg::kLd * 2) + ks * 32);
+        mma_halves<kMT>(m1, ad, b);
+        mma_pairs<kMT>(m2, yh, yl, b);
       }
       // by D; M1 by scale, M2 negated
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
-        if (n <= rb) {
-          const int c = 8 * (tile0 + n) + t2;
+      for (int n = 0; n < kMT; ++n)
+        if (cw + kCW * n < 2 * rb + 2) {
+          const int c = 8 * (cw + kCW * n) + t2;
           const bool diag = c >= 16 * rb;
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
@@ -623,9 +622,9 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
     }
     __syncthreads();
 
-    // the 64 x 64 matrices with K and Q: columns [hf d / 2, + d / 2) of dq and dk
+    // the 64 x 64 matrices with K and Q: the warp's columns of dq and dk
     {
-      const uint32_t kcol = base + Cfg::kOffK + (l8 + k8) * (Cfg::kLd * 2) + hf * kD + (lane >> 4) * 16;   // two tiles
+      const uint32_t kcol = base + Cfg::kOffK + (l8 + k8) * (Cfg::kLd * 2) + cw * (kT * 16) + (lane >> 4) * 16;   // two tiles
       const uint32_t qcol = kcol + (Cfg::kOffQ - Cfg::kOffK);
       const uint32_t mrow = base + Cfg::kOffM + ((16 * rb + (lane & 15)) * kGradLd + (lane >> 4) * 8) * 2;
 #pragma unroll 1
@@ -640,12 +639,13 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
           uint32_t b[4];   // tile n: b[0], b[1]; tile n + 1: b[2], b[3]
           ldmatrix_x4_t(b, kcol + kb * 16 * (Cfg::kLd * 2) + n * 16);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            mma_16816(dq[n + e], al, b + 2 * e);
-            mma_16816(dq[n + e], ah, b + 2 * e);
-            mma_16816(dk[n + e], cl, b + 2 * e);
-            mma_16816(dk[n + e], ch, b + 2 * e);
-          }
+          for (int e = 0; e < 2; ++e) mma_16816(dq[n + e], al, b + 2 * e);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) mma_16816(dk[n + e], cl, b + 2 * e);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) mma_16816(dq[n + e], ah, b + 2 * e);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) mma_16816(dk[n + e], ch, b + 2 * e);
         }
       }
       // transposed: rows of dk are columns of the matrices
@@ -664,12 +664,13 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
           ldmatrix_x4_t(b, qcol + kb * 16 * (Cfg::kLd * 2) + n * 16);
           ldmatrix_x4_t(c, kcol + kb * 16 * (Cfg::kLd * 2) + n * 16);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            mma_16816(dk[n + e], al, b + 2 * e);
-            mma_16816(dk[n + e], ah, b + 2 * e);
-            mma_16816(dk[n + e], cl, c + 2 * e);
-            mma_16816(dk[n + e], ch, c + 2 * e);
-          }
+          for (int e = 0; e < 2; ++e) mma_16816(dk[n + e], al, b + 2 * e);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) mma_16816(dk[n + e], cl, c + 2 * e);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) mma_16816(dk[n + e], ah, b + 2 * e);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) mma_16816(dk[n + e], ch, c + 2 * e);
         }
       }
     }
@@ -677,7 +678,7 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
     const int r0 = 16 * rb + g4;
     const uint32_t arow = (16 * rb + (lane & 15)) * (Cfg::kLd * 2) + (lane >> 4) * 16;
     auto tile_b = [&](uint32_t* b, int p, int n, int ks) {   // rows (channels) of the tile: hi, lo
-      const int row = hf * (kD / 2) + 8 * n + l8, col = 16 * ks + k8 + (lane >> 4) * 32;
+      const int row = (cw * kT + n) * 8 + l8, col = 16 * ks + k8 + (lane >> 4) * 32;
       ldmatrix_x4(b, base + Cfg::kOffTile + (p % kGradRing) * Cfg::kTile + sw128(row, col));
     };
     {
@@ -697,13 +698,14 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
           ldmatrix_x4(ad, base + Cfg::kOffDo + o);
           ldmatrix_x4(yh, base + Cfg::kOffY + o);
           ldmatrix_x4(yl, base + Cfg::kOffY + Cfg::kRows + o);
+          constexpr int kM = kT < 4 ? kT : 4;
 #pragma unroll
-          for (int n = 0; n < kT; ++n) {
-            uint32_t b[4];
-            tile_b(b, p, n, ks);
-            mma_16816(x[n], ad, b + 2);
-            mma_16816(x[n], ad, b);
-            mma_pair(y[n], yh, yl, b);
+          for (int m = 0; m < kT; m += kM) {
+            uint32_t b[kM][4];
+#pragma unroll
+            for (int n = 0; n < kM; ++n) tile_b(b[n], p, m + n, ks);
+            mma_halves<kM>(x + m, ad, b);
+            mma_pairs<kM>(y + m, yh, yl, b);
           }
         }
         cp_async_wait<1>();
@@ -735,11 +737,13 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
           const uint32_t o = arow + (2 * (p - kParts) + ks) * 32;
           ldmatrix_x4(uh, base + Cfg::kOffU + o);
           ldmatrix_x4(ul, base + Cfg::kOffU + Cfg::kRows + o);
+          constexpr int kM = kT < 4 ? kT : 4;
 #pragma unroll
-          for (int n = 0; n < kT; ++n) {
-            uint32_t b[4];
-            tile_b(b, p, n, ks);
-            mma_pair(x[n], uh, ul, b);
+          for (int m = 0; m < kT; m += kM) {
+            uint32_t b[kM][4];
+#pragma unroll
+            for (int n = 0; n < kM; ++n) tile_b(b[n], p, m + n, ks);
+            mma_pairs<kM>(x + m, uh, ul, b);
           }
         }
         cp_async_wait<1>();
@@ -759,34 +763,37 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const uint32_t qv = *reinterpret_cast<const uint32_t*>(
-              smem + Cfg::kOffQ + ((r0 + 8 * q) * Cfg::kLd + hf * (kD / 2) + 8 * n + t2) * 2);
+              smem + Cfg::kOffQ + ((r0 + 8 * q) * Cfg::kLd + (cw * kT + n) * 8 + t2) * 2);
           d[q] += dq[n][2 * q] * __uint_as_float(qv << 16) + dq[n][2 * q + 1] * __uint_as_float(qv & 0xFFFF0000u);
         }
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         d[q] += __shfl_xor_sync(0xffffffffu, d[q], 1);
         d[q] += __shfl_xor_sync(0xffffffffu, d[q], 2);
-        if ((lane & 3) == 0) qsum[hf * kChunk + r0 + 8 * q] = d[q];
+        if ((lane & 3) == 0) qsum[cw * kChunk + r0 + 8 * q] = d[q];
       }
     }
     __syncthreads();
     if (tid < kChunk) {
-      const float now = qsum[tid] + qsum[kChunk + tid];
-      const float* rw = gr.rows + sh * kParts * 4 * kChunk + tid;   // [part][which][half][token]
-      float wd = 0.f, vd = 0.f, end = 0.f;
-      for (int p = 0; p < kParts; ++p, rw += 4 * kChunk) {
-        wd += rw[0] + rw[kChunk];
-        vd += rw[2 * kChunk] + rw[3 * kChunk];
-      }
-      for (int i = 0; i < kParts * 8; ++i) end += gr.ends[sh * kParts * 8 + i];
-      fac[tid] = tid < len ? (now - before) - vd : 0.f;
+      float now = 0.f;
+#pragma unroll
+      for (int i = 0; i < kCW; ++i) now += qsum[i * kChunk + tid];
+      // the sum over the tokens from this one on: inside the warp, and the second warp's for the first
+      float x = tid < len ? (now - before) - vd : 0.f;
       before = now;
-      if (tid < len) gr.dbeta[((long long)sq.entry * a.ntok + sq.first + n0 + tid) * a.Hv + h] = wd;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float up = __shfl_down_sync(0xffffffffu, x, o);
+        if (lane + o < 32) x += up;
+      }
+      asm volatile("barrier.cta.sync 1, 64;" ::: "memory");   // (qsum has been read)
+      if (tid == 32) qsum[0] = x;
       asm volatile("barrier.cta.sync 1, 64;" ::: "memory");
-      if (tid < len) {   // the sum from this token on
-        float x = end;
-        for (int i = len - 1; i >= tid; --i) x += fac[i];
-        gr.dg[((long long)sq.entry * a.ntok + sq.first + n0 + tid) * a.Hv + h] = x;
+      if (tid < 32) x += qsum[0];
+      if (tid < len) {
+        const long long o = ((long long)sq.entry * a.ntok + sq.first + n0 + tid) * a.Hv + h;
+        gr.dbeta[o] = wd;
+        gr.dg[o] = x + end;
       }
     }
     __syncthreads();
@@ -796,8 +803,8 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
   for (int q = 0; q < 2; ++q) {
     const int r = 16 * rb + g4 + 8 * q;
     if (r < len) {
-      __nv_bfloat16* dqp = const_cast<__nv_bfloat16*>(delta_row(gr.dq, sq, n0 + r, hk)) + hf * (kD / 2) + t2;
-      __nv_bfloat16* dkp = const_cast<__nv_bfloat16*>(delta_row(gr.dk, sq, n0 + r, hk)) + hf * (kD / 2) + t2;
+      __nv_bfloat16* dqp = const_cast<__nv_bfloat16*>(delta_row(gr.dq, sq, n0 + r, hk)) + cw * kT * 8 + t2;
+      __nv_bfloat16* dkp = const_cast<__nv_bfloat16*>(delta_row(gr.dk, sq, n0 + r, hk)) + cw * kT * 8 + t2;
 #pragma unroll
       for (int n = 0; n < kT; ++n) {
         *reinterpret_cast<uint32_t*>(dqp + 8 * n) = pack_bf16(dq[n][2 * q], dq[n][2 * q + 1]);

@@ -46,10 +46,15 @@ constexpr int kChunk = 64;
 constexpr uint32_t kImgHalf = 128 * 128;
 __host__ __device__ constexpr int lane_of(int token) { return 32 * (token / 16) + token % 16; }
 constexpr uint32_t kPrepFactors = 2 * kImgHalf;
-constexpr uint32_t kPrepBytes = kPrepFactors + 1024;
+constexpr uint32_t kFactorBytes = 2304;
+constexpr uint32_t kPrepBytes = kPrepFactors + kFactorBytes;
 // fp32 at kPrepFactors: e^G [64], e^(G_C - G) [64] (0 behind the end), beta [64] (0 behind the
 // end), then e^G_C and (int32) the first token of the chunk with a non-finite L or P, or 64
 constexpr int kFacDecay = 0, kFacToEnd = 64, kFacBeta = 128, kFacChunk = 192, kFacBad = 193;
+// and what D is made of (litela_delta_prep): e^(G_r - G_m) [64]; e^(G_m - G_c) for the blocks of rows
+// 1, 2, 3 (48 each, from kFacCol + 48 on); G_r - G_m in two fp32 terms [64][2]
+constexpr int kFacRow = 196, kFacCol = kFacRow + 64 - 48, kFacRel = kFacCol + 192;
+static_assert((kFacRel + 128) * 4 <= kFactorBytes, "factors");
 
 // Chunk slots.  A batch of equal lengths: sequence s has the slots s * ceil(N / 64) + c.  Packed:
 // cu[s] / 64 + s + c, which leaves every sequence at least ceil(len / 64) slots without a sum
@@ -201,11 +206,24 @@ __device__ __forceinline__ void stmatrix_x4_t(uint32_t addr, const uint32_t* r) 
                "r"(r[1]), "r"(r[2]), "r"(r[3])
                : "memory");
 }
-// d += A B, both pairs of fragments (B: hi in b[0], b[1], lo in b[2], b[3])
-__device__ __forceinline__ void mma_pair(float* d, const uint32_t* ah, const uint32_t* al, const uint32_t* b) {
-  sm100::mma_16816(d, al, b);
-  sm100::mma_16816(d, ah, b + 2);
-  sm100::mma_16816(d, ah, b);
+// d[n] += A B[n], all pairs of fragments (B: hi in b[0], b[1], lo in b[2], b[3]); one kind of product
+// for all n after the other, so that no product waits for the one before it
+template <int kTiles>
+__device__ __forceinline__ void mma_pairs(float (*d)[4], const uint32_t* ah, const uint32_t* al, const uint32_t (*b)[4]) {
+#pragma unroll
+  for (int n = 0; n < kTiles; ++n) sm100::mma_16816(d[n], al, b[n]);
+#pragma unroll
+  for (int n = 0; n < kTiles; ++n) sm100::mma_16816(d[n], ah, b[n] + 2);
+#pragma unroll
+  for (int n = 0; n < kTiles; ++n) sm100::mma_16816(d[n], ah, b[n]);
+}
+// the same with an A that is bf16
+template <int kTiles>
+__device__ __forceinline__ void mma_halves(float (*d)[4], const uint32_t* a, const uint32_t (*b)[4]) {
+#pragma unroll
+  for (int n = 0; n < kTiles; ++n) sm100::mma_16816(d[n], a, b[n] + 2);
+#pragma unroll
+  for (int n = 0; n < kTiles; ++n) sm100::mma_16816(d[n], a, b[n]);
 }
 
 template <int kD>
@@ -276,15 +294,17 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
   }
   __syncthreads();
   uint8_t* dst = prep + ((long long)slot * a.Hv + h) * kPrepBytes;
+  float* fac = reinterpret_cast<float*>(dst + kPrepFactors);
   if (tid < kChunk) {
     const double d = G[tid] - G[tid & ~15];
     rel[tid] = make_float2((float)d, (float)(d - (double)(float)d));
     rowf[tid] = expf((float)d);
+    fac[kFacRow + tid] = rowf[tid];
+    *reinterpret_cast<float2*>(fac + kFacRel + 2 * tid) = rel[tid];
   } else if (tid < kChunk + 96) {   // blocks 1, 2, 3 of r have 16, 32, 48 columns before them
     const int i = tid - kChunk, b = i < 16 ? 1 : i < 48 ? 2 : 3, c = i - (b == 1 ? 0 : b == 2 ? 16 : 48);
-    colf[b * 48 + c] = expf((float)(G[16 * b] - G[c]));
+    fac[kFacCol + b * 48 + c] = colf[b * 48 + c] = expf((float)(G[16 * b] - G[c]));
   } else if (tid >= 192) {   // the chain's factors
-    float* fac = reinterpret_cast<float*>(dst + kPrepFactors);
     const int n = tid - 192;
     const double end = G[len - 1];
     fac[kFacDecay + n] = expf((float)G[n]);
@@ -311,12 +331,15 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
       ldmatrix_x4(a0, aa + ks * 64);
       ldmatrix_x4(a1, aa + ks * 64 + 32);
 #pragma unroll
-      for (int n = 0; n < 8; ++n)
-        if (n < 2 * rb + 2) {
-          uint32_t b[4];
-          ldmatrix_x4(b, ba + n * 8 * (Cfg::kLd * 2) + ks * 64);
-          mma_16816(acc[n], a0, b);
-          mma_16816(acc[n], a1, b + 2);
+      for (int m = 0; m < 8; m += 4)
+        if (m < 2 * rb + 2) {   // four tiles (the last ones may lie right of the diagonal block)
+          uint32_t b[4][4];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) ldmatrix_x4(b[n], ba + (m + n) * 8 * (Cfg::kLd * 2) + ks * 64);
+#pragma unroll
+          for (int n = 0; n < 4; ++n) mma_16816(acc[m + n], a0, b[n]);
+#pragma unroll
+          for (int n = 0; n < 4; ++n) mma_16816(acc[m + n], a1, b[n] + 2);
         }
     }
     float* dst = (is_p ? Pf : Lf) + (16 * rb + gr) * kPrepLd + t2;
@@ -462,13 +485,12 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
       }
 #pragma unroll
       for (int m = 0; m < 3; ++m)   // sum over X's block rows w + m before i
-        if (w + m < i)
+        if (w + m < i) {
+          uint32_t b[2][4];
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            uint32_t b[4];
-            ldmatrix_x4(b, term + img_off(16 * i + 8 * n + l8, 16 * (w + m) + k8, 1));
-            mma_pair(x[n], yh[m], yl[m], b);
-          }
+          for (int n = 0; n < 2; ++n) ldmatrix_x4(b[n], term + img_off(16 * i + 8 * n + l8, 16 * (w + m) + k8, 1));
+          mma_pairs<2>(x, yh[m], yl[m], b);
+        }
       float br[2][4];
 #pragma unroll
       for (int n = 0; n < 2; ++n)
@@ -476,12 +498,10 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
         for (int q = 0; q < 4; ++q) br[n][q] = -beta[16 * i + 8 * n + t2 + (q & 1)] * x[n][q];
       uint32_t rh[4], rl[4];
       split_frag(br, rh, rl);
+      uint32_t b[2][4];   // X_ii^T stands as rows of the K dimension
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {   // X_ii^T stands as rows of the K dimension
-        uint32_t b[4];
-        ldmatrix_x4_t(b, term + img_off(16 * i + l8 + k8, 16 * i + 8 * n, 0));
-        mma_pair(x[n], rh, rl, b);
-      }
+      for (int n = 0; n < 2; ++n) ldmatrix_x4_t(b[n], term + img_off(16 * i + l8 + k8, 16 * i + 8 * n, 0));
+      mma_pairs<2>(x, rh, rl, b);
       split_frag(x, rh, rl);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -530,13 +550,12 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
         const float2 bc = *reinterpret_cast<const float2*>(beta + c);
         split_bf16(-bc.x * v.x, -bc.y * v.y, ph[q], pl[q]);
       }
+      if (tile0 / 2 <= k) {   // (X^T is zero in the tiles of four that it does not reach, or they are not kept)
+        uint32_t b[4][4];
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
-        if (n <= rb && (tile0 + n) / 2 <= k) {
-          uint32_t b[4];
-          ldmatrix_x4(b, (xrow ^ ((k & 1) << 6)) + (k >> 1) * kImgBlock + n * 1024);
-          mma_pair(acc[n], ph, pl, b);
-        }
+        for (int n = 0; n < 4; ++n) ldmatrix_x4(b[n], (xrow ^ ((k & 1) << 6)) + (k >> 1) * kImgBlock + n * 1024);
+        mma_pairs<4>(acc, ph, pl, b);
+      }
     }
 #pragma unroll
     for (int n = 0; n < 4; ++n)

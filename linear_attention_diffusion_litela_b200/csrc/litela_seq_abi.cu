@@ -453,7 +453,7 @@ cudaError_t launch_back(const DeltaArgs& d, const DeltaGrads& g, const void* sav
                              BackCfg<kD>::kSmemBytes, st, false, d, g, prep, kept, err);
   if (e != cudaSuccess || d.ntok == 0) return e;
   const long long slots = delta_slots(d.nseq, d.ntok, d.cu != nullptr);
-  return launch_seq(litela_delta_grads<kD>, dim3((unsigned)(slots * d.Hk)), kGradThreads, GradCfg<kD>::kSmemBytes, st, true,
+  return launch_seq(litela_delta_grads<kD>, dim3((unsigned)(slots * d.Hk)), GradCfg<kD>::kThreads, GradCfg<kD>::kSmemBytes, st, true,
                     d, g, prep, kept);
 }
 
@@ -576,7 +576,7 @@ litela_status delta_bwd(const lite_la_delta_args* a, const lite_la_delta_grads* 
   gr.dstate_out = g->dstate_out, gr.state_out = g->state_out, gr.dstate_in = g->dstate_in;
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
   gr.gstates = ws;
-  gr.y = reinterpret_cast<float*>(ws + bytes.states);
+  gr.y = ws + bytes.states;
   gr.rows = reinterpret_cast<float*>(ws + bytes.states + bytes.rows);
   gr.ends = reinterpret_cast<float*>(ws + bytes.states + bytes.rows + bytes.shares);
   int* err = delta_error_word(dev);
