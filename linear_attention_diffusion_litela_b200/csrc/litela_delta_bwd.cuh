@@ -40,31 +40,31 @@ struct DeltaGrads {
 
 // ---------------------------------------------------------------------------------------
 // litela_delta_back: one CTA walks the chunks of one sequence and value head for 32 columns of the
-// state's gradient.  Per chunk, each product with M = 128 rows (tcgen05, fp32 accumulators in TMEM):
-//     X1 = [K; Q] G'                                            (the rows of K are used)
-//     X2 = X^T (-diag(beta) Z) + (P T)^T do,  Z = diag(e^(G_C - G)) K G'      (64 rows)
+// state's gradient, as litela_delta_chain.  Per chunk, each product with M = 128 rows:
+//     X1 = [K; Q] G'
+//     X2 = [X; P T]^T [do, -diag(beta) Z],  Z = diag(e^(G_C - G)) K G'
 //     X3 = [K; Q]^T [-diag(e^G) y; scale diag(e^G) do]
-// so that w = Z + X2 (T = I - diag(beta) X) and G' = e^G_C G' + X3.
-// The prepared block's image holds X^T and (P T)^T row by row, which here is a K-major A operand.  Its
-// rows are tokens in order, and so are K's and Q's here (not interleaved): Z and X2 have to meet in
-// the same TMEM lanes.  The warps of those lanes (quarters 0 and 1) do the rows of K; the others
-// prepare do.
+// Rows (TMEM lanes) of the first two alternate, 16 of K's or X's and 16 of Q's or P T's.  X1's rows of K
+// are used, and of X2 the columns of Z in X's rows and the columns of do in P T's rows, which are the
+// same tokens: w = Z + X2 (T = I - diag(beta) X) and G' = e^G_C G' + X3.
 template <int kD>
 struct BackCfg {
-  static constexpr int kCols = 32;
   static constexpr int kBlocks = kD > 64 ? 2 : 1;
-  static constexpr uint32_t kKQ = kBlocks * 16384;                // per block: 64 rows of K, 64 of Q
+  static constexpr uint32_t kKQ = kBlocks * 16384;                // per block: 64 rows of K and of Q
   static constexpr uint32_t kVLd = kCols * 2 + 16;
-  static constexpr uint32_t kOffPrep = kKQ;
-  static constexpr uint32_t kOffDo = (kKQ + kPrepBytes + 1023) / 1024 * 1024;   // do: 64 rows of 128 bytes, 32 columns
-  static constexpr uint32_t kOffV = kOffDo + 64 * 128;
+  // the factors and the second image behind them, the image on a 1024-byte boundary
+  static constexpr uint32_t kOffImage = kKQ + (kFactorBytes + 1023) / 1024 * 1024;
+  static constexpr uint32_t kOffFac = kOffImage - kFactorBytes;
+  static constexpr uint32_t kZTile = 64 * 128;                    // do and Z's three terms, two tiles
+  static constexpr uint32_t kOffZ = kOffImage + 2 * kImgHalf;
+  static constexpr uint32_t kOffV = kOffZ + 2 * kZTile;
   static constexpr uint32_t kStage = (kOffV + 64 * kVLd + 1023) / 1024 * 1024;
   static constexpr uint32_t kSTile = kD * 128, kRTile = 128 * 128;
   static constexpr uint32_t kOffS = kChainStages * kStage;
-  static constexpr uint32_t kOffR = kOffS + kSTile;               // Z, then y, in rows 0..63; do in rows 64..127
+  static constexpr uint32_t kOffR = kOffS + kSTile;               // y's and do's rows, three terms
   static constexpr uint32_t kOffBars = kOffR + 2 * kRTile;
   static constexpr uint32_t kSmemBytes = kOffBars + 256 + 1024;
-  static constexpr uint32_t kX1 = 0, kX2 = 64, kX3 = 160;
+  static constexpr uint32_t kX1 = 0, kX2 = 64, kX3 = 192, kTmem = 512;
   static_assert(kSmemBytes <= 232448, "shared memory above the 227 KB per-block limit");
 };
 enum : int { kErrBackLoad = 0x610, kErrBackMma = 0x620, kErrBackAcc = 0x630 };
@@ -75,8 +75,7 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
                   int* __restrict__ err) {
   using namespace sm100;
   using Cfg = BackCfg<kD>;
-  constexpr int kCols = Cfg::kCols, kN = 16, kParts = kD / kCols;
-  static_assert(kAccWarps == 8, "a warp has half of the columns");
+  constexpr int kParts = kD / kCols;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stile = smem + Cfg::kOffS;
@@ -94,8 +93,9 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
   const DeltaSeq sq = delta_seq(a, s);
   const int nchunk = (sq.len + kChunk - 1) / kChunk;
   const long long slot0 = delta_slot0(a, s, sq);
-  const uint8_t* blocks = prep + (slot0 * a.Hv + h) * (long long)kPrepBytes;
-  const long long block_step = (long long)a.Hv * kPrepBytes;
+  const uint8_t* blocks = prep + (slot0 * a.Hv + h) * (long long)kPrepSaveBytes + kPrepFactors;
+  const long long block_step = (long long)a.Hv * kPrepSaveBytes;
+  constexpr uint32_t kBlock = kFactorBytes + 2 * kImgHalf;
 
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
@@ -109,7 +109,7 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
     fence_mbar_init();
   }
   if (warp == kIssueWarp) {
-    tmem_alloc(tmem_holder, kChainTmem);
+    tmem_alloc(tmem_holder, Cfg::kTmem);
     tmem_relinquish();
   }
   tc_fence_before_sync();
@@ -118,9 +118,10 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
   const uint32_t tmem = *tmem_holder;
 
   if (warp < kAccWarps) {
-    const int quad = warp & 3, c0 = (warp >> 2) * kN, row = quad * 32 + lane, tok = row & 63;
-    const uint32_t ta = tmem + ((uint32_t)(quad * 32) << 16);
-    const bool has_state = row < kD, is_k = quad < 2;
+    const int quad = warp & 3, c0 = (warp >> 2) * kN, row = quad * 32 + lane;
+    const uint32_t ta = tmem + ((uint32_t)(quad * 32) << 16), tq = ta + (16u << 16);
+    const bool has_state = row < kD;
+    const int tok = quad * 16 + (lane >> 2), fc = c0 + (lane & 3) * 2;   // chain_frag: tokens tok and tok + 8
     const long long sbase = ((long long)s * a.Hv + h) * (kD * kD) + (long long)row * kD + part * kCols + c0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, int phase, int code) {
@@ -153,21 +154,20 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
       }
     if (nchunk > 0) {
       put_end(nchunk - 1, dot);
-      if (has_state) chain_put<kCols, 2, kN>(stile, Cfg::kSTile, row, c0, S);
+      if (has_state) chain_put<2>(stile, Cfg::kSTile, row, c0, S);
       hand(kBarS);
     }
     for (int it = 0; it < nchunk; ++it) {
       const int n = nchunk - 1 - it, st = it % kChainStages;
-      const uint8_t* stage = smem + st * Cfg::kStage;
+      uint8_t* stage = smem + st * Cfg::kStage;
       const long long sh = (slot0 + n) * a.Hv + h;
-      // W's row; the state before the chunk, this thread's row of it
-      float4 wrow[kN / 4];
+      // W; the state before the chunk, this thread's row of it
+      float2 wv[kN / 4];
       uint4 s0[kN / 4];
-      if (is_k) {
-        const float4* src = reinterpret_cast<const float4*>(saved.w + (sh * kChunk + tok) * kD + part * kCols + c0);
+      const float* wp = saved.w + (sh * kChunk + tok) * kD + part * kCols + fc;
 #pragma unroll
-        for (int i = 0; i < kN / 4; ++i) wrow[i] = __ldg(src + i);
-      }
+      for (int i = 0; i < kN / 4; ++i)
+        wv[i] = __ldg(reinterpret_cast<const float2*>(wp + (i & 1) * 8 * kD + (i >> 1) * 8));
       if (has_state && n > 0) {
         const uint8_t* src = saved.states + (sh * kParts + part) * (long long)Cfg::kSTile;
 #pragma unroll
@@ -177,82 +177,86 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
         }
       }
       wait(&full[st], it / kChainStages, 0);
-      const float* fac = reinterpret_cast<const float*>(stage + Cfg::kOffPrep + kPrepFactors);
-      const float decay = fac[kFacDecay + tok], to_end = fac[kFacToEnd + tok], beta = fac[kFacBeta + tok];
+      const float* fac = reinterpret_cast<const float*>(stage + Cfg::kOffFac);
+      float decay[2], to_end[2], beta[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        decay[i] = fac[kFacDecay + tok + 8 * i];
+        to_end[i] = fac[kFacToEnd + tok + 8 * i];
+        beta[i] = fac[kFacBeta + tok + 8 * i];
+      }
       const float chunk_decay = fac[kFacChunk];
-      uint4 v[kN / 8];   // v's row, or do's
+      uint32_t v[kN / 4];
+      F2 x[kN / 2], y[kN / 4], z[kN / 4];
 #pragma unroll
-      for (int i = 0; i < kN / 8; ++i)
-        v[i] = is_k ? *reinterpret_cast<const uint4*>(stage + Cfg::kOffV + tok * Cfg::kVLd + c0 * 2 + i * 16)
-                    : *reinterpret_cast<const uint4*>(stage + Cfg::kOffDo + sw128(tok, c0 + i * 8));
+      for (int i = 0; i < kN / 4; ++i) {
+        const int r = tok + (i & 1) * 8, c = fc + (i >> 1) * 8;
+        v[i] = *reinterpret_cast<const uint32_t*>(stage + Cfg::kOffV + r * Cfg::kVLd + c * 2);
+        const float f = a.scale * decay[i & 1];   // scale e^G do
+        x[i] = f2_mul(f2(f, f), f2_bf16(*reinterpret_cast<const uint32_t*>(stage + Cfg::kOffZ + sw128(r, c))));
+      }
+      chain_put_frag<3>(rtile, Cfg::kRTile, lane_of(tok) + 16, fc, x);
+      wait(&done[0], it, 1);
+      chain_frag<2>(ta + Cfg::kX1, c0, z);
+#pragma unroll
+      for (int i = 0; i < kN / 4; ++i) {
+        const float f = to_end[i & 1], mb = -beta[i & 1];
+        z[i] = f2_mul(f2(f, f), z[i]);
+        x[i] = f2_mul(f2(mb, mb), z[i]);
+      }
+      chain_put_frag<3, 1>(stage + Cfg::kOffZ, Cfg::kZTile, tok, fc, x);
+      hand(kBarR);
+      wait(&done[1], it, 2);
+      chain_frag<3>(ta + Cfg::kX2 + 32, c0, x);
+      chain_frag<1>(tq + Cfg::kX2, c0, y);
+#pragma unroll
+      for (int i = 0; i < kN / 4; ++i) {
+        const float b = beta[i & 1], md = -decay[i & 1];
+        z[i] = f2_add(z[i], f2_add(x[i], y[i]));   // w
+        y[i] = f2_mul(f2(b, b), z[i]);
+        x[i] = f2_mul(f2(md, md), y[i]);
+      }
+      chain_put_frag<3>(rtile, Cfg::kRTile, lane_of(tok), fc, x);
+      hand(kBarU);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
-      F2 x[kN / 2], z[kN / 2];
-      if (!is_k) {   // scale e^G do
-        const F2 f = f2(a.scale * decay, a.scale * decay);
+      if (lane == 0) mbar_arrive(&empty[st]);   // the stage has been read
+      // while the third product runs: dv, y and the rows' shares
+      F2 wdot[2] = {f2(0.f, 0.f), f2(0.f, 0.f)}, vdot[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+      uint8_t* yd = gr.y + ((sh * 2 * kChunk + tok) * kD + part * kCols + fc) * 2;
 #pragma unroll
-        for (int i = 0; i < kN / 2; ++i) x[i] = f2_mul(f, f2_bf16(reinterpret_cast<const uint32_t*>(v)[i]));
-        chain_put<kCols, 3, kN>(rtile, Cfg::kRTile, 64 + tok, c0, x);
-        hand(kBarR);
-        hand(kBarU);
-      } else {
-        wait(&done[0], it, 1);
-        chain_acc<kCols, 2, kN>(ta + Cfg::kX1, c0, z);
-        const F2 f = f2(to_end, to_end), mb = f2(-beta, -beta);
+      for (int i = 0; i < kN / 4; ++i) {
+        const int t = tok + (i & 1) * 8;
+        wdot[i & 1] = f2_fma(z[i], f2(wv[i].x, wv[i].y), wdot[i & 1]);
+        vdot[i & 1] = f2_fma(y[i], f2_bf16(v[i]), vdot[i & 1]);
+        const uint32_t hi = next_term(y[i], false), lo = next_term(y[i], true);   // y's pair; hi is dv
+        uint32_t* dst = reinterpret_cast<uint32_t*>(yd + ((i & 1) * 8 * kD + (i >> 1) * 8) * 2);
+        dst[0] = hi;
+        dst[kChunk * kD / 2] = lo;
+        if (n * kChunk + t < sq.len)
+          *reinterpret_cast<uint32_t*>(const_cast<__nv_bfloat16*>(delta_row(gr.dv, sq, n * kChunk + t, h)) + part * kCols +
+                                       fc + (i >> 1) * 8) = hi;
+      }
 #pragma unroll
-        for (int i = 0; i < kN / 2; ++i) {
-          z[i] = f2_mul(f, z[i]);
-          x[i] = f2_mul(mb, z[i]);
-        }
-        chain_put<kCols, 3, kN>(rtile, Cfg::kRTile, tok, c0, x);
-        hand(kBarR);
-        wait(&done[1], it, 2);
-        chain_acc<kCols, 3, kN>(ta + Cfg::kX2, c0, x);
-        const F2 b2 = f2(beta, beta), d2 = f2(-decay, -decay);
-        F2 y[kN / 2];
-#pragma unroll
-        for (int i = 0; i < kN / 2; ++i) {
-          z[i] = f2_add(z[i], x[i]);   // w
-          y[i] = f2_mul(b2, z[i]);
-          x[i] = f2_mul(d2, y[i]);
-        }
-        chain_put<kCols, 3, kN>(rtile, Cfg::kRTile, tok, c0, x);
-        hand(kBarU);
-        // while the third product runs: dv, y and the rows' shares
-        F2 wdot = f2(0.f, 0.f), vdot = f2(0.f, 0.f);
-        uint32_t o[kN / 2], ol[kN / 2];   // y's pair; the first term is dv
-#pragma unroll
-        for (int i = 0; i < kN / 2; ++i) {
-          const float* wr = reinterpret_cast<const float*>(wrow) + 2 * i;
-          wdot = f2_fma(z[i], f2(wr[0], wr[1]), wdot);
-          vdot = f2_fma(y[i], f2_bf16(reinterpret_cast<const uint32_t*>(v)[i]), vdot);
-          o[i] = next_term(y[i], false);
-          ol[i] = next_term(y[i], true);
-        }
-        uint4* yd = reinterpret_cast<uint4*>(gr.y + ((sh * 2 * kChunk + tok) * kD + part * kCols + c0) * 2);
-#pragma unroll
-        for (int i = 0; i < kN / 8; ++i) {
-          yd[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          yd[kChunk * kD / 8 + i] = make_uint4(ol[4 * i], ol[4 * i + 1], ol[4 * i + 2], ol[4 * i + 3]);
-        }
-        const float2 wd = f2_out(wdot), vd = f2_out(vdot);
-        float* rw = gr.rows + ((sh * kParts + part) * 2 * 2 + (warp >> 2)) * kChunk + tok;
-        rw[0] = wd.x + wd.y;
-        rw[2 * kChunk] = vd.x + vd.y;
-        if (n * kChunk + tok < sq.len) {
-          uint4* dst = reinterpret_cast<uint4*>(const_cast<__nv_bfloat16*>(delta_row(gr.dv, sq, n * kChunk + tok, h)) +
-                                                part * kCols + c0);
-#pragma unroll
-          for (int i = 0; i < kN / 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+      for (int i = 0; i < 2; ++i) {
+        const float2 w2 = f2_out(wdot[i]), v2 = f2_out(vdot[i]);
+        float wd = w2.x + w2.y, vd = v2.x + v2.y;
+        wd += __shfl_xor_sync(0xffffffffu, wd, 1);
+        vd += __shfl_xor_sync(0xffffffffu, vd, 1);
+        wd += __shfl_xor_sync(0xffffffffu, wd, 2);
+        vd += __shfl_xor_sync(0xffffffffu, vd, 2);
+        float* rw = gr.rows + ((sh * kParts + part) * 2 * 2 + (warp >> 2)) * kChunk + tok + 8 * i;
+        if ((lane & 3) == 0) {
+          rw[0] = wd;
+          rw[2 * kChunk] = vd;
         }
       }
       wait(&done[2], it, 3);
       if (has_state) {
-        chain_acc<kCols, 3, kN>(ta + Cfg::kX3, c0, x);
+        chain_acc<3>(ta + Cfg::kX3, c0, x);
         const F2 d2 = f2(chunk_decay, chunk_decay);
 #pragma unroll
         for (int i = 0; i < kN / 2; ++i) S[i] = f2_fma(d2, S[i], x[i]);
-        if (n > 0) chain_put<kCols, 2, kN>(stile, Cfg::kSTile, row, c0, S);
+        if (n > 0) chain_put<2>(stile, Cfg::kSTile, row, c0, S);
       }
       if (n > 0) {
         hand(kBarS);
@@ -274,18 +278,16 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
         *reinterpret_cast<float4*>(gr.dstate_in + sbase + i) =
             make_float4(f2_out(S[i / 2]).x, f2_out(S[i / 2]).y, f2_out(S[i / 2 + 1]).x, f2_out(S[i / 2 + 1]).y);
   } else if (warp == kIssueWarp) {
-    constexpr uint32_t idesc_1 = idesc_bf16_f32(128, 64, false, true);     // [K; Q] G'
-    constexpr uint32_t idesc_z = idesc_bf16_f32(128, 96, false, true);     // X^T Z, three terms
-    constexpr uint32_t idesc_z2 = idesc_bf16_f32(128, 64, false, true);    // two terms
-    constexpr uint32_t idesc_do = idesc_bf16_f32(128, 32, false, true);    // (P T)^T do
-    constexpr uint32_t idesc_3 = idesc_bf16_f32(128, 96, true, true);      // [K; Q]^T ..
-    const uint64_t sdesc = smem_desc(smem_u32(stile), 1024, 1024, kSwizzle128B);
-    const uint64_t rdesc = smem_desc(smem_u32(rtile), Cfg::kRTile, 1024, kSwizzle128B);
-    const uint64_t kqdesc = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
-    const uint64_t imgdesc = smem_desc(smem_u32(smem) + Cfg::kOffPrep, 16, 1024, kSwizzle128B);
-    const uint64_t dodesc = smem_desc(smem_u32(smem) + Cfg::kOffDo, 1024, 1024, kSwizzle128B);
+    constexpr uint32_t idesc_1 = idesc_bf16_f32(128, 64, false, true);    // [K; Q] G'
+    constexpr uint32_t idesc_z = idesc_bf16_f32(128, 128, true, true);    // [X; P T]^T [do, three terms of Z]
+    constexpr uint32_t idesc_3 = idesc_bf16_f32(128, 96, true, true);     // the lo terms' two of Z; [K; Q]^T ..
+    const Desc sdesc = desc_halves(smem_u32(stile), 1024, 1024, kSwizzle128B);
+    const Desc rdesc = desc_halves(smem_u32(rtile), Cfg::kRTile, 1024, kSwizzle128B);
+    const Desc kqdesc = desc_halves(smem_u32(smem), 16, 1024, kSwizzle128B);
+    const Desc imgdesc = desc_halves(smem_u32(smem) + Cfg::kOffImage, kImgBlock, 1024, kSwizzle128B);
+    const Desc zdesc = desc_halves(smem_u32(smem) + Cfg::kOffZ, Cfg::kZTile, 1024, kSwizzle128B);
     // [K; Q]^T: M over channels, 128 rows.  d <= 64: rows 64 on of the product take whatever follows
-    const uint64_t ktdesc = smem_desc(smem_u32(smem), kD > 64 ? 16384 : 1024, 1024, kSwizzle128B);
+    const Desc ktdesc = desc_halves(smem_u32(smem), kD > 64 ? 16384 : 1024, 1024, kSwizzle128B);
     bool ok = true;
     auto wait = [&](uint64_t* bar, int phase, int code) {
       if (ok && lane == 0) ok = mbar_spin(bar, phase & 1, abort_flag, err, kErrBackMma | code);
@@ -294,7 +296,7 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
     if (nchunk > 0) wait(&full[0], 0, 0);
     for (int it = 0; it < nchunk; ++it) {
       const int n = nchunk - 1 - it, st = it % kChainStages;
-      const uint64_t off = st * (Cfg::kStage / 16);
+      const uint32_t off = st * (Cfg::kStage / 16);
       bar_sync(kBarS, kBarThreads);
       tc_fence_after_sync();
       if (lane == 0) {
@@ -303,7 +305,7 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
         if (ok) {
 #pragma unroll
           for (int ks = 0; ks < kD / 16; ++ks)
-            umma_bf16(tmem + Cfg::kX1, kqdesc + off + (ks / 4) * 1024 + (ks % 4) * 2, sdesc + ks * 128, idesc_1, ks > 0);
+            umma(tmem + Cfg::kX1, kqdesc + off + (ks / 4) * 1024 + (ks % 4) * 2, sdesc + ks * 128, idesc_1, ks > 0);
           umma_commit(&done[0]);
         }
       }
@@ -311,21 +313,12 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
       bar_sync(kBarR, kBarThreads);
       tc_fence_after_sync();
       if (ok && lane == 0) {
-        // the image's columns: 16 tokens of X, the same 16 of P T, ..
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          umma_bf16(tmem + Cfg::kX2, imgdesc + off + (ks / 2) * (kImgBlock / 16) + (ks % 2) * 4, rdesc + ks * 128, idesc_z,
-                    ks > 0);
+          umma(tmem + Cfg::kX2, imgdesc + off + ks * 128, zdesc + off + ks * 128, idesc_z, ks > 0);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          umma_bf16(tmem + Cfg::kX2, imgdesc + off + (kImgHalf + (ks / 2) * kImgBlock) / 16 + (ks % 2) * 4, rdesc + ks * 128,
-                    idesc_z2, 1u);
-#pragma unroll
-        for (int t = 1; t >= 0; --t)
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            umma_bf16(tmem + Cfg::kX2, imgdesc + off + (t * kImgHalf + (ks / 2) * kImgBlock) / 16 + (ks % 2) * 4 + 2,
-                      dodesc + off + ks * 128, idesc_do, 1u);
+          umma(tmem + Cfg::kX2, imgdesc + off + kImgHalf / 16 + ks * 128, zdesc + off + ks * 128, idesc_3, 1u);
         umma_commit(&done[1]);
       }
       __syncwarp();
@@ -336,7 +329,7 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
         if (ok) {
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            umma_bf16(tmem + Cfg::kX3, ktdesc + off + ks * 128, rdesc + ks * 128, idesc_3, ks > 0);
+            umma(tmem + Cfg::kX3, ktdesc + off + ks * 128, rdesc + ks * 128, idesc_3, ks > 0);
           umma_commit(&done[2]);
           umma_commit(&empty[st]);
         }
@@ -354,9 +347,9 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
     int issued = 0;
     constexpr int kC = kD / 8, kStep = kLoadThreads / kC, kVC = kCols / 8, kVStep = kLoadThreads / kVC;
     const int r0 = t / kC, c = t % kC, vr0 = t / kVC, vc = t % kVC;
-    const uint32_t kq0 = smem_u32(smem) + (c / 8) * 16384 + sw128(r0, (c % 8) * 8);
+    const uint32_t kq0 = smem_u32(smem) + (c / 8) * 16384 + sw128(lane_of(r0), (c % 8) * 8);
     const uint32_t v0 = smem_u32(smem) + Cfg::kOffV + vr0 * Cfg::kVLd + vc * 16;
-    const uint32_t do0 = smem_u32(smem) + Cfg::kOffDo;
+    const uint32_t do0 = smem_u32(smem) + Cfg::kOffZ;
     const long long kstep = kStep * a.k.st, qstep = kStep * a.q.st, vstep = kVStep * a.v.st, dstep = kVStep * gr.dout.st;
     for (int it = 0; it < nchunk; ++it) {
       const int n = nchunk - 1 - it, st = it % kChainStages;
@@ -364,8 +357,8 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
                       mbar_wait(&empty[st], (it / kChainStages - 1) & 1, abort_flag, err, kErrBackLoad | st);
       if (!__all_sync(0xffffffffu, ok)) break;
       if (t == 0) {
-        mbar_arrive_expect_tx(&full[st], kPrepBytes);
-        bulk_load(smem + st * Cfg::kStage + Cfg::kOffPrep, blocks + n * block_step, kPrepBytes, &full[st]);
+        mbar_arrive_expect_tx(&full[st], kBlock);
+        bulk_load(smem + st * Cfg::kStage + Cfg::kOffFac, blocks + n * block_step, kBlock, &full[st]);
       }
       issued = it + 1;
       const int n0 = n * kChunk, len = min(kChunk, sq.len - n0);
@@ -376,10 +369,10 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
       const __nv_bfloat16* dp = delta_row(gr.dout, sq, n0 + vr0, h) + part * kCols + vc * 8;
 #pragma unroll
       for (int i = 0; i < kChunk / kStep; ++i) {
-        const uint32_t o = (dkq ^ (((i * kStep) & 7) << 4)) + i * kStep * 128;
+        const uint32_t o = (dkq ^ (((i * kStep) & 7) << 4)) + lane_of(i * kStep) * 128;
         const bool real = r0 + i * kStep < len;
         cp_async_16(o, real ? kp : a.k.p, real);
-        cp_async_16(o + 8192, real ? qp : a.q.p, real);
+        cp_async_16(o + 2048, real ? qp : a.q.p, real);
         kp += kstep;
         qp += qstep;
       }
@@ -403,7 +396,7 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
         }
         prefetch_l2(delta_row(a.v, sq, r, h) + part * kCols);
         prefetch_l2(delta_row(gr.dout, sq, r, h) + part * kCols);
-        if (t == 0) bulk_prefetch_l2(blocks + (n - 1) * block_step, kPrepBytes);
+        if (t == 0) bulk_prefetch_l2(blocks + (n - 1) * block_step, kBlock);
       }
       cp_async_commit();
       cp_async_wait<0>();
@@ -419,7 +412,7 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
   __syncthreads();
   if (warp == kIssueWarp) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem, kChainTmem);
+    tmem_dealloc(tmem, Cfg::kTmem);
   }
 }
 
@@ -525,7 +518,7 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
 #pragma unroll
       for (int i = 0; i < 2 * kChunk / kStep; ++i) cp_async_16(dst + i * kStep * (Cfg::kLd * 2), src + i * kThreads * 16, true);
     }
-    if (tid < (int)kFactorBytes / 16) cp_async_16(base + Cfg::kOffFac + tid * 16, prep + sh * kPrepBytes + kPrepFactors + tid * 16, true);
+    if (tid < (int)kFactorBytes / 16) cp_async_16(base + Cfg::kOffFac + tid * 16, prep + sh * kPrepSaveBytes + kPrepFactors + tid * 16, true);
     load_tile(0);
     cp_async_commit();
     load_tile(1);

@@ -48,6 +48,9 @@ __host__ __device__ constexpr int lane_of(int token) { return 32 * (token / 16) 
 constexpr uint32_t kPrepFactors = 2 * kImgHalf;
 constexpr uint32_t kFactorBytes = 2304;
 constexpr uint32_t kPrepBytes = kPrepFactors + kFactorBytes;
+// A training step's block has a second image behind it, X and P T not transposed: rows are tokens i,
+// columns as above for tokens j, (i, j) of X and of P T (the gradient's products take X^T and (P T)^T)
+constexpr uint32_t kPrepSaveBytes = kPrepBytes + 2 * kImgHalf;
 // fp32 at kPrepFactors: e^G [64], e^(G_C - G) [64] (0 behind the end), beta [64] (0 behind the
 // end), then e^G_C and (int32) the first token of the chunk with a non-finite L or P, or 64
 constexpr int kFacDecay = 0, kFacToEnd = 64, kFacBeta = 128, kFacChunk = 192, kFacBad = 193;
@@ -201,6 +204,11 @@ __device__ __forceinline__ void ldmatrix_x4_t(uint32_t* r, uint32_t addr) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
 }
+__device__ __forceinline__ void stmatrix_x4(uint32_t addr, const uint32_t* r) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
 __device__ __forceinline__ void stmatrix_x4_t(uint32_t addr, const uint32_t* r) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3])
@@ -226,7 +234,7 @@ __device__ __forceinline__ void mma_halves(float (*d)[4], const uint32_t* a, con
   for (int n = 0; n < kTiles; ++n) sm100::mma_16816(d[n], a, b[n]);
 }
 
-template <int kD>
+template <int kD, bool kSave>
 __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const DeltaArgs a, uint8_t* __restrict__ prep) {
   using namespace sm100;
   using Cfg = PrepCfg<kD>;
@@ -293,7 +301,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
     *bad = kChunk;
   }
   __syncthreads();
-  uint8_t* dst = prep + ((long long)slot * a.Hv + h) * kPrepBytes;
+  uint8_t* dst = prep + ((long long)slot * a.Hv + h) * (kSave ? kPrepSaveBytes : kPrepBytes);
   float* fac = reinterpret_cast<float*>(dst + kPrepFactors);
   if (tid < kChunk) {
     const double d = G[tid] - G[tid & ~15];
@@ -565,40 +573,75 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
         split_bf16(acc[n][2], acc[n][3], v[1], v[3]);
         stmatrix_x4_t((((xrow ^ 32) ^ ((rb & 1) << 6)) + (rb >> 1) * kImgBlock) + n * 1024, v);
       }
+    if constexpr (kSave) {   // the second image, hi in L's place and lo in P's
+      __syncthreads();       // (P has been read)
+      const uint32_t term2 = smem_u32((lane >> 4) ? Pf : Lf);
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        if (n <= rb) {
+          uint32_t v[4];
+          split_bf16(acc[n][0], acc[n][1], v[0], v[2]);
+          split_bf16(acc[n][2], acc[n][3], v[1], v[3]);
+          stmatrix_x4(term2 + img_off(16 * rb + k8 + l8, 8 * (tile0 + n), 1), v);
+        }
+      // X: 8 x 8 blocks (rows 8 ib, columns 8 jb) from the first image, transposed; lane / 8: hi of jb
+      // and jb + 1, lo of them
+#pragma unroll 1
+      for (int i = w; i < 32; i += 8) {
+        const int ib = i >> 2, jb = (i & 3) * 2 + ((lane >> 3) & 1);
+        uint32_t v[4];
+        ldmatrix_x4_t(v, term + img_off(8 * jb + l8, 8 * ib, 0));
+        stmatrix_x4(term2 + img_off(8 * ib + l8, 8 * jb, 0), v);
+      }
+      // right of its diagonal blocks P T is zero
+      if (tid < 192) {
+        const int blk = tid >> 5, cb = blk < 1 ? 1 : blk < 3 ? 2 : 3, r = blk - (cb == 1 ? 0 : cb == 2 ? 1 : 3);
+        const uint32_t o = img_off(16 * r + ((lane >> 1) & 15), 16 * cb + (lane & 1) * 8, 1);
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(Lf) + o) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(Pf) + o) = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
   }
   if (tid == 0) reinterpret_cast<int*>(dst + kPrepFactors)[kFacBad] = *bad;
   fence_proxy_async_smem();
   __syncthreads();
   if (tid == 0) {
     bulk_store(dst, smem, 2 * kImgHalf);
+    if (kSave) {
+      bulk_store(dst + kPrepBytes, Lf, kImgHalf);
+      bulk_store(dst + kPrepBytes + kImgHalf, Pf, kImgHalf);
+    }
     bulk_commit_group();
     bulk_wait_group_read<0>();
   }
 }
 
 // ---------------------------------------------------------------------------------------
-// litela_delta_chain: one CTA walks the chunks of one sequence and value head for kCols of the
-// state's columns (columns do not meet, so a state is cut by columns over CTAs).
+// litela_delta_chain: one CTA walks the chunks of one sequence and value head for 32 of the state's
+// columns (columns do not meet, so a state is cut by columns over CTAs).  64 columns a CTA took 3.2 us
+// a chunk against 2.0 (d = 128): less for many equal sequences (1.6 a half), but a long sequence among
+// others, or few heads, wait for the longest chain of chunks.
 //
 // Three tcgen05 products per chunk, each with M = 128 rows, fp32 accumulators in TMEM:
 //     X1 = [K; Q] S0           (rows: 16 of K, 16 of Q, 16 of K ..; K dimension d)
 //     X2 = [X; P T] R          (rows alike; K dimension 64)
 //     X3 = K^T (e^(G_C - G) U) (rows: d; K dimension 64)
-// Between them eight warps take the accumulators to registers, form E and R, then W and U, then the new state,
-// and write them as bf16 pairs into shared memory as the next product's B operand.  The chain of
-// these six steps is what a chunk costs; the loads of the next chunks, the output rows' arithmetic
-// and their stores run beside it.  All B operands are tiles of 128-byte rows (row: K index, 64 bf16 columns,
-// MN-major): with kCols = 64 one tile per bf16 term; with kCols = 32 two terms side by side in a
-// tile, whose products land in column ranges of their own that the readers add.
+// Between them eight warps take the accumulators to registers, form E and R, then W and U, then the
+// new state, and write them in bf16 terms into shared memory as the next product's B operand.  The
+// chain of these six steps is what a chunk costs; the loads of the next chunks, the output rows'
+// arithmetic and their stores run beside it.  All B operands are tiles of 128-byte rows (row: K index,
+// 64 bf16 columns, MN-major), two terms of 32 columns side by side in a tile, whose products land in
+// column ranges of their own that the readers add.
 //
 // Warps: 0-7 accumulators (warp % 4: TMEM lanes; warp / 4: which half of the columns), 8 and 9 load
 // (cp.async for the strided K, Q, V rows; one bulk copy for the prepared block), 10 issues the
 // products.  The accumulator warps hand over with named barriers (one-way ~40 cycles; an mbarrier wait
-// costs ~170 here even when its phase is over), the tensor core with mbarriers, which one lane of a
-// warp polls; waits for loads stand where a warp would idle anyway.  A tcgen05 product of 16 of the K dimension takes ~47
-// cycles whatever N <= 96 is, so the terms go side by side where that saves products.
+// costs ~170 here even when its phase is over), the tensor core with mbarriers; waits for loads stand
+// where a warp would idle anyway.  A tcgen05 product of 16 of the K dimension takes ~47 cycles whatever
+// N <= 96 is (its operands' shared-memory bytes), so terms go side by side where that saves products.
 // Every mbarrier wait is bounded; after a time-out (recorded in *err) all roles run their loops to
 // the end without waiting, so that the named barriers stay matched.
+constexpr int kCols = 32;   // of the state, a CTA's
 constexpr int kChainStages = 2;
 constexpr int kAccWarps = 8;
 constexpr int kIssueWarp = kAccWarps + 2;   // on a scheduler whose accumulator warps have rows of Q
@@ -611,7 +654,20 @@ enum : int { kErrChainLoad = 0x510, kErrChainMma = 0x520, kErrChainAcc = 0x530 }
 enum : int { kBarS = 1, kBarR = 2, kBarU = 3 };
 constexpr int kBarThreads = (kAccWarps + 1) * 32;
 
-template <int kD, int kCols>
+// a shared-memory descriptor in halves: an offset of n bytes adds n / 16 to the lower one
+struct Desc {
+  uint32_t lo, hi;
+};
+__device__ __forceinline__ Desc desc_halves(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
+  const uint64_t d = sm100::smem_desc(saddr, lbo, sbo, swizzle);
+  return Desc{(uint32_t)d, (uint32_t)(d >> 32)};
+}
+__device__ __forceinline__ Desc operator+(Desc d, uint32_t n) { return Desc{d.lo + n, d.hi}; }
+__device__ __forceinline__ void umma(uint32_t d_tmem, Desc a, Desc b, uint32_t idesc, uint32_t accumulate) {
+  sm100::umma_bf16(d_tmem, a.lo, a.hi, b.lo, b.hi, idesc, accumulate);
+}
+
+template <int kD>
 struct ChainCfg {
   static constexpr int kBlocks = kD > 64 ? 2 : 1;                 // 64-channel blocks of K and Q
   static constexpr uint32_t kKQ = kBlocks * 16384;                // per block: 64 rows of K and of Q
@@ -620,60 +676,52 @@ struct ChainCfg {
   static constexpr uint32_t kOffPrep = kKQ;
   static constexpr uint32_t kOffV = kKQ + kPrepBytes;
   static constexpr uint32_t kStage = (kOffV + kV + 1023) / 1024 * 1024;
-  static constexpr int kSTiles = kCols == 64 ? 2 : 1;             // tiles of S0 (two terms)
-  static constexpr int kRTiles = kCols == 64 ? 3 : 2;             // tiles of R and U (three terms)
-  static constexpr uint32_t kSTile = kD * 128, kRTile = 64 * 128;
+  static constexpr uint32_t kSTile = kD * 128;                    // S0 (two terms)
+  static constexpr uint32_t kRTile = 64 * 128;                    // R and U (three terms, two tiles)
   static constexpr uint32_t kOffS = kChainStages * kStage;
-  static constexpr uint32_t kOffR = kOffS + kSTiles * kSTile;
-  static constexpr uint32_t kOffBars = kOffR + kRTiles * kRTile;
-  // TMEM columns of the three products
-  static constexpr uint32_t kX1 = 0, kX2 = 64, kX3 = kCols == 64 ? 128 : 160;
+  static constexpr uint32_t kOffR = kOffS + kSTile;
+  static constexpr uint32_t kOffBars = kOffR + 2 * kRTile;
+  static constexpr uint32_t kX1 = 0, kX2 = 64, kX3 = 160;         // TMEM columns of the three products
   static constexpr uint32_t kSmemBytes = kOffBars + 256 + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory above the 227 KB per-block limit");
   static_assert(kLoadThreads == kChunk, "a loading thread prefetches one row");
 };
 
-// A warp's share of a product whose B operand has kTerms terms.  chain_acc: its 32 lanes, kN columns
-// from c on, a lane's columns to its thread.  chain_frag: 16 of its lanes, 8 kG columns from c on: thread
-// t gets the rows t / 4 and t / 4 + 8, columns 2 (t % 4) of each 8, as x[2 g + half].
-template <int kN>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r) {
-  if constexpr (kN == 32) sm100::tmem_ld_x32(taddr, r);
-  if constexpr (kN == 16) sm100::tmem_ld_x16(taddr, r);
-  if constexpr (kN == 8) sm100::tmem_ld_x8(taddr, r);
-}
-template <int kCols, int kTerms, int kN>
-__device__ __forceinline__ void chain_acc(uint32_t taddr, int c, F2* x) {
-  constexpr int kRanges = kCols == 64 ? 1 : kTerms;
-  uint32_t r[kRanges][kN];
-#pragma unroll
-  for (int t = 0; t < kRanges; ++t) tmem_ld<kN>(taddr + 32 * t + c, r[t]);
-  sm100::tmem_wait_ld();
+// A warp's share of a product whose B operand has kTerms terms, 16 columns from c on (all of one kind: fp32 pairs).
+// chain_acc: its 32 lanes, a lane's columns to its thread.  chain_frag: 16 of its lanes: thread t gets
+// the rows t / 4 and t / 4 + 8, columns 2 (t % 4) of each 8, as x[2 g + half].
+constexpr int kN = kCols * 4 / kAccWarps;   // columns of an accumulator warp
+static_assert(kN == 16, "an accumulator warp has 16 columns");
+template <int kTerms>
+__device__ __forceinline__ void add_terms(const uint32_t (*r)[kN], F2* x) {
   auto get = [&](int t, int i) { return f2(__uint_as_float(r[t][2 * i]), __uint_as_float(r[t][2 * i + 1])); };
 #pragma unroll
   for (int i = 0; i < kN / 2; ++i) {   // the small terms first
-    x[i] = get(kRanges - 1, i);
+    x[i] = get(kTerms - 1, i);
 #pragma unroll
-    for (int t = kRanges - 2; t >= 0; --t) x[i] = f2_add(x[i], get(t, i));
+    for (int t = kTerms - 2; t >= 0; --t) x[i] = f2_add(x[i], get(t, i));
   }
 }
-template <int kCols, int kTerms, int kG>
-__device__ __forceinline__ void chain_frag(uint32_t taddr, int c, F2* x) {
-  constexpr int kRanges = kCols == 64 ? 1 : kTerms;
-  uint32_t r[kRanges][4 * kG];
+template <int kTerms>
+__device__ __forceinline__ void chain_acc(uint32_t taddr, int c, F2* x) {
+  uint32_t r[kTerms][kN];
 #pragma unroll
-  for (int t = 0; t < kRanges; ++t) {
-    if constexpr (kG == 1) sm100::tmem_ld_16x256b_x1(taddr + 32 * t + c, r[t]);
-    if constexpr (kG == 2) sm100::tmem_ld_16x256b_x2(taddr + 32 * t + c, r[t]);
-    if constexpr (kG == 4) sm100::tmem_ld_16x256b_x4(taddr + 32 * t + c, r[t]);
-  }
+  for (int t = 0; t < kTerms; ++t) sm100::tmem_ld_x16(taddr + 32 * t + c, r[t]);
+  sm100::tmem_wait_ld();
+  add_terms<kTerms>(r, x);
+}
+template <int kTerms>
+__device__ __forceinline__ void chain_frag(uint32_t taddr, int c, F2* x) {
+  uint32_t r[kTerms][kN / 2];
+#pragma unroll
+  for (int t = 0; t < kTerms; ++t) sm100::tmem_ld_16x256b_x2(taddr + 32 * t + c, r[t]);
   sm100::tmem_wait_ld();
   auto get = [&](int t, int i) { return f2(__uint_as_float(r[t][2 * i]), __uint_as_float(r[t][2 * i + 1])); };
 #pragma unroll
-  for (int i = 0; i < 2 * kG; ++i) {
-    x[i] = get(kRanges - 1, i);
+  for (int i = 0; i < kN / 4; ++i) {
+    x[i] = get(kTerms - 1, i);
 #pragma unroll
-    for (int t = kRanges - 2; t >= 0; --t) x[i] = f2_add(x[i], get(t, i));
+    for (int t = kTerms - 2; t >= 0; --t) x[i] = f2_add(x[i], get(t, i));
   }
 }
 
@@ -684,8 +732,9 @@ __device__ __forceinline__ uint32_t next_term(F2& y, bool last) {
   if (!last) y = f2_fma(f2_bf16(w), f2(-1.f, -1.f), y);
   return w;
 }
-// Into a B operand: kN values (pairs) of a row, columns c .. c + kN - 1, in kTerms bf16 terms
-template <int kCols, int kTerms, int kN>
+// Into a B operand's tiles: the thread's kN values (pairs) of a row, columns c .. c + kN - 1, in kTerms
+// bf16 terms
+template <int kTerms>
 __device__ __forceinline__ void chain_put(uint8_t* tile, uint32_t tile_bytes, int row, int c, const F2* x) {
 #pragma unroll
   for (int i = 0; i < kN; i += 8) {
@@ -695,43 +744,39 @@ __device__ __forceinline__ void chain_put(uint8_t* tile, uint32_t tile_bytes, in
       uint32_t w[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) w[q] = next_term(y[q], t + 1 == kTerms);
-      uint8_t* dst = kCols == 64 ? tile + t * tile_bytes + sw128(row, c + i)
-                                 : tile + (t / 2) * tile_bytes + sw128(row, (t & 1) * 32 + c + i);
-      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(tile + (t / 2) * tile_bytes + sw128(row, (t & 1) * 32 + c + i)) =
+          make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
-// ... a thread's part of chain_frag's arrangement; row: of its first half, c: its first column
-template <int kCols, int kTerms, int kG>
+// ... a thread's part of chain_frag's arrangement; row: of its first half, c: its first column; the
+// first term goes to the tiles' columns 32 kFirst on
+template <int kTerms, int kFirst = 0>
 __device__ __forceinline__ void chain_put_frag(uint8_t* tile, uint32_t tile_bytes, int row, int c, const F2* x) {
 #pragma unroll
-  for (int i = 0; i < 2 * kG; ++i) {
+  for (int i = 0; i < kN / 4; ++i) {
     F2 y = x[i];
     const int r = row + (i & 1) * 8, cc = c + (i >> 1) * 8;
 #pragma unroll
-    for (int t = 0; t < kTerms; ++t) {
-      uint8_t* dst = kCols == 64 ? tile + t * tile_bytes + sw128(r, cc)
-                                 : tile + (t / 2) * tile_bytes + sw128(r, (t & 1) * 32 + cc);
-      *reinterpret_cast<uint32_t*>(dst) = next_term(y, t + 1 == kTerms);
-    }
+    for (int t = 0; t < kTerms; ++t)
+      *reinterpret_cast<uint32_t*>(tile + ((t + kFirst) / 2) * tile_bytes + sw128(r, ((t + kFirst) & 1) * 32 + cc)) =
+          next_term(y, t + 1 == kTerms);
   }
 }
 
 // What a training step's forward leaves for its backward, per chunk slot and value head: S0 as the B
-// operand tiles of the chain (kCols = 32: d rows x 128 bytes for each 32 columns, two terms), and
+// operand tiles of the chain (d rows x 128 bytes for each 32 columns, two terms), and
 // W in fp32 [64, d].
 struct DeltaSaved {
   uint8_t* states;
   float* w;
 };
 
-template <int kD, int kCols, bool kSave>
+template <int kD, bool kSave>
 __global__ void __launch_bounds__(kChainThreads, 1)
 litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, const DeltaSaved saved, int* __restrict__ err) {
   using namespace sm100;
-  using Cfg = ChainCfg<kD, kCols>;
-  static_assert(kCols == 32 || !kSave, "saved states are tiles of 32 columns");
-  constexpr int kN = kCols * 4 / kAccWarps;   // columns of an accumulator warp
+  using Cfg = ChainCfg<kD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stile = smem + Cfg::kOffS;
@@ -751,8 +796,9 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, const De
   const DeltaSeq sq = delta_seq(a, s);
   const int nchunk = (sq.len + kChunk - 1) / kChunk;
   const long long slot0 = delta_slot0(a, s, sq);
-  const uint8_t* blocks = prep + (slot0 * a.Hv + h) * (long long)kPrepBytes;
-  const long long block_step = (long long)a.Hv * kPrepBytes;
+  constexpr long long kBlock = kSave ? kPrepSaveBytes : kPrepBytes;
+  const uint8_t* blocks = prep + (slot0 * a.Hv + h) * kBlock;
+  const long long block_step = a.Hv * kBlock;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kChainStages; ++i) {
@@ -775,7 +821,6 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, const De
   const uint32_t tmem = *tmem_holder;
 
   if (warp < kAccWarps) {
-    constexpr int kG = kN / 8;
     const int quad = warp & 3, c0 = (warp >> 2) * kN, row = quad * 32 + lane;
     const uint32_t ta = tmem + ((uint32_t)(quad * 32) << 16), tq = ta + (16u << 16);   // lanes of K's, of Q's rows
     const bool has_state = row < kD;                                 // this thread has a row of the state
@@ -803,7 +848,7 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, const De
     };
     float decay[2] = {}, to_end[2] = {}, beta[2] = {}, chunk_decay = 0.f;
     int prep_bad = 0;
-    uint32_t v[2 * kG];
+    uint32_t v[kN / 4];
     auto fetch = [&](int n) {   // chunk n's factors and values
       const int st = n % kChainStages;
       const uint8_t* stage = smem + st * Cfg::kStage;
@@ -818,24 +863,24 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, const De
       chunk_decay = fac[kFacChunk];
       prep_bad = reinterpret_cast<const int*>(fac)[kFacBad];
 #pragma unroll
-      for (int i = 0; i < 2 * kG; ++i)
+      for (int i = 0; i < kN / 4; ++i)
         v[i] = *reinterpret_cast<const uint32_t*>(stage + Cfg::kOffV + (tok + (i & 1) * 8) * Cfg::kVLd + (fc + (i >> 1) * 8) * 2);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
     };
     if (nchunk > 0) {
-      if (has_state) chain_put<kCols, 2, kN>(stile, Cfg::kSTile, row, c0, S);
+      if (has_state) chain_put<2>(stile, Cfg::kSTile, row, c0, S);
       hand(kBarS, kBarThreads);
     }
     for (int n = 0; n < nchunk; ++n) {
       fetch(n);   // while the first product runs
-      F2 e[kN / 2], x[kN / 2], y[kN / 2];
+      F2 e[kN / 4], x[kN / 2], y[kN / 4];
       wait(&done[0], n, 2);
       // E = v - e^G K S0, R = beta E
-      chain_frag<kCols, 2, kG>(ta + Cfg::kX1, c0, e);
+      chain_frag<2>(ta + Cfg::kX1, c0, e);
       F2 zero = f2(0.f, 0.f);   // stays 0 while all are finite
 #pragma unroll
-      for (int i = 0; i < 2 * kG; ++i) {
+      for (int i = 0; i < kN / 4; ++i) {
         const float d = decay[i & 1], b = beta[i & 1];
         e[i] = f2_fma(f2(-d, -d), e[i], f2_bf16(v[i]));
         x[i] = f2_mul(f2(b, b), e[i]);
@@ -844,17 +889,17 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, const De
       const float2 z = f2_out(zero);
       if (z.x + z.y != 0.f) {
 #pragma unroll
-        for (int i = 0; i < 2 * kG; ++i) {
+        for (int i = 0; i < kN / 4; ++i) {
           const float2 xi = f2_out(x[i]);
           if (!isfinite(xi.x) || !isfinite(xi.y)) atomicMin(first_bad, n * kChunk + tok + (i & 1) * 8);
           x[i] = f2(0.f, 0.f);
         }
       }
-      chain_put_frag<kCols, 3, kG>(rtile, Cfg::kRTile, tok, fc, x);
+      chain_put_frag<3>(rtile, Cfg::kRTile, tok, fc, x);
       hand(kBarR, kBarThreads);
-      chain_frag<kCols, 2, kG>(tq + Cfg::kX1, c0, y);   // the output's share of S0
+      chain_frag<2>(tq + Cfg::kX1, c0, y);   // the output's share of S0
 #pragma unroll
-      for (int i = 0; i < 2 * kG; ++i) {
+      for (int i = 0; i < kN / 4; ++i) {
         const float d = a.scale * decay[i & 1];
         y[i] = f2_mul(f2(d, d), y[i]);
       }
@@ -862,26 +907,26 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, const De
       const int bad_from = min(prep_bad, *static_cast<volatile int*>(first_bad) - n * kChunk);
       const float nan = __int_as_float(0x7fffffff);
       // W = E - X R, e^(G_C - G) U = e^(G_C - G) beta W
-      chain_frag<kCols, 3, kG>(ta + Cfg::kX2, c0, x);
+      chain_frag<3>(ta + Cfg::kX2, c0, x);
 #pragma unroll
-      for (int i = 0; i < 2 * kG; ++i) {
+      for (int i = 0; i < kN / 4; ++i) {
         const float f = tok + (i & 1) * 8 >= bad_from ? nan : to_end[i & 1] * beta[i & 1];
         e[i] = f2_fma(f2(-1.f, -1.f), x[i], e[i]);
         x[i] = f2_mul(f2(f, f), e[i]);
       }
-      chain_put_frag<kCols, 3, kG>(rtile, Cfg::kRTile, tok, fc, x);
+      chain_put_frag<3>(rtile, Cfg::kRTile, tok, fc, x);
       hand(kBarU, kBarThreads);
       if constexpr (kSave) {
         float* w = saved.w + ((slot0 + n) * a.Hv + h) * (long long)(kChunk * kD) + part * kCols + fc;
 #pragma unroll
-        for (int i = 0; i < 2 * kG; ++i)
+        for (int i = 0; i < kN / 4; ++i)
           *reinterpret_cast<float2*>(w + (tok + (i & 1) * 8) * kD + (i >> 1) * 8) =
               tok + (i & 1) * 8 >= bad_from ? make_float2(nan, nan) : f2_out(e[i]);
       }
       // the output, while the third product runs
-      chain_frag<kCols, 3, kG>(tq + Cfg::kX2, c0, x);
+      chain_frag<3>(tq + Cfg::kX2, c0, x);
 #pragma unroll
-      for (int i = 0; i < 2 * kG; ++i) {
+      for (int i = 0; i < kN / 4; ++i) {
         const int t = tok + (i & 1) * 8;
         const float2 o = f2_out(f2_add(x[i], y[i]));
         if (n * kChunk + t < sq.len)
@@ -890,11 +935,11 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, const De
       }
       wait(&done[2], n, 4);
       if (has_state) {   // (a warp's 32 rows are all of the state, or none)
-        chain_acc<kCols, 3, kN>(ta + Cfg::kX3, c0, x);
+        chain_acc<3>(ta + Cfg::kX3, c0, x);
         const F2 d2 = f2(chunk_decay, chunk_decay);
 #pragma unroll
         for (int i = 0; i < kN / 2; ++i) S[i] = f2_fma(d2, S[i], x[i]);
-        if (n + 1 < nchunk) chain_put<kCols, 2, kN>(stile, Cfg::kSTile, row, c0, S);
+        if (n + 1 < nchunk) chain_put<2>(stile, Cfg::kSTile, row, c0, S);
       }
       if (n + 1 < nchunk) hand(kBarS, kBarThreads);
     }
@@ -904,97 +949,73 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, const De
         *reinterpret_cast<float4*>(a.state_out + sbase + i) =
             make_float4(f2_out(S[i / 2]).x, f2_out(S[i / 2]).y, f2_out(S[i / 2 + 1]).x, f2_out(S[i / 2 + 1]).y);
   } else if (warp == kIssueWarp) {
-    {
-      // kCols = 32: three terms of R and of U over two tiles
-      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 64, false, true);
-      constexpr uint32_t idesc_r = idesc_bf16_f32(128, kCols == 64 ? 64 : 96, true, true);
-      constexpr uint32_t idesc_2 = idesc_bf16_f32(128, 64, true, true);
-      // descriptors of each operand's first 16 of the K dimension; an offset of n bytes adds n / 16
-      const uint64_t sdesc = smem_desc(smem_u32(stile), 1024, 1024, kSwizzle128B);
-      const uint64_t rdesc = smem_desc(smem_u32(rtile), Cfg::kRTile, 1024, kSwizzle128B);
-      const uint64_t kqdesc = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
-      const uint64_t imgdesc = smem_desc(smem_u32(smem) + Cfg::kOffPrep, kImgBlock, 1024, kSwizzle128B);
-      // K^T: M over channels, 16 tokens every 32 rows.  d = 128: the second 64 channels are the next
-      // block.  Smaller d: rows 64 on take other rows, results that nobody reads.
-      const uint64_t ktdesc = smem_desc(smem_u32(smem), kD > 64 ? 16384 : 8192, 1024, kSwizzle128B);
-      bool ok = true;
-      auto wait = [&](uint64_t* bar, int phase, int code) {
-        if (ok && lane == 0) ok = mbar_spin(bar, phase & 1, abort_flag, err, kErrChainMma | code);
-        ok = __all_sync(0xffffffffu, ok);
-      };
-      if (nchunk > 0) {
-        wait(&full[0], 0, 0);
-      }
-      for (int n = 0; n < nchunk; ++n) {
-        const int st = n % kChainStages;
-        const uint64_t off = st * (Cfg::kStage / 16);
-        bar_sync(kBarS, kBarThreads);
-        tc_fence_after_sync();
-        if (kSave && lane == 0) {
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 64, false, true);
+    constexpr uint32_t idesc_r = idesc_bf16_f32(128, 96, true, true);    // three terms
+    constexpr uint32_t idesc_2 = idesc_bf16_f32(128, 64, true, true);    // two terms
+    // descriptors of each operand's first 16 of the K dimension
+    const Desc sdesc = desc_halves(smem_u32(stile), 1024, 1024, kSwizzle128B);
+    const Desc rdesc = desc_halves(smem_u32(rtile), Cfg::kRTile, 1024, kSwizzle128B);
+    const Desc kqdesc = desc_halves(smem_u32(smem), 16, 1024, kSwizzle128B);
+    const Desc imgdesc = desc_halves(smem_u32(smem) + Cfg::kOffPrep, kImgBlock, 1024, kSwizzle128B);
+    // K^T: M over channels, 16 tokens every 32 rows.  d = 128: the second 64 channels are the next
+    // block.  Smaller d: rows 64 on take other rows, results that nobody reads.
+    const Desc ktdesc = desc_halves(smem_u32(smem), kD > 64 ? 16384 : 8192, 1024, kSwizzle128B);
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int phase, int code) {
+      if (ok && lane == 0) ok = mbar_spin(bar, phase & 1, abort_flag, err, kErrChainMma | code);
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    if (nchunk > 0) wait(&full[0], 0, 0);
+    for (int n = 0; n < nchunk; ++n) {
+      const int st = n % kChainStages;
+      const uint32_t off = st * (Cfg::kStage / 16);
+      bar_sync(kBarS, kBarThreads);
+      tc_fence_after_sync();
+      if (lane == 0) {
+        if (kSave) {
           bulk_store(saved.states + (((slot0 + n) * a.Hv + h) * kParts + part) * (long long)Cfg::kSTile, stile, Cfg::kSTile);
           bulk_commit_group();
         }
-        if (ok && lane == 0) {
+        if (ok) {
 #pragma unroll
-          for (int t = Cfg::kSTiles - 1; t >= 0; --t)   // the small terms first
-#pragma unroll
-            for (int ks = 0; ks < kD / 16; ++ks)
-              umma_bf16(tmem + Cfg::kX1, kqdesc + off + (ks / 4) * 1024 + (ks % 4) * 2,
-                        sdesc + t * (Cfg::kSTile / 16) + ks * 128, idesc_s, ks > 0 || t < Cfg::kSTiles - 1);
+          for (int ks = 0; ks < kD / 16; ++ks)
+            umma(tmem + Cfg::kX1, kqdesc + off + (ks / 4) * 1024 + (ks % 4) * 2, sdesc + ks * 128, idesc_s, ks > 0);
           umma_commit(&done[0]);
         }
-        __syncwarp();
-        bar_sync(kBarR, kBarThreads);
-        tc_fence_after_sync();
-        if (ok && lane == 0) {
-          // hi by all three terms of R, lo by the first two
-          if (kCols == 64) {
+      }
+      __syncwarp();
+      bar_sync(kBarR, kBarThreads);
+      tc_fence_after_sync();
+      if (ok && lane == 0) {
+        // hi by all three terms of R, lo by the first two
 #pragma unroll
-            for (int t = 2; t >= 0; --t) {
-              if (t < 2)
+        for (int ks = 0; ks < 4; ++ks)
+          umma(tmem + Cfg::kX2, imgdesc + off + ks * 128, rdesc + ks * 128, idesc_r, ks > 0);
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                  umma_bf16(tmem + Cfg::kX2, imgdesc + off + kImgHalf / 16 + ks * 128,
-                            rdesc + t * (Cfg::kRTile / 16) + ks * 128, idesc_r, 1u);
+        for (int ks = 0; ks < 4; ++ks)
+          umma(tmem + Cfg::kX2, imgdesc + off + kImgHalf / 16 + ks * 128, rdesc + ks * 128, idesc_2, 1u);
+        umma_commit(&done[1]);
+      }
+      __syncwarp();
+      bar_sync(kBarU, kBarThreads);
+      tc_fence_after_sync();
+      if (lane == 0) {
+        if (kSave) bulk_wait_group_read<0>();   // before the tile of S0 is written again
+        if (ok) {
 #pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                umma_bf16(tmem + Cfg::kX2, imgdesc + off + ks * 128, rdesc + t * (Cfg::kRTile / 16) + ks * 128, idesc_r,
-                          ks > 0 || t < 2);
-            }
-          } else {
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              umma_bf16(tmem + Cfg::kX2, imgdesc + off + ks * 128, rdesc + ks * 128, idesc_r, ks > 0);
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              umma_bf16(tmem + Cfg::kX2, imgdesc + off + kImgHalf / 16 + ks * 128, rdesc + ks * 128, idesc_2, 1u);
-          }
-          umma_commit(&done[1]);
-        }
-        __syncwarp();
-        bar_sync(kBarU, kBarThreads);
-        tc_fence_after_sync();
-        if (kSave && lane == 0) bulk_wait_group_read<0>();   // before the tile of S0 is written again
-        if (ok && lane == 0) {
-#pragma unroll
-          for (int t = (kCols == 64 ? 2 : 0); t >= 0; --t)
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              umma_bf16(tmem + Cfg::kX3, ktdesc + off + ks * 256, rdesc + t * (Cfg::kRTile / 16) + ks * 128, idesc_r,
-                        ks > 0 || t < (kCols == 64 ? 2 : 0));
+          for (int ks = 0; ks < 4; ++ks)
+            umma(tmem + Cfg::kX3, ktdesc + off + ks * 256, rdesc + ks * 128, idesc_r, ks > 0);
           umma_commit(&done[2]);
           umma_commit(&empty[st]);
         }
-        __syncwarp();
-        if (n + 1 < nchunk) {   // while the accumulator warps make the next S0
-          wait(&full[(n + 1) % kChainStages], (n + 1) / kChainStages, 0);
-        }
       }
-      if (lane == 0) {
-        // products in flight end before the memory under them is given back
-        umma_commit(drained);
-        mbar_drain(drained, 0);
-      }
+      __syncwarp();
+      // while the accumulator warps make the next S0
+      if (n + 1 < nchunk) wait(&full[(n + 1) % kChainStages], (n + 1) / kChainStages, 0);
+    }
+    if (lane == 0) {   // products in flight end before the memory under them is given back
+      umma_commit(drained);
+      mbar_drain(drained, 0);
     }
   } else {
     const int t = threadIdx.x - (warp > kIssueWarp ? kAccWarps + 1 : kAccWarps) * 32;

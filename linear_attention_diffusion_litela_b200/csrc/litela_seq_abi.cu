@@ -353,17 +353,18 @@ litela_status delta_setup(int dev) {
   auto set = [&](auto* k, uint32_t bytes) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   };
-  set(litela_delta_prep<32>, PrepCfg<32>::kSmemBytes);
-  set(litela_delta_prep<64>, PrepCfg<64>::kSmemBytes);
-  set(litela_delta_prep<128>, PrepCfg<128>::kSmemBytes);
-  set(litela_delta_chain<32, 32, false>, ChainCfg<32, 32>::kSmemBytes);
-  set(litela_delta_chain<64, 32, false>, ChainCfg<64, 32>::kSmemBytes);
-  set(litela_delta_chain<64, 64, false>, ChainCfg<64, 64>::kSmemBytes);
-  set(litela_delta_chain<128, 32, false>, ChainCfg<128, 32>::kSmemBytes);
-  set(litela_delta_chain<128, 64, false>, ChainCfg<128, 64>::kSmemBytes);
-  set(litela_delta_chain<32, 32, true>, ChainCfg<32, 32>::kSmemBytes);
-  set(litela_delta_chain<64, 32, true>, ChainCfg<64, 32>::kSmemBytes);
-  set(litela_delta_chain<128, 32, true>, ChainCfg<128, 32>::kSmemBytes);
+  set(litela_delta_prep<32, false>, PrepCfg<32>::kSmemBytes);
+  set(litela_delta_prep<64, false>, PrepCfg<64>::kSmemBytes);
+  set(litela_delta_prep<128, false>, PrepCfg<128>::kSmemBytes);
+  set(litela_delta_prep<32, true>, PrepCfg<32>::kSmemBytes);
+  set(litela_delta_prep<64, true>, PrepCfg<64>::kSmemBytes);
+  set(litela_delta_prep<128, true>, PrepCfg<128>::kSmemBytes);
+  set(litela_delta_chain<32, false>, ChainCfg<32>::kSmemBytes);
+  set(litela_delta_chain<64, false>, ChainCfg<64>::kSmemBytes);
+  set(litela_delta_chain<128, false>, ChainCfg<128>::kSmemBytes);
+  set(litela_delta_chain<32, true>, ChainCfg<32>::kSmemBytes);
+  set(litela_delta_chain<64, true>, ChainCfg<64>::kSmemBytes);
+  set(litela_delta_chain<128, true>, ChainCfg<128>::kSmemBytes);
   set(litela_delta_back<32>, BackCfg<32>::kSmemBytes);
   set(litela_delta_back<64>, BackCfg<64>::kSmemBytes);
   set(litela_delta_back<128>, BackCfg<128>::kSmemBytes);
@@ -380,51 +381,32 @@ litela_status delta_setup(int dev) {
 constexpr int kRecurMaxTokens = 32;
 bool delta_recurs(int ntok) { return ntok <= kRecurMaxTokens; }
 
-template <int kD>
-cudaError_t launch_prep(const DeltaArgs& d, uint8_t* prep, cudaStream_t st) {
+// the prepared blocks, then the chain; kSave: a training step's
+template <int kD, bool kSave = false>
+cudaError_t launch_chunks(const DeltaArgs& d, uint8_t* prep, int* err, cudaStream_t st, DeltaSaved saved = {}) {
   const long long slots = delta_slots(d.nseq, d.ntok, d.cu != nullptr);
-  return launch_seq(litela_delta_prep<kD>, dim3((unsigned)(slots * d.Hv)), kPrepThreads, PrepCfg<kD>::kSmemBytes, st,
-                    false, d, prep);
-}
-
-template <int kD, int kCols, bool kSave = false>
-cudaError_t launch_chain(const DeltaArgs& d, const uint8_t* prep, int* err, cudaStream_t st, DeltaSaved saved = {}) {
-  return launch_seq(litela_delta_chain<kD, kCols, kSave>, dim3((unsigned)((long long)d.nseq * d.Hv * (kD / kCols))),
-                    kChainThreads, ChainCfg<kD, kCols>::kSmemBytes, st, true, d, prep, saved, err);
-}
-
-litela_status launch_chunks(const DeltaArgs& d, int D, void* ws, int dev, int sms, cudaStream_t st) {
-  litela_status s = delta_setup(dev);
-  if (s != LITELA_OK) return s;
-  uint8_t* prep = static_cast<uint8_t*>(ws);
-  int* err = delta_error_word(dev);
-  cudaError_t e = D == 32 ? launch_prep<32>(d, prep, st) : D == 64 ? launch_prep<64>(d, prep, st) : launch_prep<128>(d, prep, st);
-  if (e != cudaSuccess) return host_cuda_fail(e, "launch litela_delta_prep");
-  // 64 columns a CTA where that already gives every SM one, else 32
-  const bool wide = D > 32 && (long long)d.nseq * d.Hv * (D / 64) >= sms;
-  if (D == 32)
-    e = launch_chain<32, 32>(d, prep, err, st);
-  else if (D == 64)
-    e = wide ? launch_chain<64, 64>(d, prep, err, st) : launch_chain<64, 32>(d, prep, err, st);
-  else
-    e = wide ? launch_chain<128, 64>(d, prep, err, st) : launch_chain<128, 32>(d, prep, err, st);
-  return e == cudaSuccess ? LITELA_OK : host_cuda_fail(e, "launch litela_delta_chain");
+  const cudaError_t e = launch_seq(litela_delta_prep<kD, kSave>, dim3((unsigned)(slots * d.Hv)), kPrepThreads,
+                                   PrepCfg<kD>::kSmemBytes, st, false, d, prep);
+  if (e != cudaSuccess) return e;
+  return launch_seq(litela_delta_chain<kD, kSave>, dim3((unsigned)((long long)d.nseq * d.Hv * (kD / kCols))), kChainThreads,
+                    ChainCfg<kD>::kSmemBytes, st, true, d, static_cast<const uint8_t*>(prep), saved, err);
 }
 
 // bytes of a call's buffers per chunk slot and value head, and their places
 struct DeltaBytes {
   size_t n;   // slots x value heads
-  size_t prep, states, rows, shares, ends;
+  size_t prep, kept, states, rows, shares, ends;
   explicit DeltaBytes(const DeltaArgs& d, int D) : DeltaBytes(d.nseq, d.ntok, d.Hv, D, d.cu != nullptr) {}
   DeltaBytes(int B, int N, int Hv, int D, bool packed)
       : n((size_t)delta_slots(B, N, packed) * Hv),
         prep(up(n * kPrepBytes)),
+        kept(up(n * kPrepSaveBytes)),
         states(up(n * D * D * 4)),
         rows(up(n * kChunk * D * 4)),
         shares(up(n * (D / 32) * 4 * kChunk * 4)),
         ends(up(n * (D / 32) * 8 * 4)) {}
   static size_t up(size_t x) { return (x + 255) / 256 * 256; }
-  size_t saved() const { return prep + states + rows; }
+  size_t saved() const { return kept + states + rows; }
   size_t back() const { return states + rows + shares + ends; }
 };
 
@@ -434,15 +416,12 @@ bool delta_sizes_ok(int B, int N, int Hk, int Hv, int d) {
 
 DeltaSaved delta_saved(const DeltaBytes& b, void* saved) {
   uint8_t* p = static_cast<uint8_t*>(saved);
-  return DeltaSaved{p + b.prep, reinterpret_cast<float*>(p + b.prep + b.states)};
+  return DeltaSaved{p + b.kept, reinterpret_cast<float*>(p + b.kept + b.states)};
 }
 
 template <int kD>
 cudaError_t launch_save(const DeltaArgs& d, void* saved, int* err, cudaStream_t st) {
-  uint8_t* prep = static_cast<uint8_t*>(saved);
-  const cudaError_t e = launch_prep<kD>(d, prep, st);
-  if (e != cudaSuccess) return e;
-  return launch_chain<kD, 32, true>(d, prep, err, st, delta_saved(DeltaBytes(d, kD), saved));
+  return launch_chunks<kD, true>(d, static_cast<uint8_t*>(saved), err, st, delta_saved(DeltaBytes(d, kD), saved));
 }
 
 template <int kD>
@@ -511,7 +490,16 @@ litela_status delta_fwd(const lite_la_delta_args* a, bool save, void* saved, siz
       if (e != cudaSuccess) return host_cuda_fail(e, "launch the forward of a training step");
     }
   } else {
-    s = recurs ? launch_recur(d, a->d, st) : launch_chunks(d, a->d, a->workspace, dev, sms, st);
+    if (recurs) {
+      s = launch_recur(d, a->d, st);
+    } else if ((s = delta_setup(dev)) == LITELA_OK) {
+      uint8_t* ws = static_cast<uint8_t*>(a->workspace);
+      int* err = delta_error_word(dev);
+      const cudaError_t e = a->d == 32   ? launch_chunks<32>(d, ws, err, st)
+                            : a->d == 64 ? launch_chunks<64>(d, ws, err, st)
+                                         : launch_chunks<128>(d, ws, err, st);
+      if (e != cudaSuccess) return host_cuda_fail(e, "launch the gated delta rule's chunks");
+    }
   }
   if (s == LITELA_OK) host_ok();
   return s;
