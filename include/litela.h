@@ -309,14 +309,15 @@ size_t lite_la_gated_delta_workspace_bytes(int B, int N, int Hk, int Hv, int d, 
 
 /* The forward of a training step: lite_la_gated_delta_fwd that also keeps what its gradient needs in
  * `saved`, device memory of lite_la_gated_delta_saved_bytes(), 16-byte aligned (per 64 tokens and
- * value head: 66 KB + 4 d^2 + 256 d bytes).  It needs no workspace, and state_out must not be NULL.
+ * value head: 66 KB + 4 d^2 + 256 d bytes).  It needs no workspace.
  *
  * lite_la_gated_delta_bwd: the gradients of sum(dout * out) + sum(dstate_out * state_out).  args
- * are the forward's (out is not used), saved is what it left and state_out what it wrote; workspace:
- * lite_la_gated_delta_bwd_workspace_bytes().  dout: a view of the layout of out; dq, dk [B, N, Hk, d]
+ * are the forward's (out and its states are not used), saved is what it left and state_out what it
+ * wrote; workspace: lite_la_gated_delta_bwd_workspace_bytes().  dout: a view of the layout of out; dq, dk [B, N, Hk, d]
  * and dv [B, N, Hv, d]: views; a key head's gradient is the sum over its value heads, in a fixed
  * order.  dg, dbeta: fp32 [B, N, Hv], dense.  dstate_out, dstate_in: as state_out and state_in, or
- * NULL (zeros; not wanted); state_out may be NULL when dstate_out is.  All rows are written: those of
+ * NULL (zeros; not wanted); state_out may be NULL when dstate_out is, and dstate_in may be dstate_out
+ * itself.  All rows are written: those of
  * no sequence with zeros.  The sums are fp32; equal calls give equal bits.
  *
  * A NaN or infinite value of a token (or of the state before a sequence) makes out of that token, of

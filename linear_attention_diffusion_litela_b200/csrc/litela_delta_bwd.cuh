@@ -33,7 +33,7 @@ struct DeltaGrads {
   float* dstate_in;                // or null
   // between the two kernels, per chunk slot and value head
   uint8_t* gstates;                // G' as DeltaSaved's states
-  uint8_t* y;                      // bf16 pair: [2][64, d]
+  uint8_t* y;                      // [d / 32] tiles of 64 rows of 128 bytes, 128-byte swizzle: bf16 pair
   float* rows;                     // [d / 32][2][2][64]: w . W and y . v of half of 32 columns
   float* ends;                     // [d / 32][8]: shares of <S_C, G'>
 };
@@ -67,6 +67,7 @@ struct BackCfg {
   static constexpr uint32_t kX1 = 0, kX2 = 64, kX3 = 192, kTmem = 512;
   static_assert(kSmemBytes <= 232448, "shared memory above the 227 KB per-block limit");
 };
+enum : int { kBarY = 4 };   // named barrier of the accumulator warps: y is in shared memory
 enum : int { kErrBackLoad = 0x610, kErrBackMma = 0x620, kErrBackAcc = 0x630 };
 
 template <int kD>
@@ -83,7 +84,8 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::kOffBars);
   uint64_t* empty = full + kChainStages;
   uint64_t* done = empty + kChainStages;
-  uint64_t* drained = done + 3;
+  uint64_t* s0full = done + 3;
+  uint64_t* drained = s0full + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
@@ -104,6 +106,7 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
       mbar_init(&empty[i], kAccWarps + 1);
     }
     for (int i = 0; i < 3; ++i) mbar_init(&done[i], 1);
+    mbar_init(s0full, 1);
     mbar_init(drained, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -134,15 +137,15 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
       tc_fence_before_sync();
       bar_arrive(id, kBarThreads);
     };
+    F2 S[kN / 2];
+#pragma unroll
+    for (int i = 0; i < kN / 2; ++i) S[i] = f2(0.f, 0.f);
     // this warp's share of <S, G'> behind chunk n
     auto put_end = [&](int n, float dot) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
       if (lane == 0) gr.ends[(((slot0 + n) * a.Hv + h) * kParts + part) * 8 + warp] = dot;
     };
-    F2 S[kN / 2];
-#pragma unroll
-    for (int i = 0; i < kN / 2; ++i) S[i] = f2(0.f, 0.f);
     float dot = 0.f;
     if (has_state && gr.dstate_out != nullptr)
 #pragma unroll
@@ -161,21 +164,6 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
       const int n = nchunk - 1 - it, st = it % kChainStages;
       uint8_t* stage = smem + st * Cfg::kStage;
       const long long sh = (slot0 + n) * a.Hv + h;
-      // W; the state before the chunk, this thread's row of it
-      float2 wv[kN / 4];
-      uint4 s0[kN / 4];
-      const float* wp = saved.w + (sh * kChunk + tok) * kD + part * kCols + fc;
-#pragma unroll
-      for (int i = 0; i < kN / 4; ++i)
-        wv[i] = __ldg(reinterpret_cast<const float2*>(wp + (i & 1) * 8 * kD + (i >> 1) * 8));
-      if (has_state && n > 0) {
-        const uint8_t* src = saved.states + (sh * kParts + part) * (long long)Cfg::kSTile;
-#pragma unroll
-        for (int i = 0; i < kN / 8; ++i) {
-          s0[i] = __ldg(reinterpret_cast<const uint4*>(src + sw128(row, c0 + 8 * i)));
-          s0[kN / 8 + i] = __ldg(reinterpret_cast<const uint4*>(src + sw128(row, 32 + c0 + 8 * i)));
-        }
-      }
       wait(&full[st], it / kChainStages, 0);
       const float* fac = reinterpret_cast<const float*>(stage + Cfg::kOffFac);
       float decay[2], to_end[2], beta[2];
@@ -186,16 +174,14 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
         beta[i] = fac[kFacBeta + tok + 8 * i];
       }
       const float chunk_decay = fac[kFacChunk];
-      uint32_t v[kN / 4];
-      F2 x[kN / 2], y[kN / 4], z[kN / 4];
+      uint32_t v[kN / 4], dov[kN / 4];
 #pragma unroll
       for (int i = 0; i < kN / 4; ++i) {
         const int r = tok + (i & 1) * 8, c = fc + (i >> 1) * 8;
         v[i] = *reinterpret_cast<const uint32_t*>(stage + Cfg::kOffV + r * Cfg::kVLd + c * 2);
-        const float f = a.scale * decay[i & 1];   // scale e^G do
-        x[i] = f2_mul(f2(f, f), f2_bf16(*reinterpret_cast<const uint32_t*>(stage + Cfg::kOffZ + sw128(r, c))));
+        dov[i] = *reinterpret_cast<const uint32_t*>(stage + Cfg::kOffZ + sw128(r, c));
       }
-      chain_put_frag<3>(rtile, Cfg::kRTile, lane_of(tok) + 16, fc, x);
+      F2 x[kN / 2], y[kN / 4], z[kN / 4];
       wait(&done[0], it, 1);
       chain_frag<2>(ta + Cfg::kX1, c0, z);
 #pragma unroll
@@ -206,6 +192,18 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
       }
       chain_put_frag<3, 1>(stage + Cfg::kOffZ, Cfg::kZTile, tok, fc, x);
       hand(kBarR);
+      // while the second product runs: do's rows of the third, W
+      const float* wp = saved.w + (sh * kChunk + tok) * kD + part * kCols + fc;
+      float2 wv[kN / 4];
+#pragma unroll
+      for (int i = 0; i < kN / 4; ++i)
+        wv[i] = __ldg(reinterpret_cast<const float2*>(wp + (i & 1) * 8 * kD + (i >> 1) * 8));
+#pragma unroll
+      for (int i = 0; i < kN / 4; ++i) {
+        const float f = a.scale * decay[i & 1];   // scale e^G do
+        x[i] = f2_mul(f2(f, f), f2_bf16(dov[i]));
+      }
+      chain_put_frag<3>(rtile, Cfg::kRTile, lane_of(tok) + 16, fc, x);
       wait(&done[1], it, 2);
       chain_frag<3>(ta + Cfg::kX2 + 32, c0, x);
       chain_frag<1>(tq + Cfg::kX2, c0, y);
@@ -218,23 +216,50 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
       }
       chain_put_frag<3>(rtile, Cfg::kRTile, lane_of(tok), fc, x);
       hand(kBarU);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);   // the stage has been read
-      // while the third product runs: dv, y and the rows' shares
+      // while the third product runs: y's pair through Z's second tile to memory, and dv (its hi) by rows
+      uint8_t* ytile = stage + Cfg::kOffZ + Cfg::kZTile;
+      chain_put_frag<2>(ytile, 0, tok, fc, y);
+      fence_proxy_async_smem();
+      bar_sync(kBarY, kAccWarps * 32);
+      if (threadIdx.x == 0) {
+        bulk_store(gr.y + (sh * kParts + part) * (long long)Cfg::kZTile, ytile, Cfg::kZTile);
+        bulk_commit_group();
+      }
+      {
+        const int r = threadIdx.x >> 2, c = (threadIdx.x & 3) * 8;
+        if (n * kChunk + r < sq.len)
+          *reinterpret_cast<uint4*>(const_cast<__nv_bfloat16*>(delta_row(gr.dv, sq, n * kChunk + r, h)) + part * kCols + c) =
+              *reinterpret_cast<const uint4*>(ytile + sw128(r, c));
+      }
+      wait(&done[2], it, 3);
+      F2 sdot = f2(0.f, 0.f);
+      if (has_state) {
+        chain_acc<3>(ta + Cfg::kX3, c0, x);
+        const F2 d2 = f2(chunk_decay, chunk_decay);
+#pragma unroll
+        for (int i = 0; i < kN / 2; ++i) S[i] = f2_fma(d2, S[i], x[i]);
+      }
+      if (n > 0) {
+        wait(s0full, it, 4);   // the state before this chunk, in the tile's place
+        if (has_state) {
+#pragma unroll
+          for (int i = 0; i < kN / 8; ++i) {
+            const uint4 hi = *reinterpret_cast<const uint4*>(stile + sw128(row, c0 + 8 * i));
+            const uint4 lo = *reinterpret_cast<const uint4*>(stile + sw128(row, 32 + c0 + 8 * i));
+            const uint32_t h4[4] = {hi.x, hi.y, hi.z, hi.w}, l4[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) sdot = f2_fma(S[4 * i + q], f2_add(f2_bf16(h4[q]), f2_bf16(l4[q])), sdot);
+          }
+          chain_put<2>(stile, Cfg::kSTile, row, c0, S);
+        }
+        hand(kBarS);
+      }
+      // while the next chunk's first product runs: the rows' shares
       F2 wdot[2] = {f2(0.f, 0.f), f2(0.f, 0.f)}, vdot[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-      uint8_t* yd = gr.y + ((sh * 2 * kChunk + tok) * kD + part * kCols + fc) * 2;
 #pragma unroll
       for (int i = 0; i < kN / 4; ++i) {
-        const int t = tok + (i & 1) * 8;
         wdot[i & 1] = f2_fma(z[i], f2(wv[i].x, wv[i].y), wdot[i & 1]);
         vdot[i & 1] = f2_fma(y[i], f2_bf16(v[i]), vdot[i & 1]);
-        const uint32_t hi = next_term(y[i], false), lo = next_term(y[i], true);   // y's pair; hi is dv
-        uint32_t* dst = reinterpret_cast<uint32_t*>(yd + ((i & 1) * 8 * kD + (i >> 1) * 8) * 2);
-        dst[0] = hi;
-        dst[kChunk * kD / 2] = lo;
-        if (n * kChunk + t < sq.len)
-          *reinterpret_cast<uint32_t*>(const_cast<__nv_bfloat16*>(delta_row(gr.dv, sq, n * kChunk + t, h)) + part * kCols +
-                                       fc + (i >> 1) * 8) = hi;
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -250,26 +275,14 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
           rw[2 * kChunk] = vd;
         }
       }
-      wait(&done[2], it, 3);
-      if (has_state) {
-        chain_acc<3>(ta + Cfg::kX3, c0, x);
-        const F2 d2 = f2(chunk_decay, chunk_decay);
-#pragma unroll
-        for (int i = 0; i < kN / 2; ++i) S[i] = f2_fma(d2, S[i], x[i]);
-        if (n > 0) chain_put<2>(stile, Cfg::kSTile, row, c0, S);
-      }
       if (n > 0) {
-        hand(kBarS);
-        F2 d = f2(0.f, 0.f);
-        if (has_state) {
-#pragma unroll
-          for (int i = 0; i < kN / 2; ++i) {
-            const uint32_t hi = reinterpret_cast<const uint32_t*>(s0)[i], lo = reinterpret_cast<const uint32_t*>(s0)[kN / 2 + i];
-            d = f2_fma(S[i], f2_add(f2_bf16(hi), f2_bf16(lo)), d);
-          }
-        }
-        const float2 dd = f2_out(d);
+        const float2 dd = f2_out(sdot);
         put_end(n - 1, dd.x + dd.y);
+      }
+      __syncwarp();
+      if (lane == 0) {   // the stage has been read
+        if (warp == 0) bulk_wait_group_read<0>();
+        mbar_arrive(&empty[st]);
       }
     }
     if (ok && has_state && gr.dstate_in != nullptr)
@@ -312,6 +325,13 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
       __syncwarp();
       bar_sync(kBarR, kBarThreads);
       tc_fence_after_sync();
+      if (n > 0 && lane == 0) {
+        // G' has been read by the first product and stored: the state before the chunk takes its place
+        bulk_wait_group_read<0>();
+        mbar_arrive_expect_tx(s0full, Cfg::kSTile);
+        bulk_load(stile, saved.states + (((slot0 + n) * a.Hv + h) * kParts + part) * (long long)Cfg::kSTile, Cfg::kSTile,
+                  s0full);
+      }
       if (ok && lane == 0) {
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
@@ -325,7 +345,6 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
       bar_sync(kBarU, kBarThreads);
       tc_fence_after_sync();
       if (lane == 0) {
-        bulk_wait_group_read<0>();   // before G's tile is written again
         if (ok) {
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
@@ -341,6 +360,7 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
       umma_commit(drained);
       mbar_drain(drained, 0);
       bulk_wait_group<0>();
+      if (nchunk > 1) mbar_drain(s0full, (nchunk - 2) & 1);
     }
   } else {
     const int t = threadIdx.x - (warp > kIssueWarp ? kAccWarps + 1 : kAccWarps) * 32;
@@ -510,20 +530,21 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
       for (int i = tid * 16; i < (int)Cfg::kTile; i += kThreads * 16) cp_async_16(dst + i, src + i, true);
     };
     copy_rows(gr.dout, h, Cfg::kOffDo);
-    {   // y's pair: 128 rows
-      constexpr int kC = kD / 8, kStep = kThreads / kC;
-      const int c = tid % kC, r = tid / kC;
-      const uint8_t* src = gr.y + sh * (2 * kChunk * kD * 2) + tid * 16;
-      const uint32_t dst = base + Cfg::kOffY + r * (Cfg::kLd * 2) + c * 16;
+    {   // y's pair
+      const uint8_t* src = gr.y + sh * (kParts * kChunk * 128);
 #pragma unroll
-      for (int i = 0; i < 2 * kChunk / kStep; ++i) cp_async_16(dst + i * kStep * (Cfg::kLd * 2), src + i * kThreads * 16, true);
+      for (int i = tid; i < kParts * kChunk * 8; i += kThreads) {
+        const int p = i / (kChunk * 8), r = (i >> 3) % kChunk, c = i & 7;
+        cp_async_16(base + Cfg::kOffY + (c >> 2) * Cfg::kRows + (r * Cfg::kLd + p * 32 + (c & 3) * 8) * 2,
+                    src + p * (kChunk * 128) + sw128(r, c * 8), true);
+      }
     }
     if (tid < (int)kFactorBytes / 16) cp_async_16(base + Cfg::kOffFac + tid * 16, prep + sh * kPrepSaveBytes + kPrepFactors + tid * 16, true);
     load_tile(0);
     cp_async_commit();
     load_tile(1);
     cp_async_commit();
-    // this token's sums (tid < 64): w . W, y . v, and the chunk's <S, G'>; W's values: all in flight at once
+    // this token's sums (tid < 64): w . W and y . v; W's values: all in flight at once
     constexpr int kQ = kChunk * kD / 4 / kThreads;   // 4 columns of a row at a time
     float4 wv[kQ];
     const float4* wp = reinterpret_cast<const float4*>(saved.w + sh * kChunk * kD) + tid;
@@ -745,7 +766,6 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
       const float e0 = fac[kFacToEnd + r0], e1 = fac[kFacToEnd + r0 + 8];
 #pragma unroll
       for (int n = 0; n < kT; ++n)
-#pragma unroll
         for (int i = 0; i < 4; ++i) dk[n][i] += (i < 2 ? e0 : e1) * x[n][i];
     }
     // q . dq of the heads so far

@@ -465,7 +465,6 @@ litela_status delta_fwd(const lite_la_delta_args* a, bool save, void* saved, siz
   const bool recurs = !save && delta_recurs(a->N);
   const DeltaBytes bytes(a->B, a->N, a->Hv, a->d, a->cu_seqlens != nullptr);
   if (save) {
-    if (a->state_out == nullptr) return invalid("a training step's forward needs state_out");
     s = buffer_check(a, saved, saved_bytes, bytes.saved(), in, out, "saved missing, too small or misaligned",
                      "saved overlaps a buffer of the call");
   } else if (!recurs) {
@@ -535,17 +534,17 @@ litela_status delta_bwd(const lite_la_delta_args* a, const lite_la_delta_grads* 
           LITELA_OK)
     return s;
   in.add(span(saved, a->N > 0 ? bytes.saved() : 0));
-  const Span ins[2] = {span(g->dstate_out, states), span(g->state_out, states)};
+  const Span dso = span(g->dstate_out, states), so = span(g->state_out, states);
   // dq, dk, dv may be views of one buffer between one another's rows: only their spans against inputs
   // and the dense outputs are checked
   const Span outs[7] = {sp[0], sp[1], sp[2], span(g->dg, gates), span(g->dbeta, gates), span(g->dstate_in, states),
                         span(a->workspace, a->N > 0 ? bytes.back() : 0)};
   for (int i = 0; i < 7; ++i) {
-    if (in.hit(outs[i]) || (i != 5 && meet(outs[i], ins[0])) || meet(outs[i], ins[1])) return invalid("an output overlaps an input");
+    if (in.hit(outs[i]) || (i != 5 && meet(outs[i], dso)) || meet(outs[i], so)) return invalid("an output overlaps an input");
     for (int j = i + 1; j < 7; ++j)
       if (j > 2 && meet(outs[i], outs[j])) return invalid("outputs overlap");
   }
-  if (g->dstate_in != nullptr && g->dstate_in != g->dstate_out && meet(outs[5], ins[0]))
+  if (g->dstate_in != nullptr && g->dstate_in != g->dstate_out && meet(outs[5], dso))
     return invalid("dstate_in overlaps dstate_out in part");
   int dev, sms;
   if ((s = host_device(&dev, &sms)) != LITELA_OK || (s = delta_setup(dev)) != LITELA_OK) return s;

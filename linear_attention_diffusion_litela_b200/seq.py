@@ -292,7 +292,8 @@ def lite_la_gated_delta_fwd_save(q, k, v, g, beta, state_in=None, state_out=None
 def lite_la_gated_delta_bwd(q, k, v, g, beta, dout, saved, state_out=None, dstate_out=None, state_in=None,
                             cu_seqlens=None, scale=None, stream=None):
     """Gradients of sum(dout * out) + sum(dstate_out * state_out) for the forward that left `saved`
-    (lite_la_gated_delta_fwd_save with the same arguments) and wrote state_out: (dq, dk, dv bf16, dg,
+    (lite_la_gated_delta_fwd_save with the same arguments) and wrote state_out (needed with
+    dstate_out): (dq, dk, dv bf16, dg,
     dbeta fp32, dstate_in fp32 or None without state_in)."""
     torch = _torch()
     a = _Delta(q, k, v, g, beta, scale, cu_seqlens)
