@@ -31,6 +31,7 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 
+#include "f32x2.cuh"
 #include "litela_delta.cuh"
 #include "sm100_ptx.cuh"
 
@@ -92,40 +93,6 @@ __device__ __forceinline__ bool delta_find(const DeltaArgs& a, int slot, int lan
   q = delta_seq(a, s);
   n0 = (slot - (int)delta_slot0(a, s, q)) * kChunk;
   return n0 >= 0 && n0 < q.len;
-}
-
-// two fp32 values in one 64-bit register: Blackwell adds and multiplies both in one instruction
-struct F2 {
-  uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float a, float b) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 f2_out(F2 x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.v));
-  return r;
-}
-__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-// the two values of a packed bf16 word
-__device__ __forceinline__ F2 f2_bf16(uint32_t w) {
-  return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {

@@ -12,13 +12,17 @@
 // Both are bound by HBM: a row is read once and written once, all sums are in fp32.  A lane owns
 // 8 neighbouring channels (16 bytes); d / 8 lanes make a head and reduce with shuffles, so a warp
 // takes 256 channels per step.  256 is a multiple of d, so a lane meets the same channels of a
-// head in every step: its 8 cosines, sines and weights stay in registers for a whole row.  A warp
-// takes a share of `parts` of a row; parts > 1 only where the rows alone do not fill the SMs.
+// head in every step.  Work is cut by row and by q, k and v, all rows' q first: within a task the
+// weight and the angles of a lane's channels are constants in registers, and the weight's gradient
+// is one set of 8 sums.  Loads of a warp's next steps (of its next task, too) are in flight while
+// it works on the ones before.  `parts` warps share a task; more than one only where the tasks alone
+// do not fill the SMs.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cstdint>
 
+#include "f32x2.cuh"
 #include "sm100_ptx.cuh"
 
 namespace litela {
@@ -37,7 +41,8 @@ struct NormPlan {
   int N;                       // tokens per batch entry
   int pos64, table, rot;
   int q_ch, qk_ch, W;          // first channel of k, of v, channels of a row
-  int parts, steps;            // warps per row; 256-channel steps of a row
+  int shift;                   // 2^shift warps share a task
+  int regions;                 // 2: q and k; 3: v too
   bool copy_v;                 // out is another buffer than the input: v is copied
   float eps;
 };
@@ -46,25 +51,6 @@ constexpr int kNormThreads = 256;
 constexpr int kNormWarps = kNormThreads / 32;
 constexpr int kNormStep = 256;    // channels of a warp's step
 
-__device__ __forceinline__ void bf16x8_to_f32(uint4 w, float* x) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-  }
-}
-
-__device__ __forceinline__ uint4 f32_to_bf16x8(const float* x) {
-  uint32_t u[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    u[i] = *reinterpret_cast<uint32_t*>(&h);
-  }
-  return make_uint4(u[0], u[1], u[2], u[3]);
-}
-
 template <int kLanes>
 __device__ __forceinline__ float sum_lanes(float v) {
 #pragma unroll
@@ -72,10 +58,58 @@ __device__ __forceinline__ float sum_lanes(float v) {
   return v;
 }
 
-// a row's position; a negative one marks a padded row
-__device__ __forceinline__ long long norm_position(const NormPlan& p, long long row) {
-  if (p.pos == nullptr) return row % p.N;
-  return p.pos64 ? static_cast<const long long*>(p.pos)[row] : static_cast<const int*>(p.pos)[row];
+// A row's position; a negative one marks a padded row.  Loaded as its words first, so that nothing
+// waits for it before it is used.
+__device__ __forceinline__ int2 norm_position_words(const NormPlan& p, long long row) {
+  if (p.pos == nullptr)
+    return make_int2((int)(p.rows <= 0xffffffffLL ? (uint32_t)row % (uint32_t)p.N : row % p.N), 0);
+  if (p.pos64) return static_cast<const int2*>(p.pos)[row];
+  return make_int2(static_cast<const int*>(p.pos)[row], 0);
+}
+__device__ __forceinline__ long long norm_position(const NormPlan& p, int2 w) {
+  return p.pos64 ? (long long)((uint64_t)(uint32_t)w.y << 32 | (uint32_t)w.x) : w.x;
+}
+
+// Where a warp is: task t (region 0, 1, 2 = q, k, v of a row that starts at element `row` and has
+// position `at`), channels [ch, end) of it to go
+struct NormWalk {
+  long long t, row;
+  int2 at;
+  int region, ch, end;
+};
+
+__device__ __forceinline__ void norm_task(const NormPlan& p, NormWalk& w) {
+  const long long each = p.rows << p.shift;
+  long long i = w.t;
+  w.region = 0;
+  if (i >= each) i -= each, w.region = 1;
+  if (i >= each) i -= each, w.region = 2;
+  w.at = norm_position_words(p, i >> p.shift);
+  w.row = (i >> p.shift) * p.W;
+  w.ch = (w.region == 0 ? 0 : w.region == 1 ? p.q_ch : p.qk_ch) + (int)(i & ((1 << p.shift) - 1)) * kNormStep;
+  w.end = w.region == 0 ? p.q_ch : w.region == 1 ? p.qk_ch : p.W;
+}
+
+// to the next channels of a task, kU steps on, or to the next task that has any; false behind the last
+template <int kU>
+__device__ __forceinline__ bool norm_next(const NormPlan& p, NormWalk& w, long long nwarps) {
+  w.ch += (kU * kNormStep) << p.shift;
+  while (w.ch >= w.end) {
+    w.t += nwarps;
+    if (w.t >= (p.rows << p.shift) * p.regions) return false;
+    norm_task(p, w);
+  }
+  return true;
+}
+
+template <int kU>
+__device__ __forceinline__ void norm_load(const NormPlan& p, const __nv_bfloat16* x, const NormWalk& w, int lane,
+                                          uint4* raw) {
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    const int ch = w.ch + ((u * kNormStep) << p.shift) + lane * 8;
+    raw[u] = ch < w.end ? *reinterpret_cast<const uint4*>(x + w.row + ch) : make_uint4(0u, 0u, 0u, 0u);
+  }
 }
 
 // The lane's cosines and sines of channels [c, c + 8) of a head at position `at`.  Channels that
@@ -83,210 +117,294 @@ __device__ __forceinline__ long long norm_position(const NormPlan& p, long long 
 // Pairs: kInter, channels (2i, 2i + 1); else (i, i + rot / 2).  sn carries the sign of the
 // partner's share, so that a channel's result is x * cs + partner * sn.
 template <bool kInter>
-__device__ __forceinline__ void norm_angles(const NormPlan& p, long long at, int c, float* cs, float* sn) {
-  if (p.rot == 0 || c >= p.rot) {
+__device__ __forceinline__ void norm_angles(const NormPlan& p, long long at, int c, F2* cs, F2* sn) {
+  if (c >= p.rot) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      cs[i] = 1.f;
-      sn[i] = 0.f;
-    }
+    for (int i = 0; i < 4; ++i) cs[i] = f2(1.f, 1.f), sn[i] = f2(0.f, 0.f);
     return;
   }
   if (at >= p.table) {
+    const float nan = __int_as_float(0x7fffffff);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = sn[i] = __int_as_float(0x7fffffff);
+    for (int i = 0; i < 4; ++i) cs[i] = sn[i] = f2(nan, nan);
     return;
   }
   const int half = p.rot / 2;
   if (kInter) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(p.cos + at * half + c / 2));
     const float4 b = __ldg(reinterpret_cast<const float4*>(p.sin + at * half + c / 2));
-    const float ca[4] = {a.x, a.y, a.z, a.w}, sa[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      cs[2 * i] = cs[2 * i + 1] = ca[i];
-      sn[2 * i] = -sa[i];
-      sn[2 * i + 1] = sa[i];
-    }
+    cs[0] = f2(a.x, a.x), cs[1] = f2(a.y, a.y), cs[2] = f2(a.z, a.z), cs[3] = f2(a.w, a.w);
+    sn[0] = f2(-b.x, b.x), sn[1] = f2(-b.y, b.y), sn[2] = f2(-b.z, b.z), sn[3] = f2(-b.w, b.w);
   } else {
     const bool second = c >= half;
     const long long o = at * half + (second ? c - half : c);
+    const F2 sign = second ? f2(1.f, 1.f) : f2(-1.f, -1.f);
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
       const float4 a = __ldg(reinterpret_cast<const float4*>(p.cos + o) + v);
       const float4 b = __ldg(reinterpret_cast<const float4*>(p.sin + o) + v);
-      cs[4 * v] = a.x, cs[4 * v + 1] = a.y, cs[4 * v + 2] = a.z, cs[4 * v + 3] = a.w;
-      sn[4 * v] = b.x, sn[4 * v + 1] = b.y, sn[4 * v + 2] = b.z, sn[4 * v + 3] = b.w;
+      cs[2 * v] = f2(a.x, a.y), cs[2 * v + 1] = f2(a.z, a.w);
+      sn[2 * v] = f2_mul(sign, f2(b.x, b.y)), sn[2 * v + 1] = f2_mul(sign, f2(b.z, b.w));
     }
-    if (!second)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sn[i] = -sn[i];
   }
 }
 
-// x * cs + partner * sn for the lane's 8 channels; `c` is the first of them in its head, `half`
-// rot / 2 in lanes.  kBack turns back (the sines negated).  All lanes take part in the shuffles.
-template <bool kInter, bool kBack, int kD>
-__device__ __forceinline__ void norm_rotate(float* x, const float* cs, const float* sn, int rot, int lane) {
-  if (rot == 0) return;
-  float q[8];
+// 8 bf16 values of the lane's channels' partners; all lanes take part.  src: norm_partner
+template <bool kInter>
+__device__ __forceinline__ uint4 norm_swap(uint4 w, int src) {
   if (kInter) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = x[i ^ 1];
-  } else {
-    const int hl = rot / 16, l = lane % (kD / 8);   // lanes of half the rotated channels; lane in the head
-    const int src = l < hl ? lane + hl : (l < 2 * hl ? lane - hl : lane);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = __shfl_sync(0xffffffffu, x[i], src);
+    auto turn = [](uint32_t v) { return __funnelshift_l(v, v, 16); };
+    return make_uint4(turn(w.x), turn(w.y), turn(w.z), turn(w.w));
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = x[i] * cs[i] + (kBack ? -q[i] * sn[i] : q[i] * sn[i]);
+  return make_uint4(__shfl_sync(0xffffffffu, w.x, src), __shfl_sync(0xffffffffu, w.y, src),
+                    __shfl_sync(0xffffffffu, w.z, src), __shfl_sync(0xffffffffu, w.w, src));
+}
+// the lane that holds the partners (pairs of two halves), itself for channels that are not rotated
+template <int kD>
+__device__ __forceinline__ int norm_partner(int rot, int lane) {
+  const int hl = rot / 16, l = lane % (kD / 8);   // lanes of half the rotated channels; lane in the head
+  return l < hl ? lane + hl : l < 2 * hl ? lane - hl : lane;
 }
 
-__device__ __forceinline__ void load_weight(const float* w, int c, float* r) {
+__device__ __forceinline__ void f2_bf16x8(uint4 w, F2* x) {
+  x[0] = f2_bf16(w.x), x[1] = f2_bf16(w.y), x[2] = f2_bf16(w.z), x[3] = f2_bf16(w.w);
+}
+__device__ __forceinline__ uint4 f2_to_bf16x8(const F2* x) {
+  uint32_t u[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r[i] = w == nullptr ? 1.f : __ldg(w + c + i);
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = f2_out(x[i]);
+    __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+    u[i] = *reinterpret_cast<uint32_t*>(&h);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+__device__ __forceinline__ float f2_sum4(const F2* x) {
+  const float2 v = f2_out(f2_add(f2_add(x[0], x[1]), f2_add(x[2], x[3])));
+  return v.x + v.y;
 }
 
-// this warp's part of a row of zeros
-__device__ __forceinline__ void norm_zero_row(const NormPlan& p, __nv_bfloat16* dst, int part, int lane) {
-  for (int s = part; s < p.steps; s += p.parts) {
-    const int ch = s * kNormStep + lane * 8;
-    if (ch < p.W) *reinterpret_cast<uint4*>(dst + ch) = make_uint4(0u, 0u, 0u, 0u);
+// both weights, ones where there are none
+template <int kD>
+__device__ __forceinline__ void norm_weights(const NormPlan& p, float (*w)[kD]) {
+  for (int i = threadIdx.x; i < 2 * kD; i += kNormThreads) {
+    const float* src = i < kD ? p.wq : p.wk;
+    w[i / kD][i % kD] = src == nullptr ? 1.f : __ldg(src + i % kD);
+  }
+  __syncthreads();
+}
+
+// this warp's steps of the walk's channels, zeros
+template <int kU>
+__device__ __forceinline__ void norm_zero(const NormPlan& p, const NormWalk& w, int lane) {
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    const int ch = w.ch + ((u * kNormStep) << p.shift) + lane * 8;
+    if (ch < w.end) *reinterpret_cast<uint4*>(p.out + w.row + ch) = make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
-constexpr int kNormUnroll = 4;
-
+// y = r (x * a + partner * b), a = w cos, b = the partner's w times the signed sine.  80 registers
+// (three CTAs an SM) hold four steps in work and four in flight.  2 x 16384 rows of 70 + 70 + 70
+// heads of 32 channels: 176 us, 5.0 TB/s (64 registers, two steps and four CTAs: 179 us); what is left is
+// bound by the issue of instructions as much as by memory.
 template <int kD, bool kInter>
-__global__ void __launch_bounds__(kNormThreads) litela_norm_fwd(const NormPlan p) {
+__global__ void __launch_bounds__(kNormThreads, 3) litela_norm_fwd(const NormPlan p) {
+  constexpr int kU = 4;
+  __shared__ float weight[2][kD];
   const int lane = threadIdx.x & 31;
   const long long nwarps = (long long)gridDim.x * kNormWarps;
-  const int c = (lane * 8) % kD;
-  float wq[8], wk[8];
-  load_weight(p.wq, c, wq);
-  load_weight(p.wk, c, wk);
-  const int last = p.copy_v ? p.W : p.qk_ch;   // channels of a row that are written
-  for (long long t = (long long)blockIdx.x * kNormWarps + (threadIdx.x >> 5); t < p.rows * p.parts; t += nwarps) {
-    const long long row = t / p.parts;
-    const int part = (int)(t - row * p.parts);
-    const long long at = norm_position(p, row);
-    const __nv_bfloat16* src = p.x + row * p.W;
-    __nv_bfloat16* dst = p.out + row * p.W;
-    if (at < 0) {   // a padded row
-      if (p.copy_v) norm_zero_row(p, dst, part, lane);
+  const int c = (lane * 8) % kD, src = norm_partner<kD>(p.rot, lane);
+  NormWalk to{(long long)blockIdx.x * kNormWarps + (threadIdx.x >> 5) - nwarps, 0, {}, 0, 0, 0};
+  bool more = norm_next<kU>(p, to, nwarps);
+  uint4 ahead[kU];
+  if (more) norm_load<kU>(p, p.x, to, lane, ahead);
+  norm_weights<kD>(p, weight);
+  long long task = -1, pos = 0;
+  F2 a[4], b[4];
+  while (more) {
+    const NormWalk w = to;
+    uint4 raw[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) raw[u] = ahead[u];
+    more = norm_next<kU>(p, to, nwarps);
+    if (more) norm_load<kU>(p, p.x, to, lane, ahead);
+    if (w.t != task) {
+      task = w.t;
+      pos = norm_position(p, w.at);
+      if (pos >= 0 && w.region < 2) {
+        norm_angles<kInter>(p, pos, c, a, b);
+        const float* wt = weight[w.region];
+        const int pc = kInter ? c : c + (src - lane) * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 own = *reinterpret_cast<const float2*>(wt + c + 2 * i);
+          const float2 oth = *reinterpret_cast<const float2*>(wt + pc + 2 * i);
+          a[i] = f2_mul(a[i], f2(own.x, own.y));
+          b[i] = f2_mul(b[i], kInter ? f2(oth.y, oth.x) : f2(oth.x, oth.y));
+        }
+      }
+    }
+    if (pos < 0) {   // a padded row
+      if (p.copy_v) norm_zero<kU>(p, w, lane);
       continue;
     }
-    float cs[8], sn[8];
-    norm_angles<kInter>(p, at, c, cs, sn);
-    for (int s0 = part; s0 < p.steps; s0 += kNormUnroll * p.parts) {
-      uint4 raw[kNormUnroll];
+    auto step = [&](int u, bool heads) {
+      const int ch = w.ch + ((u * kNormStep) << p.shift) + lane * 8;
+      if (heads) {
+        F2 x[4], q[4], s[4];
+        f2_bf16x8(raw[u], x);
 #pragma unroll
-      for (int u = 0; u < kNormUnroll; ++u) {
-        const int ch = (s0 + u * p.parts) * kNormStep + lane * 8;
-        raw[u] = ch < last ? *reinterpret_cast<const uint4*>(src + ch) : make_uint4(0u, 0u, 0u, 0u);
-      }
+        for (int i = 0; i < 4; ++i) s[i] = f2_mul(x[i], x[i]);
+        const float r = rsqrtf(sum_lanes<kD / 8>(f2_sum4(s)) * (1.f / kD) + p.eps);
+        const F2 r2 = f2(r, r);
+        if (p.rot != 0) {
+          f2_bf16x8(norm_swap<kInter>(raw[u], src), q);
 #pragma unroll
-      for (int u = 0; u < kNormUnroll; ++u) {
-        const int first = (s0 + u * p.parts) * kNormStep, ch = first + lane * 8;
-        if (first < p.qk_ch) {   // the same for the whole warp
-          float x[8], ss = 0.f;
-          bf16x8_to_f32(raw[u], x);
+          for (int i = 0; i < 4; ++i) x[i] = f2_fma(x[i], a[i], f2_mul(q[i], b[i]));
+        } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
-          const float r = rsqrtf(sum_lanes<kD / 8>(ss) * (1.f / kD) + p.eps);
-          const bool q = ch < p.q_ch;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] *= r * (q ? wq[i] : wk[i]);
-          norm_rotate<kInter, false, kD>(x, cs, sn, p.rot, lane);
-          if (ch < p.qk_ch) raw[u] = f32_to_bf16x8(x);
+          for (int i = 0; i < 4; ++i) x[i] = f2_mul(x[i], a[i]);
         }
-        if (ch < last) *reinterpret_cast<uint4*>(dst + ch) = raw[u];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = f2_mul(r2, x[i]);
+        raw[u] = f2_to_bf16x8(x);
+      }
+      if (ch < w.end) *reinterpret_cast<uint4*>(p.out + w.row + ch) = raw[u];
+    };
+    if (w.region == 2) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) step(u, false);
+    } else if (w.ch + (((kU - 1) * kNormStep) << p.shift) < w.end) {   // all steps are there: they interleave
+#pragma unroll
+      for (int u = 0; u < kU; ++u) step(u, true);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kU - 1; ++u) {
+        if (w.ch + ((u * kNormStep) << p.shift) >= w.end) break;
+        step(u, true);
       }
     }
   }
 }
 
-// The gradient.  A warp's sums of the weights' gradients stay in registers over all its rows; the
-// CTA's sums go to `partials`, which litela_norm_weight_grad adds in a fixed order.
+// The gradient.  With t the turned-back dy: dw = sum of r t x, dx = r (w t - x r^2 mean(w t x)), so
+// that the two sums of a head do not wait for one another.  A warp's sums of a weight's gradient
+// stay in registers over all its rows; the CTA's go to `partials`, which litela_norm_weight_grad
+// adds in a fixed order.  Two CTAs an SM with two steps in work and two in flight: 2 x 4099 rows of
+// 32 + 8 + 8 heads of 128 channels in 62 us, 4.7 TB/s (80 registers for a third CTA spill: 144 us).
 template <int kD, bool kInter>
-__global__ void __launch_bounds__(kNormThreads) litela_norm_bwd(const NormPlan p) {
+__global__ void __launch_bounds__(kNormThreads, 2) litela_norm_bwd(const NormPlan p) {
+  constexpr int kU = 2;
+  __shared__ float weight[2][kD];
+  __shared__ float sums[kNormWarps][2][kD];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long nwarps = (long long)gridDim.x * kNormWarps;
-  const int c = (lane * 8) % kD;
-  float wq[8], wk[8], aq[8], ak[8];
-  load_weight(p.wq, c, wq);
-  load_weight(p.wk, c, wk);
+  const int c = (lane * 8) % kD, src = norm_partner<kD>(p.rot, lane);
+  NormWalk to{(long long)blockIdx.x * kNormWarps + warp - nwarps, 0, {}, 0, 0, 0};
+  uint4 ax[kU], ag[kU];
+  auto load = [&] {
+    if (to.region < 2) norm_load<kU>(p, p.x, to, lane, ax);
+    if (to.region < 2 || p.copy_v) norm_load<kU>(p, p.dy, to, lane, ag);
+  };
+  bool more = norm_next<kU>(p, to, nwarps);
+  if (more) load();
+  norm_weights<kD>(p, weight);
+  for (int i = threadIdx.x; i < kNormWarps * 2 * kD; i += kNormThreads) (&sums[0][0][0])[i] = 0.f;
+  __syncthreads();
+  F2 acc[4], cs[4], sn[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) aq[i] = ak[i] = 0.f;
-  const int last = p.copy_v ? p.W : p.qk_ch;
-  for (long long t = (long long)blockIdx.x * kNormWarps + warp; t < p.rows * p.parts; t += nwarps) {
-    const long long row = t / p.parts;
-    const int part = (int)(t - row * p.parts);
-    const long long at = norm_position(p, row);
-    __nv_bfloat16* dst = p.out + row * p.W;
-    if (at < 0) {   // a padded row: its gradient is zero
-      norm_zero_row(p, dst, part, lane);
+  for (int i = 0; i < 4; ++i) acc[i] = f2(0.f, 0.f);
+  // the sums of region r so far: lanes of the same channels added, and left to the CTA
+  auto put = [&](int r) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 v = f2_out(acc[i]);
+#pragma unroll
+      for (int o = kD / 8; o < 32; o <<= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+      }
+      if (lane < kD / 8) sums[warp][r][c + 2 * i] = v.x, sums[warp][r][c + 2 * i + 1] = v.y;
+      acc[i] = f2(0.f, 0.f);
+    }
+  };
+  long long task = -1, pos = 0;
+  int region = 0;
+  while (more) {
+    const NormWalk w = to;
+    uint4 rx[kU], rg[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) rx[u] = ax[u], rg[u] = ag[u];
+    more = norm_next<kU>(p, to, nwarps);
+    if (more) load();
+    if (w.t != task) {
+      task = w.t;
+      pos = norm_position(p, w.at);
+      if (w.region != region) {
+        if (region < 2) put(region);
+        region = w.region;
+      }
+      if (pos >= 0 && w.region < 2) {
+        norm_angles<kInter>(p, pos, c, cs, sn);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sn[i] = f2_mul(f2(-1.f, -1.f), sn[i]);   // back
+      }
+    }
+    if (pos < 0) {   // a padded row: its gradient is zero
+      norm_zero<kU>(p, w, lane);
       continue;
     }
-    float cs[8], sn[8];
-    norm_angles<kInter>(p, at, c, cs, sn);
-    const __nv_bfloat16 *src = p.x + row * p.W, *grad = p.dy + row * p.W;
-    constexpr int kU = kNormUnroll / 2;
-    for (int s0 = part; s0 < p.steps; s0 += kU * p.parts) {
-      uint4 rx[kU], rg[kU];
+    if (w.region == 2 && !p.copy_v) continue;
+    auto step = [&](int u, bool heads) {
+      const int ch = w.ch + ((u * kNormStep) << p.shift) + lane * 8;
+      if (heads) {
+        F2 x[4], g[4], s[4], d[4], e[4];
+        f2_bf16x8(rx[u], x);
+        f2_bf16x8(rg[u], g);
+        if (p.rot != 0) {
+          F2 q[4];
+          f2_bf16x8(norm_swap<kInter>(rg[u], src), q);
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int ch = (s0 + u * p.parts) * kNormStep + lane * 8;
-        rx[u] = ch < p.qk_ch ? *reinterpret_cast<const uint4*>(src + ch) : make_uint4(0u, 0u, 0u, 0u);
-        rg[u] = ch < last ? *reinterpret_cast<const uint4*>(grad + ch) : make_uint4(0u, 0u, 0u, 0u);
-      }
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int first = (s0 + u * p.parts) * kNormStep, ch = first + lane * 8;
-        if (first < p.qk_ch) {
-          float x[8], g[8], ss = 0.f, dot = 0.f;
-          bf16x8_to_f32(rx[u], x);
-          bf16x8_to_f32(rg[u], g);
-          norm_rotate<kInter, true, kD>(g, cs, sn, p.rot, lane);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
-          const float r = rsqrtf(sum_lanes<kD / 8>(ss) * (1.f / kD) + p.eps);
-          const bool q = ch < p.q_ch;
-          const bool real = ch < p.qk_ch;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[i] *= r;
-            const float gw = real ? g[i] * x[i] : 0.f;
-            aq[i] += q ? gw : 0.f;
-            ak[i] += q ? 0.f : gw;
-            g[i] *= q ? wq[i] : wk[i];
-            dot += g[i] * x[i];
-          }
-          dot = sum_lanes<kD / 8>(dot) * (1.f / kD);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = r * (g[i] - x[i] * dot);
-          if (real) rg[u] = f32_to_bf16x8(x);
+          for (int i = 0; i < 4; ++i) g[i] = f2_fma(g[i], cs[i], f2_mul(q[i], sn[i]));
         }
-        if (ch < last) *reinterpret_cast<uint4*>(dst + ch) = rg[u];
+        const float* wt = weight[w.region] + c;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 wv = *reinterpret_cast<const float2*>(wt + 2 * i);
+          s[i] = f2_mul(x[i], x[i]);
+          d[i] = f2_mul(g[i], x[i]);
+          g[i] = f2_mul(g[i], f2(wv.x, wv.y));
+          e[i] = f2_mul(g[i], x[i]);
+        }
+        const float ss = sum_lanes<kD / 8>(f2_sum4(s)), dot = sum_lanes<kD / 8>(f2_sum4(e));
+        const float r = rsqrtf(ss * (1.f / kD) + p.eps), m = -(dot * (1.f / kD) * r);
+        const F2 r2 = f2(r, r), m2 = f2(m, m);
+        if (ch < w.end)   // r may be infinite behind the last head
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[i] = f2_fma(d[i], r2, acc[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = f2_mul(r2, f2_fma(f2_mul(x[i], r2), m2, g[i]));
+        rg[u] = f2_to_bf16x8(x);
+      }
+      if (ch < w.end) *reinterpret_cast<uint4*>(p.out + w.row + ch) = rg[u];
+    };
+    if (w.region == 2) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) step(u, false);
+    } else if (w.ch + (((kU - 1) * kNormStep) << p.shift) < w.end) {   // all steps are there: they interleave
+#pragma unroll
+      for (int u = 0; u < kU; ++u) step(u, true);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kU - 1; ++u) {
+        if (w.ch + ((u * kNormStep) << p.shift) >= w.end) break;
+        step(u, true);
       }
     }
   }
   if (p.partials == nullptr) return;
-  // lanes of the same channels, then the CTA's warps
-  __shared__ float sums[kNormWarps][2][kD];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-#pragma unroll
-    for (int o = kD / 8; o < 32; o <<= 1) {
-      aq[i] += __shfl_xor_sync(0xffffffffu, aq[i], o);
-      ak[i] += __shfl_xor_sync(0xffffffffu, ak[i], o);
-    }
-    if (lane < kD / 8) {
-      sums[warp][0][lane * 8 + i] = aq[i];
-      sums[warp][1][lane * 8 + i] = ak[i];
-    }
-  }
+  if (region < 2) put(region);
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * kD; i += kNormThreads) {
     float s = 0.f;

@@ -69,8 +69,8 @@ cudaError_t launch_seq(void (*k)(KArgs...), dim3 grid, int threads, size_t smem,
 // ---------------------------------------------------------------------------------------
 // head norms with rotation
 
-// CTAs of the backward at most: the workspace holds one pair of partial sums for each
-constexpr int kNormMaxGrid = 2048;
+// The backward has two CTAs an SM: the workspace holds one pair of partial sums for each
+constexpr int kNormMaxSms = 256, kNormMaxGrid = 2 * kNormMaxSms;
 
 struct NormCall {
   const void *qkv, *dout;
@@ -133,14 +133,14 @@ NormPlan norm_plan(const NormCall& c, bool bwd, int num_sms, int* grid) {
   p.W = p.qk_ch + c.Hv * c.d;
   p.copy_v = bwd ? c.out != c.dout : c.out != c.qkv;
   p.eps = c.eps;
-  // the padded rows of the backward are zeroed whole, v's part of an in-place one too
-  p.steps = (p.W + kNormStep - 1) / kNormStep;
-  // warps per row: enough to give every SM 16 warps, no more than the row has steps
-  const long long want = 16LL * num_sms;
-  p.parts = (int)std::min<long long>(p.steps, std::max<long long>(1, (want + p.rows - 1) / p.rows));
-  const long long ctas = (p.rows * p.parts + kNormWarps - 1) / kNormWarps;
-  // The gradient's CTAs loop, so that few partial sums of the weights' gradients are left to add
-  *grid = (int)std::min<long long>(ctas, bwd ? std::min(kNormMaxGrid, 4 * num_sms) : 1 << 20);
+  // padded rows of the backward are zeroed whole, v's part of an in-place one too
+  p.regions = p.copy_v || (bwd && c.pos != nullptr) ? 3 : 2;
+  // warps per task: enough to give every SM 16 warps, no more than a task has steps
+  const long long tasks = p.rows * p.regions;
+  const int widest = std::max(std::max(p.q_ch, p.qk_ch - p.q_ch), p.regions == 3 ? p.W - p.qk_ch : 0);
+  while ((tasks << p.shift) < 16LL * num_sms && (kNormStep << p.shift) < widest) ++p.shift;
+  const long long ctas = ((tasks << p.shift) + kNormWarps - 1) / kNormWarps;
+  *grid = (int)std::min<long long>(ctas, (bwd ? 2 : 3) * std::min(num_sms, kNormMaxSms));   // as many as fit at once
   return p;
 }
 
