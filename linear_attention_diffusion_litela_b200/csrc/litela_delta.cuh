@@ -9,6 +9,7 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 
+#include "f32x2.cuh"
 #include "sm100_ptx.cuh"
 
 namespace litela {
@@ -32,6 +33,7 @@ struct DeltaArgs {
   int ntok;                    // tokens: of the packed buffer, or of each batch entry
   int nslots;                  // states in the pool (slots != null)
   int Hk, Hv;
+  int zero_rest;               // packed: rows of no sequence are set to zero
   float scale;
 };
 
@@ -57,29 +59,198 @@ __device__ __forceinline__ const __nv_bfloat16* delta_row(const DeltaView& v, co
 
 __device__ __forceinline__ float bf16_up(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
 
+// Rows of a packed buffer that no sequence has (those before the first one and behind the last one):
+// this thread's share of the grid's.  f(row, one of its per_row pieces)
+template <typename F>
+__device__ __forceinline__ void delta_rest(const DeltaArgs& a, int per_row, F&& f) {
+  const int b = min(max(a.cu[0], 0), a.ntok), e = min(max(a.cu[a.nseq], b), a.ntok);
+  const long long n = (long long)(b + a.ntok - e) * per_row;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
+    const int row = (int)(i / per_row);
+    f(row < b ? row : e + row - b, (int)(i - (long long)row * per_row));
+  }
+}
+// zeros there, in an output of `heads` heads of d channels
+__device__ __forceinline__ void delta_zero_rest(const DeltaArgs& a, const DeltaView& out, int heads, int d) {
+  delta_rest(a, heads * (d / 8), [&](int row, int c) {
+    *reinterpret_cast<uint4*>(out.p + (long long)row * out.st + (c / (d / 8)) * out.sh + (c % (d / 8)) * 8) =
+        make_uint4(0u, 0u, 0u, 0u);
+  });
+}
+
 // ---------------------------------------------------------------------------------------
 // litela_delta_recur: the recurrence, one token after another, the state in registers.
 //
-// A warp owns 8 columns of one state (all d rows): lane = row group (lane / 2) and 4 columns
-// (lane & 1), rows lane / 2 + 16 j.  Nothing is shared between warps.  S^T k and S^T q of the
-// state before the token are summed in the same shuffles: with them
+// A warp owns 8 columns of one state (all d rows): lane = d / 16 rows (of group lane / 2) and 4
+// columns (of half lane & 1).  Nothing is shared between warps.  S^T k and S^T q of the state
+// before the token are summed in the same shuffles (each halves the sums that a lane still holds,
+// until it has one of the 8 totals of its columns): with them
 //     u = beta (v - e^g S^T k),   out = scale * (e^g S^T q + (k . q) u),   S <- e^g S + k u^T,
 // so that the update of S is off the way from one token's sums to the next one's output.
-// One token (the serving form) moves a state once in and once out, 8 d^2 bytes per head: HBM
-// bound.  The grid is one CTA per 32 columns, so that one sequence already fills the SMs.
-// More tokens: bound by the ~0.3 us between one token's loads and the next one's.
+// Tokens come through shared memory, kRecurBatch at a time while the batch before is worked on.  Bound by
+// a token's chain of dependent sums, 0.26 us (d = 32) to 0.4 us (128): 16 sequences of 125 tokens in
+// all, the longest of 30, 8 heads of 64: 15 us (23 with each token loaded from global memory one ahead).  The grid is one CTA per 32 columns, so that one sequence already
+// fills the SMs.
 constexpr int kRecurThreads = 128;
 constexpr int kRecurCols = 32;
+constexpr int kRecurBatch = 8;
+
+// kN bf16 values, kN / 2 words
+template <int kN>
+__device__ __forceinline__ void recur_load(const uint8_t* p, uint32_t* w) {
+  if (kN == 8) {
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  } else if (kN == 4) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    w[0] = x.x, w[1] = x.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
 
 template <int kD>
 __global__ void __launch_bounds__(kRecurThreads) litela_delta_recur(const DeltaArgs a) {
+  using namespace sm100;
   constexpr int kRows = kD / 16;   // rows per lane
   constexpr int kBlocks = kD / kRecurCols;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int blk = blockIdx.x % kBlocks, h = (blockIdx.x / kBlocks) % a.Hv, s = blockIdx.x / (kBlocks * a.Hv);
   const int hk = h / (a.Hv / a.Hk);
-  const int col = blk * kRecurCols + warp * 8 + (lane & 1) * 4, r0 = lane >> 1;
+  const int half = lane & 1, r0 = (lane >> 1) * kRows;
+  const int col = blk * kRecurCols + warp * 8 + half * 4;
+  // the total that this lane ends up with: of k (0) or q (1), for column `mine` of its four
+  const int of_q = lane >> 1 & 1, mine = (lane >> 2 & 1) * 2 + (lane >> 3 & 1);
+  if (a.zero_rest) delta_zero_rest(a, a.out, a.Hv, kD);
   const DeltaSeq sq = delta_seq(a, s);
+  // a token in shared memory: k, q, v of the block's columns, g, beta
+  constexpr int kOffQ = kD * 2, kOffV = kD * 4, kOffG = kOffV + kRecurCols * 2, kToken = kOffG + 16;
+  __shared__ __align__(16) uint8_t ring[2 * kRecurBatch * kToken];
+  auto gate = [&](const float* p, long long sb, long long st, int n) { return p + sq.entry * sb + (sq.first + n) * st + h; };
+  auto fetch = [&](int n0) {   // tokens [n0, n0 + kRecurBatch) to their half of the ring
+    constexpr int kVec = kToken / 16;
+    for (int i = threadIdx.x; i < kRecurBatch * kVec; i += kRecurThreads) {
+      const int t = i / kVec, c = i - t * kVec, n = n0 + t;
+      if (n >= sq.len) break;
+      const uint32_t dst = smem_u32(ring + (n % (2 * kRecurBatch)) * kToken + c * 16);
+      if (c < kOffQ / 16) cp_async_16(dst, delta_row(a.k, sq, n, hk) + c * 8, true);
+      else if (c < kOffV / 16) cp_async_16(dst, delta_row(a.q, sq, n, hk) + c * 8 - kD, true);
+      else if (c < kOffG / 16) cp_async_16(dst, delta_row(a.v, sq, n, h) + blk * kRecurCols + c * 8 - 2 * kD, true);
+      else {
+        cp_async_4(dst, gate(a.g, a.g_sb, a.g_st, n));
+        cp_async_4(dst + 4, gate(a.beta, a.b_sb, a.b_st, n));
+      }
+    }
+    cp_async_commit();
+  };
+  fetch(0);
+  const long long base = ((long long)s * a.Hv + h) * (long long)(kD * kD) + (long long)r0 * kD + col;
+  F2 S[kRows][2];
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.state_in != nullptr) x = *reinterpret_cast<const float4*>(a.state_in + base + (long long)j * kD);
+    S[j][0] = f2(x.x, x.y), S[j][1] = f2(x.z, x.w);
+  }
+  for (int n = 0; n < sq.len; ++n) {
+    if (n % kRecurBatch == 0) {
+      cp_async_wait<0>();
+      __syncthreads();   // this batch is there, and all have left the one before it
+      fetch(n + kRecurBatch);
+    }
+    const uint8_t* tok = ring + (n % (2 * kRecurBatch)) * kToken;
+    uint32_t kw[kRows / 2], qw[kRows / 2];
+    recur_load<kRows>(tok + r0 * 2, kw);
+    recur_load<kRows>(tok + kOffQ + r0 * 2, qw);
+    const float2 gates = *reinterpret_cast<const float2*>(tok + kOffG);
+    float k[kRows], q[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows / 2; ++j) {
+      k[2 * j] = __uint_as_float(kw[j] << 16), k[2 * j + 1] = __uint_as_float(kw[j] & 0xFFFF0000u);
+      q[2 * j] = __uint_as_float(qw[j] << 16), q[2 * j + 1] = __uint_as_float(qw[j] & 0xFFFF0000u);
+    }
+    const float decay = expf(clamp_decay(gates.x));
+    const float v = bf16_up(reinterpret_cast<const uint16_t*>(tok + kOffV)[warp * 8 + half * 4 + mine]);
+    F2 sk[2] = {f2(0.f, 0.f), f2(0.f, 0.f)}, sv[2] = {sk[0], sk[1]};
+    float kq = 0.f;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const F2 k2 = f2(k[j], k[j]), q2 = f2(q[j], q[j]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        sk[c] = f2_fma(S[j][c], k2, sk[c]);
+        sv[c] = f2_fma(S[j][c], q2, sv[c]);
+      }
+      kq += k[j] * q[j];
+    }
+    float sum[4];
+    {
+      const float2 k01 = f2_out(sk[0]), k23 = f2_out(sk[1]), q01 = f2_out(sv[0]), q23 = f2_out(sv[1]);
+      const float ks[4] = {k01.x, k01.y, k23.x, k23.y}, qs[4] = {q01.x, q01.y, q23.x, q23.y};
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        sum[c] = (of_q ? qs[c] : ks[c]) + __shfl_xor_sync(0xffffffffu, of_q ? ks[c] : qs[c], 2);
+    }
+#pragma unroll
+    for (int m = 2, o = 4; m >= 1; m >>= 1, o <<= 1) {   // columns 0-1 or 2-3, then one of the two
+      const bool up = mine & m;
+#pragma unroll
+      for (int c = 0; c < m; ++c)
+        sum[c] = (up ? sum[c + m] : sum[c]) + __shfl_xor_sync(0xffffffffu, up ? sum[c] : sum[c + m], o);
+    }
+    const float total = sum[0] + __shfl_xor_sync(0xffffffffu, sum[0], 16);
+#pragma unroll
+    for (int o = 2; o < 32; o <<= 1) kq += __shfl_xor_sync(0xffffffffu, kq, o);
+    const float wrote = gates.y * (v - decay * total);   // u of the lane's column where the total is k's
+    float u[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) u[c] = __shfl_sync(0xffffffffu, wrote, half | (c & 2) << 1 | (c & 1) << 3);
+    const float mu = __shfl_xor_sync(0xffffffffu, wrote, 2);
+    if (of_q && lane < 16)
+      const_cast<__nv_bfloat16*>(delta_row(a.out, sq, n, h))[col + mine] =
+          __float2bfloat16_rn(a.scale * (decay * total + kq * mu));
+    const F2 d2 = f2(decay, decay), u01 = f2(u[0], u[1]), u23 = f2(u[2], u[3]);
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const F2 k2 = f2(k[j], k[j]);
+      S[j][0] = f2_fma(k2, u01, f2_mul(d2, S[j][0]));
+      S[j][1] = f2_fma(k2, u23, f2_mul(d2, S[j][1]));
+    }
+  }
+  if (a.state_out != nullptr)
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const float2 x = f2_out(S[j][0]), y = f2_out(S[j][1]);
+      *reinterpret_cast<float4*>(a.state_out + base + (long long)j * kD) = make_float4(x.x, x.y, y.x, y.y);
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// litela_delta_step: one token, the serving form, on a pool of states: the recurrence's formulas.
+//
+// A state is read and written once, 8 d^2 bytes per head: HBM bound.  A CTA has 32 columns of a state,
+// a warp a quarter of the rows, so that 8 lanes read 128 adjacent bytes; the warps' sums are added through
+// shared memory.  96 rows of 32 heads of 128: 64 us, 6.4 TB/s (with the recurrence's layout, 32 bytes of
+// 16 rows a load, the loads' wavefronts were at 67 % of their peak: 77 us); one row: 4.9 us.
+template <int kD>
+__global__ void __launch_bounds__(kRecurThreads, 6) litela_delta_step(const DeltaArgs a) {
+  constexpr int kRows = kD / 16;   // rows per lane, 4 apart
+  constexpr int kBlocks = kD / kRecurCols;
+  constexpr int kWarps = kRecurThreads / 32;
+  __shared__ __align__(16) float part[kWarps][2][kRecurCols];   // S^T k and S^T q of a warp's rows
+  __shared__ float part_kq[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int blk = blockIdx.x % kBlocks, h = (blockIdx.x / kBlocks) % a.Hv, s = blockIdx.x / (kBlocks * a.Hv);
+  const int hk = h / (a.Hv / a.Hk);
+  const int r0 = warp * (kD / kWarps) + (lane >> 3), c = (lane & 7) * 4, col = blk * kRecurCols + c;
+  const DeltaSeq sq{s, 0, 1};
+  const uint16_t* kp = reinterpret_cast<const uint16_t*>(delta_row(a.k, sq, 0, hk)) + r0;
+  const uint16_t* qp = reinterpret_cast<const uint16_t*>(delta_row(a.q, sq, 0, hk)) + r0;
+  float k[kRows], q[kRows];
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) k[j] = bf16_up(kp[4 * j]), q[j] = bf16_up(qp[4 * j]);
+  const uint2 vw = *reinterpret_cast<const uint2*>(delta_row(a.v, sq, 0, h) + col);
+  const float decay = expf(clamp_decay(a.g[s * a.g_sb + h])), beta = a.beta[s * a.b_sb + h];
   long long slot = s;
   if (a.slots != nullptr) {
     // A row without a state of its own (an index outside the pool, or one that an earlier row has
@@ -88,84 +259,76 @@ __global__ void __launch_bounds__(kRecurThreads) litela_delta_recur(const DeltaA
     bool dup = false;
     for (int i = threadIdx.x; i < s; i += kRecurThreads) dup |= a.slots[i] == (int)slot;
     if (__syncthreads_or(dup) || slot < 0 || slot >= a.nslots) {
-      for (int n = 0; n < sq.len; ++n)
-        if (threadIdx.x < kRecurCols / 4) {
-          __nv_bfloat16* o = const_cast<__nv_bfloat16*>(delta_row(a.out, sq, n, h)) + blk * kRecurCols + threadIdx.x * 4;
-          *reinterpret_cast<uint2*>(o) = make_uint2(0u, 0u);
-        }
+      if (threadIdx.x < kRecurCols / 4)
+        *reinterpret_cast<uint2*>(const_cast<__nv_bfloat16*>(delta_row(a.out, sq, 0, h)) + col) = make_uint2(0u, 0u);
       return;
     }
   }
   const long long base = (slot * a.Hv + h) * (long long)(kD * kD) + (long long)r0 * kD + col;
-  float S[kRows][4];
+  F2 S[kRows][2];
 #pragma unroll
   for (int j = 0; j < kRows; ++j) {
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (a.state_in != nullptr) x = *reinterpret_cast<const float4*>(a.state_in + base + (long long)j * 16 * kD);
-    S[j][0] = x.x, S[j][1] = x.y, S[j][2] = x.z, S[j][3] = x.w;
+    if (a.state_in != nullptr) x = *reinterpret_cast<const float4*>(a.state_in + base + (long long)j * 4 * kD);
+    S[j][0] = f2(x.x, x.y), S[j][1] = f2(x.z, x.w);
   }
-  for (int n = 0; n < sq.len; ++n) {
-    const uint16_t* kp = reinterpret_cast<const uint16_t*>(delta_row(a.k, sq, n, hk)) + r0;
-    const uint16_t* qp = reinterpret_cast<const uint16_t*>(delta_row(a.q, sq, n, hk)) + r0;
-    const long long tok = sq.first + n;
-    const float decay = expf(clamp_decay(a.g[sq.entry * a.g_sb + tok * a.g_st + h]));
-    const float beta = a.beta[sq.entry * a.b_sb + tok * a.b_st + h];
-    const uint2 vr = *reinterpret_cast<const uint2*>(delta_row(a.v, sq, n, h) + col);
-    float k[kRows], q[kRows], sum[9];
+  F2 sk[2] = {f2(0.f, 0.f), f2(0.f, 0.f)}, sv[2] = {sk[0], sk[1]};
+  float kq = 0.f;
 #pragma unroll
-    for (int i = 0; i < 9; ++i) sum[i] = 0.f;
+  for (int j = 0; j < kRows; ++j) {
+    const F2 k2 = f2(k[j], k[j]), q2 = f2(q[j], q[j]);
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      k[j] = bf16_up(kp[16 * j]);
-      q[j] = bf16_up(qp[16 * j]);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        sum[c] += S[j][c] * k[j];
-        sum[4 + c] += S[j][c] * q[j];
-      }
-      sum[8] += k[j] * q[j];
+    for (int i = 0; i < 2; ++i) {
+      sk[i] = f2_fma(S[j][i], k2, sk[i]);
+      sv[i] = f2_fma(S[j][i], q2, sv[i]);
     }
-#pragma unroll
-    for (int i = 0; i < 9; ++i)
-#pragma unroll
-      for (int o = 2; o < 32; o <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
-    const float v[4] = {__uint_as_float(vr.x << 16), __uint_as_float(vr.x & 0xFFFF0000u),
-                        __uint_as_float(vr.y << 16), __uint_as_float(vr.y & 0xFFFF0000u)};
-    float u[4], o[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      u[c] = beta * (v[c] - decay * sum[c]);
-      o[c] = a.scale * (decay * sum[4 + c] + sum[8] * u[c]);
-    }
-    if (r0 == 0) {
-      __nv_bfloat162 lo = __floats2bfloat162_rn(o[0], o[1]), hi = __floats2bfloat162_rn(o[2], o[3]);
-      *reinterpret_cast<uint2*>(const_cast<__nv_bfloat16*>(delta_row(a.out, sq, n, h)) + col) =
-          make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
-    }
-#pragma unroll
-    for (int j = 0; j < kRows; ++j)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) S[j][c] = decay * S[j][c] + k[j] * u[c];
+    kq += k[j] * q[j];
   }
-  if (a.state_out != nullptr)
+  const float2 k01 = f2_out(sk[0]), k23 = f2_out(sk[1]), q01 = f2_out(sv[0]), q23 = f2_out(sv[1]);
+  float x[4] = {k01.x, k01.y, k23.x, k23.y}, y[4] = {q01.x, q01.y, q23.x, q23.y};
+  // lanes 0-7 and 16-23 go on with k's sums, the others with q's
+  const bool of_q = lane & 8;
 #pragma unroll
-    for (int j = 0; j < kRows; ++j)
-      *reinterpret_cast<float4*>(a.state_out + base + (long long)j * 16 * kD) =
-          make_float4(S[j][0], S[j][1], S[j][2], S[j][3]);
-}
-
-// zeros in the rows of a packed [token, head, d] output that no sequence has: those before the
-// first one and behind the last one
-__global__ void __launch_bounds__(256) litela_delta_zero_tail(const DeltaView out, const int* cu, int nseq, int ntok,
-                                                             int heads, int d) {
-  const int b = min(max(cu[0], 0), ntok), e = min(max(cu[nseq], b), ntok);
-  const int per_row = heads * (d / 8);
-  const long long n = (long long)(b + ntok - e) * per_row;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
-    const int row = (int)(i / per_row), c = (int)(i - (long long)row * per_row);
-    const int t = row < b ? row : e + row - b;
-    *reinterpret_cast<uint4*>(out.p + (long long)t * out.st + (c / (d / 8)) * out.sh + (c % (d / 8)) * 8) =
-        make_uint4(0u, 0u, 0u, 0u);
+  for (int i = 0; i < 4; ++i) {
+    x[i] = (of_q ? y[i] : x[i]) + __shfl_xor_sync(0xffffffffu, of_q ? x[i] : y[i], 8);
+    x[i] += __shfl_xor_sync(0xffffffffu, x[i], 16);
+  }
+  kq += __shfl_xor_sync(0xffffffffu, kq, 8);
+  kq += __shfl_xor_sync(0xffffffffu, kq, 16);
+  if (lane < 16) *reinterpret_cast<float4*>(&part[warp][of_q][c]) = make_float4(x[0], x[1], x[2], x[3]);
+  if (lane == 0) part_kq[warp] = kq;
+  __syncthreads();
+  const float v[4] = {__uint_as_float(vw.x << 16), __uint_as_float(vw.x & 0xFFFF0000u), __uint_as_float(vw.y << 16),
+                      __uint_as_float(vw.y & 0xFFFF0000u)};
+  auto total = [&](int which, float* t) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float4 p = *reinterpret_cast<const float4*>(&part[w][which][c]);
+      t[0] += p.x, t[1] += p.y, t[2] += p.z, t[3] += p.w;
+    }
+  };
+  float u[4], o[4];
+  total(0, u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) u[i] = beta * (v[i] - decay * u[i]);
+  if (threadIdx.x < kRecurCols / 4) {
+    total(1, o);
+    const float all = part_kq[0] + part_kq[1] + part_kq[2] + part_kq[3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = a.scale * (decay * o[i] + all * u[i]);
+    __nv_bfloat162 lo = __floats2bfloat162_rn(o[0], o[1]), hi = __floats2bfloat162_rn(o[2], o[3]);
+    *reinterpret_cast<uint2*>(const_cast<__nv_bfloat16*>(delta_row(a.out, sq, 0, h)) + col) =
+        make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+  }
+  if (a.state_out == nullptr) return;
+  const F2 d2 = f2(decay, decay), u01 = f2(u[0], u[1]), u23 = f2(u[2], u[3]);
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    const F2 k2 = f2(k[j], k[j]);
+    const float2 l = f2_out(f2_fma(k2, u01, f2_mul(d2, S[j][0]))), r = f2_out(f2_fma(k2, u23, f2_mul(d2, S[j][1])));
+    *reinterpret_cast<float4*>(a.state_out + base + (long long)j * 4 * kD) = make_float4(l.x, l.y, r.x, r.y);
   }
 }
 

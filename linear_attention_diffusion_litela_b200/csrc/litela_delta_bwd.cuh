@@ -488,6 +488,12 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g4 = lane >> 2, t2 = (lane & 3) * 2;
   const int rb = w / kCW, cw = w % kCW, l8 = lane & 7, k8 = ((lane >> 3) & 1) * 8;
   const int slot = blockIdx.x / a.Hk, hk = blockIdx.x - slot * a.Hk, group = a.Hv / a.Hk;
+  if (a.zero_rest) {
+    delta_zero_rest(a, gr.dq, a.Hk, kD);
+    delta_zero_rest(a, gr.dk, a.Hk, kD);
+    delta_zero_rest(a, gr.dv, a.Hv, kD);
+    delta_rest(a, a.Hv, [&](int row, int h) { gr.dg[(long long)row * a.Hv + h] = gr.dbeta[(long long)row * a.Hv + h] = 0.f; });
+  }
   int s, n0;
   DeltaSeq sq;
   if (!delta_find(a, slot, lane, s, sq, n0)) return;
@@ -824,17 +830,6 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
         *reinterpret_cast<uint32_t*>(dkp + 8 * n) = pack_bf16(dk[n][2 * q], dk[n][2 * q + 1]);
       }
     }
-  }
-}
-
-// zeros in the rows of a packed [token, head] fp32 array that no sequence has
-__global__ void __launch_bounds__(256) litela_delta_zero_gates(float* dg, float* db, const int* cu, int nseq, int ntok,
-                                                              int heads) {
-  const int b = min(max(cu[0], 0), ntok), e = min(max(cu[nseq], b), ntok);
-  const long long n = (long long)(b + ntok - e) * heads;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
-    const long long o = i < (long long)b * heads ? i : i + (long long)(e - b) * heads;
-    dg[o] = db[o] = 0.f;
   }
 }
 

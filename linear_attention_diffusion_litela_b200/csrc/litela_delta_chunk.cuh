@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, gr = lane >> 2, t2 = (lane & 3) * 2;
   pdl_launch_dependents();   // the chain waits for this grid before it reads what it wrote
   const int slot = blockIdx.x / a.Hv, h = blockIdx.x - slot * a.Hv, hk = h / (a.Hv / a.Hk);
+  if (a.zero_rest) delta_zero_rest(a, a.out, a.Hv, kD);
   int s, n0;
   DeltaSeq sq;
   if (!delta_find(a, slot, lane, s, sq, n0)) return;

@@ -278,6 +278,7 @@ litela_status delta_validate(const lite_la_delta_args* a, bool with_out, DeltaSp
   if ((a->Hk == 0) != (a->Hv == 0) || (a->Hk > 0 && a->Hv % a->Hk != 0))
     return unsupported("Hv must be a multiple of Hk");
   if (!std::isfinite(a->scale)) return invalid("scale must be finite");
+  if (a->cu_seqlens != nullptr && a->B == 0 && a->N > 0) return invalid("packed tokens need a sequence");
   if (a->B == 0 || a->Hv == 0) {
     *empty = true;
     return LITELA_OK;
@@ -337,10 +338,13 @@ DeltaArgs delta_args(const lite_la_delta_args* a) {
 
 litela_status launch_recur(const DeltaArgs& d, int D, cudaStream_t st) {
   const dim3 grid((unsigned)((long long)d.nseq * d.Hv * (D / kRecurCols)));
-  const cudaError_t e = D == 32   ? launch_seq(litela_delta_recur<32>, grid, kRecurThreads, 0, st, false, d)
-                        : D == 64 ? launch_seq(litela_delta_recur<64>, grid, kRecurThreads, 0, st, false, d)
-                                  : launch_seq(litela_delta_recur<128>, grid, kRecurThreads, 0, st, false, d);
-  return e == cudaSuccess ? LITELA_OK : host_cuda_fail(e, "launch litela_delta_recur");
+  const bool one = d.cu == nullptr && d.ntok == 1;
+#define LITELA_RECUR(D)                                                            \
+  (one ? launch_seq(litela_delta_step<D>, grid, kRecurThreads, 0, st, false, d)    \
+       : launch_seq(litela_delta_recur<D>, grid, kRecurThreads, 0, st, false, d))
+  const cudaError_t e = D == 32 ? LITELA_RECUR(32) : D == 64 ? LITELA_RECUR(64) : LITELA_RECUR(128);
+#undef LITELA_RECUR
+  return e == cudaSuccess ? LITELA_OK : host_cuda_fail(e, "launch the recurrence");
 }
 
 // shared-memory limits of the chunked kernels, once per device
@@ -376,10 +380,19 @@ litela_status delta_setup(int dev) {
   return LITELA_OK;
 }
 
-// The recurrence or the chunks.  A call of at most this many tokens (of each batch entry; packed:
-// of all sequences, whose lengths only the device knows) runs the recurrence.
-constexpr int kRecurMaxTokens = 32;
-bool delta_recurs(int ntok) { return ntok <= kRecurMaxTokens; }
+// The recurrence or the chunks.  The recurrence takes 0.26 to 0.4 us a token (one sequence, d = 32
+// to 128) or what its instructions take; the chunks take a whole chunk's time for every started one.  Dense
+// (us, recurrence / chunks), N = 32: 1 x 32 heads of 128 15.0 / 13.0, 64 x 32 345 / 366; 64 x 8 heads of
+// 64 34 / 48; 1 x 70 heads of 32 10.3 / 10.5, 64 x 70 98 / 238.  N = 64: 28.0 / 12.9, 668 / 377, 65 / 49,
+// 18.5 / 10.7, 189 / 248.
+// Packed lengths are known to the device only: the recurrence where they are 8 on the average
+// (16 sequences, 125 tokens, the longest of 30, 8 heads of 64: 15 / 23; 64 sequences of 8: 106 / 359, 11 / 48
+// and 30 / 232 at the three widths) and the longest can be no more than 512 (0.2 ms).
+constexpr int kRecurMaxTokens = 32, kRecurMaxMean = 8, kRecurMaxPacked = 512;
+bool delta_recurs(int nseq, int ntok, bool packed) {
+  if (ntok <= kRecurMaxTokens) return true;
+  return packed && ntok <= kRecurMaxPacked && ntok <= (long long)kRecurMaxMean * nseq;
+}
 
 // the prepared blocks, then the chain; kSave: a training step's
 template <int kD, bool kSave = false>
@@ -449,12 +462,6 @@ litela_status buffer_check(const lite_la_delta_args* a, const void* p, size_t by
   return LITELA_OK;
 }
 
-litela_status zero_tail(const lite_la_delta_args* a, const lite_la_view& v, int heads, int sms, cudaStream_t st) {
-  const cudaError_t e = launch_seq(litela_delta_zero_tail, dim3(sms), 256, 0, st, false, view_of(v), a->cu_seqlens, a->B,
-                                   a->N, heads, a->d);
-  return e == cudaSuccess ? LITELA_OK : host_cuda_fail(e, "launch litela_delta_zero_tail");
-}
-
 litela_status delta_fwd(const lite_la_delta_args* a, bool save, void* saved, size_t saved_bytes, cudaStream_t st) {
   DeltaSpans in;
   Span out;
@@ -462,7 +469,7 @@ litela_status delta_fwd(const lite_la_delta_args* a, bool save, void* saved, siz
   litela_status s = delta_validate(a, true, &in, &out, &empty);
   if (s != LITELA_OK || empty) return s;
   if ((s = state_check(a, (size_t)a->B * a->Hv * a->d * a->d * 4, in, out)) != LITELA_OK) return s;
-  const bool recurs = !save && delta_recurs(a->N);
+  const bool recurs = !save && delta_recurs(a->B, a->N, a->cu_seqlens != nullptr);
   const DeltaBytes bytes(a->B, a->N, a->Hv, a->d, a->cu_seqlens != nullptr);
   if (save) {
     s = buffer_check(a, saved, saved_bytes, bytes.saved(), in, out, "saved missing, too small or misaligned",
@@ -474,9 +481,8 @@ litela_status delta_fwd(const lite_la_delta_args* a, bool save, void* saved, siz
   if (s != LITELA_OK) return s;
   int dev, sms;
   if ((s = host_device(&dev, &sms)) != LITELA_OK) return s;
-  const DeltaArgs d = delta_args(a);
-  if (a->zero_tail && a->cu_seqlens != nullptr && a->N > 0 && (s = zero_tail(a, a->out, a->Hv, sms, st)) != LITELA_OK)
-    return s;
+  DeltaArgs d = delta_args(a);
+  d.zero_rest = a->zero_tail != 0 && a->cu_seqlens != nullptr;
   if (save) {
     if ((s = delta_setup(dev)) != LITELA_OK) return s;
     if (d.ntok == 0) {
@@ -548,15 +554,8 @@ litela_status delta_bwd(const lite_la_delta_args* a, const lite_la_delta_grads* 
     return invalid("dstate_in overlaps dstate_out in part");
   int dev, sms;
   if ((s = host_device(&dev, &sms)) != LITELA_OK || (s = delta_setup(dev)) != LITELA_OK) return s;
-  if (a->cu_seqlens != nullptr && a->N > 0) {
-    if ((s = zero_tail(a, g->dq, a->Hk, sms, st)) != LITELA_OK || (s = zero_tail(a, g->dk, a->Hk, sms, st)) != LITELA_OK ||
-        (s = zero_tail(a, g->dv, a->Hv, sms, st)) != LITELA_OK)
-      return s;
-    const cudaError_t e = launch_seq(litela_delta_zero_gates, dim3(sms), 256, 0, st, false, g->dg, g->dbeta, a->cu_seqlens, a->B,
-                                     a->N, a->Hv);
-    if (e != cudaSuccess) return host_cuda_fail(e, "launch litela_delta_zero_gates");
-  }
   DeltaArgs d = delta_args(a);
+  d.zero_rest = a->cu_seqlens != nullptr;
   DeltaGrads gr{};
   gr.dout = view_of(g->dout), gr.dq = view_of(g->dq), gr.dk = view_of(g->dk), gr.dv = view_of(g->dv);
   gr.dg = g->dg, gr.dbeta = g->dbeta;
@@ -649,7 +648,7 @@ litela_status lite_la_gated_delta_fwd(const lite_la_delta_args* args, cudaStream
 }
 
 size_t lite_la_gated_delta_workspace_bytes(int B, int N, int Hk, int Hv, int d, int packed) {
-  if (!litela::delta_sizes_ok(B, N, Hk, Hv, d) || litela::delta_recurs(N)) return 0;
+  if (!litela::delta_sizes_ok(B, N, Hk, Hv, d) || litela::delta_recurs(B, N, packed != 0)) return 0;
   return litela::DeltaBytes(B, N, Hv, d, packed != 0).prep;
 }
 
