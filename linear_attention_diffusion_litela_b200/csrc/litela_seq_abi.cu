@@ -8,6 +8,7 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <utility>
 
 #include "../../include/litela.h"
 #include "litela_delta.cuh"
@@ -94,7 +95,6 @@ litela_status norm_validate(const NormCall& c, bool bwd, bool* empty) {
   if (c.rot > 0 && c.pos == nullptr && c.table < c.N) return invalid("the tables are shorter than N");
   const double elems = (double)c.B * c.N * ((double)c.Hq + c.Hk + c.Hv) * c.d;
   if (elems > 4.0e18) return invalid("element count overflows int64");
-  if (((long long)c.Hq + c.Hk + c.Hv) * c.d > (1 << 30)) return invalid("a row has more than 2^30 channels");
   if (elems == 0) {
     *empty = true;
     return LITELA_OK;
@@ -298,6 +298,9 @@ litela_status delta_validate(const lite_la_delta_args* a, bool with_out, DeltaSp
     if (!aligned(a->g, 4) || !aligned(a->beta, 4)) return invalid("g and beta must be 4-byte aligned");
     if (a->g_batch_stride < 0 || a->g_token_stride < 0 || a->beta_batch_stride < 0 || a->beta_token_stride < 0)
       return invalid("strides of g and beta must be >= 0");
+    for (const auto& x : {std::pair<long long, long long>(a->g_batch_stride, a->g_token_stride),
+                          std::pair<long long, long long>(a->beta_batch_stride, a->beta_token_stride)})
+      if ((double)x.first * entries + (double)x.second * a->N > 2.0e18) return invalid("a gate's extent overflows int64");
     in->add(span(a->g, gate_bytes(entries, a->N, a->Hv, a->g_batch_stride, a->g_token_stride)));
     in->add(span(a->beta, gate_bytes(entries, a->N, a->Hv, a->beta_batch_stride, a->beta_token_stride)));
   }
@@ -545,6 +548,8 @@ litela_status delta_bwd(const lite_la_delta_args* a, const lite_la_delta_grads* 
   // and the dense outputs are checked
   const Span outs[7] = {sp[0], sp[1], sp[2], span(g->dg, gates), span(g->dbeta, gates), span(g->dstate_in, states),
                         span(a->workspace, a->N > 0 ? bytes.back() : 0)};
+  for (int i = 0; i < 3; ++i)
+    if (sp[i].hi > 0 && sp[i].lo == sp[(i + 1) % 3].lo) return invalid("dq, dk and dv must be different memory");
   for (int i = 0; i < 7; ++i) {
     if (in.hit(outs[i]) || (i != 5 && meet(outs[i], dso)) || meet(outs[i], so)) return invalid("an output overlaps an input");
     for (int j = i + 1; j < 7; ++j)
