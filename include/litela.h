@@ -312,13 +312,13 @@ size_t lite_la_gated_delta_workspace_bytes(int B, int N, int Hk, int Hv, int d, 
  * value head: 66 KB + 4 d^2 + 256 d bytes).  It needs no workspace.
  *
  * lite_la_gated_delta_bwd: the gradients of sum(dout * out) + sum(dstate_out * state_out).  args
- * are the forward's (out and its states are not used), saved is what it left and state_out what it
- * wrote; workspace: lite_la_gated_delta_bwd_workspace_bytes().  dout: a view of the layout of out; dq, dk [B, N, Hk, d]
- * and dv [B, N, Hv, d]: views; a key head's gradient is the sum over its value heads, in a fixed
- * order.  dg, dbeta: fp32 [B, N, Hv], dense.  dstate_out, dstate_in: as state_out and state_in, or
- * NULL (zeros; not wanted); state_out may be NULL when dstate_out is, and dstate_in may be dstate_out
- * itself.  All rows are written: those of
- * no sequence with zeros.  The sums are fp32; equal calls give equal bits.
+ * are the forward's (out and its states are not used), saved is what it left; workspace:
+ * lite_la_gated_delta_bwd_workspace_bytes().  dout: a view of the layout of out; dq, dk
+ * [B, N, Hk, d] and dv [B, N, Hv, d]: views; a key head's gradient is the sum over its value
+ * heads, in a fixed order.  dg, dbeta: fp32 [B, N, Hv], dense.  dstate_out, dstate_in: as
+ * state_out and state_in, or NULL (zeros; not wanted); dstate_in may be dstate_out itself.
+ * All rows are written: those of no sequence with zeros.  The sums are fp32; equal calls give
+ * equal bits.
  *
  * A NaN or infinite value of a token (or of the state before a sequence) makes out of that token, of
  * all later tokens and the state NaN in the heads that read it; earlier tokens keep their values.
@@ -328,7 +328,6 @@ typedef struct {
   float* dg;
   float* dbeta;
   const float* dstate_out;
-  const float* state_out;
   float* dstate_in;
 } lite_la_delta_grads;
 

@@ -8,9 +8,13 @@
 //     dq = scale diag(e^G) do S0^T + (M1 . D) K,            M1 = scale do U^T with and below the diagonal,
 //     dk = (M1 . D)^T Q + diag(e^(G_C - G)) U G'^T - diag(e^G) y S0^T - (M2 . D) K - (M2 . D)^T K,
 //                                                           M2 = y U^T below the diagonal,
-//     dg_t = <S_C, G'> + sum over s >= t in the chunk of (q_s . dq_s - y_s . v_s).
-// The last line: a decay multiplies the state before its token, so its gradient is <state, gradient>
-// there, and from a token to the one before it <S, G'> changes by out . do - dv . v.
+// and, as the decay of token t is a factor of everything that goes from before t to t or later,
+//     dg_t = e^G_C <S0, G'> + sum over i >= t of c_i + sum over j < t of b_j + sum over j < t <= i of N_ij,
+//     N = (M1 . D) . Q K^T - (M2 . D) . K K^T,  c = the products of q and k with their terms of S0,
+//                                               b = that of k with its term of G'.
+// The last sum is one over s >= t of N's row s less its column s.  (<S_C, G'> and the sums of
+// q . dq - y . v are the same in exact arithmetic, but cancel where decays are strong, with the errors of
+// bf16 pairs: 1.8e-5 of dg against 64 bits where this form has 1e-6.)
 //
 // litela_delta_back walks a sequence's chunks from the last to the first (as litela_delta_chain, with
 // the same three products a chunk) and leaves y and each chunk's G'; litela_delta_grads makes the rest,
@@ -29,14 +33,19 @@ struct DeltaGrads {
   float* dg;                       // [entry, token, Hv], dense
   float* dbeta;
   const float* dstate_out;         // [sequence][Hv][d][d] or null (zeros)
-  const float* state_out;          // the forward's, for dstate_out
   float* dstate_in;                // or null
   // between the two kernels, per chunk slot and value head
   uint8_t* gstates;                // G' as DeltaSaved's states
   uint8_t* y;                      // [d / 32] tiles of 64 rows of 128 bytes, 128-byte swizzle: bf16 pair
-  float* rows;                     // [d / 32][2][2][64]: w . W and y . v of half of 32 columns
-  float* ends;                     // [d / 32][8]: shares of <S_C, G'>
+  float* rows;                     // [d / 32][2][64]: w . W of half of 32 columns
+  float* ends;                     // [d / 32][8]: shares of <S0, G'>
 };
+
+__device__ __forceinline__ float sum_warp(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
 
 // ---------------------------------------------------------------------------------------
 // litela_delta_back: one CTA walks the chunks of one sequence and value head for 32 columns of the
@@ -51,14 +60,12 @@ template <int kD>
 struct BackCfg {
   static constexpr int kBlocks = kD > 64 ? 2 : 1;
   static constexpr uint32_t kKQ = kBlocks * 16384;                // per block: 64 rows of K and of Q
-  static constexpr uint32_t kVLd = kCols * 2 + 16;
   // the factors and the second image behind them, the image on a 1024-byte boundary
   static constexpr uint32_t kOffImage = kKQ + (kFactorBytes + 1023) / 1024 * 1024;
   static constexpr uint32_t kOffFac = kOffImage - kFactorBytes;
   static constexpr uint32_t kZTile = 64 * 128;                    // do and Z's three terms, two tiles
   static constexpr uint32_t kOffZ = kOffImage + 2 * kImgHalf;
-  static constexpr uint32_t kOffV = kOffZ + 2 * kZTile;
-  static constexpr uint32_t kStage = (kOffV + 64 * kVLd + 1023) / 1024 * 1024;
+  static constexpr uint32_t kStage = (kOffZ + 2 * kZTile + 1023) / 1024 * 1024;
   static constexpr uint32_t kSTile = kD * 128, kRTile = 128 * 128;
   static constexpr uint32_t kOffS = kChainStages * kStage;
   static constexpr uint32_t kOffR = kOffS + kSTile;               // y's and do's rows, three terms
@@ -140,23 +147,13 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
     F2 S[kN / 2];
 #pragma unroll
     for (int i = 0; i < kN / 2; ++i) S[i] = f2(0.f, 0.f);
-    // this warp's share of <S, G'> behind chunk n
-    auto put_end = [&](int n, float dot) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      if (lane == 0) gr.ends[(((slot0 + n) * a.Hv + h) * kParts + part) * 8 + warp] = dot;
-    };
-    float dot = 0.f;
     if (has_state && gr.dstate_out != nullptr)
 #pragma unroll
       for (int i = 0; i < kN; i += 4) {
         const float4 x = *reinterpret_cast<const float4*>(gr.dstate_out + sbase + i);
-        const float4 z = *reinterpret_cast<const float4*>(gr.state_out + sbase + i);
         S[i / 2] = f2(x.x, x.y), S[i / 2 + 1] = f2(x.z, x.w);
-        dot += x.x * z.x + x.y * z.y + x.z * z.z + x.w * z.w;
       }
     if (nchunk > 0) {
-      put_end(nchunk - 1, dot);
       if (has_state) chain_put<2>(stile, Cfg::kSTile, row, c0, S);
       hand(kBarS);
     }
@@ -174,11 +171,10 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
         beta[i] = fac[kFacBeta + tok + 8 * i];
       }
       const float chunk_decay = fac[kFacChunk];
-      uint32_t v[kN / 4], dov[kN / 4];
+      uint32_t dov[kN / 4];
 #pragma unroll
       for (int i = 0; i < kN / 4; ++i) {
         const int r = tok + (i & 1) * 8, c = fc + (i >> 1) * 8;
-        v[i] = *reinterpret_cast<const uint32_t*>(stage + Cfg::kOffV + r * Cfg::kVLd + c * 2);
         dov[i] = *reinterpret_cast<const uint32_t*>(stage + Cfg::kOffZ + sw128(r, c));
       }
       F2 x[kN / 2], y[kN / 4], z[kN / 4];
@@ -231,53 +227,42 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
           *reinterpret_cast<uint4*>(const_cast<__nv_bfloat16*>(delta_row(gr.dv, sq, n * kChunk + r, h)) + part * kCols + c) =
               *reinterpret_cast<const uint4*>(ytile + sw128(r, c));
       }
-      wait(&done[2], it, 3);
       F2 sdot = f2(0.f, 0.f);
+      wait(s0full, it, 4);   // the state before this chunk, in the tile's place
+      if (has_state)
+#pragma unroll
+        for (int i = 0; i < kN / 8; ++i) {
+          const uint4 hi = *reinterpret_cast<const uint4*>(stile + sw128(row, c0 + 8 * i));
+          const uint4 lo = *reinterpret_cast<const uint4*>(stile + sw128(row, 32 + c0 + 8 * i));
+          const uint32_t h4[4] = {hi.x, hi.y, hi.z, hi.w}, l4[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) sdot = f2_fma(S[4 * i + q], f2_add(f2_bf16(h4[q]), f2_bf16(l4[q])), sdot);
+        }
+      wait(&done[2], it, 3);
       if (has_state) {
         chain_acc<3>(ta + Cfg::kX3, c0, x);
         const F2 d2 = f2(chunk_decay, chunk_decay);
 #pragma unroll
         for (int i = 0; i < kN / 2; ++i) S[i] = f2_fma(d2, S[i], x[i]);
+        if (n > 0) chain_put<2>(stile, Cfg::kSTile, row, c0, S);
       }
-      if (n > 0) {
-        wait(s0full, it, 4);   // the state before this chunk, in the tile's place
-        if (has_state) {
-#pragma unroll
-          for (int i = 0; i < kN / 8; ++i) {
-            const uint4 hi = *reinterpret_cast<const uint4*>(stile + sw128(row, c0 + 8 * i));
-            const uint4 lo = *reinterpret_cast<const uint4*>(stile + sw128(row, 32 + c0 + 8 * i));
-            const uint32_t h4[4] = {hi.x, hi.y, hi.z, hi.w}, l4[4] = {lo.x, lo.y, lo.z, lo.w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) sdot = f2_fma(S[4 * i + q], f2_add(f2_bf16(h4[q]), f2_bf16(l4[q])), sdot);
-          }
-          chain_put<2>(stile, Cfg::kSTile, row, c0, S);
-        }
-        hand(kBarS);
-      }
+      if (n > 0) hand(kBarS);
       // while the next chunk's first product runs: the rows' shares
-      F2 wdot[2] = {f2(0.f, 0.f), f2(0.f, 0.f)}, vdot[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+      F2 wdot[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
-      for (int i = 0; i < kN / 4; ++i) {
-        wdot[i & 1] = f2_fma(z[i], f2(wv[i].x, wv[i].y), wdot[i & 1]);
-        vdot[i & 1] = f2_fma(y[i], f2_bf16(v[i]), vdot[i & 1]);
-      }
+      for (int i = 0; i < kN / 4; ++i) wdot[i & 1] = f2_fma(z[i], f2(wv[i].x, wv[i].y), wdot[i & 1]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float2 w2 = f2_out(wdot[i]), v2 = f2_out(vdot[i]);
-        float wd = w2.x + w2.y, vd = v2.x + v2.y;
+        const float2 w2 = f2_out(wdot[i]);
+        float wd = w2.x + w2.y;
         wd += __shfl_xor_sync(0xffffffffu, wd, 1);
-        vd += __shfl_xor_sync(0xffffffffu, vd, 1);
         wd += __shfl_xor_sync(0xffffffffu, wd, 2);
-        vd += __shfl_xor_sync(0xffffffffu, vd, 2);
-        float* rw = gr.rows + ((sh * kParts + part) * 2 * 2 + (warp >> 2)) * kChunk + tok + 8 * i;
-        if ((lane & 3) == 0) {
-          rw[0] = wd;
-          rw[2 * kChunk] = vd;
-        }
+        if ((lane & 3) == 0) gr.rows[((sh * kParts + part) * 2 + (warp >> 2)) * kChunk + tok + 8 * i] = wd;
       }
-      if (n > 0) {
+      {   // this warp's share of <S0, G'>
         const float2 dd = f2_out(sdot);
-        put_end(n - 1, dd.x + dd.y);
+        const float dot = sum_warp(dd.x + dd.y);
+        if (lane == 0) gr.ends[(sh * kParts + part) * 8 + warp] = dot;
       }
       __syncwarp();
       if (lane == 0) {   // the stage has been read
@@ -325,13 +310,6 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
       __syncwarp();
       bar_sync(kBarR, kBarThreads);
       tc_fence_after_sync();
-      if (n > 0 && lane == 0) {
-        // G' has been read by the first product and stored: the state before the chunk takes its place
-        bulk_wait_group_read<0>();
-        mbar_arrive_expect_tx(s0full, Cfg::kSTile);
-        bulk_load(stile, saved.states + (((slot0 + n) * a.Hv + h) * kParts + part) * (long long)Cfg::kSTile, Cfg::kSTile,
-                  s0full);
-      }
       if (ok && lane == 0) {
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
@@ -340,6 +318,14 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
         for (int ks = 0; ks < 4; ++ks)
           umma(tmem + Cfg::kX2, imgdesc + off + kImgHalf / 16 + ks * 128, zdesc + off + ks * 128, idesc_3, 1u);
         umma_commit(&done[1]);
+      }
+      if (lane == 0) {
+        // G' has been read by the first product and stored: the state before the chunk takes its place
+        bulk_wait_group_read<0>();
+        if (it > 0) mbar_drain(s0full, (it - 1) & 1);   // (long done, unless the walk was given up)
+        mbar_arrive_expect_tx(s0full, Cfg::kSTile);
+        bulk_load(stile, saved.states + (((slot0 + n) * a.Hv + h) * kParts + part) * (long long)Cfg::kSTile, Cfg::kSTile,
+                  s0full);
       }
       __syncwarp();
       bar_sync(kBarU, kBarThreads);
@@ -360,7 +346,7 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
       umma_commit(drained);
       mbar_drain(drained, 0);
       bulk_wait_group<0>();
-      if (nchunk > 1) mbar_drain(s0full, (nchunk - 2) & 1);
+      if (nchunk > 0) mbar_drain(s0full, (nchunk - 1) & 1);
     }
   } else {
     const int t = threadIdx.x - (warp > kIssueWarp ? kAccWarps + 1 : kAccWarps) * 32;
@@ -368,9 +354,8 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
     constexpr int kC = kD / 8, kStep = kLoadThreads / kC, kVC = kCols / 8, kVStep = kLoadThreads / kVC;
     const int r0 = t / kC, c = t % kC, vr0 = t / kVC, vc = t % kVC;
     const uint32_t kq0 = smem_u32(smem) + (c / 8) * 16384 + sw128(lane_of(r0), (c % 8) * 8);
-    const uint32_t v0 = smem_u32(smem) + Cfg::kOffV + vr0 * Cfg::kVLd + vc * 16;
     const uint32_t do0 = smem_u32(smem) + Cfg::kOffZ;
-    const long long kstep = kStep * a.k.st, qstep = kStep * a.q.st, vstep = kVStep * a.v.st, dstep = kVStep * gr.dout.st;
+    const long long kstep = kStep * a.k.st, qstep = kStep * a.q.st, dstep = kVStep * gr.dout.st;
     for (int it = 0; it < nchunk; ++it) {
       const int n = nchunk - 1 - it, st = it % kChainStages;
       const bool ok = it < kChainStages || lane != 0 ||
@@ -382,10 +367,9 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
       }
       issued = it + 1;
       const int n0 = n * kChunk, len = min(kChunk, sq.len - n0);
-      const uint32_t dkq = kq0 + st * Cfg::kStage, dv = v0 + st * Cfg::kStage, ddo = do0 + st * Cfg::kStage;
+      const uint32_t dkq = kq0 + st * Cfg::kStage, ddo = do0 + st * Cfg::kStage;
       const __nv_bfloat16* kp = delta_row(a.k, sq, n0 + r0, hk) + c * 8;
       const __nv_bfloat16* qp = delta_row(a.q, sq, n0 + r0, hk) + c * 8;
-      const __nv_bfloat16* vp = delta_row(a.v, sq, n0 + vr0, h) + part * kCols + vc * 8;
       const __nv_bfloat16* dp = delta_row(gr.dout, sq, n0 + vr0, h) + part * kCols + vc * 8;
 #pragma unroll
       for (int i = 0; i < kChunk / kStep; ++i) {
@@ -400,9 +384,7 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
       for (int i = 0; i < kChunk / kVStep; ++i) {
         const int r = vr0 + i * kVStep;
         const bool real = r < len;
-        cp_async_16(dv + i * kVStep * Cfg::kVLd, real ? vp : a.v.p, real);
         cp_async_16(ddo + sw128(r, vc * 8), real ? dp : gr.dout.p, real);
-        vp += vstep;
         dp += dstep;
       }
       if (n > 0) {   // the chunk before into L2
@@ -414,7 +396,6 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
           prefetch_l2(k + 64);
           prefetch_l2(q + 64);
         }
-        prefetch_l2(delta_row(a.v, sq, r, h) + part * kCols);
         prefetch_l2(delta_row(gr.dout, sq, r, h) + part * kCols);
         if (t == 0) bulk_prefetch_l2(blocks + (n - 1) * block_step, kBlock);
       }
@@ -460,16 +441,11 @@ struct GradCfg {
   static constexpr uint32_t kMat = kChunk * kGradLd * 2;
   static constexpr uint32_t kOffTile = (kOffM + 4 * kMat + 127) / 128 * 128;
   static constexpr uint32_t kOffFac = kOffTile + kGradRing * kTile;   // the prepared block's factors
-  static constexpr uint32_t kOffSum = kOffFac + kFactorBytes;                // q . dq: [warps beside one another][64]
-  static constexpr uint32_t kSmemBytes = kOffSum + kCW * kChunk * 4 + 1024;
+  // sums of dg: by token for the warps beside one another (those of s >= t; b), N's columns for the 4 below
+  static constexpr uint32_t kOffSum = kOffFac + kFactorBytes;
+  static constexpr uint32_t kSmemBytes = kOffSum + (2 * kCW + 4) * kChunk * 4 + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory above the 227 KB per-block limit");
 };
-
-__device__ __forceinline__ float sum_warp(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
 
 template <int kD>
 __global__ void __launch_bounds__(GradCfg<kD>::kThreads, 1)
@@ -483,7 +459,8 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
   float* fac = reinterpret_cast<float*>(smem + Cfg::kOffFac);
   const float *rowf = fac + kFacRow, *colf = fac + kFacCol;
   const float2* rel = reinterpret_cast<const float2*>(fac + kFacRel);
-  float* qsum = reinterpret_cast<float*>(smem + Cfg::kOffSum);
+  float* rsum = reinterpret_cast<float*>(smem + Cfg::kOffSum);
+  float *bsum = rsum + kCW * kChunk, *csum = bsum + kCW * kChunk;
 
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g4 = lane >> 2, t2 = (lane & 3) * 2;
   const int rb = w / kCW, cw = w % kCW, l8 = lane & 7, k8 = ((lane >> 3) & 1) * 8;
@@ -521,7 +498,6 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
   for (int n = 0; n < kT; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i) dq[n][i] = dk[n][i] = 0.f;
-  float before = 0.f;   // tid < 64: q . dq of this token's value heads so far
 
 #pragma unroll 1
   for (int hv = 0; hv < group; ++hv) {
@@ -550,26 +526,21 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
     cp_async_commit();
     load_tile(1);
     cp_async_commit();
-    // this token's sums (tid < 64): w . W and y . v; W's values: all in flight at once
+    // this token's w . W (tid < 64); W's values: all in flight at once
     constexpr int kQ = kChunk * kD / 4 / kThreads;   // 4 columns of a row at a time
     float4 wv[kQ];
     const float4* wp = reinterpret_cast<const float4*>(saved.w + sh * kChunk * kD) + tid;
 #pragma unroll
     for (int i = 0; i < kQ; ++i) wv[i] = __ldg(wp + i * kThreads);
-    float wd = 0.f, vd = 0.f, end = 0.f;
+    float wd = 0.f, end = 0.f;
     if (tid < kChunk) {
-      const float* rw = gr.rows + sh * kParts * 4 * kChunk + tid;   // [part][which][half][token]
-      float x[kParts][4];
+      const float* rw = gr.rows + sh * kParts * 2 * kChunk + tid;   // [part][half][token]
+      float x[kParts * 2];
 #pragma unroll
-      for (int p = 0; p < kParts; ++p)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[p][i] = __ldcg(rw + (p * 4 + i) * kChunk);
+      for (int p = 0; p < kParts * 2; ++p) x[p] = __ldcg(rw + p * kChunk);
       if (lane < kParts * 8) end = __ldcg(gr.ends + sh * kParts * 8 + lane);
 #pragma unroll
-      for (int p = 0; p < kParts; ++p) {
-        wd += x[p][0] + x[p][1];
-        vd += x[p][2] + x[p][3];
-      }
+      for (int p = 0; p < kParts * 2; ++p) wd += x[p];
       end = sum_warp(end);
     }
     cp_async_wait<1>();   // do, y, the factors and the first tile (K and Q)
@@ -587,21 +558,38 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
     }
     __syncthreads();
 
-    // M1 = do U^T and M2 = y U^T: rows 16 rb .., of the 2 rb + 2 tiles of columns up to the diagonal block
+    // M1 = do U^T, M2 = y U^T, Q K^T and K K^T: rows 16 rb .., of the 2 rb + 2 tiles of columns up to the diagonal block
     // cw, cw + kCW, ..  (d: K dimension; tiles beyond are computed along and not kept)
     constexpr int kMT = 8 / kCW;
+    float sums[2];   // this thread's share of the tokens' sums, rows r0 and r0 + 8
     {
-      float m1[kMT][4], m2[kMT][4];
+      float m1[kMT][4], m2[kMT][4], qk[kMT][4], kk[kMT][4];
 #pragma unroll
       for (int n = 0; n < kMT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m1[n][i] = m2[n][i] = 0.f;
+        for (int i = 0; i < 4; ++i) m1[n][i] = m2[n][i] = qk[n][i] = kk[n][i] = 0.f;
       const uint32_t arow = (16 * rb + (lane & 15)) * (Cfg::kLd * 2) + (lane >> 4) * 16;
       // matrices by lane / 8: hi of 0..7 and 8..15 of the K dimension, lo
       const uint32_t brow = base + Cfg::kOffU + (lane >> 4) * Cfg::kRows + (8 * cw + l8) * (Cfg::kLd * 2) + k8 * 2;
+      // K's: two tiles of columns
+      const uint32_t krow = base + Cfg::kOffK + (8 * (cw + (lane >> 4) * kCW) + l8) * (Cfg::kLd * 2) + k8 * 2;
 #pragma unroll 1
       for (int ks = 0; ks < kD / 16; ++ks) {
         uint32_t ad[4], yh[4], yl[4];
+        {
+          uint32_t aq[4], ak[4];
+          ldmatrix_x4(aq, base + Cfg::kOffQ + arow + ks * 32);
+          ldmatrix_x4(ak, base + Cfg::kOffK + arow + ks * 32);
+#pragma unroll
+          for (int n = 0; n < kMT; n += 2) {
+            uint32_t b[4];
+            ldmatrix_x4(b, krow + n * 8 * kCW * (Cfg::kLd * 2) + ks * 32);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) mma_16816(qk[n + e], aq, b + 2 * e);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) mma_16816(kk[n + e], ak, b + 2 * e);
+          }
+        }
         ldmatrix_x4(ad, base + Cfg::kOffDo + arow + ks * 32);
         ldmatrix_x4(yh, base + Cfg::kOffY + arow + ks * 32);
         ldmatrix_x4(yl, base + Cfg::kOffY + Cfg::kRows + arow + ks * 32);
@@ -611,9 +599,11 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
         mma_halves<kMT>(m1, ad, b);
         mma_pairs<kMT>(m2, yh, yl, b);
       }
-      // by D; M1 by scale, M2 negated
+      // by D; M1 by scale, M2 negated; N's sums of the warp's rows and columns
+      float nrow[2] = {0.f, 0.f};
 #pragma unroll
-      for (int n = 0; n < kMT; ++n)
+      for (int n = 0; n < kMT; ++n) {
+        float ncol[2] = {0.f, 0.f};
         if (cw + kCW * n < 2 * rb + 2) {
           const int c = 8 * (cw + kCW * n) + t2;
           const bool diag = c >= 16 * rb;
@@ -631,14 +621,28 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
             }
             uint32_t hi, lo;
             uint8_t* dst = smem + Cfg::kOffM + (r * kGradLd + c) * 2;
-            split_bf16(c <= r ? a.scale * d[0] * m1[n][2 * q] : 0.f, c + 1 <= r ? a.scale * d[1] * m1[n][2 * q + 1] : 0.f, hi, lo);
+            const float p0 = c <= r ? a.scale * d[0] * m1[n][2 * q] : 0.f, p1 = c + 1 <= r ? a.scale * d[1] * m1[n][2 * q + 1] : 0.f;
+            const float l0 = c < r ? -d[0] * m2[n][2 * q] : 0.f, l1 = c + 1 < r ? -d[1] * m2[n][2 * q + 1] : 0.f;
+            const float n0 = c < r ? p0 * qk[n][2 * q] + l0 * kk[n][2 * q] : 0.f;
+            const float n1 = c + 1 < r ? p1 * qk[n][2 * q + 1] + l1 * kk[n][2 * q + 1] : 0.f;
+            nrow[q] += n0 + n1;
+            ncol[0] += n0, ncol[1] += n1;
+            split_bf16(p0, p1, hi, lo);
             *reinterpret_cast<uint32_t*>(dst) = hi;
             *reinterpret_cast<uint32_t*>(dst + Cfg::kMat) = lo;
-            split_bf16(c < r ? -d[0] * m2[n][2 * q] : 0.f, c + 1 < r ? -d[1] * m2[n][2 * q + 1] : 0.f, hi, lo);
+            split_bf16(l0, l1, hi, lo);
             *reinterpret_cast<uint32_t*>(dst + 2 * Cfg::kMat) = hi;
             *reinterpret_cast<uint32_t*>(dst + 3 * Cfg::kMat) = lo;
           }
         }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) ncol[e] += __shfl_xor_sync(0xffffffffu, ncol[e], o);
+          if (lane < 4) csum[rb * kChunk + 8 * (cw + kCW * n) + t2 + e] = ncol[e];
+        }
+      }
+      sums[0] = nrow[0], sums[1] = nrow[1];
     }
     __syncthreads();
 
@@ -701,6 +705,24 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
       const int row = (cw * kT + n) * 8 + l8, col = 16 * ks + k8 + (lane >> 4) * 32;
       ldmatrix_x4(b, base + Cfg::kOffTile + (p % kGradRing) * Cfg::kTile + sw128(row, col));
     };
+    // the warp's columns of rows r0 and r0 + 8 of x with those of K or Q; and such sums for all warps to add
+    auto with_rows = [&](uint32_t off, const float (*x)[4], float* d) {
+#pragma unroll
+      for (int n = 0; n < kT; ++n)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t v = *reinterpret_cast<const uint32_t*>(smem + off + ((r0 + 8 * q) * Cfg::kLd + (cw * kT + n) * 8 + t2) * 2);
+          d[q] += x[n][2 * q] * __uint_as_float(v << 16) + x[n][2 * q + 1] * __uint_as_float(v & 0xFFFF0000u);
+        }
+    };
+    auto put_rows = [&](float* dst, float* d) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        d[q] += __shfl_xor_sync(0xffffffffu, d[q], 1);
+        d[q] += __shfl_xor_sync(0xffffffffu, d[q], 2);
+        if ((lane & 3) == 0) dst[cw * kChunk + r0 + 8 * q] = d[q];
+      }
+    };
     {
       float x[kT][4], y[kT][4];
 #pragma unroll
@@ -737,9 +759,14 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float e = i < 2 ? e0 : e1;
-          dq[n][i] += a.scale * e * x[n][i];
-          dk[n][i] -= e * y[n][i];
+          x[n][i] *= a.scale * e;
+          y[n][i] *= -e;
+          dq[n][i] += x[n][i];
+          dk[n][i] += y[n][i];
         }
+      with_rows(Cfg::kOffQ, x, sums);
+      with_rows(Cfg::kOffK, y, sums);
+      put_rows(rsum, sums);
     }
     {
       float x[kT][4];
@@ -772,47 +799,40 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
       const float e0 = fac[kFacToEnd + r0], e1 = fac[kFacToEnd + r0 + 8];
 #pragma unroll
       for (int n = 0; n < kT; ++n)
-        for (int i = 0; i < 4; ++i) dk[n][i] += (i < 2 ? e0 : e1) * x[n][i];
-    }
-    // q . dq of the heads so far
-    {
-      float d[2] = {0.f, 0.f};
 #pragma unroll
-      for (int n = 0; n < kT; ++n)
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint32_t qv = *reinterpret_cast<const uint32_t*>(
-              smem + Cfg::kOffQ + ((r0 + 8 * q) * Cfg::kLd + (cw * kT + n) * 8 + t2) * 2);
-          d[q] += dq[n][2 * q] * __uint_as_float(qv << 16) + dq[n][2 * q + 1] * __uint_as_float(qv & 0xFFFF0000u);
+        for (int i = 0; i < 4; ++i) {
+          x[n][i] *= i < 2 ? e0 : e1;
+          dk[n][i] += x[n][i];
         }
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        d[q] += __shfl_xor_sync(0xffffffffu, d[q], 1);
-        d[q] += __shfl_xor_sync(0xffffffffu, d[q], 2);
-        if ((lane & 3) == 0) qsum[cw * kChunk + r0 + 8 * q] = d[q];
-      }
+      float b[2] = {0.f, 0.f};
+      with_rows(Cfg::kOffK, x, b);
+      put_rows(bsum, b);
     }
     __syncthreads();
     if (tid < kChunk) {
-      float now = 0.f;
+      // the sums over the tokens from this one on and over those before it: inside the warp, then the
+      // other warp's; N's columns beyond the rows of a block are zero
+      float x = 0.f, b = 0.f;
 #pragma unroll
-      for (int i = 0; i < kCW; ++i) now += qsum[i * kChunk + tid];
-      // the sum over the tokens from this one on: inside the warp, and the second warp's for the first
-      float x = tid < len ? (now - before) - vd : 0.f;
-      before = now;
+      for (int i = 0; i < kCW; ++i) x += rsum[i * kChunk + tid], b += bsum[i * kChunk + tid];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x -= csum[i * kChunk + tid];
+      const float own = b;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const float up = __shfl_down_sync(0xffffffffu, x, o);
+        const float up = __shfl_down_sync(0xffffffffu, x, o), down = __shfl_up_sync(0xffffffffu, b, o);
         if (lane + o < 32) x += up;
+        if (lane >= o) b += down;
       }
-      asm volatile("barrier.cta.sync 1, 64;" ::: "memory");   // (qsum has been read)
-      if (tid == 32) qsum[0] = x;
+      asm volatile("barrier.cta.sync 1, 64;" ::: "memory");   // (rsum and bsum have been read)
+      if (tid == 32) rsum[0] = x;
+      if (tid == 31) bsum[0] = b;
       asm volatile("barrier.cta.sync 1, 64;" ::: "memory");
-      if (tid < 32) x += qsum[0];
+      x += (b - own) + (tid < 32 ? rsum[0] : bsum[0]);
       if (tid < len) {
         const long long o = ((long long)sq.entry * a.ntok + sq.first + n0 + tid) * a.Hv + h;
         gr.dbeta[o] = wd;
-        gr.dg[o] = x + end;
+        gr.dg[o] = x + fac[kFacChunk] * end;
       }
     }
     __syncthreads();

@@ -419,7 +419,7 @@ struct DeltaBytes {
         kept(up(n * kPrepSaveBytes)),
         states(up(n * D * D * 4)),
         rows(up(n * kChunk * D * 4)),
-        shares(up(n * (D / 32) * 4 * kChunk * 4)),
+        shares(up(n * (D / 32) * 2 * kChunk * 4)),
         ends(up(n * (D / 32) * 8 * 4)) {}
   static size_t up(size_t x) { return (x + 255) / 256 * 256; }
   size_t saved() const { return kept + states + rows; }
@@ -531,9 +531,8 @@ litela_status delta_bwd(const lite_la_delta_args* a, const lite_la_delta_grads* 
     return s;
   if (a->N > 0 && (g->dg == nullptr || g->dbeta == nullptr)) return invalid("null dg or dbeta");
   if (!aligned(g->dg, 4) || !aligned(g->dbeta, 4)) return invalid("dg and dbeta must be 4-byte aligned");
-  if (!aligned(g->dstate_out, 16) || !aligned(g->dstate_in, 16) || !aligned(g->state_out, 16))
-    return invalid("states and their gradients must be 16-byte aligned");
-  if (g->dstate_out != nullptr && g->state_out == nullptr) return invalid("dstate_out needs the forward's state_out");
+  if (!aligned(g->dstate_out, 16) || !aligned(g->dstate_in, 16))
+    return invalid("the states' gradients must be 16-byte aligned");
   const DeltaBytes bytes(a->B, a->N, a->Hv, a->d, a->cu_seqlens != nullptr);
   const size_t states = (size_t)a->B * a->Hv * a->d * a->d * 4, gates = (size_t)entries * a->N * a->Hv * 4;
   if ((s = buffer_check(a, saved, saved_bytes, a->N > 0 ? bytes.saved() : 0, in, Span{}, "saved missing, too small or misaligned",
@@ -543,7 +542,7 @@ litela_status delta_bwd(const lite_la_delta_args* a, const lite_la_delta_grads* 
           LITELA_OK)
     return s;
   in.add(span(saved, a->N > 0 ? bytes.saved() : 0));
-  const Span dso = span(g->dstate_out, states), so = span(g->state_out, states);
+  const Span dso = span(g->dstate_out, states);
   // dq, dk, dv may be views of one buffer between one another's rows: only their spans against inputs
   // and the dense outputs are checked
   const Span outs[7] = {sp[0], sp[1], sp[2], span(g->dg, gates), span(g->dbeta, gates), span(g->dstate_in, states),
@@ -551,7 +550,7 @@ litela_status delta_bwd(const lite_la_delta_args* a, const lite_la_delta_grads* 
   for (int i = 0; i < 3; ++i)
     if (sp[i].hi > 0 && sp[i].lo == sp[(i + 1) % 3].lo) return invalid("dq, dk and dv must be different memory");
   for (int i = 0; i < 7; ++i) {
-    if (in.hit(outs[i]) || (i != 5 && meet(outs[i], dso)) || meet(outs[i], so)) return invalid("an output overlaps an input");
+    if (in.hit(outs[i]) || (i != 5 && meet(outs[i], dso))) return invalid("an output overlaps an input");
     for (int j = i + 1; j < 7; ++j)
       if (j > 2 && meet(outs[i], outs[j])) return invalid("outputs overlap");
   }
@@ -564,7 +563,7 @@ litela_status delta_bwd(const lite_la_delta_args* a, const lite_la_delta_grads* 
   DeltaGrads gr{};
   gr.dout = view_of(g->dout), gr.dq = view_of(g->dq), gr.dk = view_of(g->dk), gr.dv = view_of(g->dv);
   gr.dg = g->dg, gr.dbeta = g->dbeta;
-  gr.dstate_out = g->dstate_out, gr.state_out = g->state_out, gr.dstate_in = g->dstate_in;
+  gr.dstate_out = g->dstate_out, gr.dstate_in = g->dstate_in;
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
   gr.gstates = ws;
   gr.y = ws + bytes.states;

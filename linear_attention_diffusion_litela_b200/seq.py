@@ -17,7 +17,7 @@ from . import _check, _torch, lib
 # took longer than the kernel of a one-token call.  A view is (pointer, batch, token, head stride).
 _VIEW = "Pqqq"
 _DELTA_ARGS = struct.Struct("@" + 4 * _VIEW + "PPqqqqPPPiiiiifiPN")    # lite_la_delta_args
-_DELTA_GRADS = struct.Struct("@" + 4 * _VIEW + "PPPPP")                 # lite_la_delta_grads
+_DELTA_GRADS = struct.Struct("@" + 4 * _VIEW + "PPPP")                 # lite_la_delta_grads
 _NO_VIEW = (0, 0, 0, 0)
 
 
@@ -289,12 +289,11 @@ def lite_la_gated_delta_fwd_save(q, k, v, g, beta, state_in=None, state_out=None
     return _delta_forward(q, k, v, g, beta, state_in, state_out, cu_seqlens, scale, out, stream, True)
 
 
-def lite_la_gated_delta_bwd(q, k, v, g, beta, dout, saved, state_out=None, dstate_out=None, state_in=None,
-                            cu_seqlens=None, scale=None, stream=None):
+def lite_la_gated_delta_bwd(q, k, v, g, beta, dout, saved, dstate_out=None, state_in=None, cu_seqlens=None,
+                            scale=None, stream=None):
     """Gradients of sum(dout * out) + sum(dstate_out * state_out) for the forward that left `saved`
-    (lite_la_gated_delta_fwd_save with the same arguments) and wrote state_out (needed with
-    dstate_out): (dq, dk, dv bf16, dg,
-    dbeta fp32, dstate_in fp32 or None without state_in)."""
+    (lite_la_gated_delta_fwd_save with the same arguments): (dq, dk, dv bf16, dg, dbeta fp32,
+    dstate_in fp32 or None without state_in)."""
     torch = _torch()
     a = _Delta(q, k, v, g, beta, scale, cu_seqlens)
     do = _view(dout, "dout", a.vshape, a.dev)
@@ -305,10 +304,7 @@ def lite_la_gated_delta_bwd(q, k, v, g, beta, dout, saved, state_out=None, dstat
     si = dstate_in = None
     if state_in is not None:
         si, dstate_in = _states(state_in, "state_in", a.states, a.dev), new(a.states, torch.float32)
-    dso = so = 0
-    if dstate_out is not None:
-        dso = _states(dstate_out, "dstate_out", a.states, a.dev)
-        so = _states(state_out, "state_out", a.states, a.dev)
+    dso = 0 if dstate_out is None else _states(dstate_out, "dstate_out", a.states, a.dev)
     dq, dk, dv = (new(shape, torch.bfloat16) for shape in (a.qshape, a.qshape, a.vshape))
     dg, dbeta = (new(a.vshape[:3], torch.float32) for _ in range(2))
     size = a.bytes(lib().lite_la_gated_delta_bwd_workspace_bytes)
@@ -317,7 +313,7 @@ def lite_la_gated_delta_bwd(q, k, v, g, beta, dout, saved, state_out=None, dstat
         if t is not None:
             _on_stream(t, stream)
     grads = _DELTA_GRADS.pack(*do, *_view(dq, "dq", a.qshape, a.dev), *_view(dk, "dk", a.qshape, a.dev),
-                              *_view(dv, "dv", a.vshape, a.dev), dg.data_ptr(), dbeta.data_ptr(), dso, so,
+                              *_view(dv, "dv", a.vshape, a.dev), dg.data_ptr(), dbeta.data_ptr(), dso,
                               _ptr(dstate_in))
     _call(lib().lite_la_gated_delta_bwd, a.dev, stream, a.pack(_NO_VIEW, si or 0, 0, 0, ws.data_ptr(), size), grads,
           saved.data_ptr(), saved.numel())
@@ -335,14 +331,14 @@ def _delta_function():
                 ctx.set_materialize_grads(False)
                 out, state_out, saved = lite_la_gated_delta_fwd_save(q, k, v, g, beta, state_in=state_in,
                                                                      cu_seqlens=cu_seqlens, scale=scale)
-                ctx.save_for_backward(q, k, v, g, beta, state_in, cu_seqlens, state_out, saved)
+                ctx.save_for_backward(q, k, v, g, beta, state_in, cu_seqlens, saved)
                 ctx.scale = scale
                 return out, state_out
 
             @staticmethod
             @once_differentiable
             def backward(ctx, dout, dstate):
-                q, k, v, g, beta, state_in, cu_seqlens, state_out, saved = ctx.saved_tensors
+                q, k, v, g, beta, state_in, cu_seqlens, saved = ctx.saved_tensors
                 if dout is None:
                     dout = torch.zeros_like(v, memory_format=torch.contiguous_format)
                 dout = dout.to(torch.bfloat16)
@@ -350,8 +346,8 @@ def _delta_function():
                     dout = dout.contiguous()
                 if dstate is not None:
                     dstate = dstate.float().contiguous()
-                grads = lite_la_gated_delta_bwd(q, k, v, g, beta, dout, saved, state_out=state_out, dstate_out=dstate,
-                                                state_in=state_in, cu_seqlens=cu_seqlens, scale=ctx.scale)
+                grads = lite_la_gated_delta_bwd(q, k, v, g, beta, dout, saved, dstate_out=dstate, state_in=state_in,
+                                                cu_seqlens=cu_seqlens, scale=ctx.scale)
                 return (*grads, None, None)
 
         _FUNCTIONS["delta"] = GatedDelta

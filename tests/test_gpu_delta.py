@@ -455,14 +455,14 @@ def test_gradient_streams_graphs_and_equal_bits():
     assert all(torch.equal(got[n], want[n]) for n in want)
     args = [t[n] for n in ("q", "k", "v", "g", "beta")]
     out, state, saved = ll.lite_la_gated_delta_fwd_save(*args, state_in=t["state_in"], cu_seqlens=t["cu"], stream=s)
-    got = ll.lite_la_gated_delta_bwd(*args, t["dout"], saved, state_out=state, dstate_out=t["dstate"],
+    got = ll.lite_la_gated_delta_bwd(*args, t["dout"], saved, dstate_out=t["dstate"],
                                      state_in=t["state_in"], cu_seqlens=t["cu"], stream=s)
     torch.cuda.current_stream().wait_stream(s)
     assert all(torch.equal(a, want[n]) for a, n in zip(got, ("q", "k", "v", "g", "beta", "state_in")))
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         out, state, saved = ll.lite_la_gated_delta_fwd_save(*args, state_in=t["state_in"], cu_seqlens=t["cu"])
-        got = ll.lite_la_gated_delta_bwd(*args, t["dout"], saved, state_out=state, dstate_out=t["dstate"],
+        got = ll.lite_la_gated_delta_bwd(*args, t["dout"], saved, dstate_out=t["dstate"],
                                          state_in=t["state_in"], cu_seqlens=t["cu"])
     for _ in range(2):
         for x in got:

@@ -100,7 +100,7 @@ DELTA = dict(q=(1 * MB, 0, 256, 64), k=(2 * MB, 0, 256, 64), v=(3 * MB, 0, 512, 
              scale=0.125, zero_tail=0, ws=16 * MB, ws_bytes=16 * MB)
 SAVED = 64 * MB
 GRADS = dict(dout=(9 * MB, 0, 512, 64), dq=(10 * MB, 0, 256, 64), dk=(11 * MB, 0, 256, 64), dv=(12 * MB, 0, 512, 64),
-             dg=13 * MB, dbeta=13 * MB + 65536, dso=14 * MB, so=8 * MB, dsi=15 * MB)
+             dg=13 * MB, dbeta=13 * MB + 65536, dso=14 * MB, dsi=15 * MB)
 
 
 def delta(**change):
@@ -111,7 +111,7 @@ def delta(**change):
 def grads(**change):
     a = dict(GRADS, **change)
     return seq._DELTA_GRADS.pack(*(x for n in ("dout", "dq", "dk", "dv") for x in a[n]),
-                                 *(a[n] for n in ("dg", "dbeta", "dso", "so", "dsi")))
+                                 *(a[n] for n in ("dg", "dbeta", "dso", "dsi")))
 
 
 def test_struct_layouts(tmp_path):
@@ -122,7 +122,7 @@ def test_struct_layouts(tmp_path):
         pytest.skip("no C++ compiler or CUDA headers")
     fields = {"lite_la_delta_args": [(8 * 4 * 4, "g"), (128 + 16, "g_batch_stride"), (176, "state_in"), (192, "cu_seqlens"),
                                      (200, "B"), (220, "scale"), (224, "zero_tail"), (232, "workspace")],
-              "lite_la_delta_grads": [(0, "dout"), (32, "dq"), (128, "dg"), (144, "dstate_out"), (160, "dstate_in")]}
+              "lite_la_delta_grads": [(0, "dout"), (32, "dq"), (128, "dg"), (144, "dstate_out"), (152, "dstate_in")]}
     size = {"lite_la_delta_args": seq._DELTA_ARGS.size, "lite_la_delta_grads": seq._DELTA_GRADS.size}
     text = '#include <cstddef>\n#include "litela.h"\n'
     for name, fs in fields.items():
@@ -205,13 +205,12 @@ def test_delta_saved_refusals(lib, words, saved, size):
     ("output view overlaps itself", dict(dk=(11 * MB, 0, 64, 64)), {}), ("multiples of 8", dict(dv=(12 * MB, 0, 516, 64)), {}),
     ("null dg or dbeta", dict(dg=0), {}), ("null dg or dbeta", dict(dbeta=0), {}),
     ("dg and dbeta must be 4-byte", dict(dg=13 * MB + 2), {}),
-    ("states and their gradients", dict(dso=14 * MB + 4), {}), ("states and their gradients", dict(dsi=15 * MB + 4), {}),
-    ("dstate_out needs", dict(so=0), {}),
+    ("the states' gradients must be", dict(dso=14 * MB + 4), {}), ("the states' gradients must be", dict(dsi=15 * MB + 4), {}),
     ("workspace missing", {}, dict(ws=0)), ("workspace missing", {}, dict(ws_bytes=100)),
     ("workspace overlaps", {}, dict(ws=2 * MB)),
     ("different memory", dict(dq=(11 * MB, 0, 256, 64)), {}), ("different memory", dict(dv=(10 * MB, 0, 512, 64)), {}),
     ("output overlaps an input", dict(dq=(9 * MB, 0, 256, 64)), {}), ("output overlaps an input", dict(dv=(3 * MB, 0, 512, 64)), {}),
-    ("output overlaps an input", dict(dg=14 * MB), {}), ("output overlaps an input", dict(dsi=8 * MB), {}),
+    ("output overlaps an input", dict(dg=14 * MB), {}), ("output overlaps an input", dict(dsi=3 * MB), {}),
     ("output overlaps an input", dict(dk=(64 * MB, 0, 256, 64)), {}),
     ("outputs overlap", dict(dg=12 * MB), {}), ("outputs overlap", dict(dbeta=13 * MB), {}),
     ("outputs overlap", {}, dict(ws=10 * MB)), ("dstate_in overlaps dstate_out in part", dict(dsi=14 * MB + 16), {}),
