@@ -11,10 +11,10 @@
 // and, as the decay of token t is a factor of everything that goes from before t to t or later,
 //     dg_t = e^G_C <S0, G'> + sum over i >= t of c_i + sum over j < t of b_j + sum over j < t <= i of N_ij,
 //     N = (M1 . D) . Q K^T - (M2 . D) . K K^T,  c = the products of q and k with their terms of S0,
-//                                               b = that of k with its term of G'.
+//                                               b = Z U, that of k with its term of G' (Z in litela_delta_back).
 // The last sum is one over s >= t of N's row s less its column s.  (<S_C, G'> and the sums of
 // q . dq - y . v are the same in exact arithmetic, but cancel where decays are strong, with the errors of
-// bf16 pairs: 1.8e-5 of dg against 64 bits where this form has 1e-6.)
+// bf16 pairs: dg 1.8e-5 off against 64 bits for 3 x 208 tokens, 4 heads of 32, where this form is 2e-6 off.)
 //
 // litela_delta_back walks a sequence's chunks from the last to the first (as litela_delta_chain, with
 // the same three products a chunk) and leaves y and each chunk's G'; litela_delta_grads makes the rest,
@@ -37,7 +37,7 @@ struct DeltaGrads {
   // between the two kernels, per chunk slot and value head
   uint8_t* gstates;                // G' as DeltaSaved's states
   uint8_t* y;                      // [d / 32] tiles of 64 rows of 128 bytes, 128-byte swizzle: bf16 pair
-  float* rows;                     // [d / 32][2][64]: w . W of half of 32 columns
+  float* rows;                     // [d / 32][2][2][64]: w . W and b of half of 32 columns
   float* ends;                     // [d / 32][8]: shares of <S0, G'>
 };
 
@@ -59,6 +59,9 @@ __device__ __forceinline__ float sum_warp(float v) {
 template <int kD>
 struct BackCfg {
   static constexpr int kBlocks = kD > 64 ? 2 : 1;
+  // of G' in the first product: a third costs the walk 7 % and halves the errors of dbeta and dg of a few
+  // tokens (d = 64: 2.6e-6 -> 1.4e-6, 6e-6 -> 1.6e-6); for d = 128 its tile has no room
+  static constexpr int kTerms = kD > 64 ? 2 : 3;
   static constexpr uint32_t kKQ = kBlocks * 16384;                // per block: 64 rows of K and of Q
   // the factors and the second image behind them, the image on a 1024-byte boundary
   static constexpr uint32_t kOffImage = kKQ + (kFactorBytes + 1023) / 1024 * 1024;
@@ -68,10 +71,10 @@ struct BackCfg {
   static constexpr uint32_t kStage = (kOffZ + 2 * kZTile + 1023) / 1024 * 1024;
   static constexpr uint32_t kSTile = kD * 128, kRTile = 128 * 128;
   static constexpr uint32_t kOffS = kChainStages * kStage;
-  static constexpr uint32_t kOffR = kOffS + kSTile;               // y's and do's rows, three terms
+  static constexpr uint32_t kOffR = kOffS + (kTerms + 1) / 2 * kSTile;             // y's and do's rows, three terms
   static constexpr uint32_t kOffBars = kOffR + 2 * kRTile;
   static constexpr uint32_t kSmemBytes = kOffBars + 256 + 1024;
-  static constexpr uint32_t kX1 = 0, kX2 = 64, kX3 = 192, kTmem = 512;
+  static constexpr uint32_t kX1 = 0, kX2 = 96, kX3 = 224, kTmem = 512;
   static_assert(kSmemBytes <= 232448, "shared memory above the 227 KB per-block limit");
 };
 enum : int { kBarY = 4 };   // named barrier of the accumulator warps: y is in shared memory
@@ -154,13 +157,19 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
         S[i / 2] = f2(x.x, x.y), S[i / 2 + 1] = f2(x.z, x.w);
       }
     if (nchunk > 0) {
-      if (has_state) chain_put<2>(stile, Cfg::kSTile, row, c0, S);
+      if (has_state) chain_put<Cfg::kTerms>(stile, Cfg::kSTile, row, c0, S);
       hand(kBarS);
     }
     for (int it = 0; it < nchunk; ++it) {
       const int n = nchunk - 1 - it, st = it % kChainStages;
       uint8_t* stage = smem + st * Cfg::kStage;
       const long long sh = (slot0 + n) * a.Hv + h;
+      uint4 third[kN / 8];   // S0's third term, this thread's part of the row
+      if (has_state) {
+        const uint8_t* src = saved.states + ((sh * kParts + part) * 2 + 1) * (long long)Cfg::kSTile;
+#pragma unroll
+        for (int i = 0; i < kN / 8; ++i) third[i] = __ldg(reinterpret_cast<const uint4*>(src + sw128(row, c0 + 8 * i)));
+      }
       wait(&full[st], it / kChainStages, 0);
       const float* fac = reinterpret_cast<const float*>(stage + Cfg::kOffFac);
       float decay[2], to_end[2], beta[2];
@@ -179,7 +188,7 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
       }
       F2 x[kN / 2], y[kN / 4], z[kN / 4];
       wait(&done[0], it, 1);
-      chain_frag<2>(ta + Cfg::kX1, c0, z);
+      chain_frag<Cfg::kTerms>(ta + Cfg::kX1, c0, z);
 #pragma unroll
       for (int i = 0; i < kN / 4; ++i) {
         const float f = to_end[i & 1], mb = -beta[i & 1];
@@ -187,15 +196,17 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
         x[i] = f2_mul(f2(mb, mb), z[i]);
       }
       chain_put_frag<3, 1>(stage + Cfg::kOffZ, Cfg::kZTile, tok, fc, x);
-      hand(kBarR);
+      hand(kBarR);   // (x, which is -beta Z, goes into the rows' shares too)
       // while the second product runs: do's rows of the third, W
       const float* wp = saved.w + (sh * kChunk + tok) * kD + part * kCols + fc;
       float2 wv[kN / 4];
 #pragma unroll
       for (int i = 0; i < kN / 4; ++i)
         wv[i] = __ldg(reinterpret_cast<const float2*>(wp + (i & 1) * 8 * kD + (i >> 1) * 8));
+      F2 bdot[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
       for (int i = 0; i < kN / 4; ++i) {
+        bdot[i & 1] = f2_fma(x[i], f2(wv[i].x, wv[i].y), bdot[i & 1]);
         const float f = a.scale * decay[i & 1];   // scale e^G do
         x[i] = f2_mul(f2(f, f), f2_bf16(dov[i]));
       }
@@ -235,8 +246,10 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
           const uint4 hi = *reinterpret_cast<const uint4*>(stile + sw128(row, c0 + 8 * i));
           const uint4 lo = *reinterpret_cast<const uint4*>(stile + sw128(row, 32 + c0 + 8 * i));
           const uint32_t h4[4] = {hi.x, hi.y, hi.z, hi.w}, l4[4] = {lo.x, lo.y, lo.z, lo.w};
+          const uint32_t t4[4] = {third[i].x, third[i].y, third[i].z, third[i].w};
 #pragma unroll
-          for (int q = 0; q < 4; ++q) sdot = f2_fma(S[4 * i + q], f2_add(f2_bf16(h4[q]), f2_bf16(l4[q])), sdot);
+          for (int q = 0; q < 4; ++q)
+            sdot = f2_fma(S[4 * i + q], f2_add(f2_bf16(h4[q]), f2_add(f2_bf16(l4[q]), f2_bf16(t4[q]))), sdot);
         }
       wait(&done[2], it, 3);
       if (has_state) {
@@ -244,7 +257,7 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
         const F2 d2 = f2(chunk_decay, chunk_decay);
 #pragma unroll
         for (int i = 0; i < kN / 2; ++i) S[i] = f2_fma(d2, S[i], x[i]);
-        if (n > 0) chain_put<2>(stile, Cfg::kSTile, row, c0, S);
+        if (n > 0) chain_put<Cfg::kTerms>(stile, Cfg::kSTile, row, c0, S);
       }
       if (n > 0) hand(kBarS);
       // while the next chunk's first product runs: the rows' shares
@@ -254,10 +267,17 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float2 w2 = f2_out(wdot[i]);
-        float wd = w2.x + w2.y;
+        const float2 b2 = f2_out(bdot[i]);
+        float wd = w2.x + w2.y, bd = -(b2.x + b2.y);
         wd += __shfl_xor_sync(0xffffffffu, wd, 1);
+        bd += __shfl_xor_sync(0xffffffffu, bd, 1);
         wd += __shfl_xor_sync(0xffffffffu, wd, 2);
-        if ((lane & 3) == 0) gr.rows[((sh * kParts + part) * 2 + (warp >> 2)) * kChunk + tok + 8 * i] = wd;
+        bd += __shfl_xor_sync(0xffffffffu, bd, 2);
+        float* rw = gr.rows + ((sh * kParts + part) * 4 + (warp >> 2)) * kChunk + tok + 8 * i;
+        if ((lane & 3) == 0) {
+          rw[0] = wd;
+          rw[2 * kChunk] = bd;
+        }
       }
       {   // this warp's share of <S0, G'>
         const float2 dd = f2_out(sdot);
@@ -276,10 +296,10 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
         *reinterpret_cast<float4*>(gr.dstate_in + sbase + i) =
             make_float4(f2_out(S[i / 2]).x, f2_out(S[i / 2]).y, f2_out(S[i / 2 + 1]).x, f2_out(S[i / 2 + 1]).y);
   } else if (warp == kIssueWarp) {
-    constexpr uint32_t idesc_1 = idesc_bf16_f32(128, 64, false, true);    // [K; Q] G'
+    constexpr uint32_t idesc_1 = idesc_bf16_f32(128, 32 * Cfg::kTerms, false, true);    // [K; Q] G'
     constexpr uint32_t idesc_z = idesc_bf16_f32(128, 128, true, true);    // [X; P T]^T [do, three terms of Z]
     constexpr uint32_t idesc_3 = idesc_bf16_f32(128, 96, true, true);     // the lo terms' two of Z; [K; Q]^T ..
-    const Desc sdesc = desc_halves(smem_u32(stile), 1024, 1024, kSwizzle128B);
+    const Desc sdesc = desc_halves(smem_u32(stile), Cfg::kSTile, 1024, kSwizzle128B);
     const Desc rdesc = desc_halves(smem_u32(rtile), Cfg::kRTile, 1024, kSwizzle128B);
     const Desc kqdesc = desc_halves(smem_u32(smem), 16, 1024, kSwizzle128B);
     const Desc imgdesc = desc_halves(smem_u32(smem) + Cfg::kOffImage, kImgBlock, 1024, kSwizzle128B);
@@ -324,7 +344,7 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
         bulk_wait_group_read<0>();
         if (it > 0) mbar_drain(s0full, (it - 1) & 1);   // (long done, unless the walk was given up)
         mbar_arrive_expect_tx(s0full, Cfg::kSTile);
-        bulk_load(stile, saved.states + (((slot0 + n) * a.Hv + h) * kParts + part) * (long long)Cfg::kSTile, Cfg::kSTile,
+        bulk_load(stile, saved.states + (((slot0 + n) * a.Hv + h) * kParts + part) * (2LL * Cfg::kSTile), Cfg::kSTile,
                   s0full);
       }
       __syncwarp();
@@ -398,6 +418,8 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
         }
         prefetch_l2(delta_row(gr.dout, sq, r, h) + part * kCols);
         if (t == 0) bulk_prefetch_l2(blocks + (n - 1) * block_step, kBlock);
+        if (t == 32)
+          bulk_prefetch_l2(saved.states + (((slot0 + n - 1) * a.Hv + h) * kParts + part) * (2LL * Cfg::kSTile), 2 * Cfg::kSTile);
       }
       cp_async_commit();
       cp_async_wait<0>();
@@ -441,9 +463,9 @@ struct GradCfg {
   static constexpr uint32_t kMat = kChunk * kGradLd * 2;
   static constexpr uint32_t kOffTile = (kOffM + 4 * kMat + 127) / 128 * 128;
   static constexpr uint32_t kOffFac = kOffTile + kGradRing * kTile;   // the prepared block's factors
-  // sums of dg: by token for the warps beside one another (those of s >= t; b), N's columns for the 4 below
+  // sums of dg: by token for the warps beside one another, N's columns for the 4 below
   static constexpr uint32_t kOffSum = kOffFac + kFactorBytes;
-  static constexpr uint32_t kSmemBytes = kOffSum + (2 * kCW + 4) * kChunk * 4 + 1024;
+  static constexpr uint32_t kSmemBytes = kOffSum + (kCW + 4) * kChunk * 4 + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory above the 227 KB per-block limit");
 };
 
@@ -460,7 +482,7 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
   const float *rowf = fac + kFacRow, *colf = fac + kFacCol;
   const float2* rel = reinterpret_cast<const float2*>(fac + kFacRel);
   float* rsum = reinterpret_cast<float*>(smem + Cfg::kOffSum);
-  float *bsum = rsum + kCW * kChunk, *csum = bsum + kCW * kChunk;
+  float* csum = rsum + kCW * kChunk;
 
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g4 = lane >> 2, t2 = (lane & 3) * 2;
   const int rb = w / kCW, cw = w % kCW, l8 = lane & 7, k8 = ((lane >> 3) & 1) * 8;
@@ -505,7 +527,7 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
     const long long sh = (long long)slot * a.Hv + h;
     // tile p of the states (p < kParts), then of the gradients
     auto load_tile = [&](int p) {
-      const uint8_t* src = (p < kParts ? saved.states + (sh * kParts + p) * (long long)Cfg::kTile
+      const uint8_t* src = (p < kParts ? saved.states + (sh * kParts + p) * (2LL * Cfg::kTile)   // two of its terms
                                        : gr.gstates + (sh * kParts + p - kParts) * (long long)Cfg::kTile);
       const uint32_t dst = base + Cfg::kOffTile + (p % kGradRing) * Cfg::kTile;
 #pragma unroll 1
@@ -526,21 +548,26 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
     cp_async_commit();
     load_tile(1);
     cp_async_commit();
-    // this token's w . W (tid < 64); W's values: all in flight at once
+    // this token's w . W and b (tid < 64); W's values: all in flight at once
     constexpr int kQ = kChunk * kD / 4 / kThreads;   // 4 columns of a row at a time
     float4 wv[kQ];
     const float4* wp = reinterpret_cast<const float4*>(saved.w + sh * kChunk * kD) + tid;
 #pragma unroll
     for (int i = 0; i < kQ; ++i) wv[i] = __ldg(wp + i * kThreads);
-    float wd = 0.f, end = 0.f;
+    float wd = 0.f, bd = 0.f, end = 0.f;
     if (tid < kChunk) {
-      const float* rw = gr.rows + sh * kParts * 2 * kChunk + tid;   // [part][half][token]
-      float x[kParts * 2];
+      const float* rw = gr.rows + sh * kParts * 4 * kChunk + tid;   // [part][which][half][token]
+      float x[kParts][4];
 #pragma unroll
-      for (int p = 0; p < kParts * 2; ++p) x[p] = __ldcg(rw + p * kChunk);
+      for (int p = 0; p < kParts; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[p][i] = __ldcg(rw + (p * 4 + i) * kChunk);
       if (lane < kParts * 8) end = __ldcg(gr.ends + sh * kParts * 8 + lane);
 #pragma unroll
-      for (int p = 0; p < kParts * 2; ++p) wd += x[p];
+      for (int p = 0; p < kParts; ++p) {
+        wd += x[p][0] + x[p][1];
+        bd += x[p][2] + x[p][3];
+      }
       end = sum_warp(end);
     }
     cp_async_wait<1>();   // do, y, the factors and the first tile (K and Q)
@@ -800,35 +827,28 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
 #pragma unroll
       for (int n = 0; n < kT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[n][i] *= i < 2 ? e0 : e1;
-          dk[n][i] += x[n][i];
-        }
-      float b[2] = {0.f, 0.f};
-      with_rows(Cfg::kOffK, x, b);
-      put_rows(bsum, b);
+        for (int i = 0; i < 4; ++i) dk[n][i] += (i < 2 ? e0 : e1) * x[n][i];
     }
     __syncthreads();
     if (tid < kChunk) {
       // the sums over the tokens from this one on and over those before it: inside the warp, then the
       // other warp's; N's columns beyond the rows of a block are zero
-      float x = 0.f, b = 0.f;
+      float x = 0.f, b = bd;
 #pragma unroll
-      for (int i = 0; i < kCW; ++i) x += rsum[i * kChunk + tid], b += bsum[i * kChunk + tid];
+      for (int i = 0; i < kCW; ++i) x += rsum[i * kChunk + tid];
 #pragma unroll
       for (int i = 0; i < 4; ++i) x -= csum[i * kChunk + tid];
-      const float own = b;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const float up = __shfl_down_sync(0xffffffffu, x, o), down = __shfl_up_sync(0xffffffffu, b, o);
         if (lane + o < 32) x += up;
         if (lane >= o) b += down;
       }
-      asm volatile("barrier.cta.sync 1, 64;" ::: "memory");   // (rsum and bsum have been read)
+      asm volatile("barrier.cta.sync 1, 64;" ::: "memory");   // (rsum has been read)
       if (tid == 32) rsum[0] = x;
-      if (tid == 31) bsum[0] = b;
+      if (tid == 31) rsum[1] = b;
       asm volatile("barrier.cta.sync 1, 64;" ::: "memory");
-      x += (b - own) + (tid < 32 ? rsum[0] : bsum[0]);
+      x += (b - bd) + (tid < 32 ? rsum[0] : rsum[1]);
       if (tid < len) {
         const long long o = ((long long)sq.entry * a.ntok + sq.first + n0 + tid) * a.Hv + h;
         gr.dbeta[o] = wd;

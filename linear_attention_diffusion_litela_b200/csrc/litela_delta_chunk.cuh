@@ -616,7 +616,7 @@ constexpr int kIssueWarp = kAccWarps + 2;   // on a scheduler whose accumulator 
 constexpr int kLoadWarps = 2;
 constexpr int kChainThreads = (kAccWarps + 1 + kLoadWarps) * 32;   // 11 warps: up to 168 registers a thread
 constexpr int kLoadThreads = kLoadWarps * 32;
-constexpr uint32_t kChainTmem = 256;
+constexpr uint32_t kChainTmem = 512;
 enum : int { kErrChainLoad = 0x510, kErrChainMma = 0x520, kErrChainAcc = 0x530 };
 // named barriers: S0, R and U are in shared memory (accumulator warps arrive, the issuer waits)
 enum : int { kBarS = 1, kBarR = 2, kBarU = 3 };
@@ -644,12 +644,12 @@ struct ChainCfg {
   static constexpr uint32_t kOffPrep = kKQ;
   static constexpr uint32_t kOffV = kKQ + kPrepBytes;
   static constexpr uint32_t kStage = (kOffV + kV + 1023) / 1024 * 1024;
-  static constexpr uint32_t kSTile = kD * 128;                    // S0 (two terms)
+  static constexpr uint32_t kSTile = kD * 128;                    // S0 (three terms, two tiles)
   static constexpr uint32_t kRTile = 64 * 128;                    // R and U (three terms, two tiles)
   static constexpr uint32_t kOffS = kChainStages * kStage;
-  static constexpr uint32_t kOffR = kOffS + kSTile;
+  static constexpr uint32_t kOffR = kOffS + 2 * kSTile;
   static constexpr uint32_t kOffBars = kOffR + 2 * kRTile;
-  static constexpr uint32_t kX1 = 0, kX2 = 64, kX3 = 160;         // TMEM columns of the three products
+  static constexpr uint32_t kX1 = 0, kX2 = 96, kX3 = 192;         // TMEM columns of the three products
   static constexpr uint32_t kSmemBytes = kOffBars + 256 + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory above the 227 KB per-block limit");
   static_assert(kLoadThreads == kChunk, "a loading thread prefetches one row");
@@ -733,7 +733,7 @@ __device__ __forceinline__ void chain_put_frag(uint8_t* tile, uint32_t tile_byte
 }
 
 // What a training step's forward leaves for its backward, per chunk slot and value head: S0 as the B
-// operand tiles of the chain (d rows x 128 bytes for each 32 columns, two terms), and
+// operand tiles of the chain (for each 32 columns twice d rows x 128 bytes: two terms, the third), and
 // W in fp32 [64, d].
 struct DeltaSaved {
   uint8_t* states;
@@ -837,7 +837,7 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, const De
       if (lane == 0) mbar_arrive(&empty[st]);
     };
     if (nchunk > 0) {
-      if (has_state) chain_put<2>(stile, Cfg::kSTile, row, c0, S);
+      if (has_state) chain_put<3>(stile, Cfg::kSTile, row, c0, S);
       hand(kBarS, kBarThreads);
     }
     for (int n = 0; n < nchunk; ++n) {
@@ -845,7 +845,7 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, const De
       F2 e[kN / 4], x[kN / 2], y[kN / 4];
       wait(&done[0], n, 2);
       // E = v - e^G K S0, R = beta E
-      chain_frag<2>(ta + Cfg::kX1, c0, e);
+      chain_frag<3>(ta + Cfg::kX1, c0, e);
       F2 zero = f2(0.f, 0.f);   // stays 0 while all are finite
 #pragma unroll
       for (int i = 0; i < kN / 4; ++i) {
@@ -865,7 +865,7 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, const De
       }
       chain_put_frag<3>(rtile, Cfg::kRTile, tok, fc, x);
       hand(kBarR, kBarThreads);
-      chain_frag<2>(tq + Cfg::kX1, c0, y);   // the output's share of S0
+      chain_frag<3>(tq + Cfg::kX1, c0, y);   // the output's share of S0
 #pragma unroll
       for (int i = 0; i < kN / 4; ++i) {
         const float d = a.scale * decay[i & 1];
@@ -907,7 +907,7 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, const De
         const F2 d2 = f2(chunk_decay, chunk_decay);
 #pragma unroll
         for (int i = 0; i < kN / 2; ++i) S[i] = f2_fma(d2, S[i], x[i]);
-        if (n + 1 < nchunk) chain_put<2>(stile, Cfg::kSTile, row, c0, S);
+        if (n + 1 < nchunk) chain_put<3>(stile, Cfg::kSTile, row, c0, S);
       }
       if (n + 1 < nchunk) hand(kBarS, kBarThreads);
     }
@@ -917,11 +917,11 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, const De
         *reinterpret_cast<float4*>(a.state_out + sbase + i) =
             make_float4(f2_out(S[i / 2]).x, f2_out(S[i / 2]).y, f2_out(S[i / 2 + 1]).x, f2_out(S[i / 2 + 1]).y);
   } else if (warp == kIssueWarp) {
-    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 64, false, true);
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 96, false, true);
     constexpr uint32_t idesc_r = idesc_bf16_f32(128, 96, true, true);    // three terms
     constexpr uint32_t idesc_2 = idesc_bf16_f32(128, 64, true, true);    // two terms
     // descriptors of each operand's first 16 of the K dimension
-    const Desc sdesc = desc_halves(smem_u32(stile), 1024, 1024, kSwizzle128B);
+    const Desc sdesc = desc_halves(smem_u32(stile), Cfg::kSTile, 1024, kSwizzle128B);
     const Desc rdesc = desc_halves(smem_u32(rtile), Cfg::kRTile, 1024, kSwizzle128B);
     const Desc kqdesc = desc_halves(smem_u32(smem), 16, 1024, kSwizzle128B);
     const Desc imgdesc = desc_halves(smem_u32(smem) + Cfg::kOffPrep, kImgBlock, 1024, kSwizzle128B);
@@ -941,7 +941,7 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, const De
       tc_fence_after_sync();
       if (lane == 0) {
         if (kSave) {
-          bulk_store(saved.states + (((slot0 + n) * a.Hv + h) * kParts + part) * (long long)Cfg::kSTile, stile, Cfg::kSTile);
+          bulk_store(saved.states + (((slot0 + n) * a.Hv + h) * kParts + part) * (2LL * Cfg::kSTile), stile, 2 * Cfg::kSTile);
           bulk_commit_group();
         }
         if (ok) {

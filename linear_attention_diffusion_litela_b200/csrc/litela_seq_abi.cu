@@ -411,19 +411,20 @@ cudaError_t launch_chunks(const DeltaArgs& d, uint8_t* prep, int* err, cudaStrea
 // bytes of a call's buffers per chunk slot and value head, and their places
 struct DeltaBytes {
   size_t n;   // slots x value heads
-  size_t prep, kept, states, rows, shares, ends;
+  size_t prep, kept, states, gstates, rows, shares, ends;
   explicit DeltaBytes(const DeltaArgs& d, int D) : DeltaBytes(d.nseq, d.ntok, d.Hv, D, d.cu != nullptr) {}
   DeltaBytes(int B, int N, int Hv, int D, bool packed)
       : n((size_t)delta_slots(B, N, packed) * Hv),
         prep(up(n * kPrepBytes)),
         kept(up(n * kPrepSaveBytes)),
-        states(up(n * D * D * 4)),
+        states(up(n * D * D * 8)),
+        gstates(up(n * D * D * 4)),
         rows(up(n * kChunk * D * 4)),
-        shares(up(n * (D / 32) * 2 * kChunk * 4)),
+        shares(up(n * (D / 32) * 4 * kChunk * 4)),
         ends(up(n * (D / 32) * 8 * 4)) {}
   static size_t up(size_t x) { return (x + 255) / 256 * 256; }
   size_t saved() const { return kept + states + rows; }
-  size_t back() const { return states + rows + shares + ends; }
+  size_t back() const { return gstates + rows + shares + ends; }
 };
 
 bool delta_sizes_ok(int B, int N, int Hk, int Hv, int d) {
@@ -566,9 +567,9 @@ litela_status delta_bwd(const lite_la_delta_args* a, const lite_la_delta_grads* 
   gr.dstate_out = g->dstate_out, gr.dstate_in = g->dstate_in;
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
   gr.gstates = ws;
-  gr.y = ws + bytes.states;
-  gr.rows = reinterpret_cast<float*>(ws + bytes.states + bytes.rows);
-  gr.ends = reinterpret_cast<float*>(ws + bytes.states + bytes.rows + bytes.shares);
+  gr.y = ws + bytes.gstates;
+  gr.rows = reinterpret_cast<float*>(ws + bytes.gstates + bytes.rows);
+  gr.ends = reinterpret_cast<float*>(ws + bytes.gstates + bytes.rows + bytes.shares);
   int* err = delta_error_word(dev);
   const cudaError_t e = a->d == 32   ? launch_back<32>(d, gr, saved, err, st)
                         : a->d == 64 ? launch_back<64>(d, gr, saved, err, st)
