@@ -55,7 +55,8 @@ __device__ __forceinline__ float sum_warp(float v) {
 //     X3 = [K; Q]^T [-diag(e^G) y; scale diag(e^G) do]
 // Rows (TMEM lanes) of the first two alternate, 16 of K's or X's and 16 of Q's or P T's.  X1's rows of K
 // are used, and of X2 the columns of Z in X's rows and the columns of do in P T's rows, which are the
-// same tokens: w = Z + X2 (T = I - diag(beta) X) and G' = e^G_C G' + X3.
+// same tokens: w = Z + X2 (T = I - diag(beta) X) and G' = e^G_C G' + X3.  Bound by the chain of its
+// steps as litela_delta_chain: 3.4 us a chunk at d = 128 (2 x 2048 tokens, 16 heads: 108 us).
 template <int kD>
 struct BackCfg {
   static constexpr int kBlocks = kD > 64 ? 2 : 1;
@@ -444,9 +445,10 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
 // after another (their shares of dq and dk are summed in registers, in a fixed order).
 //
 // mma.sync, 16 warps (d = 32: 8): a warp has 16 rows and a quarter (half) of the columns.  States and
-// gradients stream through a ring of tiles of 32 columns; U and y are entered as bf16 pairs.  dq and dk of one head
-// take 12 products of 64 rows; the states' and the gradients' bytes (16 d^2 a chunk and head) are
-// what bounds it.
+// gradients stream through a ring of tiles of 32 columns; U and y are entered as bf16 pairs.  dq, dk and dg of one
+// head take 14 products of 64 rows.  2 x 2048 tokens of 16 heads of 128 (8 of keys): 146 us, of which the
+// products at the rate of mma.sync are a third; one CTA an SM (registers, shared memory) leaves the waits for
+// the tiles and between the steps open.
 constexpr int kGradLd = 72;   // row of the 64 x 64 matrices, padded
 constexpr int kGradRing = 3;
 
@@ -844,11 +846,13 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
         if (lane + o < 32) x += up;
         if (lane >= o) b += down;
       }
+      float pre = __shfl_up_sync(0xffffffffu, b, 1);   // (not b - bd: that loses small sums beside a large one)
+      if (lane == 0) pre = 0.f;
       asm volatile("barrier.cta.sync 1, 64;" ::: "memory");   // (rsum has been read)
       if (tid == 32) rsum[0] = x;
       if (tid == 31) rsum[1] = b;
       asm volatile("barrier.cta.sync 1, 64;" ::: "memory");
-      x += (b - bd) + (tid < 32 ? rsum[0] : rsum[1]);
+      x += pre + (tid < 32 ? rsum[0] : rsum[1]);
       if (tid < len) {
         const long long o = ((long long)sq.entry * a.ntok + sq.first + n0 + tid) * a.Hv + h;
         gr.dbeta[o] = wd;

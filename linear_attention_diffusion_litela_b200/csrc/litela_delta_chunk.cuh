@@ -18,9 +18,10 @@
 // entered as two or three bf16 terms (each the rounding of what the ones before it leave: 2^-17 and
 // 2^-25 relative) whose products are summed in fp32.  U, of which the state is a sum, takes three
 // (with two the state was 2.4e-6 off), R three and X two by all but the smallest products (with two
-// and two the state of slowly decaying heads was 1.2e-6 off, d = 128, 0.8e-6 now), S0 two: it enters
-// as a correction of V.  K, Q
-// and V are bf16 already.  G is summed in fp64: differences of large sums of decays would lose in
+// and two the state of slowly decaying heads was 1.2e-6 off, d = 128, 0.8e-6 now), S0 three: the third
+// costs the chain 5 % (the product's time does not change), and without it dg of a few tokens was up to
+// 9.6e-6 off.  What is left, up to 2e-6 of a state at d = 32, are X's two.  K, Q and V are bf16 already.  G is
+// summed in fp64: differences of large sums of decays would lose in
 // fp32.
 //
 // A NaN or an infinity must not reach the tokens before its own: 0 * NaN inside a product would
@@ -587,8 +588,8 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
 // ---------------------------------------------------------------------------------------
 // litela_delta_chain: one CTA walks the chunks of one sequence and value head for 32 of the state's
 // columns (columns do not meet, so a state is cut by columns over CTAs).  64 columns a CTA took 3.2 us
-// a chunk against 2.0 (d = 128): less for many equal sequences (1.6 a half), but a long sequence among
-// others, or few heads, wait for the longest chain of chunks.
+// a chunk where 32 take 2.0 to 2.2 (d = 128): less for many equal sequences (1.6 a half), but a long
+// sequence among others, or few heads, wait for the longest chain of chunks.
 //
 // Three tcgen05 products per chunk, each with M = 128 rows, fp32 accumulators in TMEM:
 //     X1 = [K; Q] S0           (rows: 16 of K, 16 of Q, 16 of K ..; K dimension d)
