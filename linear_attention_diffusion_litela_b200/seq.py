@@ -2,16 +2,22 @@
 
 Like the rest of the binding this module only marshals arguments to the C ABI (include/litela.h
 has the formulas, the layouts and the rules); outputs and workspaces come from torch, so every call
-can be captured into a CUDA graph and two calls share nothing.  The functions are reached through
-the package:
+can be captured into a CUDA graph and two calls share nothing.  To capture a training step, capture
+the _fwd_save and _bwd calls or torch.autograd.grad: torch's .backward() may not accumulate, inside a
+capture, into leaves that a graph of eager calls still holds.  The functions are reached through the
+package:
 
     from linear_attention_diffusion_litela_b200 import lite_la_qk_norm_rope, lite_la_gated_delta
 """
 from __future__ import annotations
 
+import functools
 import struct
 
-from . import _check, _torch, lib
+from . import _check, lib
+from . import _torch as _import_torch
+
+_torch = functools.cache(_import_torch)
 
 # The argument structs of include/litela.h, packed in one go: a ctypes.Structure filled field by field
 # took longer than the kernel of a one-token call.  A view is (pointer, batch, token, head stride).
@@ -25,10 +31,19 @@ def _ptr(t):
     return 0 if t is None else t.data_ptr()
 
 
+@functools.cache
+def _current_stream():
+    """device -> handle of torch's current stream there (without making a Stream object: 1.2 us of a call
+    of 15, where this torch can)"""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _call(fn, dev, stream, *args):
     """fn(*args, stream) on device `dev`; stream None: torch's current one there."""
     cuda = _torch().cuda
-    handle = (cuda.current_stream(dev) if stream is None else stream).cuda_stream
+    handle = _current_stream()(dev) if stream is None else stream.cuda_stream
     if cuda.current_device() == dev:
         _check(fn(*args, handle))
     else:
@@ -255,7 +270,7 @@ def _delta_forward(q, k, v, g, beta, state_in, state_out, cu_seqlens, scale, out
     so = _states(state_out, "state_out", a.states, a.dev)
     zero_tail = int(out is None)
     if out is None:
-        out = torch.empty(a.vshape, dtype=torch.bfloat16, device=a.device)
+        out = torch.empty_like(v, memory_format=torch.contiguous_format)
         _on_stream(out, stream)
     o = _view(out, "out", a.vshape, a.dev)
     L = lib()
@@ -385,7 +400,7 @@ def lite_la_gated_delta_step(q, k, v, g, beta, states, state_indices=None, scale
                                       or not state_indices.is_contiguous() or state_indices.get_device() != dev):
         raise TypeError("state_indices must be a contiguous int32 tensor [B] on q's device")
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        out = torch.empty_like(v, memory_format=torch.contiguous_format)
         _on_stream(out, stream)
     args = _DELTA_ARGS.pack(*_token_view(q, "q", (B, Hk, d), dev), *_token_view(k, "k", (B, Hk, d), dev),
                             *_token_view(v, "v", shape, dev), *_token_view(out, "out", shape, dev), gp, bp, g_sb, 0,
