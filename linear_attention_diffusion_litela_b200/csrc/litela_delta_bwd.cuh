@@ -446,9 +446,9 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
 //
 // mma.sync, 16 warps (d = 32: 8): a warp has 16 rows and a quarter (half) of the columns.  States and
 // gradients stream through a ring of tiles of 32 columns; U and y are entered as bf16 pairs.  dq, dk and dg of one
-// head take 14 products of 64 rows.  2 x 2048 tokens of 16 heads of 128 (8 of keys): 146 us, of which the
-// products at the rate of mma.sync are a third; one CTA an SM (registers, shared memory) leaves the waits for
-// the tiles and between the steps open.
+// head take 14 products of 64 rows.  2 x 2048 tokens of 16 heads of 128 (8 of keys): 146 us, with
+// the tensor pipe (mma.sync) at 45 %; one CTA an SM (registers, shared memory) leaves the waits for the tiles
+// and between the steps open, and 512 CTAs on 148 SMs a seventh of the time.
 constexpr int kGradLd = 72;   // row of the 64 x 64 matrices, padded
 constexpr int kGradRing = 3;
 

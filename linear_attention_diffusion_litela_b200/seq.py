@@ -265,7 +265,7 @@ def _delta_forward(q, k, v, g, beta, state_in, state_out, cu_seqlens, scale, out
     a = _Delta(q, k, v, g, beta, scale, cu_seqlens)
     si = 0 if state_in is None else _states(state_in, "state_in", a.states, a.dev)
     if state_out is None:
-        state_out = torch.empty(a.states, dtype=torch.float32, device=a.device)
+        state_out = torch.empty_like(state_in) if si else torch.empty(a.states, dtype=torch.float32, device=a.device)
         _on_stream(state_out, stream)
     so = _states(state_out, "state_out", a.states, a.dev)
     zero_tail = int(out is None)
