@@ -82,15 +82,18 @@ __device__ __forceinline__ void delta_zero_rest(const DeltaArgs& a, const DeltaV
 // litela_delta_recur: the recurrence, one token after another, the state in registers.
 //
 // A warp owns 8 columns of one state (all d rows): lane = d / 16 rows (of group lane / 2) and 4
-// columns (of half lane & 1).  Nothing is shared between warps.  S^T k and S^T q of the state
-// before the token are summed in the same shuffles (each halves the sums that a lane still holds,
-// until it has one of the 8 totals of its columns): with them
-//     u = beta (v - e^g S^T k),   out = scale * (e^g S^T q + (k . q) u),   S <- e^g S + k u^T,
-// so that the update of S is off the way from one token's sums to the next one's output.
+// columns (of half lane & 1).  Nothing is shared between warps.  Two tokens are taken at a time: the
+// products of the state before them with both k and both q are summed in the same shuffles (each
+// halves the sums that a lane still holds, until it has one of the 16 totals of its columns), and
+// with a, b the tokens' decays e^g and beta, S that state,
+//     u1 = b1 (v1 - a1 S^T k1),    u2 = b2 (v2 - a2 (a1 S^T k2 + (k1 . k2) u1)),
+//     out1 = scale (a1 S^T q1 + (k1 . q1) u1),
+//     out2 = scale (a1 a2 S^T q2 + a2 (k1 . q2) u1 + (k2 . q2) u2),    S <- a1 a2 S + a2 k1 u1^T + k2 u2^T.
 // Tokens come through shared memory, kRecurBatch at a time while the batch before is worked on.  Bound by
-// a token's chain of dependent sums, 0.26 us (d = 32) to 0.4 us (128): 16 sequences of 125 tokens in
-// all, the longest of 30, 8 heads of 64: 15 us (23 with each token loaded from global memory one ahead).  The grid is one CTA per 32 columns, so that one sequence already
-// fills the SMs.
+// the chain of dependent sums, 0.20 us a token (d = 32) to 0.25 us (128); one token at a time took 0.26 to 0.4.
+// 16 sequences of 125 tokens in all, the longest of 30, 8 heads of 64: 12 us (15 by single tokens; 23
+// with each token loaded from global memory one ahead).  The grid is one CTA per 32 columns, so that one
+// sequence already fills the SMs.
 constexpr int kRecurThreads = 128;
 constexpr int kRecurCols = 32;
 constexpr int kRecurBatch = 8;
@@ -119,28 +122,46 @@ __global__ void __launch_bounds__(kRecurThreads) litela_delta_recur(const DeltaA
   const int hk = h / (a.Hv / a.Hk);
   const int half = lane & 1, r0 = (lane >> 1) * kRows;
   const int col = blk * kRecurCols + warp * 8 + half * 4;
-  // the total that this lane ends up with: of k (0) or q (1), for column `mine` of its four
-  const int of_q = lane >> 1 & 1, mine = (lane >> 2 & 1) * 2 + (lane >> 3 & 1);
+  // the total that this lane ends up with: of k (0) or q (1), of the pair's first or second token, for
+  // column `mine` of its four; lanes of the u of that column
+  const bool of_q = lane & 2, second = lane & 4;
+  const int mine = (lane >> 3 & 1) * 2 + (lane >> 4 & 1);
+  const int lane_u = lane & ~6;   // | 4: the second token's
   if (a.zero_rest) delta_zero_rest(a, a.out, a.Hv, kD);
   const DeltaSeq sq = delta_seq(a, s);
   // a token in shared memory: k, q, v of the block's columns, g, beta
   constexpr int kOffQ = kD * 2, kOffV = kD * 4, kOffG = kOffV + kRecurCols * 2, kToken = kOffG + 16;
   __shared__ __align__(16) uint8_t ring[2 * kRecurBatch * kToken];
-  auto gate = [&](const float* p, long long sb, long long st, int n) { return p + sq.entry * sb + (sq.first + n) * st + h; };
-  auto fetch = [&](int n0) {   // tokens [n0, n0 + kRecurBatch) to their half of the ring
-    constexpr int kVec = kToken / 16;
-    for (int i = threadIdx.x; i < kRecurBatch * kVec; i += kRecurThreads) {
-      const int t = i / kVec, c = i - t * kVec, n = n0 + t;
-      if (n >= sq.len) break;
-      const uint32_t dst = smem_u32(ring + (n % (2 * kRecurBatch)) * kToken + c * 16);
-      if (c < kOffQ / 16) cp_async_16(dst, delta_row(a.k, sq, n, hk) + c * 8, true);
-      else if (c < kOffV / 16) cp_async_16(dst, delta_row(a.q, sq, n, hk) + c * 8 - kD, true);
-      else if (c < kOffG / 16) cp_async_16(dst, delta_row(a.v, sq, n, h) + blk * kRecurCols + c * 8 - 2 * kD, true);
-      else {
-        cp_async_4(dst, gate(a.g, a.g_sb, a.g_st, n));
-        cp_async_4(dst + 4, gate(a.beta, a.b_sb, a.b_st, n));
-      }
+  // what this thread copies of each batch: 16 bytes of a row (kIts of them at most), and one gate
+  constexpr int kVec = kOffG / 16, kItems = kRecurBatch * kVec, kIts = (kItems + kRecurThreads - 1) / kRecurThreads;
+  const int tid = threadIdx.x;
+  const __nv_bfloat16* src[kIts];
+  long long step[kIts];
+  int token[kIts];
+  uint32_t dst[kIts];
+#pragma unroll
+  for (int i = 0; i < kIts; ++i) {
+    const int item = tid + i * kRecurThreads, t = item / kVec, c = item - t * kVec;
+    const DeltaView& x = c < kOffQ / 16 ? a.k : c < kOffV / 16 ? a.q : a.v;
+    const int at = c < kOffQ / 16 ? c * 8 : c < kOffV / 16 ? c * 8 - kD : blk * kRecurCols + c * 8 - 2 * kD;
+    src[i] = delta_row(x, sq, t, c < kOffV / 16 ? hk : h) + at;
+    step[i] = kRecurBatch * x.st;
+    token[i] = item < kItems ? t : 1 << 30;   // (there are 2^30 tokens at most)
+    dst[i] = smem_u32(ring + t * kToken + c * 16);
+  }
+  const int gate_token = tid < 2 * kRecurBatch ? tid >> 1 : 1 << 30;
+  const long long gate_st = tid & 1 ? a.b_st : a.g_st;
+  const float* gate = (tid & 1 ? a.beta + sq.entry * a.b_sb : a.g + sq.entry * a.g_sb) + (sq.first + (tid >> 1)) * gate_st + h;
+  const uint32_t gate_dst = smem_u32(ring + (tid >> 1 & (kRecurBatch - 1)) * kToken + kOffG + (tid & 1) * 4);
+  auto fetch = [&](int n0) {   // the next batch, tokens [n0, n0 + kRecurBatch), to its half of the ring
+    const uint32_t o = n0 / kRecurBatch % 2 * (kRecurBatch * kToken);
+#pragma unroll
+    for (int i = 0; i < kIts; ++i) {
+      if (n0 + token[i] < sq.len) cp_async_16(dst[i] + o, src[i], true);
+      src[i] += step[i];
     }
+    if (n0 + gate_token < sq.len) cp_async_4(gate_dst + o, gate);
+    gate += kRecurBatch * gate_st;
     cp_async_commit();
   };
   fetch(0);
@@ -152,69 +173,102 @@ __global__ void __launch_bounds__(kRecurThreads) litela_delta_recur(const DeltaA
     if (a.state_in != nullptr) x = *reinterpret_cast<const float4*>(a.state_in + base + (long long)j * kD);
     S[j][0] = f2(x.x, x.y), S[j][1] = f2(x.z, x.w);
   }
-  for (int n = 0; n < sq.len; ++n) {
+  __nv_bfloat16* op = const_cast<__nv_bfloat16*>(delta_row(a.out, sq, second, h)) + col + mine;
+  for (int n = 0; n < sq.len; n += 2, op += 2 * a.out.st) {
     if (n % kRecurBatch == 0) {
       cp_async_wait<0>();
       __syncthreads();   // this batch is there, and all have left the one before it
       fetch(n + kRecurBatch);
     }
+    const bool two = n + 1 < sq.len;   // else the second token is one that changes nothing
     const uint8_t* tok = ring + (n % (2 * kRecurBatch)) * kToken;
-    uint32_t kw[kRows / 2], qw[kRows / 2];
-    recur_load<kRows>(tok + r0 * 2, kw);
-    recur_load<kRows>(tok + kOffQ + r0 * 2, qw);
-    const float2 gates = *reinterpret_cast<const float2*>(tok + kOffG);
-    float k[kRows], q[kRows];
+    float k[2][kRows], q[2][kRows], decay[2], write[2];
 #pragma unroll
-    for (int j = 0; j < kRows / 2; ++j) {
-      k[2 * j] = __uint_as_float(kw[j] << 16), k[2 * j + 1] = __uint_as_float(kw[j] & 0xFFFF0000u);
-      q[2 * j] = __uint_as_float(qw[j] << 16), q[2 * j + 1] = __uint_as_float(qw[j] & 0xFFFF0000u);
-    }
-    const float decay = expf(clamp_decay(gates.x));
-    const float v = bf16_up(reinterpret_cast<const uint16_t*>(tok + kOffV)[warp * 8 + half * 4 + mine]);
-    F2 sk[2] = {f2(0.f, 0.f), f2(0.f, 0.f)}, sv[2] = {sk[0], sk[1]};
-    float kq = 0.f;
+    for (int t = 0; t < 2; ++t) {
+      uint32_t kw[kRows / 2], qw[kRows / 2];
+      const bool real = t == 0 || two;
+      recur_load<kRows>(tok + t * kToken + r0 * 2, kw);
+      recur_load<kRows>(tok + t * kToken + kOffQ + r0 * 2, qw);
+      const float2 gates = *reinterpret_cast<const float2*>(tok + t * kToken + kOffG);
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      const F2 k2 = f2(k[j], k[j]), q2 = f2(q[j], q[j]);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        sk[c] = f2_fma(S[j][c], k2, sk[c]);
-        sv[c] = f2_fma(S[j][c], q2, sv[c]);
+      for (int j = 0; j < kRows / 2; ++j) {
+        if (!real) kw[j] = qw[j] = 0;
+        k[t][2 * j] = __uint_as_float(kw[j] << 16), k[t][2 * j + 1] = __uint_as_float(kw[j] & 0xFFFF0000u);
+        q[t][2 * j] = __uint_as_float(qw[j] << 16), q[t][2 * j + 1] = __uint_as_float(qw[j] & 0xFFFF0000u);
       }
-      kq += k[j] * q[j];
+      decay[t] = real ? expf(clamp_decay(gates.x)) : 1.f;
+      write[t] = real ? gates.y : 0.f;
     }
-    float sum[4];
+    const bool has = !second || two;
+    const float v = has ? bf16_up(reinterpret_cast<const uint16_t*>(tok + second * kToken + kOffV)[warp * 8 + half * 4 + mine]) : 0.f;
+    // S^T k and S^T q of both tokens, of this lane's rows: [q][token][column]
+    float sum[2][2][4];
+    float dots[4] = {0.f, 0.f, 0.f, 0.f};   // k1 q1, k2 q2, k1 k2, k1 q2
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      F2 x[2] = {f2(0.f, 0.f), f2(0.f, 0.f)}, y[2] = {x[0], x[1]};
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) {
+        const F2 k2 = f2(k[t][j], k[t][j]), q2 = f2(q[t][j], q[t][j]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          x[c] = f2_fma(S[j][c], k2, x[c]);
+          y[c] = f2_fma(S[j][c], q2, y[c]);
+        }
+        dots[t] += k[t][j] * q[t][j];
+        dots[2 + t] += k[0][j] * (t ? q[1][j] : k[1][j]);
+      }
+      const float2 x0 = f2_out(x[0]), x1 = f2_out(x[1]), y0 = f2_out(y[0]), y1 = f2_out(y[1]);
+      sum[0][t][0] = x0.x, sum[0][t][1] = x0.y, sum[0][t][2] = x1.x, sum[0][t][3] = x1.y;
+      sum[1][t][0] = y0.x, sum[1][t][1] = y0.y, sum[1][t][2] = y1.x, sum[1][t][3] = y1.y;
+    }
+    // each step halves what a lane holds: a lane keeps one half of its sums and gives the other one away
+    auto halve = [&](bool up, float lo, float hi, int o) {
+      return (up ? hi : lo) + __shfl_xor_sync(0xffffffffu, up ? lo : hi, o);
+    };
+    float total;
     {
-      const float2 k01 = f2_out(sk[0]), k23 = f2_out(sk[1]), q01 = f2_out(sv[0]), q23 = f2_out(sv[1]);
-      const float ks[4] = {k01.x, k01.y, k23.x, k23.y}, qs[4] = {q01.x, q01.y, q23.x, q23.y};
+      float x[2][4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        sum[c] = (of_q ? qs[c] : ks[c]) + __shfl_xor_sync(0xffffffffu, of_q ? ks[c] : qs[c], 2);
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[t][c] = halve(of_q, sum[0][t][c], sum[1][t][c], 2);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[0][c] = halve(second, x[0][c], x[1][c], 4);
+      const float y0 = halve(mine & 2, x[0][0], x[0][2], 8), y1 = halve(mine & 2, x[0][1], x[0][3], 8);
+      total = halve(mine & 1, y0, y1, 16);
     }
+    {
+      const float d0 = halve(lane & 2, dots[0], dots[1], 2), d1 = halve(lane & 2, dots[2], dots[3], 2);
+      float d = halve(lane & 4, d0, d1, 4);
+      d += __shfl_xor_sync(0xffffffffu, d, 8);
+      d += __shfl_xor_sync(0xffffffffu, d, 16);
 #pragma unroll
-    for (int m = 2, o = 4; m >= 1; m >>= 1, o <<= 1) {   // columns 0-1 or 2-3, then one of the two
-      const bool up = mine & m;
-#pragma unroll
-      for (int c = 0; c < m; ++c)
-        sum[c] = (up ? sum[c + m] : sum[c]) + __shfl_xor_sync(0xffffffffu, up ? sum[c] : sum[c + m], o);
+      for (int i = 0; i < 4; ++i) dots[i] = __shfl_sync(0xffffffffu, d, 2 * i);
     }
-    const float total = sum[0] + __shfl_xor_sync(0xffffffffu, sum[0], 16);
+    const float both = decay[0] * decay[1], carried = (second ? both : decay[0]) * total;
+    // u of the lane's token and column, where the total is k's
+    float wrote = (second ? write[1] : write[0]) * (v - carried);
+    const float first = __shfl_xor_sync(0xffffffffu, wrote, 4);
+    if (second) wrote -= write[1] * decay[1] * dots[2] * first;
+    F2 u[2][2];
 #pragma unroll
-    for (int o = 2; o < 32; o <<= 1) kq += __shfl_xor_sync(0xffffffffu, kq, o);
-    const float wrote = gates.y * (v - decay * total);   // u of the lane's column where the total is k's
-    float u[4];
+    for (int t = 0; t < 2; ++t) {
+      float x[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) u[c] = __shfl_sync(0xffffffffu, wrote, half | (c & 2) << 1 | (c & 1) << 3);
-    const float mu = __shfl_xor_sync(0xffffffffu, wrote, 2);
-    if (of_q && lane < 16)
-      const_cast<__nv_bfloat16*>(delta_row(a.out, sq, n, h))[col + mine] =
-          __float2bfloat16_rn(a.scale * (decay * total + kq * mu));
-    const F2 d2 = f2(decay, decay), u01 = f2(u[0], u[1]), u23 = f2(u[2], u[3]);
+      for (int c = 0; c < 4; ++c) x[c] = __shfl_sync(0xffffffffu, wrote, half | t << 2 | (c & 2) << 2 | (c & 1) << 4);
+      u[t][0] = f2(x[0], x[1]), u[t][1] = f2(x[2], x[3]);
+    }
+    const float u1 = __shfl_sync(0xffffffffu, wrote, lane_u), u2 = __shfl_sync(0xffffffffu, wrote, lane_u | 4);
+    if (of_q && has)
+      *op = __float2bfloat16_rn(a.scale * (carried + (second ? decay[1] * dots[3] * u1 + dots[1] * u2 : dots[0] * u1)));
+    const F2 d2 = f2(both, both);
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
-      const F2 k2 = f2(k[j], k[j]);
-      S[j][0] = f2_fma(k2, u01, f2_mul(d2, S[j][0]));
-      S[j][1] = f2_fma(k2, u23, f2_mul(d2, S[j][1]));
+      const float k1 = decay[1] * k[0][j];
+      const F2 a2 = f2(k1, k1), b2 = f2(k[1][j], k[1][j]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) S[j][c] = f2_fma(b2, u[1][c], f2_fma(a2, u[0][c], f2_mul(d2, S[j][c])));
     }
   }
   if (a.state_out != nullptr)

@@ -383,14 +383,15 @@ litela_status delta_setup(int dev) {
   return LITELA_OK;
 }
 
-// The recurrence or the chunks.  The recurrence takes 0.26 to 0.4 us a token (one sequence, d = 32
+// The recurrence or the chunks.  The recurrence takes 0.20 to 0.25 us a token (one sequence, d = 32
 // to 128) or what its instructions take; the chunks take a whole chunk's time for every started one.  Dense
-// (us, recurrence / chunks), N = 32: 1 x 32 heads of 128 15.0 / 13.0, 64 x 32 345 / 366; 64 x 8 heads of
-// 64 34 / 48; 1 x 70 heads of 32 10.3 / 10.5, 64 x 70 98 / 238.  N = 64: 28.0 / 12.9, 668 / 377, 65 / 49,
-// 18.5 / 10.7, 189 / 248.
+// (us, recurrence / chunks), N = 32: 1 x 32 heads of 128 10.8 / 13.0, 64 x 32 296 / 366; 1 x 8 heads of 64
+// 9.3 / 10.7, 64 x 8 28 / 48; 1 x 70 heads of 32 8.5 / 10.5, 64 x 70 82 / 238.  N = 48: 15.0 / 13.0, 428 / 370,
+// 12.9 / 10.8, 40 / 48, 11.9 / 10.6, 119 / 242.  N = 64: 18.9 / 12.9, 560 / 377, 16.4 / 10.8, 52 / 49,
+// 15.0 / 10.7, 156 / 248.
 // Packed lengths are known to the device only: the recurrence where they are 8 on the average
-// (16 sequences, 125 tokens, the longest of 30, 8 heads of 64: 15 / 23; 64 sequences of 8: 106 / 359, 11 / 48
-// and 30 / 232 at the three widths) and the longest can be no more than 512 (0.2 ms).
+// (16 sequences, 125 tokens, the longest of 30, 8 heads of 64: 12 / 23; 64 sequences of 8: 101 / 359, 10 / 48
+// and 26 / 232 at the three widths) and the longest can be no more than 512 (0.13 ms).
 constexpr int kRecurMaxTokens = 32, kRecurMaxMean = 8, kRecurMaxPacked = 512;
 bool delta_recurs(int nseq, int ntok, bool packed) {
   if (ntok <= kRecurMaxTokens) return true;
