@@ -320,9 +320,10 @@ size_t lite_la_gated_delta_workspace_bytes(int B, int N, int Hk, int Hv, int d, 
  * All rows are written: those of no sequence with zeros.  The sums are fp32; equal calls give
  * equal bits.
  *
- * A NaN or infinite value of a token (or of the state before a sequence) makes out of that token, of
- * all later tokens and the state NaN in the heads that read it; earlier tokens keep their values.
- * The gradients of such a sequence are unspecified; other sequences are not touched. */
+ * A NaN or infinite k, v, g or beta of a token (or state before a sequence) makes out of that token,
+ * of all later tokens and the state NaN in the heads that read it, one in q at least out of that
+ * token; earlier tokens keep their values.  The gradients of such a sequence are unspecified; other
+ * sequences are not touched. */
 typedef struct {
   lite_la_view dout, dq, dk, dv;
   float* dg;
