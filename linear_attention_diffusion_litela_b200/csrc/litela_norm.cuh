@@ -50,6 +50,7 @@ struct NormPlan {
 constexpr int kNormThreads = 256;
 constexpr int kNormWarps = kNormThreads / 32;
 constexpr int kNormStep = 256;    // channels of a warp's step
+constexpr int kNormAhead = 5120;  // bytes of a task that is fetched ahead, at most (norm_prefetch)
 
 template <int kLanes>
 __device__ __forceinline__ float sum_lanes(float v) {
@@ -100,6 +101,18 @@ __device__ __forceinline__ bool norm_next(const NormPlan& p, NormWalk& w, long l
     norm_task(p, w);
   }
   return true;
+}
+
+// A whole task's channels into L2, one task ahead of the forward's loads: more bytes in flight than
+// registers hold.  Tasks of 2240 and 4480 bytes: 206 -> 174 us, 184 -> 164 us (60000 rows of 3 x 35, 32768 of
+// 3 x 70 heads of 32); of 8192 and 16384 bytes, whose own loads are enough: 244 -> 322 us, 268 -> 377 us, and the
+// gradient (two rows a task) 62 -> 70 us: not fetched.
+__device__ __forceinline__ void norm_prefetch(const NormPlan& p, long long t, int lane) {
+  if (p.shift != 0 || lane != 0 || t >= p.rows * p.regions) return;
+  const int region = (t >= p.rows) + (t >= 2 * p.rows);
+  const int first = region == 0 ? 0 : region == 1 ? p.q_ch : p.qk_ch;
+  const int bytes = ((region == 0 ? p.q_ch : region == 1 ? p.qk_ch : p.W) - first) * 2;
+  if (bytes > 0 && bytes <= kNormAhead) sm100::bulk_prefetch_l2(p.x + (t - region * p.rows) * p.W + first, bytes);
 }
 
 template <int kU>
@@ -206,8 +219,8 @@ __device__ __forceinline__ void norm_zero(const NormPlan& p, const NormWalk& w, 
 
 // y = r (x * a + partner * b), a = w cos, b = the partner's w times the signed sine.  80 registers
 // (three CTAs an SM) hold four steps in work and four in flight.  2 x 16384 rows of 70 + 70 + 70
-// heads of 32 channels: 176 us, 5.0 TB/s (64 registers, two steps and four CTAs: 179 us); what is left is
-// bound by the issue of instructions as much as by memory.
+// heads of 32 channels: 158 us, 5.6 TB/s (176 without norm_prefetch, 179 with 64 registers, two steps and
+// four CTAs); what is left is bound by the issue of instructions as much as by memory.
 template <int kD, bool kInter>
 __global__ void __launch_bounds__(kNormThreads, 3) litela_norm_fwd(const NormPlan p) {
   constexpr int kU = 4;
@@ -231,6 +244,7 @@ __global__ void __launch_bounds__(kNormThreads, 3) litela_norm_fwd(const NormPla
     if (more) norm_load<kU>(p, p.x, to, lane, ahead);
     if (w.t != task) {
       task = w.t;
+      norm_prefetch(p, task + nwarps, lane);
       pos = norm_position(p, w.at);
       if (pos >= 0 && w.region < 2) {
         norm_angles<kInter>(p, pos, c, a, b);
