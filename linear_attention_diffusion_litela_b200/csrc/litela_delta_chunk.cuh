@@ -860,8 +860,9 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, const De
 #pragma unroll
         for (int i = 0; i < kN / 4; ++i) {
           const float2 xi = f2_out(x[i]);
-          if (!isfinite(xi.x) || !isfinite(xi.y)) atomicMin(first_bad, n * kChunk + tok + (i & 1) * 8);
-          x[i] = f2(0.f, 0.f);
+          const bool fx = isfinite(xi.x), fy = isfinite(xi.y);
+          if (!fx || !fy) atomicMin(first_bad, n * kChunk + tok + (i & 1) * 8);
+          x[i] = f2(fx ? xi.x : 0.f, fy ? xi.y : 0.f);   // (the others may be an earlier token's)
         }
       }
       chain_put_frag<3>(rtile, Cfg::kRTile, tok, fc, x);

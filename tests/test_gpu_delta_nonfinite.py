@@ -1,0 +1,49 @@
+"""A NaN or an infinity in a token's inputs leaves the outputs of earlier tokens as they are, bit for bit,
+and reaches all later ones and the state: at every place of a chunk, in both forms of the gated delta rule
+(up to 32 tokens the recurrence, more in chunks of 64).  Sequence i of a call has its bad token at place
+first + i; the others' values are those of a call without any."""
+import pytest
+import torch
+
+import linear_attention_diffusion_litela_b200 as ll
+from tests.test_gpu_delta import fwd, make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from linear_attention_diffusion_litela_b200.build import build
+    build()
+
+
+NAN, INF = float("nan"), float("inf")
+SIZES = [(32, 0, 32), (64, 0, 64), (150, 0, 64), (150, 64, 64), (150, 128, 22)]   # tokens, first place, places
+
+
+def check(name, value, d, N, first, count, channel=None):
+    """`channel`: only this one of the token's is bad, and only its outputs have to show it"""
+    t = make([N] * count, False, 1, 2, d, True, seed=N + first + d)
+    want, _ = fwd(t)
+    t[name] = t[name].clone()
+    for i in range(count):
+        if channel is None:
+            t[name][i, first + i] = value
+        else:
+            t[name][i, first + i, :, channel] = value
+    out, state = fwd(t)
+    ll.lite_la_device_status()
+    seen = slice(None) if channel is None or name == "k" else channel
+    before = torch.arange(N, device="cuda")[None] < first + torch.arange(count, device="cuda")[:, None]
+    same = (out == want).flatten(2).all(-1)
+    wrong = (before & ~same).nonzero().tolist()
+    assert not wrong, "earlier tokens of (sequence, token) %s differ" % wrong[:8]
+    assert not torch.isfinite(out[..., seen]).flatten(2).any(-1)[~before].any()
+    assert not torch.isfinite(state[..., seen]).any()
+
+
+@pytest.mark.parametrize("N,first,count", SIZES)
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("name,value,channel", [("k", NAN, None), ("k", INF, 3), ("v", NAN, None), ("v", -INF, 17)])
+def test_keys_and_values(name, value, channel, d, N, first, count):
+    check(name, value, d, N, first, count, channel)
