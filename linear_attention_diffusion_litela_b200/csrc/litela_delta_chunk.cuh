@@ -25,7 +25,7 @@
 // fp32.
 //
 // A NaN or an infinity must not reach the tokens before its own: 0 * NaN inside a product would
-// carry it there.  So non-finite entries are taken out of L, P and E, the first token that had one
+// carry it there.  So non-finite entries are taken out of L, P, beta and R, the first token that had one
 // is kept, and it and all later tokens of the sequence (and the state) get NaN.
 #pragma once
 
@@ -54,7 +54,7 @@ constexpr uint32_t kPrepBytes = kPrepFactors + kFactorBytes;
 // columns as above for tokens j, (i, j) of X and of P T (the gradient's products take X^T and (P T)^T)
 constexpr uint32_t kPrepSaveBytes = kPrepBytes + 2 * kImgHalf;
 // fp32 at kPrepFactors: e^G [64], e^(G_C - G) [64] (0 behind the end), beta [64] (0 behind the
-// end), then e^G_C and (int32) the first token of the chunk with a non-finite L or P, or 64
+// end), then e^G_C and (int32) the first token of the chunk with a non-finite L, P or beta, or 64
 constexpr int kFacDecay = 0, kFacToEnd = 64, kFacBeta = 128, kFacChunk = 192, kFacBad = 193;
 // and what D is made of (litela_delta_prep): e^(G_r - G_m) [64]; e^(G_m - G_c) for the blocks of rows
 // 1, 2, 3 (48 each, from kFacCol + 48 on); G_r - G_m in two fp32 terms [64][2]
@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
     }
     cp_async_commit();
   }
+  bool bad_beta = false;
   if (w == 0) {
     g0[1] += g0[0];
     double run = g0[1];
@@ -265,11 +266,15 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
     G[2 * lane + 1] = run;
   } else if (w < 3) {
     const int n = tid - 32;
-    beta[n] = n < len ? a.beta[sq.entry * a.b_sb + (long long)(sq.first + n0 + n) * a.b_st + h] : 0.f;
+    const float b = n < len ? a.beta[sq.entry * a.b_sb + (long long)(sq.first + n0 + n) * a.b_st + h] : 0.f;
+    // 0 for the products, in which zeros stand for earlier tokens; the token is kept as a bad one
+    bad_beta = !isfinite(b);
+    beta[n] = bad_beta ? 0.f : b;
   } else if (tid == 96) {
     *bad = kChunk;
   }
   __syncthreads();
+  if (bad_beta) atomicMin(bad, tid - 32);
   uint8_t* dst = prep + ((long long)slot * a.Hv + h) * (kSave ? kPrepSaveBytes : kPrepBytes);
   float* fac = reinterpret_cast<float*>(dst + kPrepFactors);
   if (tid < kChunk) {

@@ -47,3 +47,10 @@ def check(name, value, d, N, first, count, channel=None):
 @pytest.mark.parametrize("name,value,channel", [("k", NAN, None), ("k", INF, 3), ("v", NAN, None), ("v", -INF, 17)])
 def test_keys_and_values(name, value, channel, d, N, first, count):
     check(name, value, d, N, first, count, channel)
+
+
+@pytest.mark.parametrize("N,first,count", SIZES)
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+def test_write_strengths(value, d, N, first, count):
+    check("beta", value, d, N, first, count)
