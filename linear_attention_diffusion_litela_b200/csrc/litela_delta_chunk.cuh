@@ -255,14 +255,14 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
   }
   bool bad_beta = false;
   if (w == 0) {
-    g0[1] += g0[0];
-    double run = g0[1];
+    double run = g0[0] + g0[1];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const double y = __shfl_up_sync(0xffffffffu, run, o);
       if (lane >= o) run += y;
     }
-    G[2 * lane] = run - g0[1] + g0[0];
+    const double before = __shfl_up_sync(0xffffffffu, run, 1);   // (not run - g0[1]: that may be NaN - NaN)
+    G[2 * lane] = (lane == 0 ? 0.0 : before) + g0[0];
     G[2 * lane + 1] = run;
   } else if (w < 3) {
     const int n = tid - 32;

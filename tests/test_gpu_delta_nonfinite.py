@@ -54,3 +54,39 @@ def test_keys_and_values(name, value, channel, d, N, first, count):
 @pytest.mark.parametrize("value", [NAN, INF, -INF])
 def test_write_strengths(value, d, N, first, count):
     check("beta", value, d, N, first, count)
+
+
+@pytest.mark.parametrize("N,first,count", SIZES)
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("value", [NAN, INF])
+def test_decays(value, d, N, first, count):
+    check("g", value, d, N, first, count)
+
+
+@pytest.mark.parametrize("N,first,count", SIZES)
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("value", [NAN, INF])
+def test_queries(value, d, N, first, count):
+    """A bad query shows in its own token's outputs at least, and in no earlier ones"""
+    t = make([N] * count, False, 1, 2, d, True, seed=N + first + d)
+    want, _ = fwd(t)
+    t["q"] = t["q"].clone()
+    at = first + torch.arange(count, device="cuda")
+    t["q"][torch.arange(count, device="cuda"), at, :, 5] = value
+    out, _ = fwd(t)
+    before = torch.arange(N, device="cuda")[None] < at[:, None]
+    assert (out == want).flatten(2).all(-1)[before].all()
+    assert not torch.isfinite(out[torch.arange(count, device="cuda"), at]).any()
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("N", [20, 150])
+def test_a_state_before_the_sequence(N, d):
+    """A bad element of state_in: its value channel in all tokens, and no other sequence"""
+    t = make([N] * 3, False, 1, 2, d, True, seed=N + d)
+    want, want_s = fwd(t)
+    t["state_in"][1, 1, 4, 9] = NAN
+    out, state = fwd(t)
+    assert torch.equal(out[[0, 2]], want[[0, 2]]) and torch.equal(state[[0, 2]], want_s[[0, 2]])
+    assert torch.equal(out[1, :, 0], want[1, :, 0]) and torch.equal(state[1, 0], want_s[1, 0])
+    assert not torch.isfinite(out[1, :, 1, 9]).any() and not torch.isfinite(state[1, 1, :, 9]).any()
