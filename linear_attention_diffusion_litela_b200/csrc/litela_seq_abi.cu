@@ -415,7 +415,7 @@ struct DeltaBytes {
   size_t prep, kept, states, gstates, rows, shares, ends;
   explicit DeltaBytes(const DeltaArgs& d, int D) : DeltaBytes(d.nseq, d.ntok, d.Hv, D, d.cu != nullptr) {}
   DeltaBytes(int B, int N, int Hv, int D, bool packed)
-      : n((size_t)delta_slots(B, N, packed) * Hv),
+      : n(N > 0 ? (size_t)delta_slots(B, N, packed) * Hv : 0),   // (packed: there are slots without tokens)
         prep(up(n * kPrepBytes)),
         kept(up(n * kPrepSaveBytes)),
         states(up(n * D * D * 8)),
@@ -537,18 +537,18 @@ litela_status delta_bwd(const lite_la_delta_args* a, const lite_la_delta_grads* 
     return invalid("the states' gradients must be 16-byte aligned");
   const DeltaBytes bytes(a->B, a->N, a->Hv, a->d, a->cu_seqlens != nullptr);
   const size_t states = (size_t)a->B * a->Hv * a->d * a->d * 4, gates = (size_t)entries * a->N * a->Hv * 4;
-  if ((s = buffer_check(a, saved, saved_bytes, a->N > 0 ? bytes.saved() : 0, in, Span{}, "saved missing, too small or misaligned",
+  if ((s = buffer_check(a, saved, saved_bytes, bytes.saved(), in, Span{}, "saved missing, too small or misaligned",
                         "saved overlaps a buffer of the call")) != LITELA_OK ||
-      (s = buffer_check(a, a->workspace, a->workspace_bytes, a->N > 0 ? bytes.back() : 0, in, Span{},
+      (s = buffer_check(a, a->workspace, a->workspace_bytes, bytes.back(), in, Span{},
                         "workspace missing, too small or misaligned", "the workspace overlaps a buffer of the call")) !=
           LITELA_OK)
     return s;
-  in.add(span(saved, a->N > 0 ? bytes.saved() : 0));
+  in.add(span(saved, bytes.saved()));
   const Span dso = span(g->dstate_out, states);
   // dq, dk, dv may be views of one buffer between one another's rows: only their spans against inputs
   // and the dense outputs are checked
   const Span outs[7] = {sp[0], sp[1], sp[2], span(g->dg, gates), span(g->dbeta, gates), span(g->dstate_in, states),
-                        span(a->workspace, a->N > 0 ? bytes.back() : 0)};
+                        span(a->workspace, bytes.back())};
   for (int i = 0; i < 3; ++i)
     if (sp[i].hi > 0 && sp[i].lo == sp[(i + 1) % 3].lo) return invalid("dq, dk and dv must be different memory");
   for (int i = 0; i < 7; ++i) {
