@@ -2,7 +2,8 @@
 
 Like the rest of the binding this module only marshals arguments to the C ABI (include/litela.h
 has the formulas, the layouts and the rules); outputs and workspaces come from torch, so every call
-can be captured into a CUDA graph and two calls share nothing.  To capture a training step, capture
+can be captured into a CUDA graph and two calls share nothing.  A call with `stream` runs on that
+stream, which the caller has made wait for the inputs, and takes its buffers from its memory.  To capture a training step, capture
 the _fwd_save and _bwd calls or torch.autograd.grad: torch's .backward() may not accumulate, inside a
 capture, into leaves that a graph of eager calls still holds.  The functions are reached through the
 package:
@@ -51,11 +52,18 @@ def _call(fn, dev, stream, *args):
             _check(fn(*args, handle))
 
 
-def _on_stream(t, stream):
-    """A buffer that torch made on the current stream is used on `stream`: torch must not hand its
-    memory on before that stream is done with it."""
-    if stream is not None:
-        t.record_stream(stream)
+def _new(stream, make, returned=True):
+    """make(): a buffer of a call.  With `stream` it comes from that stream's memory: a block of the
+    current stream's may have been freed under work that is still queued there, which a caller's wait
+    before the call need not cover.  The current stream may go on to use what is returned."""
+    if stream is None:
+        return make()
+    cuda = _torch().cuda
+    with cuda.stream(stream):
+        t = make()
+    if returned:
+        t.record_stream(cuda.current_stream(t.device))
+    return t
 
 
 # ---------------------------------------------------------------------------------------
@@ -108,8 +116,7 @@ def lite_la_qk_norm_rope_fwd(qkv, Hq: int, Hk: int, d: int = 32, q_weight=None, 
     negative position is padding: left alone in place, zeros otherwise."""
     dev, args = _norm_args(qkv, Hq, Hk, d, q_weight, k_weight, cos, sin, positions, eps, interleaved)
     if out is None:
-        out = _torch().empty_like(qkv)
-        _on_stream(out, stream)
+        out = _new(stream, lambda: _torch().empty_like(qkv))
     o = _rows(out, "out", qkv.shape, dev)
     _call(lib().lite_la_qk_norm_rope_fwd, dev, stream, qkv.data_ptr(), o, _ptr(q_weight), _ptr(k_weight), *args)
     return out
@@ -123,18 +130,14 @@ def lite_la_qk_norm_rope_bwd(qkv, dout, Hq: int, Hk: int, d: int = 32, q_weight=
     torch = _torch()
     dev, args = _norm_args(qkv, Hq, Hk, d, q_weight, k_weight, cos, sin, positions, eps, interleaved)
     if dqkv is None:
-        dqkv = torch.empty_like(qkv)
-        _on_stream(dqkv, stream)
+        dqkv = _new(stream, lambda: torch.empty_like(qkv))
     do, dx = _rows(dout, "dout", qkv.shape, dev), _rows(dqkv, "dqkv", qkv.shape, dev)
-    dwq = None if q_weight is None else torch.empty_like(q_weight)
-    dwk = None if k_weight is None else torch.empty_like(k_weight)
+    dwq = None if q_weight is None else _new(stream, lambda: torch.empty_like(q_weight))
+    dwk = None if k_weight is None else _new(stream, lambda: torch.empty_like(k_weight))
     size, ws = 0, None
     if dwq is not None or dwk is not None:
         size = lib().lite_la_qk_norm_rope_workspace_bytes(d)
-        ws = torch.empty(size, dtype=torch.uint8, device=qkv.device)
-        for t in (ws, dwq, dwk):
-            if t is not None:
-                _on_stream(t, stream)
+        ws = _new(stream, lambda: torch.empty(size, dtype=torch.uint8, device=qkv.device), False)
     _call(lib().lite_la_qk_norm_rope_bwd, dev, stream, qkv.data_ptr(), do, dx, _ptr(q_weight), _ptr(k_weight),
           _ptr(dwq), _ptr(dwk), *args, _ptr(ws), size)
     return dqkv, dwq, dwk
@@ -265,19 +268,16 @@ def _delta_forward(q, k, v, g, beta, state_in, state_out, cu_seqlens, scale, out
     a = _Delta(q, k, v, g, beta, scale, cu_seqlens)
     si = 0 if state_in is None else _states(state_in, "state_in", a.states, a.dev)
     if state_out is None:
-        state_out = torch.empty_like(state_in) if si else torch.empty(a.states, dtype=torch.float32, device=a.device)
-        _on_stream(state_out, stream)
+        state_out = _new(stream, lambda: torch.empty_like(state_in) if si
+                         else torch.empty(a.states, dtype=torch.float32, device=a.device))
     so = _states(state_out, "state_out", a.states, a.dev)
     zero_tail = int(out is None)
     if out is None:
-        out = torch.empty_like(v, memory_format=torch.contiguous_format)
-        _on_stream(out, stream)
+        out = _new(stream, lambda: torch.empty_like(v, memory_format=torch.contiguous_format))
     o = _view(out, "out", a.vshape, a.dev)
     L = lib()
     size = a.bytes(L.lite_la_gated_delta_saved_bytes if save else L.lite_la_gated_delta_workspace_bytes)
-    buf = torch.empty(size, dtype=torch.uint8, device=a.device) if size or save else None
-    if buf is not None:
-        _on_stream(buf, stream)
+    buf = _new(stream, lambda: torch.empty(size, dtype=torch.uint8, device=a.device), save) if size or save else None
     if save:
         _call(L.lite_la_gated_delta_fwd_save, a.dev, stream, a.pack(o, si, so, zero_tail, 0, 0), buf.data_ptr(), size)
     else:
@@ -315,7 +315,8 @@ def lite_la_gated_delta_bwd(q, k, v, g, beta, dout, saved, dstate_out=None, stat
     if not isinstance(saved, torch.Tensor) or saved.dtype is not torch.uint8 or not saved.is_contiguous() \
             or saved.get_device() != a.dev:
         raise TypeError("saved must be what lite_la_gated_delta_fwd_save returned")
-    new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=a.device)  # noqa: E731
+    new = lambda shape, dtype, returned=True: _new(  # noqa: E731
+        stream, lambda: torch.empty(shape, dtype=dtype, device=a.device), returned)
     si = dstate_in = None
     if state_in is not None:
         si, dstate_in = _states(state_in, "state_in", a.states, a.dev), new(a.states, torch.float32)
@@ -323,10 +324,7 @@ def lite_la_gated_delta_bwd(q, k, v, g, beta, dout, saved, dstate_out=None, stat
     dq, dk, dv = (new(shape, torch.bfloat16) for shape in (a.qshape, a.qshape, a.vshape))
     dg, dbeta = (new(a.vshape[:3], torch.float32) for _ in range(2))
     size = a.bytes(lib().lite_la_gated_delta_bwd_workspace_bytes)
-    ws = new(size, torch.uint8)
-    for t in (dq, dk, dv, dg, dbeta, dstate_in, ws):
-        if t is not None:
-            _on_stream(t, stream)
+    ws = new(size, torch.uint8, False)
     grads = _DELTA_GRADS.pack(*do, *_view(dq, "dq", a.qshape, a.dev), *_view(dk, "dk", a.qshape, a.dev),
                               *_view(dv, "dv", a.vshape, a.dev), dg.data_ptr(), dbeta.data_ptr(), dso,
                               _ptr(dstate_in))
@@ -400,8 +398,7 @@ def lite_la_gated_delta_step(q, k, v, g, beta, states, state_indices=None, scale
                                       or not state_indices.is_contiguous() or state_indices.get_device() != dev):
         raise TypeError("state_indices must be a contiguous int32 tensor [B] on q's device")
     if out is None:
-        out = torch.empty_like(v, memory_format=torch.contiguous_format)
-        _on_stream(out, stream)
+        out = _new(stream, lambda: torch.empty_like(v, memory_format=torch.contiguous_format))
     args = _DELTA_ARGS.pack(*_token_view(q, "q", (B, Hk, d), dev), *_token_view(k, "k", (B, Hk, d), dev),
                             *_token_view(v, "v", shape, dev), *_token_view(out, "out", shape, dev), gp, bp, g_sb, 0,
                             b_sb, 0, st, st, 0, B, 1, Hk, Hv, d,

@@ -29,3 +29,57 @@ def test_a_training_step_without_tokens(lens, packed, d, carry):
     assert torch.equal(state, t["state_in"] if carry else torch.zeros_like(t["dstate"]))
     if carry:
         assert torch.equal(grads["state_in"], t["dstate"])
+
+
+def test_buffers_of_a_call_on_another_stream(monkeypatch):
+    """They come from that stream's memory, not from blocks that the current stream may still have in use"""
+    t = make([300, 80], True, 1, 2, 64, True)
+    qkv = torch.randn(2, 600, 6 * 64, device="cuda").bfloat16()
+    w = torch.ones(64, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    # memory that the current stream could give
+    spare = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in (1 << 9, 1 << 12, 1 << 16, 1 << 20, 1 << 22, 1 << 24) for _ in range(3)]
+    del spare
+    buffers = []
+    call = seq._call
+
+    def spy(fn, dev, stream, *args):
+        for x in args:
+            if isinstance(x, bytes) and len(x) == seq._DELTA_ARGS.size:
+                buffers.append(seq._DELTA_ARGS.unpack(x)[-2])
+        if fn is ll.lib().lite_la_qk_norm_rope_bwd:
+            buffers.append(args[-2])
+        call(fn, dev, stream, *args)
+
+    monkeypatch.setattr(seq, "_call", spy)
+    args = [t[n] for n in ("q", "k", "v", "g", "beta")]
+    kw = dict(state_in=t["state_in"], cu_seqlens=t["cu"], stream=s)
+    made = list(ll.lite_la_gated_delta_fwd(*args, **kw))
+    made += ll.lite_la_gated_delta_fwd_save(*args, **kw)
+    made += ll.lite_la_gated_delta_bwd(*args, t["dout"], made[-1], dstate_out=t["dstate"], **kw)
+    made.append(ll.lite_la_gated_delta_step(*(x[0, :2] for x in args), t["state_in"].clone(), stream=s))
+    made.append(ll.lite_la_qk_norm_rope_fwd(qkv, 2, 2, d=64, q_weight=w, stream=s))
+    made += [x for x in ll.lite_la_qk_norm_rope_bwd(qkv, qkv.clone(), 2, 2, d=64, q_weight=w, k_weight=w, stream=s)]
+    torch.cuda.synchronize()
+    at = [x.data_ptr() for x in made] + [p for p in buffers if p]
+    assert len(at) == len(made) + 3     # the forward's and both backwards' workspaces
+    segments = torch.cuda.memory_snapshot()
+    for p in at:
+        own = [g for g in segments if g["address"] <= p < g["address"] + g["total_size"]]
+        assert len(own) == 1 and own[0]["stream"] == s.cuda_stream
+
+
+def test_a_captured_call_on_another_stream():
+    t = make([150, 70], True, 1, 2, 64, True)
+    want = fwd(t)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = fwd(t, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        for x in got:
+            x.zero_()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
