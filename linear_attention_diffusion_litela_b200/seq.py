@@ -372,8 +372,10 @@ def lite_la_gated_delta(q, k, v, g, beta, state_in=None, cu_seqlens=None, scale=
     gradients for q, k, v, g, beta and state_in.  The forward keeps its states (one per 64 tokens) for
     the backward; where no gradient is wanted it does not."""
     torch = _torch()
-    if not torch.is_grad_enabled() or not any(isinstance(t, torch.Tensor) and t.requires_grad
-                                              for t in (q, k, v, g, beta, state_in)):
+    given = [t for t in (q, k, v, g, beta, state_in) if isinstance(t, torch.Tensor)]
+    # (a tangent of forward-mode differentiation goes to the function, which refuses it)
+    if not (torch.is_grad_enabled() and any(t.requires_grad for t in given)) \
+            and all(torch.autograd.forward_ad.unpack_dual(t).tangent is None for t in given):
         return lite_la_gated_delta_fwd(q, k, v, g, beta, state_in=state_in, cu_seqlens=cu_seqlens, scale=scale)
     return _delta_function().apply(q, k, v, g, beta, state_in, cu_seqlens, scale)
 

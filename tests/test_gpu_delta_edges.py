@@ -83,3 +83,24 @@ def test_a_captured_call_on_another_stream():
             x.zero_()
         graph.replay()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_tangents_are_refused_not_lost():
+    """Forward-mode differentiation is not offered: refused whether or not a gradient is wanted as well"""
+    import torch.autograd.forward_ad as forward_ad
+    t = make([40, 40], False, 1, 1, 32, False)
+    args = [t[n] for n in ("q", "k", "v", "g", "beta")]
+    with forward_ad.dual_level():
+        for i in range(5):
+            dual = list(args)
+            dual[i] = forward_ad.make_dual(args[i], torch.ones_like(args[i]))
+            with pytest.raises((RuntimeError, NotImplementedError)):
+                ll.lite_la_gated_delta(*dual)
+        plain = ll.lite_la_gated_delta(*args)     # no tangent, none lost
+    assert all(torch.equal(a, b) for a, b in zip(plain, fwd(t)))
+    with forward_ad.dual_level():
+        state = forward_ad.make_dual(torch.zeros(2, 1, 32, 32, device="cuda"), torch.ones(2, 1, 32, 32, device="cuda"))
+        with pytest.raises((RuntimeError, NotImplementedError)):
+            ll.lite_la_gated_delta(*args, state_in=state)
+        with pytest.raises((RuntimeError, NotImplementedError)):
+            ll.lite_la_qk_norm_rope(forward_ad.make_dual(t["q"].flatten(2), torch.ones_like(t["q"].flatten(2))), 1, 0)
