@@ -104,3 +104,26 @@ def test_tangents_are_refused_not_lost():
             ll.lite_la_gated_delta(*args, state_in=state)
         with pytest.raises((RuntimeError, NotImplementedError)):
             ll.lite_la_qk_norm_rope(forward_ad.make_dual(t["q"].flatten(2), torch.ones_like(t["q"].flatten(2))), 1, 0)
+
+
+@pytest.mark.parametrize("wanted", [(), (0,), (1,), (2,), (0, 2), (0, 1, 2)])
+def test_frozen_weights_of_the_head_norms(monkeypatch, wanted):
+    """Only the weights' gradients that autograd wants are computed; they are those of the full call"""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    leaves = [r(2, 50, 6 * 64).bfloat16(), 1 + 0.2 * r(64), 1 + 0.2 * r(64)]
+    dout = r(2, 50, 6 * 64).bfloat16()
+    want = ll.lite_la_qk_norm_rope_bwd(leaves[0], dout, 3, 2, d=64, q_weight=leaves[1], k_weight=leaves[2])
+    for i in wanted:
+        leaves[i].requires_grad_()
+    out = ll.lite_la_qk_norm_rope(leaves[0], 3, 2, d=64, q_weight=leaves[1], k_weight=leaves[2])
+    assert out.requires_grad == bool(wanted)
+    asked = []
+    call = seq._call
+    monkeypatch.setattr(seq, "_call", lambda fn, dev, stream, *args: (asked.append(args), call(fn, dev, stream, *args)))
+    if wanted:
+        got = torch.autograd.grad(out, [leaves[i] for i in wanted], dout)
+        assert all(torch.equal(a, want[i]) for a, i in zip(got, wanted))
+        (args,) = asked
+        assert [bool(args[5]), bool(args[6])] == [1 in wanted, 2 in wanted]      # dq_weight, dk_weight
+        assert bool(args[-2]) == (1 in wanted or 2 in wanted)                    # the workspace
