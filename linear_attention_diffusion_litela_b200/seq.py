@@ -127,15 +127,21 @@ def lite_la_qk_norm_rope_bwd(qkv, dout, Hq: int, Hk: int, d: int = 32, q_weight=
                              stream=None):
     """Gradient of sum(dout * out): returns (dqkv bf16, dq_weight, dk_weight fp32; None for a
     weight that is None).  dqkv=dout works in place."""
+    return _norm_bwd(qkv, dout, Hq, Hk, d, q_weight, k_weight, cos, sin, positions, eps, interleaved, dqkv, stream,
+                     q_weight is not None, k_weight is not None)
+
+
+def _norm_bwd(qkv, dout, Hq, Hk, d, q_weight, k_weight, cos, sin, positions, eps, interleaved, dqkv, stream, want_q, want_k):
+    """... with the weights' gradients that are wanted"""
     torch = _torch()
     dev, args = _norm_args(qkv, Hq, Hk, d, q_weight, k_weight, cos, sin, positions, eps, interleaved)
     if dqkv is None:
         dqkv = _new(stream, lambda: torch.empty_like(qkv))
     do, dx = _rows(dout, "dout", qkv.shape, dev), _rows(dqkv, "dqkv", qkv.shape, dev)
-    dwq = None if q_weight is None else _new(stream, lambda: torch.empty_like(q_weight))
-    dwk = None if k_weight is None else _new(stream, lambda: torch.empty_like(k_weight))
+    dwq = _new(stream, lambda: torch.empty_like(q_weight)) if want_q else None
+    dwk = _new(stream, lambda: torch.empty_like(k_weight)) if want_k else None
     size, ws = 0, None
-    if dwq is not None or dwk is not None:
+    if want_q or want_k:
         size = lib().lite_la_qk_norm_rope_workspace_bytes(d)
         ws = _new(stream, lambda: torch.empty(size, dtype=torch.uint8, device=qkv.device), False)
     _call(lib().lite_la_qk_norm_rope_bwd, dev, stream, qkv.data_ptr(), do, dx, _ptr(q_weight), _ptr(k_weight),
@@ -144,6 +150,12 @@ def lite_la_qk_norm_rope_bwd(qkv, dout, Hq: int, Hk: int, d: int = 32, q_weight=
 
 
 _FUNCTIONS = {}
+
+
+def _dense(t):
+    """A gradient as autograd hands it, contiguous and aligned as the calls want it."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
 def _norm_function():
@@ -164,10 +176,11 @@ def _norm_function():
             @once_differentiable
             def backward(ctx, grad):
                 qkv, q_weight, k_weight, cos, sin, positions = ctx.saved_tensors
-                if grad.dtype != torch.bfloat16 or not grad.is_contiguous():
-                    grad = grad.to(torch.bfloat16).contiguous()
-                dqkv, dwq, dwk = lite_la_qk_norm_rope_bwd(qkv, grad, q_weight=q_weight, k_weight=k_weight, cos=cos,
-                                                          sin=sin, positions=positions, **ctx.kw)
+                grad = _dense(grad.to(torch.bfloat16))
+                _, want_q, want_k = ctx.needs_input_grad[:3]     # (frozen weights cost nothing)
+                dqkv, dwq, dwk = _norm_bwd(qkv, grad, q_weight=q_weight, k_weight=k_weight, cos=cos, sin=sin,
+                                           positions=positions, dqkv=None, stream=None, want_q=want_q, want_k=want_k,
+                                           **ctx.kw)
                 return dqkv, dwq, dwk, None, None, None, None
 
         _FUNCTIONS["norm"] = QKNormRope
@@ -356,9 +369,9 @@ def _delta_function():
                     dout = torch.zeros_like(v, memory_format=torch.contiguous_format)
                 dout = dout.to(torch.bfloat16)
                 if dout.stride(-1) != 1 or dout.data_ptr() % 16 != 0 or any(x % 8 for x in dout.stride()[:3]):
-                    dout = dout.contiguous()
+                    dout = _dense(dout)
                 if dstate is not None:
-                    dstate = dstate.float().contiguous()
+                    dstate = _dense(dstate.float())
                 grads = lite_la_gated_delta_bwd(q, k, v, g, beta, dout, saved, dstate_out=dstate, state_in=state_in,
                                                 cu_seqlens=cu_seqlens, scale=ctx.scale)
                 return (*grads, None, None)

@@ -127,3 +127,22 @@ def test_frozen_weights_of_the_head_norms(monkeypatch, wanted):
         (args,) = asked
         assert [bool(args[5]), bool(args[6])] == [1 in wanted, 2 in wanted]      # dq_weight, dk_weight
         assert bool(args[-2]) == (1 in wanted or 2 in wanted)                    # the workspace
+
+
+def odd(x):
+    """x's values, contiguous, 4 bytes from a 16-byte boundary: as a gradient may be a part of something"""
+    pad = 4 // x.element_size()
+    y = torch.empty(x.numel() + pad, dtype=x.dtype, device=x.device)[pad:].view(x.shape).copy_(x)
+    assert y.is_contiguous() and y.data_ptr() % 16 == 4
+    return y
+
+
+def test_incoming_gradients_off_the_alignment():
+    t = make([90, 50], True, 1, 2, 64, True)
+    want = autograd(t)[2]
+    got = autograd(dict(t, dout=odd(t["dout"]), dstate=odd(t["dstate"])))[2]
+    assert all(torch.equal(got[n], want[n]) for n in want)
+    x = torch.randn(2, 50, 6 * 64, device="cuda").bfloat16().requires_grad_()
+    dout = torch.randn(2, 50, 6 * 64, device="cuda").bfloat16()
+    grads = [torch.autograd.grad(ll.lite_la_qk_norm_rope(x, 3, 2, d=64), x, g)[0] for g in (dout, odd(dout))]
+    assert torch.equal(*grads)
