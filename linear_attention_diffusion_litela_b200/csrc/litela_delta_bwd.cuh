@@ -497,7 +497,10 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
   }
   int s, n0;
   DeltaSeq sq;
-  if (!delta_find(a, slot, lane, s, sq, n0)) return;
+  if (!delta_find(a, slot, lane, s, sq, n0)) {
+    pdl_wait_primary();   // (a grid that is all such blocks may not end before litela_delta_back)
+    return;
+  }
   const int len = min(kChunk, sq.len - n0);
   const uint32_t base = smem_u32(smem);
 

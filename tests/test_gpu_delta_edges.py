@@ -146,3 +146,13 @@ def test_incoming_gradients_off_the_alignment():
     dout = torch.randn(2, 50, 6 * 64, device="cuda").bfloat16()
     grads = [torch.autograd.grad(ll.lite_la_qk_norm_rope(x, 3, 2, d=64), x, g)[0] for g in (dout, odd(dout))]
     assert torch.equal(*grads)
+
+
+def test_gradient_of_sequences_without_tokens():
+    """Rows, but none of them a sequence's: the state's gradient passes through, the rows' are zero"""
+    t = make([0, 0], True, 1, 2, 64, True)
+    for n in ("q", "k", "v", "g", "beta", "dout"):
+        t[n] = torch.ones((1, 200) + t[n].shape[2:], dtype=t[n].dtype, device="cuda")
+    _, state, grads = autograd(t)
+    assert torch.equal(state, t["state_in"]) and torch.equal(grads["state_in"], t["dstate"])
+    assert not any(grads[n].any() for n in ("q", "k", "v", "g", "beta"))
