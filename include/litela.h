@@ -309,7 +309,7 @@ size_t lite_la_gated_delta_workspace_bytes(int B, int N, int Hk, int Hv, int d, 
 
 /* The forward of a training step: lite_la_gated_delta_fwd that also keeps what its gradient needs in
  * `saved`, device memory of lite_la_gated_delta_saved_bytes(), 16-byte aligned (per 64 tokens and
- * value head: 66 KB + 8 d^2 + 256 d bytes).  It needs no workspace.
+ * value head: 98 KB + 8 d^2 + 256 d bytes).  It needs no workspace.
  *
  * lite_la_gated_delta_bwd: the gradients of sum(dout * out) + sum(dstate_out * state_out).  args
  * are the forward's (out and its states are not used), saved is what it left; workspace:

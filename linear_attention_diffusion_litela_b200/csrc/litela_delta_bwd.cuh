@@ -68,7 +68,7 @@ struct BackCfg {
   static constexpr uint32_t kOffImage = kKQ + (kFactorBytes + 1023) / 1024 * 1024;
   static constexpr uint32_t kOffFac = kOffImage - kFactorBytes;
   static constexpr uint32_t kZTile = 64 * 128;                    // do and Z's three terms, two tiles
-  static constexpr uint32_t kOffZ = kOffImage + 2 * kImgHalf;
+  static constexpr uint32_t kOffZ = kOffImage + 2 * kImgTerm;
   static constexpr uint32_t kStage = (kOffZ + 2 * kZTile + 1023) / 1024 * 1024;
   static constexpr uint32_t kSTile = kD * 128, kRTile = 128 * 128;
   static constexpr uint32_t kOffS = kChainStages * kStage;
@@ -108,7 +108,7 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
   const long long slot0 = delta_slot0(a, s, sq);
   const uint8_t* blocks = prep + (slot0 * a.Hv + h) * (long long)kPrepSaveBytes + kPrepFactors;
   const long long block_step = (long long)a.Hv * kPrepSaveBytes;
-  constexpr uint32_t kBlock = kFactorBytes + 2 * kImgHalf;
+  constexpr uint32_t kBlock = kFactorBytes + 2 * kImgTerm;
 
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
@@ -337,7 +337,7 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
           umma(tmem + Cfg::kX2, imgdesc + off + ks * 128, zdesc + off + ks * 128, idesc_z, ks > 0);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          umma(tmem + Cfg::kX2, imgdesc + off + kImgHalf / 16 + ks * 128, zdesc + off + ks * 128, idesc_3, 1u);
+          umma(tmem + Cfg::kX2, imgdesc + off + kImgTerm / 16 + ks * 128, zdesc + off + ks * 128, idesc_3, 1u);
         umma_commit(&done[1]);
       }
       if (lane == 0) {

@@ -15,14 +15,12 @@
 // gradient of beta, where beta may be 0.)
 //
 // Precision.  States are fp32 and stay in registers.  An fp32 operand of a tensor-core product is
-// entered as two or three bf16 terms (each the rounding of what the ones before it leave: 2^-17 and
-// 2^-25 relative) whose products are summed in fp32.  U, of which the state is a sum, takes three
-// (with two the state was 2.4e-6 off), R three and X two by all but the smallest products (with two
-// and two the state of slowly decaying heads was 1.2e-6 off, d = 128, 0.8e-6 now), S0 three: the third
-// costs the chain 5 % (the product's time does not change), and without it dg of a few tokens was up to
-// 9.6e-6 off.  What is left, up to 2e-6 of a state at d = 32, are X's two.  K, Q and V are bf16 already.  G is
-// summed in fp64: differences of large sums of decays would lose in
-// fp32.
+// entered in three bf16 terms (each the rounding of what the ones before it leave: 2^-9, 2^-17 and 2^-25
+// relative), all products of terms that reach 2^-25 of the first, summed in fp32: states are 1 to 3e-7 off
+// against 64 bits, as with plain fp32 operations.  With two terms of X, P T and of the blocks that X is made of
+// they were up to 2e-6 off (d = 32); the third costs the blocks a fifth (16384 tokens, 32 heads of 128: 209 ->
+// 249 us) and the chain 6 % (532 -> 564).  K, Q and V are bf16 already.  G is summed in fp64: differences
+// of large sums of decays would lose in fp32.
 //
 // A NaN or an infinity must not reach the tokens before its own: 0 * NaN inside a product would
 // carry it there.  So non-finite entries are taken out of L, P, beta and R, the first token that had one
@@ -31,6 +29,7 @@
 
 #include <cuda_bf16.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "f32x2.cuh"
 #include "litela_delta.cuh"
@@ -41,18 +40,18 @@ namespace litela {
 constexpr int kChunk = 64;
 
 // One chunk and value head's prepared block: X^T and (P T)^T as images of tcgen05 A operands (MN-major:
-// 64 rows x 128 columns bf16 in two blocks of 64 columns, 128-byte swizzle), the hi terms, the lo
-// terms, then per-token factors.  The columns (the product's rows, TMEM lanes) hold 16 rows of X,
-// the same 16 rows of P T, the next 16 rows of X and so on, as do the rows of K and Q in the chain's
-// tile: every warp's quarter of the lanes then has 16 tokens of either kind.
-constexpr uint32_t kImgHalf = 128 * 128;
+// 64 rows x 128 columns bf16 in two blocks of 64 columns, 128-byte swizzle), one image for each of
+// the three bf16 terms, then per-token factors.  The columns (the product's rows, TMEM lanes) hold 16 rows
+// of X, the same 16 rows of P T, the next 16 rows of X and so on, as do the rows of K and Q in the
+// chain's tile: every warp's quarter of the lanes then has 16 tokens of either kind.
+constexpr uint32_t kImgTerm = 128 * 128;   // one of them
 __host__ __device__ constexpr int lane_of(int token) { return 32 * (token / 16) + token % 16; }
-constexpr uint32_t kPrepFactors = 2 * kImgHalf;
+constexpr uint32_t kPrepFactors = 3 * kImgTerm;
 constexpr uint32_t kFactorBytes = 2304;
 constexpr uint32_t kPrepBytes = kPrepFactors + kFactorBytes;
 // A training step's block has a second image behind it, X and P T not transposed: rows are tokens i,
 // columns as above for tokens j, (i, j) of X and of P T (the gradient's products take X^T and (P T)^T)
-constexpr uint32_t kPrepSaveBytes = kPrepBytes + 2 * kImgHalf;
+constexpr uint32_t kPrepSaveBytes = kPrepBytes + 3 * kImgTerm;
 // fp32 at kPrepFactors: e^G [64], e^(G_C - G) [64] (0 behind the end), beta [64] (0 behind the
 // end), then e^G_C and (int32) the first token of the chunk with a non-finite L, P or beta, or 64
 constexpr int kFacDecay = 0, kFacToEnd = 64, kFacBeta = 128, kFacChunk = 192, kFacBad = 193;
@@ -105,12 +104,25 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint3
   hi = pack_bf16(a, b);
   lo = pack_bf16(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
 }
-// 16 x 16 accumulators (two 16 x 8 tiles) as an A operand, hi and lo
-__device__ __forceinline__ void split_frag(const float (*c)[4], uint32_t* hi, uint32_t* lo) {
-  split_bf16(c[0][0], c[0][1], hi[0], lo[0]);
-  split_bf16(c[0][2], c[0][3], hi[1], lo[1]);
-  split_bf16(c[1][0], c[1][1], hi[2], lo[2]);
-  split_bf16(c[1][2], c[1][3], hi[3], lo[3]);
+// the next bf16 term of a pair, which it leaves
+__device__ __forceinline__ uint32_t next_term(F2& y, bool last) {
+  const float2 z = f2_out(y);
+  const uint32_t w = pack_bf16(z.x, z.y);
+  if (!last) y = f2_fma(f2_bf16(w), f2(-1.f, -1.f), y);
+  return w;
+}
+// (a, b) in three terms, w[0], w[step], w[2 step]
+__device__ __forceinline__ void split_terms(float a, float b, uint32_t* w, int step) {
+  F2 y = f2(a, b);
+#pragma unroll
+  for (int t = 0; t < 3; ++t) w[t * step] = next_term(y, t == 2);
+}
+// 16 x 16 accumulators (two 16 x 8 tiles) as an A operand in three terms
+__device__ __forceinline__ void split_frag(const float (*c)[4], uint32_t (*a)[4]) {
+  split_terms(c[0][0], c[0][1], &a[0][0], 4);
+  split_terms(c[0][2], c[0][3], &a[0][1], 4);
+  split_terms(c[1][0], c[1][1], &a[0][2], 4);
+  split_terms(c[1][2], c[1][3], &a[0][3], 4);
 }
 // byte offset of bf16 element (row, column < 64) in a tile of 128-byte rows, 128-byte swizzle
 __device__ __forceinline__ uint32_t sw128(int row, int col) {
@@ -126,14 +138,16 @@ __device__ __forceinline__ uint32_t sw128(int row, int col) {
 //   1. K and Q by cp.async; G, and D's factors.  With m the first row of r's block of 16 and c
 //      before it, D_rc = e^(G_r - G_m) e^(G_m - G_c): 160 exponentials instead of 1536, both
 //      factors at most 1.
-//   2. K K^T and Q K^T up to the diagonal, to shared memory in fp32; there D makes them L (bf16 pairs;
-//      the diagonal blocks stay in fp32) and P.
+//   2. K K^T and Q K^T up to the diagonal, to shared memory in fp32; there D makes them L and P.
 //   3. X's diagonal blocks by substitution, one lane a column: x_i = L_ij - sum_m<i L_im beta_m x_m.
 //   4. The blocks below them, block column j by one warp:
 //      X_ij = (I - X_ii diag(beta)) (L_ij - sum_m L_im diag(beta) X_mj),
 //      computed transposed, so that a product's accumulators are the next one's left operand in
-//      registers, and the image's values.
+//      registers.  X^T takes the places above L's diagonal, which are free.
 //   5. P T = P - (P diag(beta)) X.
+//   6. The images' terms, from X's fp32 values and P T's accumulators.
+// Operands are fp32 in shared memory (as much as two bf16 terms would take) and cut into three terms in
+// registers.
 // A chunk is a chain of latencies, a fetch of instructions being one of them: a CTA runs through its
 // code once.  So loops stay rolled, and three CTAs an SM overlap.
 constexpr int kPrepThreads = 256;
@@ -149,7 +163,7 @@ template <int kD>
 struct PrepCfg {
   static constexpr int kLd = kD + 8;   // row of K and Q, padded
   static constexpr uint32_t kRows = 2 * kChunk * kLd * 2;
-  static constexpr uint32_t kUnion = kRows > 2 * kImgHalf ? kRows : 2 * kImgHalf;   // K, Q; then the image
+  static constexpr uint32_t kUnion = kRows > 2 * kImgTerm ? kRows : 2 * kImgTerm;   // K, Q; then the image
   static constexpr uint32_t kOffL = kUnion;                                  // L, fp32
   static constexpr uint32_t kOffP = kOffL + kChunk * kPrepLd * 4;
   static constexpr uint32_t kOffG = kOffP + kChunk * kPrepLd * 4;
@@ -177,6 +191,12 @@ __device__ __forceinline__ void stmatrix_x4(uint32_t addr, const uint32_t* r) {
                "r"(r[2]), "r"(r[3])
                : "memory");
 }
+__device__ __forceinline__ void stmatrix_x2(uint32_t addr, uint32_t r0, uint32_t r1) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x2.shared.b16 [%0], {%1, %2};" ::"r"(addr), "r"(r0), "r"(r1) : "memory");
+}
+__device__ __forceinline__ void stmatrix_x2_t(uint32_t addr, uint32_t r0, uint32_t r1) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1, %2};" ::"r"(addr), "r"(r0), "r"(r1) : "memory");
+}
 __device__ __forceinline__ void stmatrix_x4_t(uint32_t addr, const uint32_t* r) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3])
@@ -202,17 +222,36 @@ __device__ __forceinline__ void mma_halves(float (*d)[4], const uint32_t* a, con
   for (int n = 0; n < kTiles; ++n) sm100::mma_16816(d[n], a, b[n]);
 }
 
+// d[n] + small[n] += A B[n], fp32 operands in three terms each, all products that reach 2^-25 of the first;
+// two accumulators, so that a product waits for every other one before it only
+template <int kTiles>
+__device__ __forceinline__ void mma_terms(float (*d)[4], float (*small)[4], const uint32_t (*a)[4], const uint32_t (*b)[3][2]) {
+  auto all = [&](float (*to)[4], int ta, int tb) {
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n) sm100::mma_16816(to[n], a[ta], b[n][tb]);
+  };
+  all(small, 2, 0), all(d, 1, 0), all(small, 1, 1), all(d, 0, 1), all(small, 0, 2), all(d, 0, 0);
+}
+// a B operand tile (16 x 8) in three terms: B[k][n] = src[n * kPrepLd + k]
+__device__ __forceinline__ void prep_tile(const float* src, int lane, uint32_t (*b)[2]) {
+  const float* p = src + (lane >> 2) * kPrepLd + (lane & 3) * 2;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 v = *reinterpret_cast<const float2*>(p + 8 * i);
+    split_terms(v.x, v.y, &b[0][i], 2);
+  }
+}
+
 template <int kD, bool kSave>
 __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const DeltaArgs a, uint8_t* __restrict__ prep) {
   using namespace sm100;
   using Cfg = PrepCfg<kD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-  // the image, hi and lo; until (P T)^T is made L's pair stands in its places, (row, column) of L at
-  // img_off(row, column, 1)
-  uint8_t *Ih = smem, *Il = smem + kImgHalf;
-  float* Lf = reinterpret_cast<float*>(smem + Cfg::kOffL);
+  float* Lf = reinterpret_cast<float*>(smem + Cfg::kOffL);   // L; X^T with and above its diagonal
   float* Pf = reinterpret_cast<float*>(smem + Cfg::kOffP);
+  // the image's terms, the third one in P's place
+  auto image = [&](int t) { return t < 2 ? smem + t * kImgTerm : smem + Cfg::kOffP; };
   double* G = reinterpret_cast<double*>(smem + Cfg::kOffG);
   float* beta = reinterpret_cast<float*>(smem + Cfg::kOffBeta);
   float* rowf = reinterpret_cast<float*>(smem + Cfg::kOffRow);
@@ -341,9 +380,6 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
     const float2 rr = rel[r];
     const float4* cf = reinterpret_cast<const float4*>(colf + rb * 48 + c0);
     float4 *ls = reinterpret_cast<float4*>(Lf + r * kPrepLd + c0), *ps = reinterpret_cast<float4*>(Pf + r * kPrepLd + c0);
-    // L's pair in the image: block cb of 16 columns stands 64 bytes (before the swizzle) or a block on
-    uint8_t* image = Ih + r * 128 + (c0 & 4) * 2;
-    const uint32_t chunk = (uint32_t)(((2 + (c0 >> 3)) ^ r) & 7) << 4;
     auto scaled = [&](float4* src, const float* f, int real = 4) {   // the first `real` columns, zeros
       const float4 x = *src;
       float4 y = make_float4(real > 0 ? x.x * f[0] : 0.f, real > 1 ? x.y * f[1] : 0.f, real > 2 ? x.z * f[2] : 0.f,
@@ -359,13 +395,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
     for (int cb = 0; cb < rb; ++cb) {
       const float4 c4 = cf[4 * cb];
       float f[4] = {rf * c4.x, rf * c4.y, rf * c4.z, rf * c4.w};
-      const float4 y = scaled(ls + 4 * cb, f);
-      uint32_t hi[2], lo[2];
-      split_bf16(y.x, y.y, hi[0], lo[0]);
-      split_bf16(y.z, y.w, hi[1], lo[1]);
-      uint8_t* dst = image + (cb >> 1) * kImgBlock + (chunk ^ ((cb & 1) << 6));
-      *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(dst + kImgHalf) = make_uint2(lo[0], lo[1]);
+      ls[4 * cb] = scaled(ls + 4 * cb, f);
 #pragma unroll
       for (int e = 0; e < 4; ++e) f[e] *= a.scale;
       ps[4 * cb] = scaled(ps + 4 * cb, f);
@@ -383,22 +413,12 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
     ps[4 * rb] = scaled(ps + 4 * rb, f, below + 1);
   }
   if (first < kChunk) atomicMin(bad, first);
-  // the blocks of X^T (P T) left of its diagonal blocks are zero: six of 16 rows x 32 bytes
-  auto clear = [&](int p) {
-    if (tid < 192) {
-      const int blk = tid >> 5, rb = blk < 1 ? 1 : blk < 3 ? 2 : 3, cb = blk - (rb == 1 ? 0 : rb == 2 ? 1 : 3);
-      const uint32_t o = img_off(16 * rb + ((lane >> 1) & 15), 16 * cb + (lane & 1) * 8, p);
-      *reinterpret_cast<uint4*>(Ih + o) = make_uint4(0u, 0u, 0u, 0u);
-      *reinterpret_cast<uint4*>(Il + o) = make_uint4(0u, 0u, 0u, 0u);
-    }
-  };
-  clear(0);
   __syncthreads();
 
-  // X's diagonal block w: lane j solves for column j
+  // X's diagonal block w: lane j solves for column j; it takes L's place, transposed
   if (w < 4 && lane < 16) {
     float x[16], bx[16];
-    const float* blk = Lf + 16 * w * kPrepLd + 16 * w;
+    float* blk = Lf + 16 * w * kPrepLd + 16 * w;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float v[4] = {blk[i * kPrepLd + lane], 0.f, 0.f, 0.f};
@@ -413,180 +433,188 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
       x[i] = i > lane ? (v[0] + v[1]) + (v[2] + v[3]) : 0.f;
       bx[i] = beta[16 * w + i] * x[i];
     }
+    __syncwarp(0xffffu);
 #pragma unroll
-    for (int i = 0; i < 16; i += 8) {
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) split_bf16(x[i + 2 * q], x[i + 2 * q + 1], hi[q], lo[q]);
-      const uint32_t o = img_off(16 * w + lane, 16 * w + i, 0);
-      *reinterpret_cast<uint4*>(Ih + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(Il + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    }
+    for (int i = 0; i < 16; i += 4)
+      *reinterpret_cast<float4*>(blk + lane * kPrepLd + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
   }
   __syncthreads();
 
-  // the blocks below them, block column w
+  // the blocks below them, block column w; X_iw goes to the free block (w, i), transposed
   if (w < 3) {
-    uint32_t yh[3][4], yl[3][4];   // -(diag(beta) X)^T of the block rows w, w + 1, w + 2 (zero: not made yet)
+    uint32_t y[3][3][4];   // -(diag(beta) X)^T of the block rows w, w + 1, w + 2 (zero: not made yet), by term
 #pragma unroll
-    for (int m = 0; m < 3; ++m)
+    for (int m = 1; m < 3; ++m)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) yh[m][q] = yl[m][q] = 0u;
+      for (int q = 0; q < 12; ++q) y[m][q / 4][q % 4] = 0u;
+    float* own = Lf + (16 * w + gr) * kPrepLd + t2;   // rows of X^T: 8 q; columns: 16 times a block, 8 n
     {
-      float y[2][4];
+      float v[2][4];
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const int i = 16 * w + 8 * n + t2;
-          const uint32_t o = img_off(16 * w + gr + q * 8, i, 0);
-          const uint32_t hi = *reinterpret_cast<const uint32_t*>(Ih + o), lo = *reinterpret_cast<const uint32_t*>(Il + o);
-          const float2 v = f2_out(f2_add(f2_bf16(hi), f2_bf16(lo)));
-          y[n][2 * q] = -beta[i] * v.x;
-          y[n][2 * q + 1] = -beta[i + 1] * v.y;
+          const int i = 16 * w + 8 * n;
+          const float2 x = *reinterpret_cast<const float2*>(own + 8 * q * kPrepLd + i);
+          v[n][2 * q] = -beta[i + t2] * x.x;
+          v[n][2 * q + 1] = -beta[i + t2 + 1] * x.y;
         }
-      split_frag(y, yh[0], yl[0]);
+      split_frag(v, y[0]);
     }
-    // matrices by lane / 8: hi of 0..7 and 8..15 of the K dimension, then lo
-    const uint32_t term = smem_u32(smem) + (lane >> 4) * kImgHalf;
-    const int l8 = lane & 7, k8 = ((lane >> 3) & 1) * 8;
 #pragma unroll 1
     for (int i = w + 1; i < 4; ++i) {   // X's block row i
-      float x[2][4];
-      {   // L_ij transposed: matrices by lane / 8: rows 0..7 of L, columns 0..7 and 8..15; rows 8..15
-        uint32_t hi[4], lo[4];
-        const uint32_t o = smem_u32(smem) + img_off(16 * i + l8 + (lane >> 4) * 8, 16 * w + k8, 1);
-        ldmatrix_x4_t(hi, o);
-        ldmatrix_x4_t(lo, o + kImgHalf);
+      float x[2][4], xs[2][4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float2 v = f2_out(f2_add(f2_bf16(hi[q]), f2_bf16(lo[q])));
-          x[q >> 1][2 * (q & 1)] = v.x;
-          x[q >> 1][2 * (q & 1) + 1] = v.y;
-        }
-      }
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)   // L_iw transposed
+          xs[n][e] = 0.f, x[n][e] = Lf[(16 * i + 8 * n + t2 + (e & 1)) * kPrepLd + 16 * w + gr + 8 * (e >> 1)];
 #pragma unroll
       for (int m = 0; m < 3; ++m)   // sum over X's block rows w + m before i
         if (w + m < i) {
-          uint32_t b[2][4];
+          uint32_t b[2][3][2];
 #pragma unroll
-          for (int n = 0; n < 2; ++n) ldmatrix_x4(b[n], term + img_off(16 * i + 8 * n + l8, 16 * (w + m) + k8, 1));
-          mma_pairs<2>(x, yh[m], yl[m], b);
+          for (int n = 0; n < 2; ++n) prep_tile(Lf + (16 * i + 8 * n) * kPrepLd + 16 * (w + m), lane, b[n]);
+          mma_terms<2>(x, xs, y[m], b);
         }
       float br[2][4];
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) br[n][q] = -beta[16 * i + 8 * n + t2 + (q & 1)] * x[n][q];
-      uint32_t rh[4], rl[4];
-      split_frag(br, rh, rl);
-      uint32_t b[2][4];   // X_ii^T stands as rows of the K dimension
+        for (int q = 0; q < 4; ++q) {
+          x[n][q] += xs[n][q], xs[n][q] = 0.f;
+          br[n][q] = -beta[16 * i + 8 * n + t2 + (q & 1)] * x[n][q];
+        }
+      uint32_t r[3][4], b[2][3][2];
+      split_frag(br, r);
 #pragma unroll
-      for (int n = 0; n < 2; ++n) ldmatrix_x4_t(b[n], term + img_off(16 * i + l8 + k8, 16 * i + 8 * n, 0));
-      mma_pairs<2>(x, rh, rl, b);
-      split_frag(x, rh, rl);
+      for (int n = 0; n < 2; ++n)   // X_ii^T stands as rows of the K dimension
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t o = img_off(16 * w + gr + (q & 1) * 8, 16 * i + t2 + (q >> 1) * 8, 0);
-        *reinterpret_cast<uint32_t*>(Ih + o) = rh[q];
-        *reinterpret_cast<uint32_t*>(Il + o) = rl[q];
-      }
+        for (int h = 0; h < 2; ++h) {
+          const float* v = Lf + (16 * i + t2 + 8 * h) * kPrepLd + 16 * i + 8 * n + gr;
+          split_terms(v[0], v[kPrepLd], &b[n][0][h], 2);
+        }
+      mma_terms<2>(x, xs, r, b);
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) x[n][q] *= -beta[16 * i + 8 * n + t2 + (q & 1)];
-      split_frag(x, rh, rl);
+        for (int q = 0; q < 2; ++q) {
+          x[n][2 * q] += xs[n][2 * q], x[n][2 * q + 1] += xs[n][2 * q + 1];
+          *reinterpret_cast<float2*>(own + 8 * q * kPrepLd + 16 * i + 8 * n) = make_float2(x[n][2 * q], x[n][2 * q + 1]);
+          x[n][2 * q] *= -beta[16 * i + 8 * n + t2];
+          x[n][2 * q + 1] *= -beta[16 * i + 8 * n + t2 + 1];
+        }
+      split_frag(x, r);
 #pragma unroll
       for (int m = 1; m < 3; ++m)
         if (i == w + m)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) yh[m][q] = rh[q], yl[m][q] = rl[q];
+          for (int q = 0; q < 12; ++q) y[m][q / 4][q % 4] = r[q / 4][q % 4];
     }
   }
   __syncthreads();
 
-  // P T = P - (P diag(beta)) X: rows 16 rb .., the warp's rb + 1 tiles of 8 columns of the 2 rb + 2
-  clear(1);   // (all of L has been read)
-  {
-    const int rb = w >> 1, tile0 = (w & 1) * (rb + 1), r0 = 16 * rb + gr;
-    const uint32_t term = smem_u32(smem) + (lane >> 4) * kImgHalf;
-    const int l8 = lane & 7, k8 = ((lane >> 3) & 1) * 8;
-    const uint32_t xrow = term + img_off(8 * tile0 + l8, k8, 0);   // X^T's row; block k: 64 bytes (xor), a block on
-    float acc[4][4];
+  // P T = P - (P diag(beta)) X in blocks (row, column) of 16 x 16, row - column + 1 products each: a
+  // warp has one block, the last two warps have two on the diagonal (2 blocks apart); four products at most
+  constexpr uint32_t kBlockRow = 0x10321323u, kBlockCol = 0x10210100u;   // by warp, 4 bits each
+  const int rb0 = kBlockRow >> (4 * w) & 15, cb0 = kBlockCol >> (4 * w) & 15, blocks = w < 6 ? 1 : 2;
+  float acc[2][2][4];
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
+  for (int u = 0; u < 2; ++u)
+    if (u < blocks) {
+      const int rb = rb0 + 2 * u, cb = cb0 + 2 * u;
+      const float* prow = Pf + (16 * rb + gr) * kPrepLd + t2;
+      float small[2][4];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        float2 v = make_float2(0.f, 0.f);
-        if (n <= rb) v = *reinterpret_cast<const float2*>(Pf + (r0 + 8 * q) * kPrepLd + 8 * (tile0 + n) + t2);
-        acc[n][2 * q] = v.x;
-        acc[n][2 * q + 1] = v.y;
-      }
-#pragma unroll 1
-    for (int k = 0; k <= rb; ++k) {
-      uint32_t ph[4], pl[4];
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int c = 16 * k + t2 + (q >> 1) * 8;
-        const float2 v = *reinterpret_cast<const float2*>(Pf + (r0 + (q & 1) * 8) * kPrepLd + c);
-        const float2 bc = *reinterpret_cast<const float2*>(beta + c);
-        split_bf16(-bc.x * v.x, -bc.y * v.y, ph[q], pl[q]);
-      }
-      if (tile0 / 2 <= k) {   // (X^T is zero in the tiles of four that it does not reach, or they are not kept)
-        uint32_t b[4][4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) ldmatrix_x4(b[n], (xrow ^ ((k & 1) << 6)) + (k >> 1) * kImgBlock + n * 1024);
-        mma_pairs<4>(acc, ph, pl, b);
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-      if (n <= rb) {   // matrices by lane / 8: hi of rows 0..7 and 8..15, lo
-        uint32_t v[4];
-        split_bf16(acc[n][0], acc[n][1], v[0], v[2]);
-        split_bf16(acc[n][2], acc[n][3], v[1], v[3]);
-        stmatrix_x4_t((((xrow ^ 32) ^ ((rb & 1) << 6)) + (rb >> 1) * kImgBlock) + n * 1024, v);
-      }
-    if constexpr (kSave) {   // the second image, hi in L's place and lo in P's
-      __syncthreads();       // (P has been read)
-      const uint32_t term2 = smem_u32((lane >> 4) ? Pf : Lf);
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-        if (n <= rb) {
-          uint32_t v[4];
-          split_bf16(acc[n][0], acc[n][1], v[0], v[2]);
-          split_bf16(acc[n][2], acc[n][3], v[1], v[3]);
-          stmatrix_x4(term2 + img_off(16 * rb + k8 + l8, 8 * (tile0 + n), 1), v);
+        for (int q = 0; q < 2; ++q) {
+          const float2 v = *reinterpret_cast<const float2*>(prow + 8 * q * kPrepLd + 16 * cb + 8 * n);
+          acc[u][n][2 * q] = v.x, acc[u][n][2 * q + 1] = v.y;
+          small[n][2 * q] = small[n][2 * q + 1] = 0.f;
         }
-      // X: 8 x 8 blocks (rows 8 ib, columns 8 jb) from the first image, transposed; lane / 8: hi of jb
-      // and jb + 1, lo of them
 #pragma unroll 1
-      for (int i = w; i < 32; i += 8) {
-        const int ib = i >> 2, jb = (i & 3) * 2 + ((lane >> 3) & 1);
-        uint32_t v[4];
-        ldmatrix_x4_t(v, term + img_off(8 * jb + l8, 8 * ib, 0));
-        stmatrix_x4(term2 + img_off(8 * ib + l8, 8 * jb, 0), v);
+      for (int k = cb; k <= rb; ++k) {
+        uint32_t p[3][4], b[2][3][2];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c = 16 * k + (q >> 1) * 8;
+          const float2 v = *reinterpret_cast<const float2*>(prow + (q & 1) * 8 * kPrepLd + c);
+          const float2 bc = *reinterpret_cast<const float2*>(beta + c + t2);
+          split_terms(-bc.x * v.x, -bc.y * v.y, &p[0][q], 4);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) prep_tile(Lf + (16 * cb + 8 * e) * kPrepLd + 16 * k, lane, b[e]);
+        mma_terms<2>(acc[u], small, p, b);
       }
-      // right of its diagonal blocks P T is zero
-      if (tid < 192) {
-        const int blk = tid >> 5, cb = blk < 1 ? 1 : blk < 3 ? 2 : 3, r = blk - (cb == 1 ? 0 : cb == 2 ? 1 : 3);
-        const uint32_t o = img_off(16 * r + ((lane >> 1) & 15), 16 * cb + (lane & 1) * 8, 1);
-        *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(Lf) + o) = make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(Pf) + o) = make_uint4(0u, 0u, 0u, 0u);
-      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[u][n][q] += small[n][q];
     }
-  }
+  __syncthreads();   // P has been read
+
+  // An image's three terms into shared memory: X's from its fp32 values, P T's from the accumulators.
+  // kSecond: not transposed (a training step's)
+  const int l8 = lane & 7, k8 = ((lane >> 3) & 1) * 8;
+  auto write_image = [&](auto second) {
+    constexpr bool kSecond = decltype(second)::value;
+#pragma unroll 1
+    for (int i = tid; i < kChunk * 8; i += kPrepThreads) {   // a row and 8 of its columns
+      const int row = i & 63, c0 = (i >> 6) * 8;
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+      if (kSecond ? (c0 >> 4) <= (row >> 4) : (c0 >> 4) >= (row >> 4))
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = kSecond ? Lf[(c0 + e) * kPrepLd + row] : Lf[row * kPrepLd + c0 + e];
+      uint32_t t[3][4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) split_terms(v[2 * q], v[2 * q + 1], &t[0][q], 4);
+#pragma unroll
+      for (int h = 0; h < 3; ++h)
+        *reinterpret_cast<uint4*>(image(h) + img_off(row, c0, 0)) = make_uint4(t[h][0], t[h][1], t[h][2], t[h][3]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i / 2 < blocks) {   // matrices by lane / 8: the first term of rows 0..7 and 8..15, the second
+        const float* x = acc[i / 2][i % 2];
+        uint32_t v[3][2];
+        split_terms(x[0], x[1], &v[0][0], 2);
+        split_terms(x[2], x[3], &v[0][1], 2);
+        const int r = 16 * (rb0 + i / 2 * 2), c = 16 * (cb0 + i / 2 * 2) + 8 * (i % 2);
+        const uint32_t o = kSecond ? img_off(r + k8 + l8, c, 1) : img_off(c + l8, r + k8, 1);
+        const uint32_t first = smem_u32(image(lane >> 4)) + o, third = smem_u32(image(2)) + o;
+        if (kSecond) {
+          stmatrix_x4(first, &v[0][0]);
+          stmatrix_x2(third, v[2][0], v[2][1]);
+        } else {
+          stmatrix_x4_t(first, &v[0][0]);
+          stmatrix_x2_t(third, v[2][0], v[2][1]);
+        }
+      }
+    // the blocks of (P T)^T left of its diagonal blocks are zero (of P T, right of them): six of 16 rows x 32 bytes
+    if (tid < 192) {
+      const int blk = tid >> 5, hi = blk < 1 ? 1 : blk < 3 ? 2 : 3, lo = blk - (hi == 1 ? 0 : hi == 2 ? 1 : 3);
+      const uint32_t o = img_off(16 * (kSecond ? lo : hi) + ((lane >> 1) & 15), 16 * (kSecond ? hi : lo) + (lane & 1) * 8, 1);
+#pragma unroll
+      for (int h = 0; h < 3; ++h) *reinterpret_cast<uint4*>(image(h) + o) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+      uint8_t* to = dst + (kSecond ? kPrepBytes : 0u);
+      bulk_store(to, image(0), 2 * kImgTerm);
+      bulk_store(to + 2 * kImgTerm, image(2), kImgTerm);
+      bulk_commit_group();
+      bulk_wait_group_read<0>();
+    }
+  };
   if (tid == 0) reinterpret_cast<int*>(dst + kPrepFactors)[kFacBad] = *bad;
-  fence_proxy_async_smem();
-  __syncthreads();
-  if (tid == 0) {
-    bulk_store(dst, smem, 2 * kImgHalf);
-    if (kSave) {
-      bulk_store(dst + kPrepBytes, Lf, kImgHalf);
-      bulk_store(dst + kPrepBytes + kImgHalf, Pf, kImgHalf);
-    }
-    bulk_commit_group();
-    bulk_wait_group_read<0>();
+  write_image(std::false_type{});
+  if constexpr (kSave) {
+    __syncthreads();   // (the first image has been taken)
+    write_image(std::true_type{});
   }
 }
 
@@ -699,13 +727,6 @@ __device__ __forceinline__ void chain_frag(uint32_t taddr, int c, F2* x) {
   }
 }
 
-// the next bf16 term of a pair, which it leaves
-__device__ __forceinline__ uint32_t next_term(F2& y, bool last) {
-  const float2 z = f2_out(y);
-  const uint32_t w = pack_bf16(z.x, z.y);
-  if (!last) y = f2_fma(f2_bf16(w), f2(-1.f, -1.f), y);
-  return w;
-}
 // Into a B operand's tiles: the thread's kN values (pairs) of a row, columns c .. c + kN - 1, in kTerms
 // bf16 terms
 template <int kTerms>
@@ -927,6 +948,7 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, const De
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, 96, false, true);
     constexpr uint32_t idesc_r = idesc_bf16_f32(128, 96, true, true);    // three terms
     constexpr uint32_t idesc_2 = idesc_bf16_f32(128, 64, true, true);    // two terms
+    constexpr uint32_t idesc_1 = idesc_bf16_f32(128, 32, true, true);    // one
     // descriptors of each operand's first 16 of the K dimension
     const Desc sdesc = desc_halves(smem_u32(stile), Cfg::kSTile, 1024, kSwizzle128B);
     const Desc rdesc = desc_halves(smem_u32(rtile), Cfg::kRTile, 1024, kSwizzle128B);
@@ -962,13 +984,16 @@ litela_delta_chain(const DeltaArgs a, const uint8_t* __restrict__ prep, const De
       bar_sync(kBarR, kBarThreads);
       tc_fence_after_sync();
       if (ok && lane == 0) {
-        // hi by all three terms of R, lo by the first two
+        // X's and P T's first term by all three of R, the second by two, the third by one
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
           umma(tmem + Cfg::kX2, imgdesc + off + ks * 128, rdesc + ks * 128, idesc_r, ks > 0);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          umma(tmem + Cfg::kX2, imgdesc + off + kImgHalf / 16 + ks * 128, rdesc + ks * 128, idesc_2, 1u);
+          umma(tmem + Cfg::kX2, imgdesc + off + kImgTerm / 16 + ks * 128, rdesc + ks * 128, idesc_2, 1u);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          umma(tmem + Cfg::kX2, imgdesc + off + 2 * kImgTerm / 16 + ks * 128, rdesc + ks * 128, idesc_1, 1u);
         umma_commit(&done[1]);
       }
       __syncwarp();
