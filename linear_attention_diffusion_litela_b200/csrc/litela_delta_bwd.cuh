@@ -36,10 +36,16 @@ struct DeltaGrads {
   float* dstate_in;                // or null
   // between the two kernels, per chunk slot and value head
   uint8_t* gstates;                // G' as DeltaSaved's states
-  uint8_t* y;                      // [d / 32] tiles of 64 rows of 128 bytes, 128-byte swizzle: bf16 pair
+  float* y;                        // [d / 32] tiles of 64 rows of 32 columns, placed by y_off
   float* rows;                     // [d / 32][2][2][64]: w . W and b of half of 32 columns
   float* ends;                     // [d / 32][8]: shares of <S0, G'>
 };
+
+// place of (row, column < 32) in a tile of y, in floats: 16-byte pieces of a row change places with the row, so
+// that eight rows' equal columns lie in different banks
+__device__ __forceinline__ int y_off(int row, int col) {
+  return row * 32 + ((((col >> 2) ^ ((row & 3) << 1) ^ ((row >> 2) & 1)) & 7) << 2) + (col & 3);
+}
 
 __device__ __forceinline__ float sum_warp(float v) {
 #pragma unroll
@@ -55,24 +61,24 @@ __device__ __forceinline__ float sum_warp(float v) {
 //     X3 = [K; Q]^T [-diag(e^G) y; scale diag(e^G) do]
 // Rows (TMEM lanes) of the first two alternate, 16 of K's or X's and 16 of Q's or P T's.  X1's rows of K
 // are used, and of X2 the columns of Z in X's rows and the columns of do in P T's rows, which are the
-// same tokens: w = Z + X2 (T = I - diag(beta) X) and G' = e^G_C G' + X3.  Bound by the chain of its
-// steps as litela_delta_chain: 3.4 us a chunk at d = 128 (2 x 2048 tokens, 16 heads: 108 us).
+// same tokens: w = Z + X2 (T = I - diag(beta) X) and G' = e^G_C G' + X3.  G', Z, y, X and P T in three terms
+// as in litela_delta_chain: dbeta and dstate_in are 2 to 5e-7 off (with two of G', X and P T 1.8 to 2.7e-6
+// and 0.9e-6; the third costs 4 %).  Bound by the chain of its steps: 3.4 us a chunk at d = 128 (2 x 2048
+// tokens, 16 heads: 109 us).
 template <int kD>
 struct BackCfg {
   static constexpr int kBlocks = kD > 64 ? 2 : 1;
-  // of G' in the first product: a third costs the walk 7 % and halves the errors of dbeta and dg of a few
-  // tokens (d = 64: 2.6e-6 -> 1.4e-6, 6e-6 -> 1.6e-6); for d = 128 its tile has no room
-  static constexpr int kTerms = kD > 64 ? 2 : 3;
   static constexpr uint32_t kKQ = kBlocks * 16384;                // per block: 64 rows of K and of Q
-  // the factors and the second image behind them, the image on a 1024-byte boundary
-  static constexpr uint32_t kOffImage = kKQ + (kFactorBytes + 1023) / 1024 * 1024;
-  static constexpr uint32_t kOffFac = kOffImage - kFactorBytes;
+  static constexpr uint32_t kOffFac = kKQ;
   static constexpr uint32_t kZTile = 64 * 128;                    // do and Z's three terms, two tiles
-  static constexpr uint32_t kOffZ = kOffImage + 2 * kImgTerm;
-  static constexpr uint32_t kStage = (kOffZ + 2 * kZTile + 1023) / 1024 * 1024;
+  static constexpr uint32_t kOffZ = kOffFac + (kFactorBytes + 1023) / 1024 * 1024;
+  static constexpr uint32_t kStage = kOffZ + 2 * kZTile;
+  // the second image, three terms: one chunk's at a time (there is no room for two at d = 128), loaded when
+  // the second product of the chunk before is done with it, a product and three steps before its own
+  static constexpr uint32_t kOffImage = kChainStages * kStage;
   static constexpr uint32_t kSTile = kD * 128, kRTile = 128 * 128;
-  static constexpr uint32_t kOffS = kChainStages * kStage;
-  static constexpr uint32_t kOffR = kOffS + (kTerms + 1) / 2 * kSTile;             // y's and do's rows, three terms
+  static constexpr uint32_t kOffS = kOffImage + 3 * kImgTerm;                      // G', three terms
+  static constexpr uint32_t kOffR = kOffS + 2 * kSTile;                            // y's and do's rows, three terms
   static constexpr uint32_t kOffBars = kOffR + 2 * kRTile;
   static constexpr uint32_t kSmemBytes = kOffBars + 256 + 1024;
   static constexpr uint32_t kX1 = 0, kX2 = 96, kX3 = 224, kTmem = 512;
@@ -96,7 +102,8 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
   uint64_t* empty = full + kChainStages;
   uint64_t* done = empty + kChainStages;
   uint64_t* s0full = done + 3;
-  uint64_t* drained = s0full + 1;
+  uint64_t* imgfull = s0full + 1;
+  uint64_t* drained = imgfull + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
@@ -108,7 +115,7 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
   const long long slot0 = delta_slot0(a, s, sq);
   const uint8_t* blocks = prep + (slot0 * a.Hv + h) * (long long)kPrepSaveBytes + kPrepFactors;
   const long long block_step = (long long)a.Hv * kPrepSaveBytes;
-  constexpr uint32_t kBlock = kFactorBytes + 2 * kImgTerm;
+  constexpr uint32_t kBlock = kFactorBytes + 3 * kImgTerm;
 
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
@@ -118,6 +125,7 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
     }
     for (int i = 0; i < 3; ++i) mbar_init(&done[i], 1);
     mbar_init(s0full, 1);
+    mbar_init(imgfull, 1);
     mbar_init(drained, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -158,19 +166,13 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
         S[i / 2] = f2(x.x, x.y), S[i / 2 + 1] = f2(x.z, x.w);
       }
     if (nchunk > 0) {
-      if (has_state) chain_put<Cfg::kTerms>(stile, Cfg::kSTile, row, c0, S);
+      if (has_state) chain_put<3>(stile, Cfg::kSTile, row, c0, S);
       hand(kBarS);
     }
     for (int it = 0; it < nchunk; ++it) {
       const int n = nchunk - 1 - it, st = it % kChainStages;
       uint8_t* stage = smem + st * Cfg::kStage;
       const long long sh = (slot0 + n) * a.Hv + h;
-      uint4 third[kN / 8];   // S0's third term, this thread's part of the row
-      if (has_state) {
-        const uint8_t* src = saved.states + ((sh * kParts + part) * 2 + 1) * (long long)Cfg::kSTile;
-#pragma unroll
-        for (int i = 0; i < kN / 8; ++i) third[i] = __ldg(reinterpret_cast<const uint4*>(src + sw128(row, c0 + 8 * i)));
-      }
       wait(&full[st], it / kChainStages, 0);
       const float* fac = reinterpret_cast<const float*>(stage + Cfg::kOffFac);
       float decay[2], to_end[2], beta[2];
@@ -189,7 +191,7 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
       }
       F2 x[kN / 2], y[kN / 4], z[kN / 4];
       wait(&done[0], it, 1);
-      chain_frag<Cfg::kTerms>(ta + Cfg::kX1, c0, z);
+      chain_frag<3>(ta + Cfg::kX1, c0, z);
 #pragma unroll
       for (int i = 0; i < kN / 4; ++i) {
         const float f = to_end[i & 1], mb = -beta[i & 1];
@@ -224,20 +226,24 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
       }
       chain_put_frag<3>(rtile, Cfg::kRTile, lane_of(tok), fc, x);
       hand(kBarU);
-      // while the third product runs: y's pair through Z's second tile to memory, and dv (its hi) by rows
-      uint8_t* ytile = stage + Cfg::kOffZ + Cfg::kZTile;
-      chain_put_frag<2>(ytile, 0, tok, fc, y);
+      // while the third product runs: y through Z's second tile to memory, and dv by rows
+      float* ytile = reinterpret_cast<float*>(stage + Cfg::kOffZ + Cfg::kZTile);
+#pragma unroll
+      for (int i = 0; i < kN / 4; ++i)
+        *reinterpret_cast<float2*>(ytile + y_off(tok + (i & 1) * 8, fc + (i >> 1) * 8)) = f2_out(y[i]);
       fence_proxy_async_smem();
       bar_sync(kBarY, kAccWarps * 32);
       if (threadIdx.x == 0) {
-        bulk_store(gr.y + (sh * kParts + part) * (long long)Cfg::kZTile, ytile, Cfg::kZTile);
+        bulk_store(gr.y + (sh * kParts + part) * (long long)(Cfg::kZTile / 4), ytile, Cfg::kZTile);
         bulk_commit_group();
       }
       {
         const int r = threadIdx.x >> 2, c = (threadIdx.x & 3) * 8;
+        const float4 lo = *reinterpret_cast<const float4*>(ytile + y_off(r, c));
+        const float4 hi = *reinterpret_cast<const float4*>(ytile + y_off(r, c + 4));
         if (n * kChunk + r < sq.len)
           *reinterpret_cast<uint4*>(const_cast<__nv_bfloat16*>(delta_row(gr.dv, sq, n * kChunk + r, h)) + part * kCols + c) =
-              *reinterpret_cast<const uint4*>(ytile + sw128(r, c));
+              make_uint4(pack_bf16(lo.x, lo.y), pack_bf16(lo.z, lo.w), pack_bf16(hi.x, hi.y), pack_bf16(hi.z, hi.w));
       }
       F2 sdot = f2(0.f, 0.f);
       wait(s0full, it, 4);   // the state before this chunk, in the tile's place
@@ -246,8 +252,9 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
         for (int i = 0; i < kN / 8; ++i) {
           const uint4 hi = *reinterpret_cast<const uint4*>(stile + sw128(row, c0 + 8 * i));
           const uint4 lo = *reinterpret_cast<const uint4*>(stile + sw128(row, 32 + c0 + 8 * i));
+          const uint4 third = *reinterpret_cast<const uint4*>(stile + Cfg::kSTile + sw128(row, c0 + 8 * i));
           const uint32_t h4[4] = {hi.x, hi.y, hi.z, hi.w}, l4[4] = {lo.x, lo.y, lo.z, lo.w};
-          const uint32_t t4[4] = {third[i].x, third[i].y, third[i].z, third[i].w};
+          const uint32_t t4[4] = {third.x, third.y, third.z, third.w};
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             sdot = f2_fma(S[4 * i + q], f2_add(f2_bf16(h4[q]), f2_add(f2_bf16(l4[q]), f2_bf16(t4[q]))), sdot);
@@ -258,7 +265,7 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
         const F2 d2 = f2(chunk_decay, chunk_decay);
 #pragma unroll
         for (int i = 0; i < kN / 2; ++i) S[i] = f2_fma(d2, S[i], x[i]);
-        if (n > 0) chain_put<Cfg::kTerms>(stile, Cfg::kSTile, row, c0, S);
+        if (n > 0) chain_put<3>(stile, Cfg::kSTile, row, c0, S);
       }
       if (n > 0) hand(kBarS);
       // while the next chunk's first product runs: the rows' shares
@@ -297,9 +304,10 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
         *reinterpret_cast<float4*>(gr.dstate_in + sbase + i) =
             make_float4(f2_out(S[i / 2]).x, f2_out(S[i / 2]).y, f2_out(S[i / 2 + 1]).x, f2_out(S[i / 2 + 1]).y);
   } else if (warp == kIssueWarp) {
-    constexpr uint32_t idesc_1 = idesc_bf16_f32(128, 32 * Cfg::kTerms, false, true);    // [K; Q] G'
+    constexpr uint32_t idesc_1 = idesc_bf16_f32(128, 96, false, true);    // [K; Q] G'
     constexpr uint32_t idesc_z = idesc_bf16_f32(128, 128, true, true);    // [X; P T]^T [do, three terms of Z]
-    constexpr uint32_t idesc_3 = idesc_bf16_f32(128, 96, true, true);     // the lo terms' two of Z; [K; Q]^T ..
+    constexpr uint32_t idesc_3 = idesc_bf16_f32(128, 96, true, true);     // .. of the second terms, [do, two of Z]; [K; Q]^T ..
+    constexpr uint32_t idesc_2 = idesc_bf16_f32(128, 64, true, true);     // .. of the third terms, [do, one of Z]
     const Desc sdesc = desc_halves(smem_u32(stile), Cfg::kSTile, 1024, kSwizzle128B);
     const Desc rdesc = desc_halves(smem_u32(rtile), Cfg::kRTile, 1024, kSwizzle128B);
     const Desc kqdesc = desc_halves(smem_u32(smem), 16, 1024, kSwizzle128B);
@@ -312,7 +320,16 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
       if (ok && lane == 0) ok = mbar_spin(bar, phase & 1, abort_flag, err, kErrBackMma | code);
       ok = __all_sync(0xffffffffu, ok);
     };
-    if (nchunk > 0) wait(&full[0], 0, 0);
+    int images = 0;   // loads of an image (lane 0)
+    auto load_image = [&](int n) {
+      mbar_arrive_expect_tx(imgfull, 3 * kImgTerm);
+      bulk_load(smem + Cfg::kOffImage, blocks + n * block_step + kFactorBytes, 3 * kImgTerm, imgfull);
+      ++images;
+    };
+    if (nchunk > 0) {
+      if (lane == 0) load_image(nchunk - 1);
+      wait(&full[0], 0, 0);
+    }
     for (int it = 0; it < nchunk; ++it) {
       const int n = nchunk - 1 - it, st = it % kChainStages;
       const uint32_t off = st * (Cfg::kStage / 16);
@@ -329,23 +346,27 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
         }
       }
       __syncwarp();
+      wait(imgfull, it, 3);
       bar_sync(kBarR, kBarThreads);
       tc_fence_after_sync();
       if (ok && lane == 0) {
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          umma(tmem + Cfg::kX2, imgdesc + off + ks * 128, zdesc + off + ks * 128, idesc_z, ks > 0);
+          umma(tmem + Cfg::kX2, imgdesc + ks * 128, zdesc + off + ks * 128, idesc_z, ks > 0);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          umma(tmem + Cfg::kX2, imgdesc + off + kImgTerm / 16 + ks * 128, zdesc + off + ks * 128, idesc_3, 1u);
+          umma(tmem + Cfg::kX2, imgdesc + kImgTerm / 16 + ks * 128, zdesc + off + ks * 128, idesc_3, 1u);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          umma(tmem + Cfg::kX2, imgdesc + 2 * kImgTerm / 16 + ks * 128, zdesc + off + ks * 128, idesc_2, 1u);
         umma_commit(&done[1]);
       }
       if (lane == 0) {
         // G' has been read by the first product and stored: the state before the chunk takes its place
         bulk_wait_group_read<0>();
         if (it > 0) mbar_drain(s0full, (it - 1) & 1);   // (long done, unless the walk was given up)
-        mbar_arrive_expect_tx(s0full, Cfg::kSTile);
-        bulk_load(stile, saved.states + (((slot0 + n) * a.Hv + h) * kParts + part) * (2LL * Cfg::kSTile), Cfg::kSTile,
+        mbar_arrive_expect_tx(s0full, 2 * Cfg::kSTile);
+        bulk_load(stile, saved.states + (((slot0 + n) * a.Hv + h) * kParts + part) * (2LL * Cfg::kSTile), 2 * Cfg::kSTile,
                   s0full);
       }
       __syncwarp();
@@ -358,6 +379,8 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
             umma(tmem + Cfg::kX3, ktdesc + off + ks * 128, rdesc + ks * 128, idesc_3, ks > 0);
           umma_commit(&done[2]);
           umma_commit(&empty[st]);
+          // (the accumulator warps have the second product's results: it has read the image)
+          if (n > 0) load_image(n - 1);
         }
       }
       __syncwarp();
@@ -367,7 +390,10 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
       umma_commit(drained);
       mbar_drain(drained, 0);
       bulk_wait_group<0>();
-      if (nchunk > 0) mbar_drain(s0full, (nchunk - 1) & 1);
+      if (nchunk > 0) {
+        mbar_drain(s0full, (nchunk - 1) & 1);
+        mbar_drain(imgfull, (images - 1) & 1);
+      }
     }
   } else {
     const int t = threadIdx.x - (warp > kIssueWarp ? kAccWarps + 1 : kAccWarps) * 32;
@@ -383,8 +409,8 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
                       mbar_wait(&empty[st], (it / kChainStages - 1) & 1, abort_flag, err, kErrBackLoad | st);
       if (!__all_sync(0xffffffffu, ok)) break;
       if (t == 0) {
-        mbar_arrive_expect_tx(&full[st], kBlock);
-        bulk_load(smem + st * Cfg::kStage + Cfg::kOffFac, blocks + n * block_step, kBlock, &full[st]);
+        mbar_arrive_expect_tx(&full[st], kFactorBytes);
+        bulk_load(smem + st * Cfg::kStage + Cfg::kOffFac, blocks + n * block_step, kFactorBytes, &full[st]);
       }
       issued = it + 1;
       const int n0 = n * kChunk, len = min(kChunk, sq.len - n0);
@@ -539,15 +565,6 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
       for (int i = tid * 16; i < (int)Cfg::kTile; i += kThreads * 16) cp_async_16(dst + i, src + i, true);
     };
     copy_rows(gr.dout, h, Cfg::kOffDo);
-    {   // y's pair
-      const uint8_t* src = gr.y + sh * (kParts * kChunk * 128);
-#pragma unroll
-      for (int i = tid; i < kParts * kChunk * 8; i += kThreads) {
-        const int p = i / (kChunk * 8), r = (i >> 3) % kChunk, c = i & 7;
-        cp_async_16(base + Cfg::kOffY + (c >> 2) * Cfg::kRows + (r * Cfg::kLd + p * 32 + (c & 3) * 8) * 2,
-                    src + p * (kChunk * 128) + sw128(r, c * 8), true);
-      }
-    }
     if (tid < (int)kFactorBytes / 16) cp_async_16(base + Cfg::kOffFac + tid * 16, prep + sh * kPrepSaveBytes + kPrepFactors + tid * 16, true);
     load_tile(0);
     cp_async_commit();
@@ -559,6 +576,12 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
     const float4* wp = reinterpret_cast<const float4*>(saved.w + sh * kChunk * kD) + tid;
 #pragma unroll
     for (int i = 0; i < kQ; ++i) wv[i] = __ldg(wp + i * kThreads);
+    float4 yv[kQ];
+#pragma unroll
+    for (int i = 0; i < kQ; ++i) {
+      const int q = i * kThreads + tid, r = q / (kD / 4), c = (q % (kD / 4)) * 4;
+      yv[i] = __ldcg(reinterpret_cast<const float4*>(gr.y + (sh * kParts + c / 32) * (kChunk * 32) + y_off(r, c % 32)));
+    }
     float wd = 0.f, bd = 0.f, end = 0.f;
     if (tid < kChunk) {
       const float* rw = gr.rows + sh * kParts * 4 * kChunk + tid;   // [part][which][half][token]
@@ -575,16 +598,21 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
       }
       end = sum_warp(end);
     }
-    cp_async_wait<1>();   // do, y, the factors and the first tile (K and Q)
+    cp_async_wait<1>();   // do, the factors and the first tile (K and Q)
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kQ; ++i) {   // U = beta W
+    for (int i = 0; i < kQ; ++i) {   // U = beta W, and y
       const int q = i * kThreads + tid, r = q / (kD / 4), c = (q % (kD / 4)) * 4;
       const float f = fac[kFacBeta + r];
       uint32_t hi[2], lo[2];
       split_bf16(f * wv[i].x, f * wv[i].y, hi[0], lo[0]);
       split_bf16(f * wv[i].z, f * wv[i].w, hi[1], lo[1]);
       uint8_t* dst = smem + Cfg::kOffU + (r * Cfg::kLd + c) * 2;
+      *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(dst + Cfg::kRows) = make_uint2(lo[0], lo[1]);
+      split_bf16(yv[i].x, yv[i].y, hi[0], lo[0]);
+      split_bf16(yv[i].z, yv[i].w, hi[1], lo[1]);
+      dst += Cfg::kOffY - Cfg::kOffU;
       *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
       *reinterpret_cast<uint2*>(dst + Cfg::kRows) = make_uint2(lo[0], lo[1]);
     }

@@ -568,7 +568,7 @@ litela_status delta_bwd(const lite_la_delta_args* a, const lite_la_delta_grads* 
   gr.dstate_out = g->dstate_out, gr.dstate_in = g->dstate_in;
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
   gr.gstates = ws;
-  gr.y = ws + bytes.gstates;
+  gr.y = reinterpret_cast<float*>(ws + bytes.gstates);
   gr.rows = reinterpret_cast<float*>(ws + bytes.gstates + bytes.rows);
   gr.ends = reinterpret_cast<float*>(ws + bytes.gstates + bytes.rows + bytes.shares);
   int* err = delta_error_word(dev);

@@ -44,3 +44,31 @@ def test_states(lens, packed, Hk, Hv, d, carry, rate):
     ll.lite_la_device_status()
     far = [off(state[i], S) for i, _, _, (_, S) in ref(t)]
     assert max(far) <= STATE, far
+
+
+# dbeta_i = w_i . W_i: the gradient of what a token writes and what the state before it got wrong, each a result
+# of three products like a state's: sqrt(2) 2^-21, and of a dot product of signed terms again 2^-21 of their norms
+DBETA = 2.0 ** -20
+
+
+def gradients(t):
+    """dstate_in, dbeta and dg of every sequence as (how far off, over the result's norm)"""
+    args = [t[n] for n in ("q", "k", "v", "g", "beta")]
+    kw = dict(state_in=t["state_in"], cu_seqlens=t["cu"])
+    _, _, saved = ll.lite_la_gated_delta_fwd_save(*args, **kw)
+    got = ll.lite_la_gated_delta_bwd(*args, t["dout"], saved, dstate_out=t["dstate"], **kw)
+    ll.lite_la_device_status()
+    far = dict(dstate=[], dbeta=[], dg=[])
+    for i, e, sl, (_, _, (_, _, _, dg, db, dS)) in ref(t, grads=True):
+        if t["state_in"] is not None:
+            far["dstate"].append(off(got[5][i], dS))
+        far["dbeta"].append(off(got[4][e, sl], db))
+        far["dg"].append(off(got[3][e, sl], dg))
+    return far
+
+
+@pytest.mark.parametrize("lens,packed,Hk,Hv,d,carry", CASES)
+@pytest.mark.parametrize("rate", [1.0, 0.1])
+def test_gradients_of_states_and_write_strengths(lens, packed, Hk, Hv, d, carry, rate):
+    far = gradients(make(lens, packed, Hk, Hv, d, carry, seed=sum(lens) + d, rate=rate))
+    assert max(far["dstate"], default=0.0) <= STATE and max(far["dbeta"]) <= DBETA, far
