@@ -14,7 +14,8 @@
 //                                               b = Z U, that of k with its term of G' (Z in litela_delta_back).
 // The last sum is one over s >= t of N's row s less its column s.  (<S_C, G'> and the sums of
 // q . dq - y . v are the same in exact arithmetic, but cancel where decays are strong, with the errors of
-// bf16 pairs: dg 1.8e-5 off against 64 bits for 3 x 208 tokens, 4 heads of 32, where this form is 2e-6 off.)
+// bf16 pairs: dg 1.8e-5 off against 64 bits for 3 x 208 tokens, 4 heads of 32, where this form was 2e-6 off with
+// pairs and is 3e-7 off now.)
 //
 // litela_delta_back walks a sequence's chunks from the last to the first (as litela_delta_chain, with
 // the same three products a chunk) and leaves y and each chunk's G'; litela_delta_grads makes the rest,
@@ -471,12 +472,23 @@ litela_delta_back(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __restr
 // after another (their shares of dq and dk are summed in registers, in a fixed order).
 //
 // mma.sync, 16 warps (d = 32: 8): a warp has 16 rows and a quarter (half) of the columns.  States and
-// gradients stream through a ring of tiles of 32 columns; U and y are entered as bf16 pairs.  dq, dk and dg of one
-// head take 14 products of 64 rows.  2 x 2048 tokens of 16 heads of 128 (8 of keys): 146 us, with
-// the tensor pipe (mma.sync) at 45 %; one CTA an SM (registers, shared memory) leaves the waits for the tiles
-// and between the steps open, and 512 CTAs on 148 SMs a seventh of the time.
+// gradients stream through a ring of tiles of 32 columns.  dg is a sum over do, y, U and S0: the last three
+// are entered in three bf16 terms (dg is 2 to 5e-7 off against 64 bits, 1 to 6e-6 with two).  The matrices and
+// G', of which dq and dk alone are made, are bf16 pairs: 2^-18 beside the 2^-9 of their results' rounding.  2 x
+// 2048 tokens of 16 heads of 128 (8 of keys): 184 us (148 with pairs only), bound by the tensor pipe
+// (mma.sync) and, one CTA an SM (registers, shared memory), the waits for the tiles and between the steps;
+// 512 CTAs on 148 SMs leave a seventh of the time open.
 constexpr int kGradLd = 72;   // row of the 64 x 64 matrices, padded
-constexpr int kGradRing = 3;
+
+// d[n] += A B[n] for the first kTerms terms of B[n], the smallest first; one term for all n after the other, so
+// that no product waits for the one before it
+template <int kTiles, int kTerms, int kWords>
+__device__ __forceinline__ void mma_row(float (*d)[4], const uint32_t* a, const uint32_t (*b)[kWords]) {
+#pragma unroll
+  for (int t = kTerms - 1; t >= 0; --t)
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n) sm100::mma_16816(d[n], a, b[n] + 2 * t);
+}
 
 template <int kD>
 struct GradCfg {
@@ -486,11 +498,17 @@ struct GradCfg {
   static constexpr uint32_t kRows = kChunk * kLd * 2;              // 64 rows of d, bf16
   static constexpr uint32_t kTile = kD * 128;
   static constexpr uint32_t kOffK = 0, kOffQ = kRows, kOffDo = 2 * kRows;
-  static constexpr uint32_t kOffU = 3 * kRows, kOffY = 5 * kRows;  // pairs
-  static constexpr uint32_t kOffM = 7 * kRows;                     // M1 . D and M2 . D, pairs
+  static constexpr uint32_t kOffU = 3 * kRows, kOffY = 6 * kRows;  // three terms each
+  static constexpr uint32_t kOffM = 9 * kRows;                     // M1 . D and M2 . D, pairs
   static constexpr uint32_t kMat = kChunk * kGradLd * 2;
   static constexpr uint32_t kOffTile = (kOffM + 4 * kMat + 127) / 128 * 128;
-  static constexpr uint32_t kOffFac = kOffTile + kGradRing * kTile;   // the prepared block's factors
+  static constexpr int kRing = kD > 64 ? 2 : 3;                    // tiles of states in shared memory
+  // S0's third terms, a tile of 64-byte rows for each 32 columns; at d = 128 in the matrices' place, after them
+  static constexpr uint32_t kThirdTile = kD * 64;
+  static constexpr bool kThirdLate = kD > 64;
+  static constexpr uint32_t kOffThird = kThirdLate ? kOffM : kOffTile + kRing * kTile;
+  static_assert(!kThirdLate || kD / 32 * kThirdTile <= 4 * kMat, "third terms");
+  static constexpr uint32_t kOffFac = kThirdLate ? kOffTile + kRing * kTile : kOffThird + kD / 32 * kThirdTile;   // the prepared block's factors
   // sums of dg: by token for the warps beside one another, N's columns for the 4 below
   static constexpr uint32_t kOffSum = kOffFac + kFactorBytes;
   static constexpr uint32_t kSmemBytes = kOffSum + (kCW + 4) * kChunk * 4 + 1024;
@@ -558,18 +576,28 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
     const long long sh = (long long)slot * a.Hv + h;
     // tile p of the states (p < kParts), then of the gradients
     auto load_tile = [&](int p) {
-      const uint8_t* src = (p < kParts ? saved.states + (sh * kParts + p) * (2LL * Cfg::kTile)   // two of its terms
+      const uint8_t* src = (p < kParts ? saved.states + (sh * kParts + p) * (2LL * Cfg::kTile)   // the first two terms
                                        : gr.gstates + (sh * kParts + p - kParts) * (long long)Cfg::kTile);
-      const uint32_t dst = base + Cfg::kOffTile + (p % kGradRing) * Cfg::kTile;
+      const uint32_t dst = base + Cfg::kOffTile + (p % Cfg::kRing) * Cfg::kTile;
 #pragma unroll 1
       for (int i = tid * 16; i < (int)Cfg::kTile; i += kThreads * 16) cp_async_16(dst + i, src + i, true);
     };
     copy_rows(gr.dout, h, Cfg::kOffDo);
     if (tid < (int)kFactorBytes / 16) cp_async_16(base + Cfg::kOffFac + tid * 16, prep + sh * kPrepSaveBytes + kPrepFactors + tid * 16, true);
-    load_tile(0);
-    cp_async_commit();
-    load_tile(1);
-    cp_async_commit();
+    auto load_thirds = [&] {   // rows of 4 pieces of 16 bytes, from S0's second tiles; row pairs share 128 bytes
+#pragma unroll 1
+      for (int i = tid; i < kParts * kD * 4; i += kThreads) {
+        const int p = i / (kD * 4), r = (i >> 2) % kD, c = i & 3;
+        cp_async_16(base + Cfg::kOffThird + p * Cfg::kThirdTile + r * 64 + ((c ^ (r >> 1)) & 3) * 16,
+                    saved.states + ((sh * kParts + p) * 2 + 1) * (long long)Cfg::kTile + sw128(r, c * 8), true);
+      }
+    };
+    if (!Cfg::kThirdLate) load_thirds();
+#pragma unroll
+    for (int p = 0; p < Cfg::kRing - 1; ++p) {
+      load_tile(p);
+      cp_async_commit();
+    }
     // this token's w . W and b (tid < 64); W's values: all in flight at once
     constexpr int kQ = kChunk * kD / 4 / kThreads;   // 4 columns of a row at a time
     float4 wv[kQ];
@@ -598,23 +626,23 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
       }
       end = sum_warp(end);
     }
-    cp_async_wait<1>();   // do, the factors and the first tile (K and Q)
+    cp_async_wait<Cfg::kRing - 2>();   // do, the factors and the first tile (K and Q)
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kQ; ++i) {   // U = beta W, and y
       const int q = i * kThreads + tid, r = q / (kD / 4), c = (q % (kD / 4)) * 4;
       const float f = fac[kFacBeta + r];
-      uint32_t hi[2], lo[2];
-      split_bf16(f * wv[i].x, f * wv[i].y, hi[0], lo[0]);
-      split_bf16(f * wv[i].z, f * wv[i].w, hi[1], lo[1]);
+      uint32_t u[3][2], y[3][2];
+      split_terms(f * wv[i].x, f * wv[i].y, &u[0][0], 2);
+      split_terms(f * wv[i].z, f * wv[i].w, &u[0][1], 2);
+      split_terms(yv[i].x, yv[i].y, &y[0][0], 2);
+      split_terms(yv[i].z, yv[i].w, &y[0][1], 2);
       uint8_t* dst = smem + Cfg::kOffU + (r * Cfg::kLd + c) * 2;
-      *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(dst + Cfg::kRows) = make_uint2(lo[0], lo[1]);
-      split_bf16(yv[i].x, yv[i].y, hi[0], lo[0]);
-      split_bf16(yv[i].z, yv[i].w, hi[1], lo[1]);
-      dst += Cfg::kOffY - Cfg::kOffU;
-      *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(dst + Cfg::kRows) = make_uint2(lo[0], lo[1]);
+#pragma unroll
+      for (int t = 0; t < 3; ++t) {
+        *reinterpret_cast<uint2*>(dst + t * Cfg::kRows) = make_uint2(u[t][0], u[t][1]);
+        *reinterpret_cast<uint2*>(dst + Cfg::kOffY - Cfg::kOffU + t * Cfg::kRows) = make_uint2(y[t][0], y[t][1]);
+      }
     }
     __syncthreads();
 
@@ -629,13 +657,14 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
 #pragma unroll
         for (int i = 0; i < 4; ++i) m1[n][i] = m2[n][i] = qk[n][i] = kk[n][i] = 0.f;
       const uint32_t arow = (16 * rb + (lane & 15)) * (Cfg::kLd * 2) + (lane >> 4) * 16;
-      // matrices by lane / 8: hi of 0..7 and 8..15 of the K dimension, lo
+      // matrices by lane / 8: first term of 0..7 and 8..15 of the K dimension, second; third of two tiles of columns
       const uint32_t brow = base + Cfg::kOffU + (lane >> 4) * Cfg::kRows + (8 * cw + l8) * (Cfg::kLd * 2) + k8 * 2;
+      const uint32_t trow = base + Cfg::kOffU + 2 * Cfg::kRows + (8 * (cw + (lane >> 4) * kCW) + l8) * (Cfg::kLd * 2) + k8 * 2;
       // K's: two tiles of columns
       const uint32_t krow = base + Cfg::kOffK + (8 * (cw + (lane >> 4) * kCW) + l8) * (Cfg::kLd * 2) + k8 * 2;
 #pragma unroll 1
       for (int ks = 0; ks < kD / 16; ++ks) {
-        uint32_t ad[4], yh[4], yl[4];
+        uint32_t ad[4], ya[3][4];
         {
           uint32_t aq[4], ak[4];
           ldmatrix_x4(aq, base + Cfg::kOffQ + arow + ks * 32);
@@ -651,13 +680,23 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
           }
         }
         ldmatrix_x4(ad, base + Cfg::kOffDo + arow + ks * 32);
-        ldmatrix_x4(yh, base + Cfg::kOffY + arow + ks * 32);
-        ldmatrix_x4(yl, base + Cfg::kOffY + Cfg::kRows + arow + ks * 32);
-        uint32_t b[kMT][4];
 #pragma unroll
-        for (int n = 0; n < kMT; ++n) ldmatrix_x4(b[n], brow + n * 8 * kCW * (Cfg::kLd * 2) + ks * 32);
-        mma_halves<kMT>(m1, ad, b);
-        mma_pairs<kMT>(m2, yh, yl, b);
+        for (int t = 0; t < 3; ++t) ldmatrix_x4(ya[t], base + Cfg::kOffY + t * Cfg::kRows + arow + ks * 32);
+        uint32_t b[kMT][6];   // terms of 8 columns
+#pragma unroll
+        for (int n = 0; n < kMT; n += 2) {
+          uint32_t third[4];
+          ldmatrix_x4(third, trow + n * 8 * kCW * (Cfg::kLd * 2) + ks * 32);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            ldmatrix_x4(b[n + e], brow + (n + e) * 8 * kCW * (Cfg::kLd * 2) + ks * 32);
+            b[n + e][4] = third[2 * e], b[n + e][5] = third[2 * e + 1];
+          }
+        }
+        mma_row<kMT, 3, 6>(m1, ad, b);
+        mma_row<kMT, 1, 6>(m2, ya[2], b);
+        mma_row<kMT, 2, 6>(m2, ya[1], b);
+        mma_row<kMT, 3, 6>(m2, ya[0], b);
       }
       // by D; M1 by scale, M2 negated; N's sums of the warp's rows and columns
       float nrow[2] = {0.f, 0.f};
@@ -763,7 +802,7 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
     const uint32_t arow = (16 * rb + (lane & 15)) * (Cfg::kLd * 2) + (lane >> 4) * 16;
     auto tile_b = [&](uint32_t* b, int p, int n, int ks) {   // rows (channels) of the tile: hi, lo
       const int row = (cw * kT + n) * 8 + l8, col = 16 * ks + k8 + (lane >> 4) * 32;
-      ldmatrix_x4(b, base + Cfg::kOffTile + (p % kGradRing) * Cfg::kTile + sw128(row, col));
+      ldmatrix_x4(b, base + Cfg::kOffTile + (p % Cfg::kRing) * Cfg::kTile + sw128(row, col));
     };
     // the warp's columns of rows r0 and r0 + 8 of x with those of K or Q; and such sums for all warps to add
     auto with_rows = [&](uint32_t off, const float (*x)[4], float* d) {
@@ -791,27 +830,54 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
         for (int i = 0; i < 4; ++i) x[n][i] = y[n][i] = 0.f;
 #pragma unroll 1
       for (int p = 0; p < kParts; ++p) {
-        if (p + 2 < 2 * kParts) load_tile(p + 2);
+        if (p + Cfg::kRing - 1 < 2 * kParts) load_tile(p + Cfg::kRing - 1);
         cp_async_commit();
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-          uint32_t ad[4], yh[4], yl[4];
+          uint32_t ad[4], ya[3][4];
           const uint32_t o = arow + (2 * p + ks) * 32;
           ldmatrix_x4(ad, base + Cfg::kOffDo + o);
-          ldmatrix_x4(yh, base + Cfg::kOffY + o);
-          ldmatrix_x4(yl, base + Cfg::kOffY + Cfg::kRows + o);
+#pragma unroll
+          for (int t = 0; t < 3; ++t) ldmatrix_x4(ya[t], base + Cfg::kOffY + t * Cfg::kRows + o);
           constexpr int kM = kT < 4 ? kT : 4;
 #pragma unroll
           for (int m = 0; m < kT; m += kM) {
             uint32_t b[kM][4];
 #pragma unroll
             for (int n = 0; n < kM; ++n) tile_b(b[n], p, m + n, ks);
-            mma_halves<kM>(x + m, ad, b);
-            mma_pairs<kM>(y + m, yh, yl, b);
+            mma_row<kM, 2, 4>(x + m, ad, b);
+            mma_row<kM, 1, 4>(y + m, ya[2], b);
+            mma_row<kM, 2, 4>(y + m, ya[1], b);
+            mma_row<kM, 2, 4>(y + m, ya[0], b);
           }
         }
-        cp_async_wait<1>();
+        cp_async_wait<Cfg::kRing - 2>();
         __syncthreads();   // the next tile has landed, and everyone is done with this one's neighbour
+        if (Cfg::kThirdLate && p == 0) {   // (and with the matrices)
+          load_thirds();
+          cp_async_commit();
+        }
+      }
+      // S0's third terms: matrices by lane / 8: 8 of the 32 columns
+#pragma unroll 1
+      for (int p = 0; p < kParts; ++p) {
+        uint32_t ad[2][4], ya[2][4];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          ldmatrix_x4(ad[ks], base + Cfg::kOffDo + arow + (2 * p + ks) * 32);
+          ldmatrix_x4(ya[ks], base + Cfg::kOffY + arow + (2 * p + ks) * 32);
+        }
+#pragma unroll
+        for (int n = 0; n < kT; ++n) {
+          uint32_t b[4];
+          const int row = (cw * kT + n) * 8 + l8;
+          ldmatrix_x4(b, base + Cfg::kOffThird + p * Cfg::kThirdTile + row * 64 + (((lane >> 3) ^ (row >> 1)) & 3) * 16);
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            mma_16816(x[n], ad[ks], b + 2 * ks);
+            mma_16816(y[n], ya[ks], b + 2 * ks);
+          }
+        }
       }
       const float e0 = fac[kFacDecay + r0], e1 = fac[kFacDecay + r0 + 8];
 #pragma unroll
@@ -836,7 +902,7 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
         for (int i = 0; i < 4; ++i) x[n][i] = 0.f;
 #pragma unroll 1
       for (int p = kParts; p < 2 * kParts; ++p) {
-        if (p + 2 < 2 * kParts) load_tile(p + 2);
+        if (p + Cfg::kRing - 1 < 2 * kParts) load_tile(p + Cfg::kRing - 1);
         cp_async_commit();
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
@@ -850,10 +916,11 @@ litela_delta_grads(const DeltaArgs a, const DeltaGrads gr, const uint8_t* __rest
             uint32_t b[kM][4];
 #pragma unroll
             for (int n = 0; n < kM; ++n) tile_b(b[n], p, m + n, ks);
-            mma_pairs<kM>(x + m, uh, ul, b);
+            mma_row<kM, 1, 4>(x + m, ul, b);
+            mma_row<kM, 2, 4>(x + m, uh, b);
           }
         }
-        cp_async_wait<1>();
+        cp_async_wait<Cfg::kRing - 2>();
         __syncthreads();
       }
       const float e0 = fac[kFacToEnd + r0], e1 = fac[kFacToEnd + r0 + 8];

@@ -202,26 +202,6 @@ __device__ __forceinline__ void stmatrix_x4_t(uint32_t addr, const uint32_t* r) 
                "r"(r[1]), "r"(r[2]), "r"(r[3])
                : "memory");
 }
-// d[n] += A B[n], all pairs of fragments (B: hi in b[0], b[1], lo in b[2], b[3]); one kind of product
-// for all n after the other, so that no product waits for the one before it
-template <int kTiles>
-__device__ __forceinline__ void mma_pairs(float (*d)[4], const uint32_t* ah, const uint32_t* al, const uint32_t (*b)[4]) {
-#pragma unroll
-  for (int n = 0; n < kTiles; ++n) sm100::mma_16816(d[n], al, b[n]);
-#pragma unroll
-  for (int n = 0; n < kTiles; ++n) sm100::mma_16816(d[n], ah, b[n] + 2);
-#pragma unroll
-  for (int n = 0; n < kTiles; ++n) sm100::mma_16816(d[n], ah, b[n]);
-}
-// the same with an A that is bf16
-template <int kTiles>
-__device__ __forceinline__ void mma_halves(float (*d)[4], const uint32_t* a, const uint32_t (*b)[4]) {
-#pragma unroll
-  for (int n = 0; n < kTiles; ++n) sm100::mma_16816(d[n], a, b[n] + 2);
-#pragma unroll
-  for (int n = 0; n < kTiles; ++n) sm100::mma_16816(d[n], a, b[n]);
-}
-
 // d[n] + small[n] += A B[n], fp32 operands in three terms each, all products that reach 2^-25 of the first;
 // two accumulators, so that a product waits for every other one before it only
 template <int kTiles>

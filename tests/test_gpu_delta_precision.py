@@ -72,3 +72,16 @@ def gradients(t):
 def test_gradients_of_states_and_write_strengths(lens, packed, Hk, Hv, d, carry, rate):
     far = gradients(make(lens, packed, Hk, Hv, d, carry, seed=sum(lens) + d, rate=rate))
     assert max(far["dstate"], default=0.0) <= STATE and max(far["dbeta"]) <= DBETA, far
+
+
+# dg_t = <G, A>, the state that decays and its gradient, each 2^-21 off at random: sqrt(2) 2^-21 of it.  It comes
+# from sums over the 64 tokens of a chunk of terms that are up to a few times dg: 64 roundings of 2^-24 of them
+# add up to 8 2^-24 times three, 2^-19.4 if all were at their most, a quarter of that as they fall: 2^-20.2 together
+DG = 2.0 ** -20
+
+
+@pytest.mark.parametrize("lens,packed,Hk,Hv,d,carry", CASES)
+@pytest.mark.parametrize("rate", [1.0, 0.1])
+def test_gradients_of_decays(lens, packed, Hk, Hv, d, carry, rate):
+    far = gradients(make(lens, packed, Hk, Hv, d, carry, seed=sum(lens) + d + 1, rate=rate))
+    assert max(far["dg"]) <= DG, far
