@@ -1,12 +1,11 @@
 """Calls at the edges of the gated delta rule's and the head norms' entry points: no tokens, streams,
 frozen weights, gradients as autograd hands them, rows far apart."""
-import numpy as np
 import pytest
 import torch
 
 import linear_attention_diffusion_litela_b200 as ll
 from linear_attention_diffusion_litela_b200 import seq
-from tests.test_gpu_delta import autograd, fwd, make, ref
+from tests.test_gpu_delta import autograd, fwd, make
 
 pytestmark = pytest.mark.gpu
 
@@ -156,3 +155,54 @@ def test_gradient_of_sequences_without_tokens():
     _, state, grads = autograd(t)
     assert torch.equal(state, t["state_in"]) and torch.equal(grads["state_in"], t["dstate"])
     assert not any(grads[n].any() for n in ("q", "k", "v", "g", "beta"))
+
+
+def wide(N, stride, heads, d, at=0, buffer=None):
+    """[1, N, heads, d] with its rows `stride` elements apart, from element `at` on of a buffer"""
+    buffer = torch.empty(N * stride, dtype=torch.bfloat16, device="cuda") if buffer is None else buffer
+    return buffer.as_strided((1, N, heads, d), (0, stride, d, 1), at), buffer
+
+
+@pytest.mark.parametrize("N,stride", [(30, 2 ** 27), (200, 2 ** 24)])     # the recurrence; chunks
+def test_outputs_beyond_2_31_elements(N, stride):
+    t = make([N], False, 1, 2, 32, True, seed=4)
+    want, want_s = fwd(t)
+    out, _ = wide(N, stride, 2, 32)
+    _, state = fwd(t, out=out)
+    assert torch.equal(out, want) and torch.equal(state, want_s)
+
+
+def test_one_token_outputs_beyond_2_31_elements():
+    B, stride = 20, 2 ** 27
+    t = make([1] * B, False, 1, 2, 32, True, seed=6)
+    one = [t[n][:, 0] for n in ("q", "k", "v", "g", "beta")]
+    states = [t["state_in"].clone() for _ in range(2)]
+    want = ll.lite_la_gated_delta_step(*one, states[0])
+    v, _ = wide(B, stride, 2, 32)
+    out, _ = wide(B, stride, 2, 32)
+    v.copy_(t["v"].transpose(0, 1))
+    one[2] = v[0]
+    ll.lite_la_gated_delta_step(*one, states[1], out=out[0])
+    assert torch.equal(out[0], want) and torch.equal(*states)
+
+
+def test_gradients_beyond_2_31_elements():
+    """dq, dk and dv in one buffer, each between the others' rows, dout far apart too (the C call takes views)"""
+    N, stride, d = 200, 2 ** 24, 32
+    t = make([N], False, 1, 2, d, True, seed=4)
+    args = [t[n] for n in ("q", "k", "v", "g", "beta")]
+    _, _, saved = ll.lite_la_gated_delta_fwd_save(*args, state_in=t["state_in"])
+    want = ll.lite_la_gated_delta_bwd(*args, t["dout"], saved, dstate_out=t["dstate"], state_in=t["state_in"])
+    a = seq._Delta(*args, None, None)
+    dout, _ = wide(N, stride, 2, d)
+    dout.copy_(t["dout"])
+    dq, buffer = wide(N, stride, 1, d)
+    dk, dv = wide(N, stride, 1, d, 64, buffer)[0], wide(N, stride, 2, d, 128, buffer)[0]
+    dg, dbeta, dstate = (torch.empty_like(x) for x in want[3:])
+    size = a.bytes(ll.lib().lite_la_gated_delta_bwd_workspace_bytes)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    views = [seq._view(x, "", x.shape, a.dev) for x in (dout, dq, dk, dv)]
+    grads = seq._DELTA_GRADS.pack(*sum(views, ()), dg.data_ptr(), dbeta.data_ptr(), t["dstate"].data_ptr(), dstate.data_ptr())
+    seq._call(ll.lib().lite_la_gated_delta_bwd, a.dev, None,
+              a.pack(seq._NO_VIEW, t["state_in"].data_ptr(), 0, 0, ws.data_ptr(), size), grads, saved.data_ptr(), saved.numel())
+    assert all(torch.equal(x, y) for x, y in zip((dq, dk, dv, dg, dbeta, dstate), want))
