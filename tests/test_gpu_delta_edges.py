@@ -206,3 +206,50 @@ def test_gradients_beyond_2_31_elements():
     seq._call(ll.lib().lite_la_gated_delta_bwd, a.dev, None,
               a.pack(seq._NO_VIEW, t["state_in"].data_ptr(), 0, 0, ws.data_ptr(), size), grads, saved.data_ptr(), saved.numel())
     assert all(torch.equal(x, y) for x, y in zip((dq, dk, dv, dg, dbeta, dstate), want))
+
+
+def test_buffers_written_in_place_are_known_to_autograd():
+    """A backward that needs what a later call has written over says so, as torch's own in-place operations make it"""
+    t = make([70, 70], False, 1, 2, 64, True)
+    args = [t[n] for n in ("q", "k", "v", "g", "beta")]
+    weight = torch.ones((), device="cuda", requires_grad=True)
+
+    def lost(y):   # `y` is needed for weight's gradient
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            torch.autograd.grad(y.sum(), weight)
+
+    qkv = torch.randn(2, 50, 6 * 64, device="cuda").bfloat16()
+    for write in (lambda x: ll.lite_la_qk_norm_rope_fwd(x, 3, 2, d=64, out=x),
+                  lambda x: ll.lite_la_qk_norm_rope_bwd(qkv, x, 3, 2, d=64, dqkv=x)):
+        x = qkv.clone()
+        y = x * weight
+        write(x)
+        lost(y)
+    for write in (lambda x: ll.lite_la_gated_delta_fwd(*args, state_in=x, state_out=x),
+                  lambda x: ll.lite_la_gated_delta_fwd_save(*args, state_in=t["state_in"], state_out=x),
+                  lambda x: ll.lite_la_gated_delta_step(*(a[:, 0] for a in args), x)):
+        x = t["state_in"].clone()
+        y = x * weight
+        write(x)
+        lost(y)
+    x = torch.zeros_like(t["v"])
+    y = x * weight
+    ll.lite_la_gated_delta_fwd(*args, out=x)
+    lost(y)
+    x = torch.zeros_like(t["v"][:, 0])
+    y = x * weight
+    ll.lite_la_gated_delta_step(*(a[:, 0] for a in args), t["state_in"].clone(), out=x)
+    lost(y)
+    # nothing given, nothing written: the gradient is there
+    y = qkv * weight
+    ll.lite_la_qk_norm_rope_fwd(qkv, 3, 2, d=64)
+    assert torch.isfinite(torch.autograd.grad(y.sum(), weight)[0])
+    # and a saved state that a later token is put into
+    q = t["q"].clone().requires_grad_()
+    S = t["state_in"].clone()
+    out, _ = ll.lite_la_gated_delta(q, *args[1:], state_in=S)
+    ll.lite_la_gated_delta_step(*(a[:, 0] for a in args), S)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        torch.autograd.grad(out.float().sum(), q)
+    with torch.inference_mode():
+        ll.lite_la_gated_delta_step(*(a[:, 0] for a in args), t["state_in"].clone())
