@@ -52,18 +52,22 @@ def _call(fn, dev, stream, *args):
             _check(fn(*args, handle))
 
 
-def _new(stream, make, returned=True):
-    """make(): a buffer of a call.  With `stream` it comes from that stream's memory: a block of the
+def _on(stream, make, *args, returned=True, **kw):
+    """make(*args, **kw): a buffer of a call with `stream`, from that stream's memory.  A block of the
     current stream's may have been freed under work that is still queued there, which a caller's wait
     before the call need not cover.  The current stream may go on to use what is returned."""
-    if stream is None:
-        return make()
     cuda = _torch().cuda
     with cuda.stream(stream):
-        t = make()
+        t = make(*args, **kw)
     if returned:
         t.record_stream(cuda.current_stream(t.device))
     return t
+
+
+@functools.cache
+def _wrote():
+    """f(t): the caller's buffer t has been written; a backward that needs what was in it must not take this"""
+    return _torch().autograd.graph.increment_version
 
 
 # ---------------------------------------------------------------------------------------
@@ -115,10 +119,14 @@ def lite_la_qk_norm_rope_fwd(qkv, Hq: int, Hk: int, d: int = 32, q_weight=None, 
     by position; returns out in qkv's layout (v copied).  out=qkv works in place.  A row at a
     negative position is padding: left alone in place, zeros otherwise."""
     dev, args = _norm_args(qkv, Hq, Hk, d, q_weight, k_weight, cos, sin, positions, eps, interleaved)
-    if out is None:
-        out = _new(stream, lambda: _torch().empty_like(qkv))
+    given = out is not None
+    if not given:
+        like = _torch().empty_like
+        out = like(qkv) if stream is None else _on(stream, like, qkv)
     o = _rows(out, "out", qkv.shape, dev)
     _call(lib().lite_la_qk_norm_rope_fwd, dev, stream, qkv.data_ptr(), o, _ptr(q_weight), _ptr(k_weight), *args)
+    if given:
+        _wrote()(out)
     return out
 
 
@@ -135,17 +143,21 @@ def _norm_bwd(qkv, dout, Hq, Hk, d, q_weight, k_weight, cos, sin, positions, eps
     """... with the weights' gradients that are wanted"""
     torch = _torch()
     dev, args = _norm_args(qkv, Hq, Hk, d, q_weight, k_weight, cos, sin, positions, eps, interleaved)
-    if dqkv is None:
-        dqkv = _new(stream, lambda: torch.empty_like(qkv))
+    like, given = torch.empty_like, dqkv is not None
+    if not given:
+        dqkv = like(qkv) if stream is None else _on(stream, like, qkv)
     do, dx = _rows(dout, "dout", qkv.shape, dev), _rows(dqkv, "dqkv", qkv.shape, dev)
-    dwq = _new(stream, lambda: torch.empty_like(q_weight)) if want_q else None
-    dwk = _new(stream, lambda: torch.empty_like(k_weight)) if want_k else None
+    dwq, dwk = (None if not want else like(w) if stream is None else _on(stream, like, w)
+                for want, w in ((want_q, q_weight), (want_k, k_weight)))
     size, ws = 0, None
     if want_q or want_k:
         size = lib().lite_la_qk_norm_rope_workspace_bytes(d)
-        ws = _new(stream, lambda: torch.empty(size, dtype=torch.uint8, device=qkv.device), False)
+        kw = dict(dtype=torch.uint8, device=qkv.device)
+        ws = torch.empty(size, **kw) if stream is None else _on(stream, torch.empty, size, returned=False, **kw)
     _call(lib().lite_la_qk_norm_rope_bwd, dev, stream, qkv.data_ptr(), do, dx, _ptr(q_weight), _ptr(k_weight),
           _ptr(dwq), _ptr(dwk), *args, _ptr(ws), size)
+    if given:
+        _wrote()(dqkv)
     return dqkv, dwq, dwk
 
 
@@ -280,21 +292,31 @@ def _delta_forward(q, k, v, g, beta, state_in, state_out, cu_seqlens, scale, out
     torch = _torch()
     a = _Delta(q, k, v, g, beta, scale, cu_seqlens)
     si = 0 if state_in is None else _states(state_in, "state_in", a.states, a.dev)
+    given = [x for x in (state_out, out) if x is not None]
     if state_out is None:
-        state_out = _new(stream, lambda: torch.empty_like(state_in) if si
-                         else torch.empty(a.states, dtype=torch.float32, device=a.device))
+        kw = dict(dtype=torch.float32, device=a.device)
+        if stream is not None:
+            state_out = _on(stream, torch.empty, a.states, **kw)
+        else:
+            state_out = torch.empty_like(state_in) if si else torch.empty(a.states, **kw)
     so = _states(state_out, "state_out", a.states, a.dev)
     zero_tail = int(out is None)
     if out is None:
-        out = _new(stream, lambda: torch.empty_like(v, memory_format=torch.contiguous_format))
+        kw = dict(memory_format=torch.contiguous_format)
+        out = torch.empty_like(v, **kw) if stream is None else _on(stream, torch.empty_like, v, **kw)
     o = _view(out, "out", a.vshape, a.dev)
     L = lib()
     size = a.bytes(L.lite_la_gated_delta_saved_bytes if save else L.lite_la_gated_delta_workspace_bytes)
-    buf = _new(stream, lambda: torch.empty(size, dtype=torch.uint8, device=a.device), save) if size or save else None
+    buf = None
+    if size or save:
+        kw = dict(dtype=torch.uint8, device=a.device)
+        buf = torch.empty(size, **kw) if stream is None else _on(stream, torch.empty, size, returned=save, **kw)
     if save:
         _call(L.lite_la_gated_delta_fwd_save, a.dev, stream, a.pack(o, si, so, zero_tail, 0, 0), buf.data_ptr(), size)
     else:
         _call(L.lite_la_gated_delta_fwd, a.dev, stream, a.pack(o, si, so, zero_tail, _ptr(buf), size))
+    for x in given:
+        _wrote()(x)
     return out, state_out, buf
 
 
@@ -328,8 +350,10 @@ def lite_la_gated_delta_bwd(q, k, v, g, beta, dout, saved, dstate_out=None, stat
     if not isinstance(saved, torch.Tensor) or saved.dtype is not torch.uint8 or not saved.is_contiguous() \
             or saved.get_device() != a.dev:
         raise TypeError("saved must be what lite_la_gated_delta_fwd_save returned")
-    new = lambda shape, dtype, returned=True: _new(  # noqa: E731
-        stream, lambda: torch.empty(shape, dtype=dtype, device=a.device), returned)
+    def new(shape, dtype, returned=True):
+        kw = dict(dtype=dtype, device=a.device)
+        return torch.empty(shape, **kw) if stream is None else _on(stream, torch.empty, shape, returned=returned, **kw)
+
     si = dstate_in = None
     if state_in is not None:
         si, dstate_in = _states(state_in, "state_in", a.states, a.dev), new(a.states, torch.float32)
@@ -412,11 +436,16 @@ def lite_la_gated_delta_step(q, k, v, g, beta, states, state_indices=None, scale
     if state_indices is not None and (state_indices.dtype is not torch.int32 or state_indices.shape != (B,)
                                       or not state_indices.is_contiguous() or state_indices.get_device() != dev):
         raise TypeError("state_indices must be a contiguous int32 tensor [B] on q's device")
-    if out is None:
-        out = _new(stream, lambda: torch.empty_like(v, memory_format=torch.contiguous_format))
+    given = out is not None
+    if not given:
+        kw = dict(memory_format=torch.contiguous_format)
+        out = torch.empty_like(v, **kw) if stream is None else _on(stream, torch.empty_like, v, **kw)
     args = _DELTA_ARGS.pack(*_token_view(q, "q", (B, Hk, d), dev), *_token_view(k, "k", (B, Hk, d), dev),
                             *_token_view(v, "v", shape, dev), *_token_view(out, "out", shape, dev), gp, bp, g_sb, 0,
                             b_sb, 0, st, st, 0, B, 1, Hk, Hv, d,
                             float(d) ** -0.5 if scale is None and d > 0 else float(scale or 0.0), 0, 0, 0)
     _call(lib().lite_la_gated_delta_step, dev, stream, args, _ptr(state_indices), pool)
+    _wrote()(states)
+    if given:
+        _wrote()(out)
     return out
