@@ -320,10 +320,11 @@ size_t lite_la_gated_delta_workspace_bytes(int B, int N, int Hk, int Hv, int d, 
  * All rows are written: those of no sequence with zeros.  The sums are fp32; equal calls give
  * equal bits.
  *
- * A NaN or infinite k, v, g or beta of a token (or state before a sequence) makes out of that token,
- * of all later tokens and the state NaN in the heads that read it, one in q at least out of that
- * token; earlier tokens keep their values.  The gradients of such a sequence are unspecified; other
- * sequences are not touched. */
+ * A NaN or an infinity in k, g or beta of a token makes out of that token and of all later tokens of its
+ * sequence, and the state, NaN or infinite in the heads that read it; one in a channel of v, or in the
+ * state before the sequence, at least in that value channel (chunks: up to 32 channels together); one in q
+ * at least out of its own token.  Earlier tokens keep their values, bit for bit.  The gradients of such a
+ * sequence are unspecified; other sequences are not touched. */
 typedef struct {
   lite_la_view dout, dq, dk, dv;
   float* dg;

@@ -600,9 +600,9 @@ __global__ void __launch_bounds__(kPrepThreads, 3) litela_delta_prep(const Delta
 
 // ---------------------------------------------------------------------------------------
 // litela_delta_chain: one CTA walks the chunks of one sequence and value head for 32 of the state's
-// columns (columns do not meet, so a state is cut by columns over CTAs).  64 columns a CTA took 3.2 us
-// a chunk where 32 take 2.0 to 2.2 (d = 128): less for many equal sequences (1.6 a half), but a long
-// sequence among others, or few heads, wait for the longest chain of chunks.
+// columns (columns do not meet, so a state is cut by columns over CTAs): 2.2 us a chunk at d = 128.  64
+// columns a CTA took 3.2 us a chunk where 32 took 2.0 to 2.2: less for many equal sequences (1.6 a half), but a
+// long sequence among others, or few heads, wait for the longest chain of chunks.
 //
 // Three tcgen05 products per chunk, each with M = 128 rows, fp32 accumulators in TMEM:
 //     X1 = [K; Q] S0           (rows: 16 of K, 16 of Q, 16 of K ..; K dimension d)

@@ -106,7 +106,7 @@ __device__ __forceinline__ bool norm_next(const NormPlan& p, NormWalk& w, long l
 // A whole task's channels into L2, one task ahead of the forward's loads: more bytes in flight than
 // registers hold.  Tasks of 2240 and 4480 bytes: 206 -> 174 us, 184 -> 164 us (60000 rows of 3 x 35, 32768 of
 // 3 x 70 heads of 32); of 8192 and 16384 bytes, whose own loads are enough: 244 -> 322 us, 268 -> 377 us, and the
-// gradient (two rows a task) 62 -> 70 us: not fetched.
+// gradient (two rows a task) 62 -> 70 us: not fetched.  Nothing between 4480 and 8192 bytes was measured.
 __device__ __forceinline__ void norm_prefetch(const NormPlan& p, long long t, int lane) {
   if (p.shift != 0 || lane != 0 || t >= p.rows * p.regions) return;
   const int region = (t >= p.rows) + (t >= 2 * p.rows);
@@ -220,7 +220,7 @@ __device__ __forceinline__ void norm_zero(const NormPlan& p, const NormWalk& w, 
 // y = r (x * a + partner * b), a = w cos, b = the partner's w times the signed sine.  80 registers
 // (three CTAs an SM) hold four steps in work and four in flight.  2 x 16384 rows of 70 + 70 + 70
 // heads of 32 channels: 158 us, 5.6 TB/s (176 without norm_prefetch, 179 with 64 registers, two steps and
-// four CTAs); what is left is bound by the issue of instructions as much as by memory.
+// four CTAs); neither the issue slots (59 %) nor DRAM (67 %) are full, warps wait for loads most.
 template <int kD, bool kInter>
 __global__ void __launch_bounds__(kNormThreads, 3) litela_norm_fwd(const NormPlan p) {
   constexpr int kU = 4;
@@ -306,7 +306,8 @@ __global__ void __launch_bounds__(kNormThreads, 3) litela_norm_fwd(const NormPla
 // that the two sums of a head do not wait for one another.  A warp's sums of a weight's gradient
 // stay in registers over all its rows; the CTA's go to `partials`, which litela_norm_weight_grad
 // adds in a fixed order.  Two CTAs an SM with two steps in work and two in flight: 2 x 4099 rows of
-// 32 + 8 + 8 heads of 128 channels in 62 us, 4.7 TB/s (80 registers for a third CTA spill: 144 us).
+// 32 + 8 + 8 heads of 128 channels in 62 us, 4.7 TB/s (80 registers for a third CTA spill: 144 us).  With 15.5 warps an
+// SM too few bytes are in flight: 58 % of the issue slots, 49 % of DRAM.
 template <int kD, bool kInter>
 __global__ void __launch_bounds__(kNormThreads, 2) litela_norm_bwd(const NormPlan p) {
   constexpr int kU = 2;

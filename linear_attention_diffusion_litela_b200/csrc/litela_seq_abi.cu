@@ -385,13 +385,14 @@ litela_status delta_setup(int dev) {
 
 // The recurrence or the chunks.  The recurrence takes 0.20 to 0.25 us a token (one sequence, d = 32
 // to 128) or what its instructions take; the chunks take a whole chunk's time for every started one.  Dense
-// (us, recurrence / chunks), N = 32: 1 x 32 heads of 128 10.8 / 13.0, 64 x 32 296 / 366; 1 x 8 heads of 64
-// 9.3 / 10.7, 64 x 8 28 / 48; 1 x 70 heads of 32 8.5 / 10.5, 64 x 70 82 / 238.  N = 48: 15.0 / 13.0, 428 / 370,
-// 12.9 / 10.8, 40 / 48, 11.9 / 10.6, 119 / 242.  N = 64: 18.9 / 12.9, 560 / 377, 16.4 / 10.8, 52 / 49,
-// 15.0 / 10.7, 156 / 248.
-// Packed lengths are known to the device only: the recurrence where they are 8 on the average
-// (16 sequences, 125 tokens, the longest of 30, 8 heads of 64: 12 / 23; 64 sequences of 8: 101 / 359, 10 / 48
-// and 26 / 232 at the three widths) and the longest can be no more than 512 (0.13 ms).
+// (us in a graph, recurrence / chunks), N = 32: 1 x 32 heads of 128 12 / 17, 64 x 32 291 / 381; 1 x 8 heads of 64
+// 10 / 14, 64 x 8 30 / 55; 1 x 70 heads of 32 10 / 14, 64 x 70 83 / 274.  N = 48: 17 / 17, 424 / 385,
+// 14 / 14, 42 / 56, 14 / 14, 121 / 277.  N = 64: 21 / 17, 557 / 392, 19 / 14, 54 / 56, 17 / 14, 158 / 280.
+// Packed lengths are known to the device only, and all tokens may be one sequence's: the recurrence where
+// they are 8 on the average and no sequence can have more than 512 (the same heads: 64 sequences of 8
+// 105 / 385, 12 / 56, 29 / 271; one of 512 and 63 without tokens 295 / 201, 119 / 45, 128 / 105).  The rule
+// guards the second kind and gives up some of the first: 16 sequences of 12 take 107, 21 and 72 as chunks
+// where the recurrence would take 39, 8 and 12; 128 of 5 762, 103 and 519 where it would take 174, 18 and 44.
 constexpr int kRecurMaxTokens = 32, kRecurMaxMean = 8, kRecurMaxPacked = 512;
 bool delta_recurs(int nseq, int ntok, bool packed) {
   if (ntok <= kRecurMaxTokens) return true;
