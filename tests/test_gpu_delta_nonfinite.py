@@ -90,3 +90,38 @@ def test_a_state_before_the_sequence(N, d):
     assert torch.equal(out[[0, 2]], want[[0, 2]]) and torch.equal(state[[0, 2]], want_s[[0, 2]])
     assert torch.equal(out[1, :, 0], want[1, :, 0]) and torch.equal(state[1, 0], want_s[1, 0])
     assert not torch.isfinite(out[1, :, 1, 9]).any() and not torch.isfinite(state[1, 1, :, 9]).any()
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("name,value", [("k", NAN), ("v", INF), ("g", NAN), ("beta", INF), ("q", NAN)])
+def test_the_forward_of_a_training_step(name, value, d):
+    """It keeps to the same: the same bits as the forward alone, bad tokens and all"""
+    t = make([150] * 64, False, 1, 2, d, True, seed=d)
+    at = torch.arange(64, device="cuda")
+    t[name][at, 64 + at] = value
+    args = [t[n] for n in ("q", "k", "v", "g", "beta")]
+    out, state, _ = ll.lite_la_gated_delta_fwd_save(*args, state_in=t["state_in"])
+    want, want_s = fwd(t)
+    assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+    assert torch.equal(state.isnan(), want_s.isnan()) and torch.equal(state.nan_to_num(), want_s.nan_to_num())
+
+
+@pytest.mark.parametrize("name", ["k", "v", "g", "beta", "q", "dout"])
+def test_gradients_of_other_sequences(name):
+    """A bad token leaves the gradients of all other sequences as they are, bit for bit"""
+    t = make([100, 70, 64], True, 2, 4, 64, True, seed=3)
+
+    def grads():
+        args = [t[n] for n in ("q", "k", "v", "g", "beta")]
+        kw = dict(state_in=t["state_in"], cu_seqlens=t["cu"])
+        _, _, saved = ll.lite_la_gated_delta_fwd_save(*args, **kw)
+        got = ll.lite_la_gated_delta_bwd(*args, t["dout"], saved, dstate_out=t["dstate"], **kw)
+        ll.lite_la_device_status()
+        return got
+
+    want = grads()
+    t[name][0, 120] = NAN
+    got = grads()
+    for a, b in zip(got[:5], want[:5]):
+        assert torch.equal(a[:, :100], b[:, :100]) and torch.equal(a[:, 170:], b[:, 170:])
+    assert torch.equal(got[5][[0, 2]], want[5][[0, 2]])
