@@ -36,7 +36,7 @@ struct DeltaGrads {
   const float* dstate_out;         // [sequence][Hv][d][d] or null (zeros)
   float* dstate_in;                // or null
   // between the two kernels, per chunk slot and value head
-  uint8_t* gstates;                // G' as DeltaSaved's states
+  uint8_t* gstates;                // G', two terms, as the first tiles of DeltaSaved's states
   float* y;                        // [d / 32] tiles of 64 rows of 32 columns, placed by y_off
   float* rows;                     // [d / 32][2][2][64]: w . W and b of half of 32 columns
   float* ends;                     // [d / 32][8]: shares of <S0, G'>

@@ -18,7 +18,7 @@
 // entered in three bf16 terms (each the rounding of what the ones before it leave: 2^-9, 2^-17 and 2^-25
 // relative), all products of terms that reach 2^-25 of the first, summed in fp32: states are 1 to 3e-7 off
 // against 64 bits, as with plain fp32 operations.  With two terms of X, P T and of the blocks that X is made of
-// they were up to 2e-6 off (d = 32); the third costs the blocks a fifth (16384 tokens, 32 heads of 128: 209 ->
+// they were up to 2e-6 off (d = 32); the third costs the blocks a fifth to a quarter (16384 tokens, 32 heads of 128: 209 ->
 // 249 us) and the chain 6 % (532 -> 564).  K, Q and V are bf16 already.  G is summed in fp64: differences
 // of large sums of decays would lose in fp32.
 //
