@@ -3,10 +3,11 @@
 Like the rest of the binding this module only marshals arguments to the C ABI (include/litela.h
 has the formulas, the layouts and the rules); outputs and workspaces come from torch, so every call
 can be captured into a CUDA graph and two calls share nothing.  A call with `stream` runs on that
-stream, which the caller has made wait for the inputs (and for which it keeps them), and takes its buffers
-from that stream's memory.  Buffers that a caller gives to be written count as modified for autograd.  To capture a training step, capture
-the _fwd_save and _bwd calls or torch.autograd.grad: torch's .backward() may not accumulate, inside a
-capture, into leaves that a graph of eager calls still holds.  The functions are reached through the
+stream, which the caller has made wait for the inputs (and for which it keeps them), and takes its
+buffers from that stream's memory.  Buffers that a caller gives to be written count as modified for
+autograd.  To capture a training step, capture the _fwd_save and _bwd calls or torch.autograd.grad:
+torch's .backward() may not accumulate, inside a capture, into leaves that a graph of eager calls still
+holds.  The functions are reached through the
 package:
 
     from linear_attention_diffusion_litela_b200 import lite_la_qk_norm_rope, lite_la_gated_delta
